@@ -389,6 +389,191 @@ muon_status_t muon_newton_schulz_batched_noalloc(int device, void* stream,
 const char* muon_noalloc_last_error(void);
 
 /* ------------------------------------------------------------------------ */
+/* The losses in front of the step: log-probabilities of chosen tokens       */
+/* ------------------------------------------------------------------------ */
+
+/* A batch of rows of scores over a vocabulary: element (b, t, v) at data +
+ * (b * batch_stride + t * row_stride + v) elements of `dtype`; strides in
+ * elements, so that a padded vocabulary (row_stride > vocab), logits shifted
+ * against their labels (a batch_stride longer than seq rows) and sequence-major
+ * storage are all described without a copy.  Inputs may overlap themselves
+ * (strides of 0 included); rows that are written must be disjoint.  Strides
+ * are >= 0; that of a dimension of size one is ignored. */
+typedef struct {
+  void* data;
+  int32_t dtype;                    /* MUON_BF16 or MUON_F32 */
+  int64_t batch, seq, vocab;        /* vocab in [1, 2^30], batch * seq <= 2^30 */
+  int64_t batch_stride, row_stride; /* elements */
+} muon_logits_t;
+
+/* Conventions of the calls below, beside those of every entry point.
+ *   - R = batch * seq tokens; arrays "per token" are dense [batch][seq].
+ *   - labels (device, int64 per token): the chosen token of each row.  A
+ *     negative label leaves the token out: its row is not read, nothing of it
+ *     enters a sum (whatever the other per-token inputs hold there), its
+ *     log-probability is 0 and its gradient row is zeros.  A label >= vocab
+ *     names no score: the token's log-probability and gradient are NaN.
+ *   - z = x / temperature are the scores that the softmax sees; temperature
+ *     > 0 and finite.  Scores of -infinity have probability 0; a row of
+ *     nothing else, or with NaN or +infinity in it, gives NaN, as the formula
+ *     does.
+ *   - Sums over a vocabulary run in fp32 in a fixed order around the row's
+ *     maximum; log-probabilities are formed, and everything per token or
+ *     sequence summed, in binary64 and rounded to fp32 once when stored.
+ *     Two calls on identical inputs, rows at the same alignment to 16 bytes,
+ *     give identical bits.
+ *   - Gradients are of `weight` times the loss with respect to x and have
+ *     x's dtype (fp32 arithmetic, one rounding).  They may replace the scores
+ *     in place (same address, strides and dtype); any other overlap between
+ *     what a call writes and what it reads or also writes is refused.
+ *   - The context's workspace holds what the kernels hand each other
+ *     (muon_loss_workspace_bytes), so calls on one context are ordered.  Every
+ *     call may be recorded into a HIP graph.
+ * Errors of all of them: MUON_EINVAL (ctx or another required pointer NULL,
+ * misaligned pointers, bad parameters, overlaps), MUON_ESHAPE, MUON_EDTYPE,
+ * MUON_EWORKSPACE, MUON_EHIP.  A batch or seq of 0 is no error: the losses of
+ * no token follow (and 0 for no pair), per-token arrays are empty and may be
+ * NULL. */
+
+/* Workspace in bytes of any one of the loss calls on batch x seq tokens (pure
+ * host function; 0 for sizes out of range). */
+size_t muon_loss_workspace_bytes(int64_t batch, int64_t seq);
+
+/* Log-probability of every token: logps[t] = z[y] - log sum_v exp(z[v]).
+ * logps: fp32 per token.  row_stats (may be NULL): two floats per token, the
+ * row's maximum score and its sum of exponentials around it, which
+ * muon_token_logps_backward takes. */
+muon_status_t muon_token_logps(muon_ctx_t* ctx, void* stream, const muon_logits_t* logits,
+                               const int64_t* labels, float temperature, float* logps,
+                               float* row_stats);
+
+/* Its gradient: grad_logits[t][v] = grad_logps[t] / temperature *
+ * ([v = y] - exp(z[v]) / sum).  logits, labels, temperature as given to
+ * muon_token_logps, row_stats as it left them. */
+muon_status_t muon_token_logps_backward(muon_ctx_t* ctx, void* stream, const muon_logits_t* logits,
+                                        const int64_t* labels, float temperature,
+                                        const float* row_stats, const float* grad_logps,
+                                        const muon_logits_t* grad_logits);
+
+/* How the per-token terms l_t of the policy loss become one number.
+ *   MUON_REDUCE_TOKEN:    sum_t l_t / N over the N tokens that count
+ *   MUON_REDUCE_SEQUENCE: (1 / batch) sum_b (mean of l_t over b's tokens); a
+ *                         sequence with no token contributes 0
+ *   MUON_REDUCE_SUM:      sum_t l_t */
+typedef enum {
+  MUON_REDUCE_TOKEN = 0,
+  MUON_REDUCE_SEQUENCE = 1,
+  MUON_REDUCE_SUM = 2
+} muon_reduce_t;
+
+typedef struct {
+  float clip_low, clip_high;     /* ratio range [1 - clip_low, 1 + clip_high]; in [0, 1], >= 0 */
+  float kl_coef;                 /* >= 0; > 0 needs ref_logps */
+  float temperature;
+  float weight;                  /* factor of loss and gradient, e.g. 1 / accumulation steps */
+  int32_t reduce;                /* muon_reduce_t */
+  int32_t advantage_per_token;   /* advantages: 0 = [batch], 1 = per token */
+} muon_policy_params_t;
+
+/* Clipped policy loss with a KL term, and its gradient.  Per token that
+ * counts, with lp the policy's log-probability, A its advantage:
+ *     r  = exp(lp - old_logps)           (old_logps NULL: r = 1, its
+ *                                         gradient that of lp - constant)
+ *     pg = max(-A r, -A min(max(r, 1 - clip_low), 1 + clip_high))
+ *     kl = exp(e) - 1 - e,  e = ref_logps - lp       (ref_logps NULL: 0)
+ *     l  = pg + kl_coef kl,   dl/dlp = -A r [-A r >= the clipped one]
+ *                                      + kl_coef (1 - exp(e))
+ * out: four floats {weight * loss, and reduced as the loss is, without
+ * `weight`: pg, kl, [the clipped term is the larger]}.  logps (may be NULL): the log-probabilities, fp32 per token.
+ * grad_logits (may be NULL: no gradient is formed). */
+muon_status_t muon_policy_loss(muon_ctx_t* ctx, void* stream, const muon_logits_t* logits,
+                               const int64_t* labels, const muon_policy_params_t* params,
+                               const float* advantages, const float* old_logps,
+                               const float* ref_logps, float* out, float* logps,
+                               const muon_logits_t* grad_logits);
+
+/* MUON_PREFERENCE_SIGMOID: -(1 - s) log sigma(h) - s log sigma(-h), h = beta m
+ * MUON_PREFERENCE_IPO:     (m - 1 / (2 beta))^2 */
+typedef enum { MUON_PREFERENCE_SIGMOID = 0, MUON_PREFERENCE_IPO = 1 } muon_preference_t;
+
+typedef struct {
+  float beta;             /* > 0 */
+  float label_smoothing;  /* s, in [0, 0.5]; sigmoid only (else 0) */
+  float temperature;
+  float weight;           /* factor of loss and gradient */
+  int32_t kind;           /* muon_preference_t */
+  int32_t average;        /* 0: a sequence's score is the sum over its tokens, 1: the mean */
+} muon_preference_params_t;
+
+/* Preference loss over pairs, and its gradient.  batch = 2 P sequences:
+ * sequence i < P was preferred over sequence P + i.  With s_i the sum (or the
+ * mean) of lp - ref_logps over sequence i's tokens (ref_logps NULL: of lp; no
+ * token: 0) and the margin m = s_i - s_{P+i}, the loss is the mean of the
+ * pairs' terms (muon_preference_t).  out: three floats {weight * loss, mean of
+ * beta m, share of pairs with m > 0}.  rewards (may be NULL): beta s_i, fp32
+ * per sequence.  logps, grad_logits: as for muon_policy_loss.  An odd batch:
+ * MUON_ESHAPE. */
+muon_status_t muon_preference_loss(muon_ctx_t* ctx, void* stream, const muon_logits_t* logits,
+                                   const int64_t* labels, const muon_preference_params_t* params,
+                                   const float* ref_logps, float* out, float* rewards,
+                                   float* logps, const muon_logits_t* grad_logits);
+
+/* ------------------------------------------------------------------------ */
+/* Global gradient norm and clipping                                         */
+/* ------------------------------------------------------------------------ */
+
+/* One tensor of a list: numel contiguous elements at data (device), aligned to
+ * the element. */
+typedef struct {
+  void* data;
+  int64_t numel;   /* >= 0 */
+  int32_t dtype;   /* MUON_BF16 or MUON_F32 */
+} muon_tensor_t;
+
+/* Workspace in bytes of muon_grad_norm over these tensors (host array; pure
+ * host function; 0 when count <= 0 or an entry is invalid). */
+size_t muon_grad_norm_workspace_bytes(const muon_tensor_t* grads, int64_t count);
+
+/* Norm over all elements of `count` tensors of any mix of sizes and dtypes:
+ * norm (device, three doubles) receives {S, sqrt(S), coefficient}, S the sum
+ * of the squares of every element -- each square exact in binary64, summed in
+ * a fixed order, so the result is reproducible bit for bit and nothing
+ * overflows -- and coefficient = min(1, max_norm / (sqrt(S) + eps)), NaN when
+ * S is NaN.  max_norm > 0 (infinity: the coefficient of a finite S is 1), eps
+ * >= 0.  Where gradients are sharded, sum norm[0] over the ranks and call
+ * muon_clip_coef.  The tensor list is read during the call only (host array);
+ * it travels in kernel arguments, so the call may be recorded into a HIP
+ * graph.  count == 0: S = 0.  Errors: MUON_EINVAL, MUON_ESHAPE (numel < 0 or
+ * too large), MUON_EDTYPE, MUON_EWORKSPACE, MUON_EHIP. */
+muon_status_t muon_grad_norm(muon_ctx_t* ctx, void* stream, const muon_tensor_t* grads,
+                             int64_t count, double max_norm, double eps, double* norm);
+
+/* norm[1] and norm[2] from norm[0] (device), as muon_grad_norm forms them. */
+muon_status_t muon_clip_coef(muon_ctx_t* ctx, void* stream, double max_norm, double eps,
+                             double* norm);
+
+/* out[i] = c * grads[i] with c = norm[2] rounded to fp32 (device, read by the
+ * kernels: no host synchronisation), each product rounded to fp32 and then to
+ * out[i]'s dtype.  out NULL: in place; a coefficient of exactly 1 then writes
+ * nothing.  Otherwise out[i] has grads[i]'s numel, any dtype, and is disjoint
+ * from every other tensor of both lists (out[i] == grads[i], same dtype, is
+ * in place).  Errors: as for muon_grad_norm. */
+muon_status_t muon_scale_grads(muon_ctx_t* ctx, void* stream, const muon_tensor_t* grads,
+                               const muon_tensor_t* out, int64_t count, const double* norm);
+
+/* muon_momentum_update_sq on the clipped gradient g' = c * g (one binary32
+ * rounding), c = norm[2] rounded to binary32, norm as muon_grad_norm leaves it
+ * on the device: the momentum pass reads the gradient anyway, so clipping
+ * costs no pass of its own and the gradient stays as it is.  sq_partials may
+ * be NULL (no partials).  Errors: those of muon_momentum_update_sq, and
+ * MUON_EINVAL for a NULL or misaligned norm. */
+muon_status_t muon_momentum_update_clipped(muon_ctx_t* ctx, void* stream, const void* grad,
+                                           int32_t grad_dtype, float* momentum, void* update_out,
+                                           int32_t update_dtype, int64_t numel, float beta,
+                                           int32_t nesterov, const double* norm,
+                                           double* sq_partials);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics                                                               */
 /* ------------------------------------------------------------------------ */
 
@@ -396,8 +581,9 @@ const char* muon_noalloc_last_error(void);
  * enum).  Error reporting is part of the per-bucket diagnostics the blog's
  * section "Metrics to record" asks for. */
 const char* muon_status_string(muon_status_t s);
-/* Text of the last error recorded on ctx (empty string when none; NULL ctx
- * gives a static text), blog section "Metrics to record". */
+/* Text of the last error recorded on ctx (empty string when none), blog
+ * section "Metrics to record".  NULL ctx: a static text, that of the calling
+ * thread's last refusal of a call made without a context (empty when none). */
 const char* muon_last_error(const muon_ctx_t* ctx);
 
 /* Per-kernel-class timing with HIP events recorded on the launch stream
@@ -414,7 +600,9 @@ typedef enum {
   MUON_K_APPLY = 5,
   MUON_K_PROD = 6,   /* m x m products of MUON_NS_GRAM (P_k Q_k, P_k A_k, (P_k A_k) P_k) */
   MUON_K_FUSED = 7,  /* whole-iteration launches of small units (muon_fuse_t) */
-  MUON_K_COUNT = 8
+  MUON_K_LOSS = 8,   /* token log-probabilities, the losses and their gradients */
+  MUON_K_CLIP = 9,   /* global gradient norm and gradient scaling */
+  MUON_K_COUNT = 10
 } muon_kernel_class_t;
 
 muon_status_t muon_timing_enable(muon_ctx_t* ctx, int32_t enable, int32_t capacity);

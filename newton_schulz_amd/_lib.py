@@ -11,7 +11,8 @@ MUON_OK, MUON_EINVAL, MUON_ESHAPE, MUON_EDTYPE, MUON_EWORKSPACE, MUON_EHIP, MUON
 MUON_F32, MUON_BF16 = 0, 1
 MUON_CAP_FULL_BYTES, MUON_CAP_WORKSPACE = 0, 1
 MUON_NOALLOC_SCRATCH_BYTES = 256 << 20
-KERNEL_CLASSES = ["momentum", "norm", "gram", "symsq", "update", "apply", "prod", "fused"]
+KERNEL_CLASSES = ["momentum", "norm", "gram", "symsq", "update", "apply", "prod", "fused",
+                  "loss", "clip"]
 
 # every symbol include/muon.h declares
 EXPORTS = [
@@ -23,6 +24,9 @@ EXPORTS = [
     "muon_timing_enable", "muon_timing_select", "muon_timing_reset", "muon_timing_read",
     "muon_newton_schulz_batched_noalloc", "muon_noalloc_last_error",
     "muon_plan", "muon_plan_total_elems", "muon_workspace_bytes",
+    "muon_loss_workspace_bytes", "muon_token_logps", "muon_token_logps_backward",
+    "muon_policy_loss", "muon_preference_loss", "muon_grad_norm_workspace_bytes",
+    "muon_grad_norm", "muon_clip_coef", "muon_scale_grads", "muon_momentum_update_clipped",
 ]
 
 
@@ -47,6 +51,27 @@ class BucketInfo(ctypes.Structure):
                 ("elem_offset", ctypes.c_int64)]
 
 
+class Logits(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("batch", ctypes.c_int64),
+                ("seq", ctypes.c_int64), ("vocab", ctypes.c_int64), ("batch_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64)]
+
+
+class PolicyParams(ctypes.Structure):
+    _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
+                ("temperature", ctypes.c_float), ("weight", ctypes.c_float), ("reduce", ctypes.c_int32),
+                ("advantage_per_token", ctypes.c_int32)]
+
+
+class PreferenceParams(ctypes.Structure):
+    _fields_ = [("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float), ("temperature", ctypes.c_float),
+                ("weight", ctypes.c_float), ("kind", ctypes.c_int32), ("average", ctypes.c_int32)]
+
+
+class Tensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
 _LIB = None
 
 
@@ -61,7 +86,7 @@ def load() -> ctypes.CDLL:
             "`python -c 'import __graft_entry__ as g; g.build()'` (hipcc, gfx950)")
     lib = ctypes.CDLL(LIB_PATH)
     vp, i32, i64, sz, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
-    P = ctypes.POINTER
+    f64, P = ctypes.c_double, ctypes.POINTER
     sig = {
         "muon_create": (i32, [ctypes.c_int, sz, P(vp)]),
         "muon_destroy": (i32, [vp]),
@@ -91,6 +116,16 @@ def load() -> ctypes.CDLL:
         "muon_newton_schulz_batched_noalloc": (i32, [ctypes.c_int, vp, P(vp), i64, Shape, i32,
                                                       P(NsParams), P(vp), vp]),
         "muon_noalloc_last_error": (ctypes.c_char_p, []),
+        "muon_loss_workspace_bytes": (sz, [i64, i64]),
+        "muon_token_logps": (i32, [vp, vp, P(Logits), vp, f32, vp, vp]),
+        "muon_token_logps_backward": (i32, [vp, vp, P(Logits), vp, f32, vp, vp, P(Logits)]),
+        "muon_policy_loss": (i32, [vp, vp, P(Logits), vp, P(PolicyParams), vp, vp, vp, vp, vp, P(Logits)]),
+        "muon_preference_loss": (i32, [vp, vp, P(Logits), vp, P(PreferenceParams), vp, vp, vp, vp, P(Logits)]),
+        "muon_grad_norm_workspace_bytes": (sz, [P(Tensor), i64]),
+        "muon_grad_norm": (i32, [vp, vp, P(Tensor), i64, f64, f64, vp]),
+        "muon_clip_coef": (i32, [vp, vp, f64, f64, vp]),
+        "muon_scale_grads": (i32, [vp, vp, P(Tensor), P(Tensor), i64, vp]),
+        "muon_momentum_update_clipped": (i32, [vp, vp, vp, i32, vp, vp, i32, i64, f32, i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)

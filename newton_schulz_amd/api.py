@@ -13,7 +13,10 @@ from typing import List, Optional, Sequence, Tuple
 import torch
 
 from . import _lib
-from ._lib import MUON_BF16, MUON_CAP_FULL_BYTES, MUON_CAP_WORKSPACE, MUON_F32, NsParams, Shape
+from ._lib import (
+    MUON_BF16, MUON_CAP_FULL_BYTES, MUON_CAP_WORKSPACE, MUON_F32, Logits, NsParams, PolicyParams,
+    PreferenceParams, Shape, Tensor,
+)
 
 
 class MuonError(RuntimeError):
@@ -136,6 +139,63 @@ def newton_schulz_noalloc(mats: Sequence[torch.Tensor], out: Optional[Sequence[t
         raise MuonError(st, f"muon_newton_schulz_batched_noalloc: {lib.muon_noalloc_last_error().decode()}")
 
 
+LOSS_REDUCE = {"token": 0, "sequence": 1, "sum": 2}
+PREFERENCE_KINDS = {"sigmoid": 0, "ipo": 1}
+
+
+def loss_workspace_bytes(batch: int, seq: int) -> int:
+    """Workspace a context needs for any loss call on batch x seq tokens."""
+    return int(_lib.load().muon_loss_workspace_bytes(batch, seq))
+
+
+def grad_norm_workspace_bytes(tensors: Sequence[torch.Tensor]) -> int:
+    """Workspace a context needs for grad_norm over these tensors."""
+    arr = (Tensor * max(len(tensors), 1))(*[Tensor(t.data_ptr(), t.numel(), _dtype(t)) for t in tensors])
+    return int(_lib.load().muon_grad_norm_workspace_bytes(arr, len(tensors)))
+
+
+def _logits(t: torch.Tensor, name: str, device: torch.device) -> Logits:
+    """Scores as [batch, seq, vocab] or [rows, vocab]: any strides, the
+    vocabulary contiguous."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        shape, stride = (1, *shape), (0, *stride)
+    elif len(shape) != 3:
+        raise ValueError(f"{name} must be [batch, seq, vocab] or [rows, vocab]")
+    if shape[2] > 1 and stride[2] != 1:
+        raise ValueError(f"the vocabulary of {name} must be contiguous")
+    return Logits(t.data_ptr(), _dtype(t), shape[0], shape[1], shape[2], stride[0], stride[1])
+
+
+def _tokens(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype, device: torch.device):
+    """Device address of a dense per-token (or per-sequence) array, or None."""
+    if t is None:
+        return None
+    _check(t, name, device)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+class TensorList:
+    """A list of tensors as libmuon takes it (Context.tensor_list): made once
+    for tensors that stay where they are, kept while they live."""
+
+    def __init__(self, tensors: Sequence[torch.Tensor], device: torch.device):
+        for i, t in enumerate(tensors):
+            _check(t, f"tensors[{i}]", device)
+        self.tensors = list(tensors)
+        self.array = (Tensor * max(len(self.tensors), 1))(
+            *[Tensor(t.data_ptr(), t.numel(), _dtype(t)) for t in self.tensors])
+
+    def __len__(self):
+        return len(self.tensors)
+
+
 class Context:
     """A libmuon context: one device and one preallocated workspace slab."""
 
@@ -169,9 +229,12 @@ class Context:
     # -- the three steps ----------------------------------------------------
     def momentum_update(self, grad: torch.Tensor, momentum: torch.Tensor, update_out: torch.Tensor,
                         beta: float = 0.95, nesterov: bool = True, stream=None,
-                        sq_partials: Optional[torch.Tensor] = None):
+                        sq_partials: Optional[torch.Tensor] = None,
+                        grad_scale: Optional[torch.Tensor] = None):
         """Momentum step; with `sq_partials` (float64, ceil(numel / 4096)
-        elements) also the per-block sums of squares of the stored update."""
+        elements) also the per-block sums of squares of the stored update;
+        with `grad_scale` (grad_norm's float64 triple) on the gradient times
+        the clip coefficient in it."""
         for t, n in ((grad, "grad"), (momentum, "momentum"), (update_out, "update_out")):
             _check(t, n, self.device)
         if momentum.dtype != torch.float32:
@@ -182,13 +245,18 @@ class Context:
         args = (self.handle, _stream(self.device, stream), ctypes.c_void_p(grad.data_ptr()), _dtype(grad),
                 ctypes.c_void_p(momentum.data_ptr()), ctypes.c_void_p(update_out.data_ptr()),
                 _dtype(update_out), numel, float(beta), 1 if nesterov else 0)
-        if sq_partials is None:
-            st = self.lib.muon_momentum_update(*args)
-        else:
+        sq = None
+        if sq_partials is not None:
             _check(sq_partials, "sq_partials", self.device)
             if sq_partials.dtype != torch.float64 or sq_partials.numel() < sq_blocks(numel):
                 raise ValueError(f"sq_partials must be float64 with at least {sq_blocks(numel)} elements")
-            st = self.lib.muon_momentum_update_sq(*args, ctypes.c_void_p(sq_partials.data_ptr()))
+            sq = ctypes.c_void_p(sq_partials.data_ptr())
+        if grad_scale is not None:
+            st = self.lib.muon_momentum_update_clipped(*args, self._norm(grad_scale), sq)
+        elif sq is not None:
+            st = self.lib.muon_momentum_update_sq(*args, sq)
+        else:
+            st = self.lib.muon_momentum_update(*args)
         self._raise(st, "muon_momentum_update")
 
     def newton_schulz(self, mats: Sequence[torch.Tensor], out: Optional[Sequence[torch.Tensor]] = None,
@@ -263,6 +331,145 @@ class Context:
                                  ctypes.c_void_p(master.data_ptr()), ctypes.c_void_p(update.data_ptr()),
                                  _dtype(update), wb, numel, float(lr), float(scale), float(weight_decay))
         self._raise(st, "muon_apply")
+
+    # -- the losses in front of the step --------------------------------------
+    def token_logps(self, logits: torch.Tensor, labels: torch.Tensor, logps: torch.Tensor,
+                    row_stats: Optional[torch.Tensor] = None, temperature: float = 1.0, stream=None):
+        """Log-probability of every row's label under softmax(logits /
+        temperature) into `logps` (float32, the labels' shape; 0 where the
+        label is negative).  `row_stats` (float32, [..., 2]) keeps what
+        token_logps_backward needs of each row."""
+        x, shape = _logits(logits, "logits", self.device), logits.shape[:-1]
+        st = self.lib.muon_token_logps(
+            self.handle, _stream(self.device, stream), ctypes.byref(x),
+            _tokens(labels, "labels", shape, torch.int64, self.device), temperature,
+            _tokens(logps, "logps", shape, torch.float32, self.device),
+            _tokens(row_stats, "row_stats", (*shape, 2), torch.float32, self.device))
+        self._raise(st, "muon_token_logps")
+
+    def token_logps_backward(self, logits: torch.Tensor, labels: torch.Tensor, row_stats: torch.Tensor,
+                             grad_logps: torch.Tensor, grad_logits: torch.Tensor,
+                             temperature: float = 1.0, stream=None):
+        """Gradient of token_logps into `grad_logits` (the logits' dtype; may
+        be the logits themselves)."""
+        x, shape = _logits(logits, "logits", self.device), logits.shape[:-1]
+        gx = self._grad(logits, grad_logits)
+        st = self.lib.muon_token_logps_backward(
+            self.handle, _stream(self.device, stream), ctypes.byref(x),
+            _tokens(labels, "labels", shape, torch.int64, self.device), temperature,
+            _tokens(row_stats, "row_stats", (*shape, 2), torch.float32, self.device),
+            _tokens(grad_logps, "grad_logps", shape, torch.float32, self.device), ctypes.byref(gx))
+        self._raise(st, "muon_token_logps_backward")
+
+    def policy_loss(self, logits: torch.Tensor, labels: torch.Tensor, advantages: torch.Tensor,
+                    out: torch.Tensor, old_logps: Optional[torch.Tensor] = None,
+                    ref_logps: Optional[torch.Tensor] = None, logps: Optional[torch.Tensor] = None,
+                    grad_logits: Optional[torch.Tensor] = None, clip_low: float = 0.2,
+                    clip_high: float = 0.2, kl_coef: float = 0.0, reduce: str = "token",
+                    weight: float = 1.0, temperature: float = 1.0, stream=None):
+        """Clipped policy loss with a KL term, and the gradient of weight *
+        loss in the logits (`grad_logits`; None: none is formed; may be the
+        logits themselves).  advantages: float32, one per sequence ([batch])
+        or per token.  old_logps None: the logits' own policy.  out: four
+        float32 {weight * loss, policy term, KL, share clipped}.  reduce:
+        "token", "sequence" or "sum"."""
+        x, shape = _logits(logits, "logits", self.device), logits.shape[:-1]
+        gx = self._grad(logits, grad_logits)
+        if reduce not in LOSS_REDUCE:
+            raise ValueError(f"unknown reduction {reduce!r}; one of {list(LOSS_REDUCE)}")
+        # 2-D logits are one sequence of rows
+        sequences = (x.batch,)
+        per_token = advantages.shape != sequences
+        p = PolicyParams(clip_low, clip_high, kl_coef, temperature, weight, LOSS_REDUCE[reduce], 1 if per_token else 0)
+        st = self.lib.muon_policy_loss(
+            self.handle, _stream(self.device, stream), ctypes.byref(x),
+            _tokens(labels, "labels", shape, torch.int64, self.device), ctypes.byref(p),
+            _tokens(advantages, "advantages", shape if per_token else sequences, torch.float32, self.device),
+            _tokens(old_logps, "old_logps", shape, torch.float32, self.device),
+            _tokens(ref_logps, "ref_logps", shape, torch.float32, self.device),
+            _tokens(out, "out", (4,), torch.float32, self.device),
+            _tokens(logps, "logps", shape, torch.float32, self.device),
+            None if gx is None else ctypes.byref(gx))
+        self._raise(st, "muon_policy_loss")
+
+    def preference_loss(self, logits: torch.Tensor, labels: torch.Tensor,
+                        ref_logps: Optional[torch.Tensor], out: torch.Tensor,
+                        rewards: Optional[torch.Tensor] = None, logps: Optional[torch.Tensor] = None,
+                        grad_logits: Optional[torch.Tensor] = None, kind: str = "sigmoid",
+                        beta: float = 0.1, label_smoothing: float = 0.0, average: bool = False,
+                        weight: float = 1.0, temperature: float = 1.0, stream=None):
+        """Preference loss over batch / 2 pairs (sequence i was preferred over
+        sequence batch / 2 + i), and the gradient of weight * loss in the
+        logits.  ref_logps None: no reference.  out: three float32 {weight *
+        loss, mean of beta * margin, share of pairs ranked right}.  rewards:
+        float32 [batch], beta times each sequence's score.  kind: "sigmoid" or
+        "ipo"; average: scores are means over a sequence's tokens."""
+        x, shape = _logits(logits, "logits", self.device), logits.shape[:-1]
+        gx = self._grad(logits, grad_logits)
+        if kind not in PREFERENCE_KINDS:
+            raise ValueError(f"unknown preference loss {kind!r}; one of {list(PREFERENCE_KINDS)}")
+        p = PreferenceParams(beta, label_smoothing, temperature, weight, PREFERENCE_KINDS[kind], 1 if average else 0)
+        st = self.lib.muon_preference_loss(
+            self.handle, _stream(self.device, stream), ctypes.byref(x),
+            _tokens(labels, "labels", shape, torch.int64, self.device), ctypes.byref(p),
+            _tokens(ref_logps, "ref_logps", shape, torch.float32, self.device),
+            _tokens(out, "out", (3,), torch.float32, self.device),
+            _tokens(rewards, "rewards", (x.batch,), torch.float32, self.device),
+            _tokens(logps, "logps", shape, torch.float32, self.device),
+            None if gx is None else ctypes.byref(gx))
+        self._raise(st, "muon_preference_loss")
+
+    def _grad(self, logits: torch.Tensor, grad_logits: Optional[torch.Tensor]) -> Optional[Logits]:
+        if grad_logits is None:
+            return None
+        if grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype:
+            raise ValueError("grad_logits must have the logits' shape and dtype")
+        return _logits(grad_logits, "grad_logits", self.device)
+
+    # -- gradient norm and clipping -------------------------------------------
+    def tensor_list(self, tensors: Sequence[torch.Tensor]) -> TensorList:
+        """`tensors` as grad_norm and scale_grads take them, described once
+        (those take a plain sequence too and describe it at each call)."""
+        return TensorList(tensors, self.device)
+
+    def _list(self, tensors) -> TensorList:
+        return tensors if isinstance(tensors, TensorList) else TensorList(tensors, self.device)
+
+    def _norm(self, norm: torch.Tensor) -> int:
+        return _tokens(norm, "norm", (3,), torch.float64, self.device)
+
+    def grad_norm(self, grads, norm: torch.Tensor, max_norm: float = float("inf"), eps: float = 1e-6, stream=None):
+        """Global norm of a list of tensors: `norm` (float64 [3]) receives the
+        sum of squares, its root, and min(1, max_norm / (root + eps))."""
+        grads = self._list(grads)
+        st = self.lib.muon_grad_norm(self.handle, _stream(self.device, stream), grads.array, len(grads),
+                                     max_norm, eps, self._norm(norm))
+        self._raise(st, "muon_grad_norm")
+
+    def clip_coef(self, norm: torch.Tensor, max_norm: float, eps: float = 1e-6, stream=None):
+        """norm[1:] from norm[0], e.g. after it was summed over ranks."""
+        st = self.lib.muon_clip_coef(self.handle, _stream(self.device, stream), max_norm, eps, self._norm(norm))
+        self._raise(st, "muon_clip_coef")
+
+    def scale_grads(self, grads, norm: torch.Tensor, out=None, stream=None):
+        """grads times the coefficient in `norm`, in place or into the tensors
+        `out` (either dtype)."""
+        grads = self._list(grads)
+        dst = None
+        if out is not None:
+            out = self._list(out)
+            if len(out) != len(grads):
+                raise ValueError("out must have one tensor per gradient")
+            dst = out.array
+        st = self.lib.muon_scale_grads(self.handle, _stream(self.device, stream), grads.array, dst, len(grads),
+                                       self._norm(norm))
+        self._raise(st, "muon_scale_grads")
+
+    def clip_grads(self, grads, norm: torch.Tensor, max_norm: float, eps: float = 1e-6, out=None, stream=None):
+        """grad_norm, then scale_grads."""
+        grads = self._list(grads)
+        self.grad_norm(grads, norm, max_norm, eps, stream)
+        self.scale_grads(grads, norm, out, stream)
 
     # -- timing ---------------------------------------------------------------
     def timing_enable(self, enable: bool = True, capacity: int = 8192):

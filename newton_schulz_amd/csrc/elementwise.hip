@@ -109,13 +109,18 @@ __device__ __forceinline__ double block_sum(double v) {
   return (ws[0] + ws[1]) + (ws[2] + ws[3]);
 }
 
-template <typename G, typename U, bool SQ>
+// CLIP: the gradient is first multiplied by the clip coefficient norm[2]
+// (grad_clip.hip leaves it on the device), rounded to binary32.  The pass
+// stays bound by HBM: one multiplication an element more.
+template <typename G, typename U, bool SQ, bool CLIP>
 __global__ __launch_bounds__(EW_BS) void momentum_vec_kernel(const G* __restrict__ grad,
                                                              float* __restrict__ mom,
                                                              U* __restrict__ upd, int64_t numel,
                                                              float beta, float c1, int nesterov,
-                                                             double* __restrict__ sq) {
+                                                             double* __restrict__ sq,
+                                                             const double* __restrict__ norm) {
   const bool nes = nesterov != 0;
+  const float clip = CLIP ? static_cast<float>(norm[2]) : 1.0f;
   const int64_t nvec = numel / 8;
   const int64_t base = static_cast<int64_t>(blockIdx.x) * (EW_U * EW_BS) + threadIdx.x;
   double acc = 0.0;
@@ -135,7 +140,8 @@ __global__ __launch_bounds__(EW_BS) void momentum_vec_kernel(const G* __restrict
     if (i < nvec) {
       Vec8<U> u;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) momentum_one(g[k].v[e], m[k].v[e], u.v[e], beta, c1, nes);
+      for (int e = 0; e < 8; ++e)
+        momentum_one(CLIP ? clip * g[k].v[e] : g[k].v[e], m[k].v[e], u.v[e], beta, c1, nes);
       // the momentum is next read a whole step later: do not keep it cached;
       // U is read next by a launch that streams far more than the caches
       // hold (non-temporal stores measured 1% faster here, and no slower for
@@ -155,7 +161,8 @@ __global__ __launch_bounds__(EW_BS) void momentum_vec_kernel(const G* __restrict
   if (blockIdx.x == gridDim.x - 1) {
     for (int64_t i = nvec * 8 + threadIdx.x; i < numel; i += EW_BS) {
       float mm = mom[i], u;
-      momentum_one(muon::Elem<G>::load(grad + i), mm, u, beta, c1, nes);
+      const float gi = muon::Elem<G>::load(grad + i);
+      momentum_one(CLIP ? clip * gi : gi, mm, u, beta, c1, nes);
       mom[i] = mm;
       muon::Elem<U>::store(upd + i, u);
       if (SQ) acc += sq64(muon::Elem<U>::round(u));
@@ -183,17 +190,20 @@ __global__ __launch_bounds__(EW_BS) void sq_blocks_kernel(const U* __restrict__ 
   if (threadIdx.x == 0) sq[blockIdx.x] = t;
 }
 
-template <typename G, typename U>
+template <typename G, typename U, bool CLIP>
 __global__ __launch_bounds__(256) void momentum_scalar_kernel(const G* __restrict__ grad,
                                                               float* __restrict__ mom,
                                                               U* __restrict__ upd, int64_t numel,
-                                                              float beta, float c1, int nesterov) {
+                                                              float beta, float c1, int nesterov,
+                                                              const double* __restrict__ norm) {
+  const float clip = CLIP ? static_cast<float>(norm[2]) : 1.0f;
   const int64_t tid = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
   const int64_t nth = static_cast<int64_t>(gridDim.x) * blockDim.x;
   const bool nes = nesterov != 0;
   for (int64_t i = tid; i < numel; i += nth) {
     float m = mom[i], u;
-    momentum_one(muon::Elem<G>::load(grad + i), m, u, beta, c1, nes);
+    const float gi = muon::Elem<G>::load(grad + i);
+    momentum_one(CLIP ? clip * gi : gi, m, u, beta, c1, nes);
     mom[i] = m;
     muon::Elem<U>::store(upd + i, u);
   }
@@ -283,29 +293,39 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 }  // namespace
 
+namespace {
+
+template <typename G, typename U, bool CLIP>
+void momentum_launches(hipStream_t s, int cus, const G* grad, float* mom, U* upd, int64_t numel,
+                       float beta, float c1, int nesterov, double* sq, const double* norm) {
+  if (aligned(grad, 16) && aligned(mom, 16) && aligned(upd, 16)) {
+    if (sq)
+      momentum_vec_kernel<G, U, true, CLIP><<<vec_grid(numel), EW_BS, 0, s>>>(
+          grad, mom, upd, numel, beta, c1, nesterov, sq, norm);
+    else
+      momentum_vec_kernel<G, U, false, CLIP><<<vec_grid(numel), EW_BS, 0, s>>>(
+          grad, mom, upd, numel, beta, c1, nesterov, nullptr, norm);
+    return;
+  }
+  momentum_scalar_kernel<G, U, CLIP><<<stream_grid(numel, cus), 256, 0, s>>>(
+      grad, mom, upd, numel, beta, c1, nesterov, norm);
+  if (sq) sq_blocks_kernel<U><<<vec_grid(numel), EW_BS, 0, s>>>(upd, numel, sq);
+}
+
+}  // namespace
+
 hipError_t launch_momentum(hipStream_t s, int cus, const void* grad, int gdt, float* mom,
                            void* upd, int udt, int64_t numel, float beta, float c1,
-                           int nesterov, double* sq) {
+                           int nesterov, double* sq, const double* norm) {
   if (numel <= 0) return hipSuccess;
   // one workgroup per 4096 elements must fit a 1-D grid
   if ((numel + MUON_SQ_BLOCK - 1) / MUON_SQ_BLOCK > 0x7fffffff) return hipErrorInvalidValue;
-  const bool vec = aligned(grad, 16) && aligned(mom, 16) && aligned(upd, 16);
-#define MUON_MOM(G, U)                                                                        \
-  do {                                                                                        \
-    if (vec && sq)                                                                            \
-      momentum_vec_kernel<G, U, true><<<vec_grid(numel), EW_BS, 0, s>>>(                      \
-          static_cast<const G*>(grad), mom, static_cast<U*>(upd), numel, beta, c1, nesterov,  \
-          sq);                                                                                \
-    else if (vec)                                                                             \
-      momentum_vec_kernel<G, U, false><<<vec_grid(numel), EW_BS, 0, s>>>(                     \
-          static_cast<const G*>(grad), mom, static_cast<U*>(upd), numel, beta, c1, nesterov,  \
-          nullptr);                                                                           \
-    else                                                                                      \
-      momentum_scalar_kernel<G, U><<<stream_grid(numel, cus), 256, 0, s>>>(                   \
-          static_cast<const G*>(grad), mom, static_cast<U*>(upd), numel, beta, c1, nesterov);  \
-    if (!vec && sq)                                                                           \
-      sq_blocks_kernel<U><<<vec_grid(numel), EW_BS, 0, s>>>(static_cast<const U*>(upd), numel, \
-                                                             sq);                             \
+#define MUON_MOM(G, U)                                                                             \
+  do {                                                                                             \
+    const G* g = static_cast<const G*>(grad);                                                      \
+    U* u = static_cast<U*>(upd);                                                                   \
+    if (norm) momentum_launches<G, U, true>(s, cus, g, mom, u, numel, beta, c1, nesterov, sq, norm); \
+    else momentum_launches<G, U, false>(s, cus, g, mom, u, numel, beta, c1, nesterov, sq, nullptr); \
   } while (0)
   if (gdt == 1 && udt == 1) MUON_MOM(bf16_t, bf16_t);
   else if (gdt == 1 && udt == 0) MUON_MOM(bf16_t, float);

@@ -1,0 +1,289 @@
+// Global gradient norm over a list of tensors, and scaling by the clip
+// coefficient.
+//
+// S = sum of g^2 over every element of every tensor, each square exact in
+// binary64 (bf16 and fp32 values have at most 24 significant bits), norm =
+// sqrt S, coefficient = min(1, max_norm / (norm + eps)).  The tensors are cut
+// into chunks of one workgroup each; a chunk leaves one partial sum, and one
+// workgroup adds the partials.  Every sum runs in a fixed order.
+//
+// Both kernels are HBM-bound streams.  The list travels in the kernel
+// arguments (kTabTensors entries per launch): no table has to be uploaded, so
+// the calls can be recorded into a graph, and a list of any length is a few
+// launches.
+#include "loss_kernels.h"
+#include "muon_device.h"
+
+using muon::bf16_t;
+
+namespace {
+
+constexpr int kTabTensors = 128;  // two per lane: a wave finds its chunk's tensor with two ballots
+constexpr int kThreads = 256;
+constexpr int kGroup = 8;         // elements per thread and trip
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+
+struct NormTab {
+  const char* data[kTabTensors];
+  int64_t numel[kTabTensors];
+  int32_t first[kTabTensors];   // first chunk of the tensor within this launch
+  uint32_t bf16[kTabTensors / 32];
+  int32_t n;
+};
+struct ScaleTab {
+  NormTab in;
+  char* out[kTabTensors];
+  uint32_t out_bf16[kTabTensors / 32];
+};
+static_assert(sizeof(ScaleTab) + 64 <= 4096, "kernel arguments");
+
+// The tensor that chunk b lies in: the last with first[i] <= b.
+__device__ __forceinline__ int find_tensor(const NormTab& t, int b) {
+  const int lane = threadIdx.x & 63;
+  const int lo = lane < t.n && t.first[lane] <= b;
+  const int hi = 64 + lane < t.n && t.first[64 + lane] <= b;
+  return __builtin_amdgcn_readfirstlane(__popcll(__ballot(lo)) + __popcll(__ballot(hi)) - 1);
+}
+
+// Groups of 8 elements start at 16-byte addresses: group q holds elements
+// [8 q - lead, 8 q - lead + 8), lead = elements of the first group that lie
+// before the tensor.
+template <typename T> __device__ __forceinline__ int tensor_lead(const char* p) {
+  return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
+}
+
+template <typename T> __device__ __forceinline__ void load_group(const T* p, int64_t e0, int64_t n, float* v) {
+  if (e0 >= 0 && e0 + kGroup <= n) {
+    if (sizeof(T) == 2) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(p + e0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+      const u32x4 a = *reinterpret_cast<const u32x4*>(p + e0), b = *reinterpret_cast<const u32x4*>(p + e0 + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[i] = __uint_as_float(a[i]);
+        v[4 + i] = __uint_as_float(b[i]);
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i) v[i] = e0 + i >= 0 && e0 + i < n ? muon::Elem<T>::load(p + e0 + i) : 0.0f;
+}
+
+template <typename T> __device__ __forceinline__ void store_group(T* p, int64_t e0, int64_t n, const float* v) {
+  if (e0 >= 0 && e0 + kGroup <= n) {
+    // the output may lie at another alignment than the input
+    if (sizeof(T) == 2) {
+      *reinterpret_cast<u32x4_any*>(p + e0) = u32x4{muon::pack_bf16x2(v[0], v[1]), muon::pack_bf16x2(v[2], v[3]),
+                                                    muon::pack_bf16x2(v[4], v[5]), muon::pack_bf16x2(v[6], v[7])};
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<u32x4_any*>(p + e0 + 4 * h) =
+            u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                  __float_as_uint(v[4 * h + 3])};
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kGroup; ++i)
+    if (e0 + i >= 0 && e0 + i < n) muon::Elem<T>::store(p + e0 + i, v[i]);
+}
+
+// Sum over the 256 threads in a fixed order; thread 0 has it.
+__device__ __forceinline__ double block_sum(double v) {
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  __shared__ double ws[kThreads / 64];
+  if ((threadIdx.x & 63) == 0) ws[threadIdx.x >> 6] = v;
+  __syncthreads();
+  return (ws[0] + ws[1]) + (ws[2] + ws[3]);
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const char* data, int64_t numel, int64_t q0, int groups) {
+  const T* p = reinterpret_cast<const T*>(data);
+  const int lead = tensor_lead<T>(data);
+  double acc[kGroup] = {};
+  constexpr int U = 4;
+  for (int q = threadIdx.x; q < groups; q += kThreads * U) {
+    float v[U][kGroup];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      load_group<T>(p, q + u * kThreads < groups ? (q0 + q + u * kThreads) * kGroup - lead : numel, numel, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) {
+        const double d = static_cast<double>(v[u][i]);
+        acc[i] = fma(d, d, acc[i]);
+      }
+  }
+  return ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+}
+
+__global__ __launch_bounds__(kThreads) void sum_squares_kernel(NormTab t, int groups, double* __restrict__ partial) {
+  const int b = static_cast<int>(blockIdx.x), i = find_tensor(t, b);
+  const int64_t q0 = static_cast<int64_t>(b - t.first[i]) * groups;
+  const bool bf = (t.bf16[i >> 5] >> (i & 31)) & 1u;
+  const double s = block_sum(bf ? chunk_squares<bf16_t>(t.data[i], t.numel[i], q0, groups)
+                                : chunk_squares<float>(t.data[i], t.numel[i], q0, groups));
+  if (threadIdx.x == 0) partial[b] = s;
+}
+
+__device__ __forceinline__ void write_norm(double s, double max_norm, double eps, double* norm) {
+  const double size = sqrt(s);
+  double c = max_norm / (size + eps);
+  if (c > 1.0) c = 1.0;  // a NaN stays
+  norm[0] = s;
+  norm[1] = size;
+  norm[2] = c;
+}
+
+__global__ __launch_bounds__(kThreads) void sum_partials_kernel(const double* __restrict__ partial, int64_t n,
+                                                                double max_norm, double eps, double* norm) {
+  double acc = 0.0;
+  constexpr int U = 8;
+  for (int64_t p = threadIdx.x; p < n; p += U * kThreads) {
+    double v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[u] = p + u * kThreads < n ? partial[p + u * kThreads] : 0.0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) acc += v[u];
+  }
+  const double s = block_sum(acc);
+  if (threadIdx.x == 0) write_norm(s, max_norm, eps, norm);
+}
+
+__global__ void clip_coef_kernel(double max_norm, double eps, double* norm) {
+  write_norm(norm[0], max_norm, eps, norm);
+}
+
+template <typename T, typename U>
+__device__ __forceinline__ void chunk_scale(const char* data, char* out, int64_t numel, int64_t q0, int groups,
+                                            float c) {
+  const T* p = reinterpret_cast<const T*>(data);
+  U* o = reinterpret_cast<U*>(out);
+  const int lead = tensor_lead<T>(data);
+  constexpr int N = 2;
+  for (int q = threadIdx.x; q < groups; q += kThreads * N) {
+    float v[N][kGroup];
+#pragma unroll
+    for (int u = 0; u < N; ++u)
+      load_group<T>(p, q + u * kThreads < groups ? (q0 + q + u * kThreads) * kGroup - lead : numel, numel, v[u]);
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      if (q + u * kThreads >= groups) continue;
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) v[u][i] *= c;
+      store_group<U>(o, (q0 + q + u * kThreads) * kGroup - lead, numel, v[u]);
+    }
+  }
+}
+
+__global__ __launch_bounds__(kThreads) void scale_kernel(ScaleTab t, int groups, const double* __restrict__ norm) {
+  const int b = static_cast<int>(blockIdx.x), i = find_tensor(t.in, b);
+  const float c = static_cast<float>(norm[2]);
+  const char* src = t.in.data[i];
+  char* dst = t.out[i];
+  if (src == dst && c == 1.0f) return;  // in place, and nothing changes
+  const int64_t n = t.in.numel[i], q0 = static_cast<int64_t>(b - t.in.first[i]) * groups;
+  const bool bi = (t.in.bf16[i >> 5] >> (i & 31)) & 1u, bo = (t.out_bf16[i >> 5] >> (i & 31)) & 1u;
+  if (bi && bo) chunk_scale<bf16_t, bf16_t>(src, dst, n, q0, groups, c);
+  else if (bi) chunk_scale<bf16_t, float>(src, dst, n, q0, groups, c);
+  else if (bo) chunk_scale<float, bf16_t>(src, dst, n, q0, groups, c);
+  else chunk_scale<float, float>(src, dst, n, q0, groups, c);
+}
+
+// Walks the list in launches of at most kTabTensors tensors and kMaxChunks
+// chunks; calls launch(table, index of each entry, chunks, first chunk overall).
+constexpr int64_t kMaxChunks = 1 << 23;
+
+}  // namespace
+
+int64_t clip_chunk(int64_t total) {
+  // small lists in small chunks, so that they still fill the device; large
+  // ones in chunks that keep the partial sums few
+  int64_t c = 4096;
+  while (c < 65536 && total / c > 4096) c *= 2;
+  return c;
+}
+
+int64_t clip_chunks(const muon_tensor_t& t, int64_t chunk) {
+  if (t.numel == 0) return 0;
+  const int64_t e = t.dtype == MUON_BF16 ? 2 : 4;
+  const int64_t lead = static_cast<int64_t>(reinterpret_cast<uintptr_t>(t.data) & 15u) / e;
+  return (t.numel + lead + chunk - 1) / chunk;
+}
+
+namespace {
+
+// fill(slot, i) describes tensor i, launch(chunks, first chunk overall) runs
+// the table of n entries.
+template <typename Launch>
+hipError_t walk(const muon_tensor_t* t, const muon_tensor_t* out, int64_t count, int64_t chunk, Launch launch) {
+  ScaleTab tab;
+  int64_t i = 0, base = 0;
+  while (i < count) {
+    tab.in.n = 0;
+    for (int k = 0; k < kTabTensors / 32; ++k) tab.in.bf16[k] = tab.out_bf16[k] = 0;
+    int64_t chunks = 0;
+    for (; i < count && tab.in.n < kTabTensors; ++i) {
+      const int64_t c = clip_chunks(t[i], chunk);
+      if (c == 0) continue;
+      if (tab.in.n > 0 && chunks + c > kMaxChunks) break;
+      const int k = tab.in.n++;
+      tab.in.data[k] = static_cast<const char*>(t[i].data);
+      tab.in.numel[k] = t[i].numel;
+      tab.in.first[k] = static_cast<int32_t>(chunks);
+      if (t[i].dtype == MUON_BF16) tab.in.bf16[k >> 5] |= 1u << (k & 31);
+      if (out) {
+        tab.out[k] = static_cast<char*>(out[i].data);
+        if (out[i].dtype == MUON_BF16) tab.out_bf16[k >> 5] |= 1u << (k & 31);
+      }
+      chunks += c;
+    }
+    if (chunks == 0) break;
+    const hipError_t e = launch(tab, chunks, base);
+    if (e != hipSuccess) return e;
+    base += chunks;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_grad_norm(hipStream_t s, const muon_tensor_t* t, int64_t count, int64_t chunk,
+                            double* partial, double max_norm, double eps, double* norm) {
+  int64_t total = 0;
+  const int groups = static_cast<int>(chunk / kGroup);
+  const hipError_t e = walk(t, nullptr, count, chunk, [&](const ScaleTab& tab, int64_t chunks, int64_t base) {
+    sum_squares_kernel<<<static_cast<unsigned>(chunks), kThreads, 0, s>>>(tab.in, groups, partial + base);
+    total = base + chunks;
+    return hipGetLastError();
+  });
+  if (e != hipSuccess) return e;
+  sum_partials_kernel<<<1, kThreads, 0, s>>>(partial, total, max_norm, eps, norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_clip_coef(hipStream_t s, double max_norm, double eps, double* norm) {
+  clip_coef_kernel<<<1, 1, 0, s>>>(max_norm, eps, norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_scale_grads(hipStream_t s, const muon_tensor_t* t, const muon_tensor_t* out,
+                              int64_t count, int64_t chunk, const double* norm) {
+  const int groups = static_cast<int>(chunk / kGroup);
+  return walk(t, out, count, chunk, [&](const ScaleTab& tab, int64_t chunks, int64_t) {
+    scale_kernel<<<static_cast<unsigned>(chunks), kThreads, 0, s>>>(tab, groups, norm);
+    return hipGetLastError();
+  });
+}

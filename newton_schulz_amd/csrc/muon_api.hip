@@ -16,87 +16,13 @@
 #include <vector>
 
 #include "muon.h"
+#include "muon_ctx.h"
 #include "muon_internal.h"
 #include "ns_layout.h"
 
-namespace {
-
-constexpr int kTabSlots = 4;
-constexpr int64_t kTabCap = 65536;  // pointers per table (per in/out) per slot
-
-struct DeviceGuard {
-  int prev = -1;
-  bool ok = false;
-  explicit DeviceGuard(int dev) {
-    if (hipGetDevice(&prev) != hipSuccess) prev = -1;
-    ok = hipSetDevice(dev) == hipSuccess;
-  }
-  ~DeviceGuard() {
-    if (prev >= 0) (void)hipSetDevice(prev);
-  }
-};
-
-}  // namespace
-
-struct muon_ctx {
-  int device = 0;
-  int cus = 256;
-  char* ws = nullptr;
-  size_t ws_bytes = 0;
-  uint64_t* host_tab = nullptr;  // pinned staging, kTabSlots * 2 * kTabCap
-  uint64_t* dev_tab = nullptr;   // device tables, same layout
-  hipEvent_t tab_ev[kTabSlots] = {};
-  bool tab_used[kTabSlots] = {};
-  int tab_next = 0;
-  // timing
-  bool timing = false;
-  uint32_t tmask = (1u << MUON_K_COUNT) - 1;  // classes that record events
-  std::vector<hipEvent_t> tev;
-  std::vector<int> tcls;
-  size_t tused = 0;  // events recorded (pairs * 2)
-  std::string err;
-};
+thread_local const char* muon_thread_err = "";
 
 namespace {
-
-muon_status_t fail(muon_ctx* c, muon_status_t s, const char* what) {
-  if (c) c->err = what;
-  return s;
-}
-
-muon_status_t hip_fail(muon_ctx* c, hipError_t e, const char* where) {
-  if (c) {
-    c->err = std::string(where) + ": " + hipGetErrorString(e);
-  }
-  return MUON_EHIP;
-}
-
-// Record the start event of a timed launch; returns the pair index or -1.
-long tstart(muon_ctx* c, hipStream_t s, int cls) {
-  if (!c->timing || !((c->tmask >> cls) & 1u) || c->tused + 2 > c->tev.size()) return -1;
-  // launches recorded into a graph are not timed (the events would be
-  // re-recorded by every replay)
-  hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
-  if (hipStreamIsCapturing(s, &cs) != hipSuccess || cs != hipStreamCaptureStatusNone) return -1;
-  const long k = static_cast<long>(c->tused);
-  if (hipEventRecord(c->tev[k], s) != hipSuccess) return -1;
-  c->tcls[k / 2] = cls;
-  return k;
-}
-void tstop(muon_ctx* c, hipStream_t s, long k) {
-  if (k < 0) return;
-  if (hipEventRecord(c->tev[k + 1], s) == hipSuccess) c->tused = static_cast<size_t>(k) + 2;
-}
-
-bool is_dtype(int32_t d) { return d == MUON_F32 || d == MUON_BF16; }
-size_t esize(int32_t d) { return d == MUON_BF16 ? 2 : 4; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-bool ranges_overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const char* x = static_cast<const char*>(a);
-  const char* y = static_cast<const char*>(b);
-  return na && nb && x < y + nb && y < x + na;
-}
 
 // Does some out[j] (bytes long) overlap an in[k] other than in[j] == out[j]
 // exactly?  Inputs sorted by address; each output checks the inputs starting
@@ -133,7 +59,7 @@ const char* muon_status_string(muon_status_t s) {
   return "unknown status";
 }
 
-const char* muon_last_error(const muon_ctx_t* ctx) { return ctx ? ctx->err.c_str() : ""; }
+const char* muon_last_error(const muon_ctx_t* ctx) { return ctx ? ctx->err.c_str() : muon_thread_err; }
 
 void muon_ns_params_default(muon_ns_params_t* p) {
   if (!p) return;
@@ -254,7 +180,8 @@ muon_status_t muon_timing_read(muon_ctx_t* c, int32_t cls, double* total_ms, int
 
 static muon_status_t momentum_impl(muon_ctx_t* c, void* stream, const void* grad, int32_t grad_dtype,
                             float* momentum, void* update_out, int32_t update_dtype,
-                            int64_t numel, float beta, int32_t nesterov, double* sq) {
+                            int64_t numel, float beta, int32_t nesterov, double* sq,
+                            const double* norm) {
   if (c == nullptr) return MUON_EINVAL;
   if (numel < 0) return fail(c, MUON_EINVAL, "numel < 0");
   if (!is_dtype(grad_dtype) || !is_dtype(update_dtype)) return fail(c, MUON_EDTYPE, "dtype");
@@ -277,12 +204,19 @@ static muon_status_t momentum_impl(muon_ctx_t* c, void* stream, const void* grad
         ranges_overlap(sq, qb, update_out, nb * esize(update_dtype)))
       return fail(c, MUON_EINVAL, "sq_partials overlaps a buffer");
   }
+  if (norm != nullptr) {
+    if (reinterpret_cast<uintptr_t>(norm) % 8) return fail(c, MUON_EINVAL, "misaligned norm");
+    const size_t qb = sq ? static_cast<size_t>((numel + MUON_SQ_BLOCK - 1) / MUON_SQ_BLOCK) * 8 : 0;
+    if (ranges_overlap(norm, 24, momentum, nb * 4) ||
+        ranges_overlap(norm, 24, update_out, nb * esize(update_dtype)) || ranges_overlap(norm, 24, sq, qb))
+      return fail(c, MUON_EINVAL, "norm overlaps an output");
+  }
   DeviceGuard g(c->device);
   hipStream_t s = static_cast<hipStream_t>(stream);
   const float c1 = 1.0f - beta;
   const long tk = tstart(c, s, MUON_K_MOMENTUM);
   const hipError_t e = launch_momentum(s, c->cus, grad, grad_dtype, momentum, update_out,
-                                       update_dtype, numel, beta, c1, nesterov ? 1 : 0, sq);
+                                       update_dtype, numel, beta, c1, nesterov ? 1 : 0, sq, norm);
   tstop(c, s, tk);
   if (e != hipSuccess) return hip_fail(c, e, "momentum launch");
   return MUON_OK;
@@ -293,7 +227,7 @@ muon_status_t muon_momentum_update(muon_ctx_t* c, void* stream, const void* grad
                                    int32_t update_dtype, int64_t numel, float beta,
                                    int32_t nesterov) {
   return momentum_impl(c, stream, grad, grad_dtype, momentum, update_out, update_dtype, numel,
-                       beta, nesterov, nullptr);
+                       beta, nesterov, nullptr, nullptr);
 }
 
 muon_status_t muon_momentum_update_sq(muon_ctx_t* c, void* stream, const void* grad,
@@ -303,7 +237,18 @@ muon_status_t muon_momentum_update_sq(muon_ctx_t* c, void* stream, const void* g
   if (c == nullptr) return MUON_EINVAL;
   if (sq_partials == nullptr) return fail(c, MUON_EINVAL, "sq_partials NULL");
   return momentum_impl(c, stream, grad, grad_dtype, momentum, update_out, update_dtype, numel,
-                       beta, nesterov, sq_partials);
+                       beta, nesterov, sq_partials, nullptr);
+}
+
+muon_status_t muon_momentum_update_clipped(muon_ctx_t* c, void* stream, const void* grad,
+                                           int32_t grad_dtype, float* momentum, void* update_out,
+                                           int32_t update_dtype, int64_t numel, float beta,
+                                           int32_t nesterov, const double* norm,
+                                           double* sq_partials) {
+  if (c == nullptr) return MUON_EINVAL;
+  if (norm == nullptr) return fail(c, MUON_EINVAL, "norm NULL");
+  return momentum_impl(c, stream, grad, grad_dtype, momentum, update_out, update_dtype, numel,
+                       beta, nesterov, sq_partials, norm);
 }
 
 muon_status_t muon_apply(muon_ctx_t* c, void* stream, float* master, const void* update,

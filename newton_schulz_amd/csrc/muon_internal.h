@@ -92,7 +92,7 @@ hipError_t launch_ns_small(hipStream_t s, const NsSmallArgs& a);
 
 hipError_t launch_momentum(hipStream_t s, int cus, const void* grad, int gdt, float* mom,
                            void* upd, int udt, int64_t numel, float beta, float c1,
-                           int nesterov, double* sq);
+                           int nesterov, double* sq, const double* norm);
 hipError_t launch_apply(hipStream_t s, int cus, float* master, const void* upd, int udt,
                         void* wbf, int64_t numel, float eta, float decay, int has_wd);
 
