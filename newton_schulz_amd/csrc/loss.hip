@@ -18,6 +18,7 @@
 //
 // All kernels are bound by HBM: the statistics read each row once, the
 // gradient reads and writes it once.
+#include <algorithm>
 #include <cfloat>
 
 #include "loss_kernels.h"
@@ -63,51 +64,26 @@ template <> struct Scores<float> {
   static constexpr uint32_t kMasked = 0xff800000u;
 };
 
-// A row is walked in pieces of 16 bytes that start at 16-byte addresses: piece
-// i holds scores [i * kVec - lead, ...), lead = scores of the first piece that
-// lie before the row (rows of an odd vocabulary start at odd addresses).  The
-// first and the last piece may be partial.
-template <typename T> __device__ __forceinline__ int row_lead(const T* row) {
-  return static_cast<int>((reinterpret_cast<uintptr_t>(row) & 15u) / sizeof(T));
+// A row is walked in pieces of 16 bytes at 16-byte addresses.  What lies
+// before the first and after the last of them (rows of an odd vocabulary start
+// at odd addresses) are edges: at most 2 (kVec - 1) single scores, taken by as
+// many threads of the first wave.
+struct RowShape {
+  int head;   // scores before the first piece
+  int full;   // pieces
+  int edges;  // single scores in all
+};
+template <typename T> __device__ __forceinline__ RowShape row_shape(const T* row, int vocab) {
+  RowShape s;
+  s.head = static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(row) & 15u)) & 15u) / sizeof(T));
+  if (s.head > vocab) s.head = vocab;
+  s.full = (vocab - s.head) / kVec<T>;
+  s.edges = vocab - s.full * kVec<T>;
+  return s;
 }
-template <typename T> __device__ __forceinline__ int row_pieces(int vocab, int lead) {
-  return (vocab + lead + kVec<T> - 1) / kVec<T>;
-}
-
-// Piece with first score e0; scores outside [0, vocab) read as -infinity.
-template <typename T>
-__device__ __forceinline__ u32x4 load_piece(const T* row, int e0, int vocab) {
-  if (e0 >= 0 && e0 + kVec<T> <= vocab) return *reinterpret_cast<const u32x4*>(row + e0);
-  u32x4 w = {Scores<T>::kMasked, Scores<T>::kMasked, Scores<T>::kMasked, Scores<T>::kMasked};
-#pragma unroll
-  for (int i = 0; i < kVec<T>; ++i) {
-    const int e = e0 + i;
-    if (e >= 0 && e < vocab) {
-      if (sizeof(T) == 4) {
-        w[i] = reinterpret_cast<const uint32_t*>(row)[e];
-      } else {
-        const uint32_t h = reinterpret_cast<const bf16_t*>(row)[e];
-        w[i / 2] = (i & 1) ? (w[i / 2] & 0xffffu) | (h << 16) : (w[i / 2] & 0xffff0000u) | h;
-      }
-    }
-  }
-  return w;
-}
-
-template <typename T>
-__device__ __forceinline__ void store_piece(T* row, int e0, int vocab, u32x4 w) {
-  if (e0 >= 0 && e0 + kVec<T> <= vocab) {
-    *reinterpret_cast<u32x4_any*>(row + e0) = w;  // the gradient's rows have their own alignment
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < kVec<T>; ++i) {
-    const int e = e0 + i;
-    if (e >= 0 && e < vocab) {
-      if (sizeof(T) == 4) reinterpret_cast<uint32_t*>(row)[e] = w[i];
-      else reinterpret_cast<bf16_t*>(row)[e] = static_cast<bf16_t>((i & 1) ? w[i / 2] >> 16 : w[i / 2] & 0xffffu);
-    }
-  }
+// The score that edge i < edges is.
+template <typename T> __device__ __forceinline__ int edge_score(const RowShape& s, int i) {
+  return i < s.head ? i : i + s.full * kVec<T>;
 }
 
 template <typename T> __device__ __forceinline__ T* row_at(const RowsRef& x, int r, int seq) {
@@ -125,29 +101,40 @@ __device__ __forceinline__ void join(float& m, float& s, float mo, float so, flo
   m = mn;
 }
 
+// The pair of N neighbouring lanes, in each of them.
+template <int N = 64> __device__ __forceinline__ void wave_join(float& m, float& s, float k) {
+#pragma unroll
+  for (int d = N / 2; d > 0; d >>= 1) {
+    const float mo = __shfl_xor(m, d, 64), so = __shfl_xor(s, d, 64);
+    const float mn = fmaxf(m, mo);
+    // a + b commutes: both partners form the same sum
+    const float a = s * exp2_fast((m - mn) * k), b = so * exp2_fast((mo - mn) * k);
+    s = a + b;
+    m = mn;
+  }
+}
+
 // The pair of all threads of the workgroup, in every thread.
 template <int NT> __device__ __forceinline__ void block_join(float& m, float& s, float k) {
   constexpr int W = NT / 64;
   __shared__ float2 wave[W];
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) {
-    const float mo = __shfl_xor(m, d, 64), so = __shfl_xor(s, d, 64);
-    // both partners join in the same order: lower lane's pair first
-    if (threadIdx.x & d) {
-      float m2 = mo, s2 = so;
-      join(m2, s2, m, s, k);
-      m = m2;
-      s = s2;
-    } else {
-      join(m, s, mo, so, k);
-    }
-  }
+  wave_join(m, s, k);
   if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = make_float2(m, s);
   __syncthreads();
   m = wave[0].x;
   s = wave[0].y;
 #pragma unroll
   for (int w = 1; w < W; ++w) join(m, s, wave[w].x, wave[w].y, k);
+}
+
+// z_y - M - log S with T = 1 / inv_t, xm = x_y - max x.  log S = ln 2 (e +
+// log2 f), S = 2^e f with f in [1/2, 1): the large part is exact, so the
+// absolute error is that of log2 f, below 2^-23, at any S.
+__device__ __forceinline__ double token_lp(float xm, float s, double inv_t) {
+  int e = 0;
+  const float f = frexpf(s, &e);
+  const double log2s = static_cast<double>(e) + static_cast<double>(__builtin_amdgcn_logf(f));
+  return static_cast<double>(xm) * inv_t - log2s * 0.69314718055994530942;
 }
 
 // What the row's pair makes of token r (one thread).
@@ -157,8 +144,8 @@ __device__ __forceinline__ void finish_row(const LossArgs& a, int r, int64_t y, 
   if (y >= a.vocab) {
     lp = __longlong_as_double(0x7ff8000000000000ll);
   } else if (y >= 0) {
-    const float z = muon::Elem<T>::load(row_at<const T>(a.x, r, a.seq) + y) - m;
-    lp = static_cast<double>(z) / static_cast<double>(a.temperature) - log(static_cast<double>(s));
+    const float xm = muon::Elem<T>::load(row_at<const T>(a.x, r, a.seq) + y) - m;
+    lp = token_lp(xm, s, 1.0 / static_cast<double>(a.temperature));
   }
   if (a.lp) a.lp[r] = lp;
   if (a.logps) a.logps[r] = static_cast<float>(lp);
@@ -166,7 +153,25 @@ __device__ __forceinline__ void finish_row(const LossArgs& a, int r, int64_t y, 
 }
 
 constexpr int kStatsThreads = 256;
-constexpr int kStatsUnroll = 8;  // pieces in flight per thread
+constexpr int kStatsUnroll = 4;  // pieces in flight per thread, twice
+
+// (m, s) with the scores of one piece.
+template <typename T> __device__ __forceinline__ void take_piece(u32x4 w, float& m, float& s, float k) {
+  float v[kVec<T>];
+  Scores<T>::unpack(w, v);
+  float mn = m;
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) mn = fmaxf(mn, v[i]);
+  s *= exp2_fast((m - mn) * k);
+  m = mn;
+#pragma unroll
+  for (int i = 0; i < kVec<T>; ++i) s += exp2_fast((v[i] - m) * k);
+}
+__device__ __forceinline__ void take_score(float v, float& m, float& s, float k) {
+  const float mn = fmaxf(m, v);
+  s = s * exp2_fast((m - mn) * k) + exp2_fast((v - mn) * k);
+  m = mn;
+}
 
 // Statistics of row blockIdx / splits, pieces of split blockIdx % splits.
 template <typename T>
@@ -179,32 +184,41 @@ __global__ __launch_bounds__(kStatsThreads) void row_stats_kernel(LossArgs a) {
   }
   const float k = kLog2e / a.temperature;
   const T* row = row_at<const T>(a.x, r, a.seq);
-  const int lead = row_lead(row), pieces = row_pieces<T>(a.vocab, lead);
-  const int per = (pieces + a.splits - 1) / a.splits;
-  const int p0 = sp * per, p1 = min(pieces, p0 + per);
+  const RowShape sh = row_shape(row, a.vocab);
+  const u32x4* body = reinterpret_cast<const u32x4*>(row + sh.head);
+  const int per = (sh.full + a.splits - 1) / a.splits;
+  const int p0 = sp * per, p1 = min(sh.full, p0 + per);
+  constexpr int U = kStatsUnroll, step = kStatsThreads * U;
+  const u32x4 masked = {Scores<T>::kMasked, Scores<T>::kMasked, Scores<T>::kMasked, Scores<T>::kMasked};
   float m = kLowest, s = 0.0f;
-  for (int p = p0 + static_cast<int>(threadIdx.x); p < p1; p += kStatsThreads * kStatsUnroll) {
-    u32x4 w[kStatsUnroll];
+  const int t = static_cast<int>(threadIdx.x);
+  auto load = [&](u32x4* w, int base) {
+    if (base + step <= p1) {
 #pragma unroll
-    for (int u = 0; u < kStatsUnroll; ++u) {
-      const int q = p + u * kStatsThreads;
-      w[u] = load_piece<T>(row, q < p1 ? q * kVec<T> - lead : a.vocab, a.vocab);
+      for (int u = 0; u < U; ++u) w[u] = body[base + u * kStatsThreads + t];
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int q = base + u * kStatsThreads + t;
+        w[u] = masked;
+        if (q < p1) w[u] = body[q];
+      }
     }
+  };
+  // two sets of loads: one in flight while the other is taken
+  u32x4 w[2][U];
+  load(w[0], p0);
+  for (int base = p0; base < p1; base += 2 * step) {
+    load(w[1], base + step);
 #pragma unroll
-    for (int u = 0; u < kStatsUnroll; ++u) {
-      float v[kVec<T>];
-      Scores<T>::unpack(w[u], v);
-      float mn = m;
+    for (int u = 0; u < U; ++u) take_piece<T>(w[0][u], m, s, k);
+    load(w[0], base + 2 * step);
 #pragma unroll
-      for (int i = 0; i < kVec<T>; ++i) mn = fmaxf(mn, v[i]);
-      s *= exp2_fast((m - mn) * k);
-      m = mn;
-#pragma unroll
-      for (int i = 0; i < kVec<T>; ++i) s += exp2_fast((v[i] - m) * k);
-    }
+    for (int u = 0; u < U; ++u) take_piece<T>(w[1][u], m, s, k);
   }
+  if (sp == 0 && t < sh.edges) take_score(muon::Elem<T>::load(row + edge_score<T>(sh, t)), m, s, k);
   block_join<kStatsThreads>(m, s, k);
-  if (threadIdx.x == 0) {
+  if (t == 0) {
     if (a.splits == 1) finish_row<T>(a, r, y, m, s);
     else a.part[static_cast<int64_t>(r) * a.splits + sp] = make_float2(m, s);
   }
@@ -231,7 +245,8 @@ template <typename T> __global__ __launch_bounds__(64) void row_join_kernel(Loss
 constexpr int kGradThreads = 256;
 constexpr int kGradUnroll = 4;
 
-// Gradient of row blockIdx / chunks, pieces of chunk blockIdx % chunks.
+// Gradient of row blockIdx / chunks, pieces of chunk blockIdx % chunks (the
+// first chunk takes the edges).
 template <typename T>
 __global__ __launch_bounds__(kGradThreads) void logits_grad_kernel(LossArgs a, RowsRef grad,
                                                                    const float* __restrict__ g, int chunks) {
@@ -239,14 +254,19 @@ __global__ __launch_bounds__(kGradThreads) void logits_grad_kernel(LossArgs a, R
   const int64_t y = a.labels[r];
   const T* row = row_at<const T>(a.x, r, a.seq);
   T* out = row_at<T>(grad, r, a.seq);
-  const int lead = row_lead(row), pieces = row_pieces<T>(a.vocab, lead);
-  const int p0 = c * kGradThreads * kGradUnroll + static_cast<int>(threadIdx.x);
+  const RowShape sh = row_shape(row, a.vocab);
+  const u32x4* body = reinterpret_cast<const u32x4*>(row + sh.head);
+  // the gradient's rows have an alignment of their own
+  u32x4_any* obody = reinterpret_cast<u32x4_any*>(out + sh.head);
+  const int t = static_cast<int>(threadIdx.x), p0 = c * kGradThreads * kGradUnroll + t;
+  const bool edge = c == 0 && t < sh.edges;
   if (y < 0) {
 #pragma unroll
     for (int u = 0; u < kGradUnroll; ++u) {
       const int p = p0 + u * kGradThreads;
-      if (p < pieces) store_piece<T>(out, p * kVec<T> - lead, a.vocab, u32x4{0, 0, 0, 0});
+      if (p < sh.full) obody[p] = u32x4{0, 0, 0, 0};
     }
+    if (edge) muon::Elem<T>::store(out + edge_score<T>(sh, t), 0.0f);
     return;
   }
   const float k = kLog2e / a.temperature;
@@ -258,24 +278,31 @@ __global__ __launch_bounds__(kGradThreads) void logits_grad_kernel(LossArgs a, R
 #pragma unroll
   for (int u = 0; u < kGradUnroll; ++u) {
     const int p = p0 + u * kGradThreads;
-    if (p < pieces) w[u] = load_piece<T>(row, p * kVec<T> - lead, a.vocab);
+    if (p < sh.full) w[u] = body[p];
   }
+  // the label's place: piece py, score iy of it (no piece when it is an edge)
+  const int ly = static_cast<int>(y < a.vocab ? y : 0) - sh.head;
+  const int py = ly >= 0 ? ly / kVec<T> : -1, iy = ly - py * kVec<T>;
 #pragma unroll
   for (int u = 0; u < kGradUnroll; ++u) {
     const int p = p0 + u * kGradThreads;
-    if (p >= pieces) continue;
-    const int e0 = p * kVec<T> - lead;
+    if (p >= sh.full) continue;
     float v[kVec<T>];
     Scores<T>::unpack(w[u], v);
 #pragma unroll
     for (int i = 0; i < kVec<T>; ++i) v[i] = scale * exp2_fast((v[i] - st.x) * k);
-    const int64_t at = y - e0;
-    if (at >= 0 && at < kVec<T>) {
+    if (p == py) {
 #pragma unroll
       for (int i = 0; i < kVec<T>; ++i)
-        if (i == at) v[i] += G;
+        if (i == iy) v[i] += G;
     }
-    store_piece<T>(out, e0, a.vocab, Scores<T>::pack(v));
+    obody[p] = Scores<T>::pack(v);
+  }
+  if (edge) {
+    const int e = edge_score<T>(sh, t);
+    float v = scale * exp2_fast((muon::Elem<T>::load(row + e) - st.x) * k);
+    if (e == y) v += G;
+    muon::Elem<T>::store(out + e, v);
   }
 }
 
@@ -311,7 +338,65 @@ __device__ __forceinline__ void count_tokens(const int64_t* labels, int batch, i
 }
 
 // max(a, b) that hands a NaN on, as the formula does.
-__device__ __forceinline__ double max_nan(double a, double b) { return (a > b || a != a) ? a : b; }
+__device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
+
+// exp(e) - 1 - e.  Below 1 by its series e^2 (1/2! + e/3! + ...), which keeps
+// the relative accuracy that the difference loses; the term after the last is
+// e^12 / 14! < 2e-11 of the first.
+__device__ __forceinline__ float exp_excess(float e) {
+  if (fabsf(e) < 1.0f) {
+    float q = 1.6059044e-10f;  // 1 / 13!
+    q = q * e + 2.0876757e-9f;
+    q = q * e + 2.5052108e-8f;
+    q = q * e + 2.7557319e-7f;
+    q = q * e + 2.7557319e-6f;
+    q = q * e + 2.4801587e-5f;
+    q = q * e + 1.9841270e-4f;
+    q = q * e + 1.3888889e-3f;
+    q = q * e + 8.3333333e-3f;
+    q = q * e + 4.1666667e-2f;
+    q = q * e + 1.6666667e-1f;
+    q = q * e + 0.5f;
+    return q * e * e;
+  }
+  return expf(e) - 1.0f - e;
+}
+
+// One token of the policy loss: its terms and the gradient of pg + kl_coef kl
+// in lp.  The differences of log-probabilities are formed in binary64; what
+// follows has no cancellation left and is done in fp32 (a few roundings, far
+// below the error of lp itself).
+struct TokenTerms {
+  float pg, kl, clipped, g;
+};
+__device__ __forceinline__ TokenTerms policy_token(const PolicyArgs& a, int t, int b, double lp) {
+  TokenTerms o;
+  const float A = a.adv[a.p.advantage_per_token ? t : b];
+  // without an old policy it is the policy itself: ratio 1 (NaN when lp is)
+  const float ratio = a.old_lp ? expf(static_cast<float>(lp - a.old_lp[t])) : lp == lp ? 1.0f : __uint_as_float(0x7fc00000u);
+  const float lo = 1.0f - a.p.clip_low, hi = 1.0f + a.p.clip_high;
+  const float held = -A * (ratio < lo ? lo : ratio > hi ? hi : ratio);
+  const float free = -A * ratio;
+  o.pg = max_nan(free, held);
+  o.clipped = held > free ? 1.0f : 0.0f;
+  o.g = held > free ? 0.0f : free;
+  o.kl = 0.0f;
+  if (a.ref_lp) {
+    const float e = static_cast<float>(static_cast<double>(a.ref_lp[t]) - lp);
+    o.kl = exp_excess(e);
+    if (a.p.kl_coef != 0.0f) o.g -= a.p.kl_coef * (o.kl + e);  // kl + e = exp(e) - 1
+  }
+  return o;
+}
+
+__device__ __forceinline__ void write_policy(const PolicyArgs& a, double pg, double kl, double clipped) {
+  double loss = pg;
+  if (a.p.kl_coef != 0.0f) loss += static_cast<double>(a.p.kl_coef) * kl;
+  a.out[0] = static_cast<float>(static_cast<double>(a.p.weight) * loss);
+  a.out[1] = static_cast<float>(pg);
+  a.out[2] = static_cast<float>(kl);
+  a.out[3] = static_cast<float>(clipped);
+}
 
 __global__ __launch_bounds__(kTermThreads) void policy_terms_kernel(PolicyArgs a) {
   const int rows = a.batch * a.seq;
@@ -329,31 +414,182 @@ __global__ __launch_bounds__(kTermThreads) void policy_terms_kernel(PolicyArgs a
     const double w = a.p.reduce == MUON_REDUCE_TOKEN      ? 1.0 / n
                      : a.p.reduce == MUON_REDUCE_SEQUENCE ? 1.0 / (static_cast<double>(a.counts[b]) * a.batch)
                                                           : 1.0;
-    const double lp = a.lp[t], A = a.adv[a.p.advantage_per_token ? t : b];
-    // without an old policy it is the policy itself: ratio 1 (NaN when lp is)
-    const double ratio = a.old_lp ? exp(lp - a.old_lp[t]) : lp == lp ? 1.0 : lp;
-    const double lo = 1.0 - static_cast<double>(a.p.clip_low), hi = 1.0 + static_cast<double>(a.p.clip_high);
-    const double held = -A * (ratio < lo ? lo : ratio > hi ? hi : ratio);
-    const double free = -A * ratio;
-    sum_pg += w * max_nan(free, held);
-    if (held > free) sum_clip += w;
-    double g = held > free ? 0.0 : free;
-    if (a.ref_lp) {
-      const double e = static_cast<double>(a.ref_lp[t]) - lp, em = expm1(e);
-      sum_kl += w * (em - e);
-      if (a.p.kl_coef != 0.0f) g -= static_cast<double>(a.p.kl_coef) * em;
-    }
-    if (a.g) a.g[t] = static_cast<float>(static_cast<double>(a.p.weight) * w * g);
+    const TokenTerms o = policy_token(a, t, b, a.lp[t]);
+    sum_pg += w * static_cast<double>(o.pg);
+    sum_kl += w * static_cast<double>(o.kl);
+    sum_clip += w * static_cast<double>(o.clipped);
+    if (a.g) a.g[t] = static_cast<float>(static_cast<double>(a.p.weight) * w * static_cast<double>(o.g));
   }
   const double pg = block_total(sum_pg), kl = block_total(sum_kl), clipped = block_total(sum_clip);
-  if (threadIdx.x == 0) {
-    double loss = pg;
-    if (a.p.kl_coef != 0.0f) loss += static_cast<double>(a.p.kl_coef) * kl;
-    a.out[0] = static_cast<float>(static_cast<double>(a.p.weight) * loss);
-    a.out[1] = static_cast<float>(pg);
-    a.out[2] = static_cast<float>(kl);
-    a.out[3] = static_cast<float>(clipped);
+  if (threadIdx.x == 0) write_policy(a, pg, kl, clipped);
+}
+
+// ---------------------------------------------------------------------------
+// rows held in registers
+// ---------------------------------------------------------------------------
+// One workgroup holds a whole row (NV pieces a thread: 304 KB of the 512 KB of
+// a compute unit's registers at 151936 bf16 scores), so the policy loss, whose
+// gradient of a token needs nothing of other rows but their number, reads
+// every score once and writes every gradient once.  The workgroup walks rows
+// blockIdx, + gridDim, ...; as soon as a piece's gradient has gone out, the
+// same registers receive the next row's piece, so loads are in flight through
+// the whole second half of a row.
+template <typename T, int NT, int NV>
+__global__ __launch_bounds__(NT, 4) void policy_rows_kernel(LossArgs a, RowsRef grad, PolicyArgs p) {
+  constexpr int W = NT / 64;
+  const int t = static_cast<int>(threadIdx.x), lane = t & 63, wave = t >> 6;
+  const int stride = static_cast<int>(gridDim.x);
+  const float k = kLog2e / a.temperature;
+  const u32x4 masked = {Scores<T>::kMasked, Scores<T>::kMasked, Scores<T>::kMasked, Scores<T>::kMasked};
+  __shared__ float2 part[2][W];
+  __shared__ int found[2][W];
+  __shared__ float coef[2][3];
+  __shared__ double weight, sums[3];  // of wave 0
+
+  // The next row from r on that counts; rows left out on the way get their zeros.
+  auto next_row = [&](int r) {
+    for (; r < a.rows && a.labels[r] < 0; r += stride) {
+      if (t == 0 && a.logps) a.logps[r] = 0.0f;
+      if (grad.base == nullptr) continue;
+      T* out = row_at<T>(grad, r, a.seq);
+      const RowShape sh = row_shape(row_at<const T>(a.x, r, a.seq), a.vocab);
+      u32x4_any* body = reinterpret_cast<u32x4_any*>(out + sh.head);
+      for (int q = t; q < sh.full; q += NT) body[q] = u32x4{0, 0, 0, 0};
+      if (t < sh.edges) muon::Elem<T>::store(out + edge_score<T>(sh, t), 0.0f);
+    }
+    return r;
+  };
+
+  u32x4 w[NV];
+  float we = -INFINITY;  // this thread's edge
+  int r = next_row(static_cast<int>(blockIdx.x));
+  const T* row = row_at<const T>(a.x, r < a.rows ? r : 0, a.seq);
+  RowShape sh = row_shape(row, a.vocab);
+  if (r < a.rows) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      w[i] = masked;
+      if (i * NT + t < sh.full) w[i] = reinterpret_cast<const u32x4*>(row + sh.head)[i * NT + t];
+    }
+    if (t < sh.edges) we = muon::Elem<T>::load(row + edge_score<T>(sh, t));
   }
+  int counted = -1;  // the sequence (or 0: all) whose tokens the weight goes by
+  if (t == 0) sums[0] = sums[1] = sums[2] = 0.0;
+  const double inv_t = 1.0 / static_cast<double>(a.temperature);
+  for (int parity = 0; r < a.rows; parity ^= 1) {
+    const int b = r / a.seq;
+    const int64_t y = a.labels[r];
+    const bool named = y < a.vocab;
+    const float xy = muon::Elem<T>::load(row + (named ? y : 0));
+    // tokens that share the loss's mean with this one
+    const int set = p.p.reduce == MUON_REDUCE_SEQUENCE ? b : 0;
+    const bool count = set != counted;
+    if (count && p.p.reduce != MUON_REDUCE_SUM) {
+      const int lo = p.p.reduce == MUON_REDUCE_SEQUENCE ? b * a.seq : 0;
+      const int hi = p.p.reduce == MUON_REDUCE_SEQUENCE ? lo + a.seq : a.rows;
+      int n = 0;
+      for (int j = lo + t; j - t < hi; j += NT) n += __popcll(__ballot(j < hi && a.labels[j < hi ? j : lo] >= 0));
+      if (lane == 0) found[parity][wave] = n;
+    }
+    counted = set;
+    float m = kLowest, s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      take_piece<T>(w[i], m, s, k);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (t < sh.edges) take_score(we, m, s, k);
+    wave_join(m, s, k);
+    if (lane == 0) part[parity][wave] = make_float2(m, s);
+    const int rn = next_row(r + stride);
+    __syncthreads();
+    if (wave == 0) {
+      const float2 q = part[parity][lane % W];
+      m = q.x;
+      s = q.y;
+      wave_join<W>(m, s, k);
+      if (count && lane == 0) {
+        double n = 0.0;
+        for (int i = 0; i < W; ++i) n += found[parity][i];
+        weight = p.p.reduce == MUON_REDUCE_TOKEN      ? 1.0 / n
+                 : p.p.reduce == MUON_REDUCE_SEQUENCE ? 1.0 / (n * p.batch)
+                                                      : 1.0;
+      }
+      double lp = token_lp(xy - m, s, inv_t);
+      if (!named) lp = __longlong_as_double(0x7ff8000000000000ll);
+      const TokenTerms o = policy_token(p, r, b, lp);
+      if (lane == 0) {
+        const double wt = weight;
+        sums[0] += wt * static_cast<double>(o.pg);
+        sums[1] += wt * static_cast<double>(o.kl);
+        sums[2] += wt * static_cast<double>(o.clipped);
+        const float G = static_cast<float>(static_cast<double>(p.p.weight) * wt * static_cast<double>(o.g)) / a.temperature;
+        coef[parity][0] = m;
+        coef[parity][1] = -G / s;
+        coef[parity][2] = G;
+        if (a.logps) a.logps[r] = static_cast<float>(lp);
+      }
+    }
+    __syncthreads();
+    const float M = coef[parity][0], scale = coef[parity][1], G = coef[parity][2];
+    // The pieces are unpacked again: as far as the compiler knows they may
+    // have changed, so it keeps 4 registers a piece across the join, not 8
+    // more of widened scores.
+#pragma unroll
+    for (int i = 0; i < NV; ++i) asm volatile("" : "+v"(w[i]));
+    const T* nrow = row_at<const T>(a.x, rn < a.rows ? rn : r, a.seq);
+    const RowShape nsh = row_shape(nrow, a.vocab);
+    const u32x4* nbody = reinterpret_cast<const u32x4*>(nrow + nsh.head);
+    const int nfull = rn < a.rows ? nsh.full : 0;
+    if (grad.base) {
+      T* out = row_at<T>(grad, r, a.seq);
+      u32x4_any* obody = reinterpret_cast<u32x4_any*>(out + sh.head);
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float v[kVec<T>];
+        Scores<T>::unpack(w[i], v);
+#pragma unroll
+        for (int e = 0; e < kVec<T>; ++e) v[e] = scale * exp2_fast((v[e] - M) * k);
+        if (i * NT + t < sh.full) obody[i * NT + t] = Scores<T>::pack(v);
+        w[i] = masked;
+        if (i * NT + t < nfull) w[i] = nbody[i * NT + t];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (t < sh.edges) muon::Elem<T>::store(out + edge_score<T>(sh, t), scale * exp2_fast((we - M) * k));
+      // the label's score, by the thread whose piece or edge has just gone out
+      if (named) {
+        const int ly = static_cast<int>(y) - sh.head;
+        const bool in_piece = ly >= 0 && ly < sh.full * kVec<T>;
+        const int owner = in_piece ? (ly / kVec<T>) % NT : ly < 0 ? static_cast<int>(y) : ly - sh.full * kVec<T> + sh.head;
+        if (t == owner) muon::Elem<T>::store(out + y, scale * exp2_fast((xy - M) * k) + G);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        w[i] = masked;
+        if (i * NT + t < nfull) w[i] = nbody[i * NT + t];
+      }
+    }
+    if (rn < a.rows && t < nsh.edges) we = muon::Elem<T>::load(nrow + edge_score<T>(nsh, t));
+    r = rn;
+    row = nrow;
+    sh = nsh;
+  }
+  if (t == 0) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) p.sums[static_cast<int64_t>(blockIdx.x) * 3 + i] = sums[i];
+  }
+}
+
+// The losses of `n` workgroups, in index order per thread.
+__global__ __launch_bounds__(kTermThreads) void policy_sums_kernel(PolicyArgs p, int n) {
+  double v[3] = {0.0, 0.0, 0.0};
+  for (int i = threadIdx.x; i < n; i += kTermThreads)
+#pragma unroll
+    for (int j = 0; j < 3; ++j) v[j] += p.sums[static_cast<int64_t>(i) * 3 + j];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) v[j] = block_total(v[j]);
+  if (threadIdx.x == 0) write_policy(p, v[0], v[1], v[2]);
 }
 
 // -log sigma(h) and sigma(h), without overflow.
@@ -466,9 +702,8 @@ hipError_t launch_row_stats(hipStream_t s, const LossArgs& a) {
 
 hipError_t launch_logits_grad(hipStream_t s, const LossArgs& a, RowsRef grad, const float* g) {
   const int vec = a.bf16 ? 8 : 4;
-  // pieces of a row that starts as late in a piece as it can
-  const int64_t pieces = (static_cast<int64_t>(a.vocab) + 2 * vec - 2) / vec;
-  const int chunks = static_cast<int>((pieces + kGradThreads * kGradUnroll - 1) / (kGradThreads * kGradUnroll));
+  const int pieces = a.vocab / vec;  // the most a row can have
+  const int chunks = std::max(1, (pieces + kGradThreads * kGradUnroll - 1) / (kGradThreads * kGradUnroll));
   LossArgs c = a;
   const int step = rows_per_launch(chunks);
   for (c.row0 = 0; c.row0 < a.rows; c.row0 += step) {
@@ -485,6 +720,39 @@ hipError_t launch_logits_grad(hipStream_t s, const LossArgs& a, RowsRef grad, co
 hipError_t launch_policy_terms(hipStream_t s, const PolicyArgs& a) {
   policy_terms_kernel<<<1, kTermThreads, 0, s>>>(a);
   return hipGetLastError();
+}
+
+namespace {
+
+template <typename T, int NT, int NV>
+hipError_t run_policy_rows(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p, int cus) {
+  const int grid = std::min(a.rows, cus * (1024 / NT));
+  policy_rows_kernel<T, NT, NV><<<static_cast<unsigned>(grid), NT, 0, s>>>(a, grad, p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  policy_sums_kernel<<<1, kTermThreads, 0, s>>>(p, grid);
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t policy_rows(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p, int cus) {
+  const int pieces = a.vocab / kVec<T>;
+  if (pieces <= 256 * 5) return run_policy_rows<T, 256, 5>(s, a, grad, p, cus);
+  if (pieces <= 256 * 10) return run_policy_rows<T, 256, 10>(s, a, grad, p, cus);
+  if (pieces <= 256 * 15) return run_policy_rows<T, 256, 15>(s, a, grad, p, cus);
+  if (pieces <= 256 * 19) return run_policy_rows<T, 256, 19>(s, a, grad, p, cus);
+  if (pieces <= 512 * 15) return run_policy_rows<T, 512, 15>(s, a, grad, p, cus);
+  if (pieces <= 512 * 19) return run_policy_rows<T, 512, 19>(s, a, grad, p, cus);
+  if (pieces <= 1024 * 15) return run_policy_rows<T, 1024, 15>(s, a, grad, p, cus);
+  return run_policy_rows<T, 1024, 19>(s, a, grad, p, cus);
+}
+
+}  // namespace
+
+bool policy_rows_fit(const LossArgs& a) { return a.vocab / (a.bf16 ? 8 : 4) <= 1024 * 19; }
+
+hipError_t launch_policy_rows(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p, int cus) {
+  return a.bf16 ? policy_rows<bf16_t>(s, a, grad, p, cus) : policy_rows<float>(s, a, grad, p, cus);
 }
 
 hipError_t launch_preference_terms(hipStream_t s, const PreferenceArgs& a) {

@@ -16,12 +16,13 @@ namespace {
 constexpr int64_t kMostTokens = int64_t{1} << 30;
 constexpr int64_t kMostVocab = int64_t{1} << 30;
 constexpr int kMostSplitRows = 8192;  // partial pairs of rows that are split: rows * splits stays under this
+constexpr int kMostRowGroups = 4096;  // workgroups that hold rows: four on each of at most 1024 compute units
 
 inline size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
 // What the kernels of one loss call hand each other.
 struct LossLayout {
-  size_t part, stats, lp, g, counts, score, total;
+  size_t part, sums, stats, lp, g, counts, score, total;
 };
 
 LossLayout loss_layout(int64_t batch, int64_t seq) {
@@ -34,6 +35,7 @@ LossLayout loss_layout(int64_t batch, int64_t seq) {
     return p;
   };
   l.part = take(sizeof(float2) * kMostSplitRows);
+  l.sums = take(sizeof(double) * 3 * kMostRowGroups);
   l.stats = take(sizeof(float2) * rows);
   l.lp = take(sizeof(double) * rows);
   l.g = take(sizeof(float) * rows);
@@ -272,8 +274,11 @@ muon_status_t muon_policy_loss(muon_ctx_t* c, void* stream, const muon_logits_t*
   t.out = out;
   t.g = grad_logits ? reinterpret_cast<float*>(c->ws + l.g) : nullptr;
   t.counts = reinterpret_cast<int*>(c->ws + l.counts);
+  t.sums = reinterpret_cast<double*>(c->ws + l.sums);
   hipStream_t s = static_cast<hipStream_t>(stream);
   return timed(c, s, MUON_K_LOSS, "policy loss launch", [&] {
+    if (a.rows > 64 && policy_rows_fit(a))
+      return launch_policy_rows(s, a, grad_logits ? rows_ref(*grad_logits) : RowsRef{}, t, std::min(c->cus, kMostRowGroups / 4));
     hipError_t e = launch_row_stats(s, a);
     if (e == hipSuccess) e = launch_policy_terms(s, t);
     if (e == hipSuccess && grad_logits) e = launch_logits_grad(s, a, rows_ref(*grad_logits), t.g);

@@ -47,9 +47,14 @@ struct PolicyArgs {
   const float* ref_lp;
   float* out;
   float* g;
-  int* counts;  // [batch]
+  int* counts;   // [batch]
+  double* sums;  // three per workgroup of launch_policy_rows
 };
 hipError_t launch_policy_terms(hipStream_t s, const PolicyArgs& a);
+
+// Loss and gradient in one pass over rows that a workgroup's registers hold.
+bool policy_rows_fit(const LossArgs& a);
+hipError_t launch_policy_rows(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p, int cus);
 
 struct PreferenceArgs {
   muon_preference_params_t p;
