@@ -399,10 +399,11 @@ const char* muon_noalloc_last_error(void);
  * storage are all described without a copy.  Inputs may overlap themselves
  * (strides of 0 included); rows that are written must be disjoint.  Strides
  * are >= 0; that of a dimension of size one is ignored. */
+#define MUON_MAX_VOCAB (1 << 19)
 typedef struct {
   void* data;
   int32_t dtype;                    /* MUON_BF16 or MUON_F32 */
-  int64_t batch, seq, vocab;        /* vocab in [1, 2^30], batch * seq <= 2^30 */
+  int64_t batch, seq, vocab;        /* vocab in [1, MUON_MAX_VOCAB], batch * seq <= 2^30 */
   int64_t batch_stride, row_stride; /* elements */
 } muon_logits_t;
 
@@ -435,9 +436,10 @@ typedef struct {
  * no token follow (and 0 for no pair), per-token arrays are empty and may be
  * NULL. */
 
-/* Workspace in bytes of any one of the loss calls on batch x seq tokens (pure
- * host function; 0 for sizes out of range). */
-size_t muon_loss_workspace_bytes(int64_t batch, int64_t seq);
+/* Workspace in bytes of any one of the loss calls on batch x seq rows of
+ * `vocab` scores of `dtype` (pure host function; 0 for arguments out of
+ * range).  8 bytes per row and slice of a row, about 28 per row beside. */
+size_t muon_loss_workspace_bytes(int64_t batch, int64_t seq, int64_t vocab, int32_t dtype);
 
 /* Log-probability of every token: logps[t] = z[y] - log sum_v exp(z[v]).
  * logps: fp32 per token.  row_stats (may be NULL): two floats per token, the
@@ -606,6 +608,11 @@ typedef enum {
 } muon_kernel_class_t;
 
 muon_status_t muon_timing_enable(muon_ctx_t* ctx, int32_t enable, int32_t capacity);
+/* How often a workgroup of muon_policy_loss polls for what the other
+ * workgroups of its row publish before it computes that itself (default
+ * 16384, tens of milliseconds; the results are the same bits either way).
+ * 0: at once.  Errors: MUON_EINVAL (ctx NULL, polls < 0). */
+muon_status_t muon_loss_set_polls(muon_ctx_t* ctx, int32_t polls);
 /* Time only the kernel classes whose bit (1u << muon_kernel_class_t) is set
  * in class_mask: launches of the other classes record no events, and so
  * add no event markers to their stream (every class is timed by default;

@@ -24,7 +24,7 @@ EXPORTS = [
     "muon_timing_enable", "muon_timing_select", "muon_timing_reset", "muon_timing_read",
     "muon_newton_schulz_batched_noalloc", "muon_noalloc_last_error",
     "muon_plan", "muon_plan_total_elems", "muon_workspace_bytes",
-    "muon_loss_workspace_bytes", "muon_token_logps", "muon_token_logps_backward",
+    "muon_loss_workspace_bytes", "muon_loss_set_polls", "muon_token_logps", "muon_token_logps_backward",
     "muon_policy_loss", "muon_preference_loss", "muon_grad_norm_workspace_bytes",
     "muon_grad_norm", "muon_clip_coef", "muon_scale_grads", "muon_momentum_update_clipped",
 ]
@@ -116,7 +116,8 @@ def load() -> ctypes.CDLL:
         "muon_newton_schulz_batched_noalloc": (i32, [ctypes.c_int, vp, P(vp), i64, Shape, i32,
                                                       P(NsParams), P(vp), vp]),
         "muon_noalloc_last_error": (ctypes.c_char_p, []),
-        "muon_loss_workspace_bytes": (sz, [i64, i64]),
+        "muon_loss_workspace_bytes": (sz, [i64, i64, i64, i32]),
+        "muon_loss_set_polls": (i32, [vp, i32]),
         "muon_token_logps": (i32, [vp, vp, P(Logits), vp, f32, vp, vp]),
         "muon_token_logps_backward": (i32, [vp, vp, P(Logits), vp, f32, vp, vp, P(Logits)]),
         "muon_policy_loss": (i32, [vp, vp, P(Logits), vp, P(PolicyParams), vp, vp, vp, vp, vp, P(Logits)]),

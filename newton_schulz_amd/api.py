@@ -143,9 +143,10 @@ LOSS_REDUCE = {"token": 0, "sequence": 1, "sum": 2}
 PREFERENCE_KINDS = {"sigmoid": 0, "ipo": 1}
 
 
-def loss_workspace_bytes(batch: int, seq: int) -> int:
-    """Workspace a context needs for any loss call on batch x seq tokens."""
-    return int(_lib.load().muon_loss_workspace_bytes(batch, seq))
+def loss_workspace_bytes(batch: int, seq: int, vocab: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    """Workspace a context needs for any loss call on batch x seq rows of
+    `vocab` scores."""
+    return int(_lib.load().muon_loss_workspace_bytes(batch, seq, vocab, _DT.get(dtype, -1)))
 
 
 def grad_norm_workspace_bytes(tensors: Sequence[torch.Tensor]) -> int:
@@ -470,6 +471,11 @@ class Context:
         grads = self._list(grads)
         self.grad_norm(grads, norm, max_norm, eps, stream)
         self.scale_grads(grads, norm, out, stream)
+
+    def set_loss_polls(self, polls: int):
+        """muon_loss_set_polls: how long a workgroup of policy_loss waits for
+        its row's others before it does their part itself."""
+        self._raise(self.lib.muon_loss_set_polls(self.handle, polls), "muon_loss_set_polls")
 
     # -- timing ---------------------------------------------------------------
     def timing_enable(self, enable: bool = True, capacity: int = 8192):

@@ -97,14 +97,17 @@ template <typename T> __device__ __forceinline__ void store_group(T* p, int64_t 
     if (e0 + i >= 0 && e0 + i < n) muon::Elem<T>::store(p + e0 + i, v[i]);
 }
 
-// Sum over the 256 threads in a fixed order; thread 0 has it.
-__device__ __forceinline__ double block_sum(double v) {
+// Sum over the NT threads in a fixed order, in every thread.
+template <int NT> __device__ __forceinline__ double block_sum(double v) {
 #pragma unroll
   for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  __shared__ double ws[kThreads / 64];
+  __shared__ double ws[NT / 64];
   if ((threadIdx.x & 63) == 0) ws[threadIdx.x >> 6] = v;
   __syncthreads();
-  return (ws[0] + ws[1]) + (ws[2] + ws[3]);
+  double t = ws[0];
+#pragma unroll
+  for (int w = 1; w < NT / 64; ++w) t += ws[w];
+  return t;
 }
 
 template <typename T>
@@ -133,7 +136,7 @@ __global__ __launch_bounds__(kThreads) void sum_squares_kernel(NormTab t, int gr
   const int b = static_cast<int>(blockIdx.x), i = find_tensor(t, b);
   const int64_t q0 = static_cast<int64_t>(b - t.first[i]) * groups;
   const bool bf = (t.bf16[i >> 5] >> (i & 31)) & 1u;
-  const double s = block_sum(bf ? chunk_squares<bf16_t>(t.data[i], t.numel[i], q0, groups)
+  const double s = block_sum<kThreads>(bf ? chunk_squares<bf16_t>(t.data[i], t.numel[i], q0, groups)
                                 : chunk_squares<float>(t.data[i], t.numel[i], q0, groups));
   if (threadIdx.x == 0) partial[b] = s;
 }
@@ -147,18 +150,19 @@ __device__ __forceinline__ void write_norm(double s, double max_norm, double eps
   norm[2] = c;
 }
 
-__global__ __launch_bounds__(kThreads) void sum_partials_kernel(const double* __restrict__ partial, int64_t n,
+constexpr int kJoinThreads = 1024;
+__global__ __launch_bounds__(kJoinThreads) void sum_partials_kernel(const double* __restrict__ partial, int64_t n,
                                                                 double max_norm, double eps, double* norm) {
   double acc = 0.0;
   constexpr int U = 8;
-  for (int64_t p = threadIdx.x; p < n; p += U * kThreads) {
+  for (int64_t p = threadIdx.x; p < n; p += U * kJoinThreads) {
     double v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = p + u * kThreads < n ? partial[p + u * kThreads] : 0.0;
+    for (int u = 0; u < U; ++u) v[u] = p + u * kJoinThreads < n ? partial[p + u * kJoinThreads] : 0.0;
 #pragma unroll
     for (int u = 0; u < U; ++u) acc += v[u];
   }
-  const double s = block_sum(acc);
+  const double s = block_sum<kJoinThreads>(acc);
   if (threadIdx.x == 0) write_norm(s, max_norm, eps, norm);
 }
 
@@ -212,7 +216,7 @@ int64_t clip_chunk(int64_t total) {
   // small lists in small chunks, so that they still fill the device; large
   // ones in chunks that keep the partial sums few
   int64_t c = 4096;
-  while (c < 65536 && total / c > 4096) c *= 2;
+  while (c < 65536 && total / c > 16384) c *= 2;
   return c;
 }
 
@@ -270,7 +274,7 @@ hipError_t launch_grad_norm(hipStream_t s, const muon_tensor_t* t, int64_t count
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;
-  sum_partials_kernel<<<1, kThreads, 0, s>>>(partial, total, max_norm, eps, norm);
+  sum_partials_kernel<<<1, kJoinThreads, 0, s>>>(partial, total, max_norm, eps, norm);
   return hipGetLastError();
 }
 

@@ -8,16 +8,28 @@
 // has seen, and a larger maximum m' turns s into s exp(m - m').  Partial pairs
 // join the same way, in a fixed order.
 //
-// Precision.  Scores are widened to fp32 and subtracted before they are
-// scaled: (x - m) * (log2 e / T) is exact in the subtraction for bf16 and has
-// no large cancelling terms at any magnitude of x, where x * k - m * k loses
-// |m| k 2^-24 (and overflows for masks of the type's lowest value).  m starts
-// at the lowest finite number, not at -infinity, so that a masked score gives
-// exp2(-inf) = 0 and never inf - inf.  The log-probability is formed from
-// (x_y - M), S in binary64: what follows takes differences of two of them.
+// Arithmetic.  Scores are widened to fp32; with k = log2 e / T and a reference
+// m, exp(z - m / T) is exp2(x k - c), c = m k rounded: one fused multiply-add
+// and one exponential.  The rounding of c is the same in S, in the gradient
+// and in the log-probability (x_y k - c - log2 S, in binary64: what follows
+// takes differences of two of them), so it cancels.  The reference is a
+// running maximum; it is raised, and s scaled, only when some lane of the wave
+// has met a larger score (rescaling at every piece took 10% more VALU cycles).
 //
-// All kernels are bound by HBM: the statistics read each row once, the
-// gradient reads and writes it once.
+// c has to stay finite and -infinity (a masked score) must give 0, so the
+// reference starts at -1e30 instead of -infinity.  Rows whose maximum is not
+// inside (-1e30, 1e30) -- nothing but masks of the type's lowest value or of
+// -infinity, +infinity, values near the type's limit -- are done again as
+// exp2((x - m) k) with the exact maximum (far_row), where no large terms
+// cancel at any magnitude.
+//
+// Shape of the kernels.  All are bound by HBM (a pass that only reads reaches
+// 6.1-6.3 TB/s on MI355X, one that reads and writes alike 5.7-6.0), and HBM is
+// fastest when the workgroups in flight cover a compact, moving window of
+// addresses: copying in 16 KB pieces per workgroup reaches 6.0 TB/s, in 300 KB
+// rows per workgroup 4.9.  So a row is cut into slices of at most kSlicePieces
+// pieces, one workgroup of 256 threads each, in address order; a slice is held
+// in registers.
 #include <algorithm>
 #include <cfloat>
 
@@ -30,6 +42,7 @@ namespace {
 
 constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLowest = -FLT_MAX;
+constexpr float kFar = 1e30f;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));  // 16 bytes at an element's alignment
@@ -86,6 +99,16 @@ template <typename T> __device__ __forceinline__ int edge_score(const RowShape& 
   return i < s.head ? i : i + s.full * kVec<T>;
 }
 
+// Piece `base` + t of a row: a uniform base in scalar registers and one 32-bit
+// offset per thread, whatever the base (indexing with base + t keeps a 64-bit
+// address alive for every piece of an unrolled loop).
+__device__ __forceinline__ const u32x4* piece_at(const u32x4* body, int base, int t) {
+  return reinterpret_cast<const u32x4*>(reinterpret_cast<const char*>(body + base) + static_cast<uint32_t>(t) * 16u);
+}
+__device__ __forceinline__ u32x4_any* piece_at(u32x4_any* body, int base, int t) {
+  return reinterpret_cast<u32x4_any*>(reinterpret_cast<char*>(body + base) + static_cast<uint32_t>(t) * 16u);
+}
+
 template <typename T> __device__ __forceinline__ T* row_at(const RowsRef& x, int r, int seq) {
   const int b = r / seq;
   return reinterpret_cast<T*>(x.base + static_cast<int64_t>(b) * x.bs +
@@ -94,47 +117,81 @@ template <typename T> __device__ __forceinline__ T* row_at(const RowsRef& x, int
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-// (m, s) joined with (mo, so); k = log2 e / T.
+// exp2(x k - c), c = m k.
+__device__ __forceinline__ float exp_at(float x, float k, float c) { return exp2_fast(__builtin_fmaf(x, k, -c)); }
+
+// Whether a row of maximum m takes the exact form, exp2((x - m) k).
+__device__ __forceinline__ bool far_row(float m, float k) { return !(fabsf(m) < kFar) || k > 1e6f; }
+
+// (m, s) joined with (mo, so).
+template <bool EXACT = false>
 __device__ __forceinline__ void join(float& m, float& s, float mo, float so, float k) {
   const float mn = fmaxf(m, mo);
-  s = s * exp2_fast((m - mn) * k) + so * exp2_fast((mo - mn) * k);
+  if (EXACT) s = s * exp2_fast((m - mn) * k) + so * exp2_fast((mo - mn) * k);
+  else s = s * exp2_fast(m * k - mn * k) + so * exp2_fast(mo * k - mn * k);
   m = mn;
 }
 
-// The pair of N neighbouring lanes, in each of them.
-template <int N = 64> __device__ __forceinline__ void wave_join(float& m, float& s, float k) {
+// The pair of N neighbouring lanes, in each of them (the two terms of a join
+// commute, so both partners form the same sum).
+template <int N = 64, bool EXACT = false> __device__ __forceinline__ void wave_join(float& m, float& s, float k) {
 #pragma unroll
-  for (int d = N / 2; d > 0; d >>= 1) {
-    const float mo = __shfl_xor(m, d, 64), so = __shfl_xor(s, d, 64);
-    const float mn = fmaxf(m, mo);
-    // a + b commutes: both partners form the same sum
-    const float a = s * exp2_fast((m - mn) * k), b = so * exp2_fast((mo - mn) * k);
-    s = a + b;
-    m = mn;
-  }
+  for (int d = N / 2; d > 0; d >>= 1) join<EXACT>(m, s, __shfl_xor(m, d, 64), __shfl_xor(s, d, 64), k);
 }
 
 // The pair of all threads of the workgroup, in every thread.
-template <int NT> __device__ __forceinline__ void block_join(float& m, float& s, float k) {
+template <int NT, bool EXACT = false> __device__ __forceinline__ void block_join(float& m, float& s, float k) {
   constexpr int W = NT / 64;
   __shared__ float2 wave[W];
-  wave_join(m, s, k);
+  wave_join<64, EXACT>(m, s, k);
+  __syncthreads();  // an earlier call's values have been read
   if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = make_float2(m, s);
   __syncthreads();
-  m = wave[0].x;
-  s = wave[0].y;
-#pragma unroll
-  for (int w = 1; w < W; ++w) join(m, s, wave[w].x, wave[w].y, k);
+  const float2 q = wave[threadIdx.x & (W - 1)];
+  m = q.x;
+  s = q.y;
+  wave_join<W, EXACT>(m, s, k);
 }
 
-// z_y - M - log S with T = 1 / inv_t, xm = x_y - max x.  log S = ln 2 (e +
-// log2 f), S = 2^e f with f in [1/2, 1): the large part is exact, so the
-// absolute error is that of log2 f, below 2^-23, at any S.
-__device__ __forceinline__ double token_lp(float xm, float s, double inv_t) {
+// (m, s) with one more score, in the exact form.
+__device__ __forceinline__ void take_exact(float v, float& m, float& s, float k) {
+  const float mn = fmaxf(m, v);
+  s = s * exp2_fast((m - mn) * k) + exp2_fast((v - mn) * k);
+  m = mn;
+}
+
+// (m, s) with more scores; c = m k.
+template <int N> __device__ __forceinline__ void take_scores(const float (&v)[N], float& m, float& c, float& s, float k) {
+  float mn = m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) mn = fmaxf(mn, v[i]);
+  if (__any(mn > m)) {
+    const float cn = mn * k;
+    s *= exp2_fast(c - cn);
+    m = mn;
+    c = cn;
+    asm volatile("" : "+v"(s));  // stays a branch
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) s += exp_at(v[i], k, c);
+}
+template <typename T> __device__ __forceinline__ void take_piece(u32x4 w, float& m, float& c, float& s, float k) {
+  float v[kVec<T>];
+  Scores<T>::unpack(w, v);
+  take_scores(v, m, c, s, k);
+}
+
+// lp of score xy in a row of pair (m, s).  log2 S = e + log2 f, S = 2^e f
+// with f in [1/2, 1): the large part is exact, so the absolute error is that
+// of log2 f, below 2^-23, at any S.
+__device__ __forceinline__ double token_lp(float xy, float m, float s, float k) {
   int e = 0;
   const float f = frexpf(s, &e);
   const double log2s = static_cast<double>(e) + static_cast<double>(__builtin_amdgcn_logf(f));
-  return static_cast<double>(xm) * inv_t - log2s * 0.69314718055994530942;
+  const double kd = static_cast<double>(k);
+  const double z = far_row(m, k) ? static_cast<double>(xy - m) * kd
+                                 : static_cast<double>(xy) * kd - static_cast<double>(m * k);
+  return (z - log2s) * 0.69314718055994530942;
 }
 
 // What the row's pair makes of token r (one thread).
@@ -144,198 +201,78 @@ __device__ __forceinline__ void finish_row(const LossArgs& a, int r, int64_t y, 
   if (y >= a.vocab) {
     lp = __longlong_as_double(0x7ff8000000000000ll);
   } else if (y >= 0) {
-    const float xm = muon::Elem<T>::load(row_at<const T>(a.x, r, a.seq) + y) - m;
-    lp = token_lp(xm, s, 1.0 / static_cast<double>(a.temperature));
+    lp = token_lp(muon::Elem<T>::load(row_at<const T>(a.x, r, a.seq) + y), m, s, kLog2e / a.temperature);
   }
   if (a.lp) a.lp[r] = lp;
   if (a.logps) a.logps[r] = static_cast<float>(lp);
   if (a.stats) a.stats[r] = make_float2(m, s);
 }
 
-constexpr int kStatsThreads = 256;
-constexpr int kStatsUnroll = 4;  // pieces in flight per thread, twice
+// ---------------------------------------------------------------------------
+// slices of a row
+// ---------------------------------------------------------------------------
+constexpr int kThreads = 256;
 
-// (m, s) with the scores of one piece.
-template <typename T> __device__ __forceinline__ void take_piece(u32x4 w, float& m, float& s, float k) {
-  float v[kVec<T>];
-  Scores<T>::unpack(w, v);
-  float mn = m;
-#pragma unroll
-  for (int i = 0; i < kVec<T>; ++i) mn = fmaxf(mn, v[i]);
-  s *= exp2_fast((m - mn) * k);
-  m = mn;
-#pragma unroll
-  for (int i = 0; i < kVec<T>; ++i) s += exp2_fast((v[i] - m) * k);
-}
-__device__ __forceinline__ void take_score(float v, float& m, float& s, float k) {
-  const float mn = fmaxf(m, v);
-  s = s * exp2_fast((m - mn) * k) + exp2_fast((v - mn) * k);
-  m = mn;
+// Slice j of a row: pieces [first, first + count), and with slice 0 the edges.
+struct Slice {
+  int first, count;
+};
+__device__ __forceinline__ Slice slice_of(const RowShape& sh, int slices, int j) {
+  const int per = (sh.full + slices - 1) / slices, first = min(sh.full, j * per);
+  return {first, min(per, sh.full - first)};
 }
 
-// Statistics of row blockIdx / splits, pieces of split blockIdx % splits.
+// The pair of one slice of a far row, in every thread.
 template <typename T>
-__global__ __launch_bounds__(kStatsThreads) void row_stats_kernel(LossArgs a) {
-  const int r = a.row0 + static_cast<int>(blockIdx.x) / a.splits, sp = static_cast<int>(blockIdx.x) % a.splits;
-  const int64_t y = a.labels[r];
-  if (y < 0 || y >= a.vocab) {
-    if (a.splits == 1 && threadIdx.x == 0) finish_row<T>(a, r, y, 0.0f, 1.0f);
-    return;
-  }
-  const float k = kLog2e / a.temperature;
-  const T* row = row_at<const T>(a.x, r, a.seq);
-  const RowShape sh = row_shape(row, a.vocab);
-  const u32x4* body = reinterpret_cast<const u32x4*>(row + sh.head);
-  const int per = (sh.full + a.splits - 1) / a.splits;
-  const int p0 = sp * per, p1 = min(sh.full, p0 + per);
-  constexpr int U = kStatsUnroll, step = kStatsThreads * U;
-  const u32x4 masked = {Scores<T>::kMasked, Scores<T>::kMasked, Scores<T>::kMasked, Scores<T>::kMasked};
-  float m = kLowest, s = 0.0f;
+__device__ __forceinline__ void far_slice(const T* row, const RowShape& sh, Slice sl, bool edges, float k, float& m,
+                                          float& s) {
+  m = kLowest;
+  s = 0.0f;
+  const T* x = row + sh.head + static_cast<int64_t>(sl.first) * kVec<T>;
+#pragma unroll 1
+  for (int e = threadIdx.x; e < sl.count * kVec<T>; e += kThreads) take_exact(muon::Elem<T>::load(x + e), m, s, k);
+  if (edges && static_cast<int>(threadIdx.x) < sh.edges)
+    take_exact(muon::Elem<T>::load(row + edge_score<T>(sh, threadIdx.x)), m, s, k);
+  block_join<kThreads, true>(m, s, k);
+}
+
+// The pair of slice j read from memory, in every thread: the sums of
+// slice_kernel in its order, so the same bits.
+template <typename T>
+__device__ __forceinline__ void slice_pair(const T* row, const RowShape& sh, int slices, int j, float k, float& m,
+                                           float& s) {
+  const Slice sl = slice_of(sh, slices, j);
+  const u32x4* body = reinterpret_cast<const u32x4*>(row + sh.head) + sl.first;
   const int t = static_cast<int>(threadIdx.x);
-  auto load = [&](u32x4* w, int base) {
-    if (base + step <= p1) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) w[u] = body[base + u * kStatsThreads + t];
-    } else {
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int q = base + u * kStatsThreads + t;
-        w[u] = masked;
-        if (q < p1) w[u] = body[q];
-      }
-    }
-  };
-  // two sets of loads: one in flight while the other is taken
-  u32x4 w[2][U];
-  load(w[0], p0);
-  for (int base = p0; base < p1; base += 2 * step) {
-    load(w[1], base + step);
-#pragma unroll
-    for (int u = 0; u < U; ++u) take_piece<T>(w[0][u], m, s, k);
-    load(w[0], base + 2 * step);
-#pragma unroll
-    for (int u = 0; u < U; ++u) take_piece<T>(w[1][u], m, s, k);
+  float c = -kFar * k;
+  m = -kFar;
+  s = 0.0f;
+#pragma unroll 1
+  for (int q = t; q < sl.count; q += kThreads) take_piece<T>(body[q], m, c, s, k);
+  if (j == 0 && t < sh.edges) {
+    const float v[1] = {muon::Elem<T>::load(row + edge_score<T>(sh, t))};
+    take_scores(v, m, c, s, k);
   }
-  if (sp == 0 && t < sh.edges) take_score(muon::Elem<T>::load(row + edge_score<T>(sh, t)), m, s, k);
-  block_join<kStatsThreads>(m, s, k);
-  if (t == 0) {
-    if (a.splits == 1) finish_row<T>(a, r, y, m, s);
-    else a.part[static_cast<int64_t>(r) * a.splits + sp] = make_float2(m, s);
-  }
+  block_join<kThreads>(m, s, k);
+  if (far_row(m, k)) far_slice(row, sh, sl, j == 0, k, m, s);
 }
 
-// Joins the splits of each row in index order; one thread per row.
-template <typename T> __global__ __launch_bounds__(64) void row_join_kernel(LossArgs a) {
-  const int r = blockIdx.x * 64 + threadIdx.x;
-  if (r >= a.rows) return;
-  const int64_t y = a.labels[r];
-  float m = 0.0f, s = 1.0f;
-  if (y >= 0 && y < a.vocab) {
-    const float k = kLog2e / a.temperature;
-    m = kLowest;
-    s = 0.0f;
-    for (int i = 0; i < a.splits; ++i) {
-      const float2 q = a.part[static_cast<int64_t>(r) * a.splits + i];
-      join(m, s, q.x, q.y, k);
-    }
-  }
-  finish_row<T>(a, r, y, m, s);
+// The pair of a row from those of its slices, one in each of N lanes (lanes
+// without one hold (-kFar, 0)), in each of them.
+template <int N> __device__ __forceinline__ void join_slices(float& m, float& s, float k) {
+  float top = m;
+#pragma unroll
+  for (int d = N / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
+  if (far_row(top, k)) wave_join<N, true>(m, s, k);
+  else wave_join<N>(m, s, k);
 }
 
-constexpr int kGradThreads = 256;
-constexpr int kGradUnroll = 4;
-
-// Gradient of row blockIdx / chunks, pieces of chunk blockIdx % chunks (the
-// first chunk takes the edges).
-template <typename T>
-__global__ __launch_bounds__(kGradThreads) void logits_grad_kernel(LossArgs a, RowsRef grad,
-                                                                   const float* __restrict__ g, int chunks) {
-  const int r = a.row0 + static_cast<int>(blockIdx.x) / chunks, c = static_cast<int>(blockIdx.x) % chunks;
-  const int64_t y = a.labels[r];
-  const T* row = row_at<const T>(a.x, r, a.seq);
-  T* out = row_at<T>(grad, r, a.seq);
-  const RowShape sh = row_shape(row, a.vocab);
-  const u32x4* body = reinterpret_cast<const u32x4*>(row + sh.head);
-  // the gradient's rows have an alignment of their own
-  u32x4_any* obody = reinterpret_cast<u32x4_any*>(out + sh.head);
-  const int t = static_cast<int>(threadIdx.x), p0 = c * kGradThreads * kGradUnroll + t;
-  const bool edge = c == 0 && t < sh.edges;
-  if (y < 0) {
-#pragma unroll
-    for (int u = 0; u < kGradUnroll; ++u) {
-      const int p = p0 + u * kGradThreads;
-      if (p < sh.full) obody[p] = u32x4{0, 0, 0, 0};
-    }
-    if (edge) muon::Elem<T>::store(out + edge_score<T>(sh, t), 0.0f);
-    return;
-  }
-  const float k = kLog2e / a.temperature;
-  const float2 st = a.stats[r];
-  float G = g[r] / a.temperature;
-  if (y >= a.vocab) G = __uint_as_float(0x7fc00000u);  // the label names no score
-  const float scale = -G / st.y;
-  u32x4 w[kGradUnroll];
-#pragma unroll
-  for (int u = 0; u < kGradUnroll; ++u) {
-    const int p = p0 + u * kGradThreads;
-    if (p < sh.full) w[u] = body[p];
-  }
-  // the label's place: piece py, score iy of it (no piece when it is an edge)
-  const int ly = static_cast<int>(y < a.vocab ? y : 0) - sh.head;
-  const int py = ly >= 0 ? ly / kVec<T> : -1, iy = ly - py * kVec<T>;
-#pragma unroll
-  for (int u = 0; u < kGradUnroll; ++u) {
-    const int p = p0 + u * kGradThreads;
-    if (p >= sh.full) continue;
-    float v[kVec<T>];
-    Scores<T>::unpack(w[u], v);
-#pragma unroll
-    for (int i = 0; i < kVec<T>; ++i) v[i] = scale * exp2_fast((v[i] - st.x) * k);
-    if (p == py) {
-#pragma unroll
-      for (int i = 0; i < kVec<T>; ++i)
-        if (i == iy) v[i] += G;
-    }
-    obody[p] = Scores<T>::pack(v);
-  }
-  if (edge) {
-    const int e = edge_score<T>(sh, t);
-    float v = scale * exp2_fast((muon::Elem<T>::load(row + e) - st.x) * k);
-    if (e == y) v += G;
-    muon::Elem<T>::store(out + e, v);
-  }
+// A slice's pair as one 64-bit word, never 0 (S is 0 only where m is far).
+__device__ __forceinline__ uint64_t pair_word(float m, float s) {
+  return (static_cast<uint64_t>(__float_as_uint(s)) << 32) | __float_as_uint(m);
 }
-
-// ---------------------------------------------------------------------------
-// per-token terms
-// ---------------------------------------------------------------------------
-constexpr int kTermThreads = 1024;
-
-// Sum over the workgroup in a fixed order, in every thread.
-__device__ __forceinline__ double block_total(double v) {
-  __shared__ double wave[kTermThreads / 64];
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  __syncthreads();  // the last call's values have been read
-  if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double t = 0.0;
-#pragma unroll
-  for (int w = 0; w < kTermThreads / 64; ++w) t += wave[w];
-  return t;
-}
-
-// Tokens that count of each sequence, one wave per sequence in turn.
-__device__ __forceinline__ void count_tokens(const int64_t* labels, int batch, int seq, int* counts) {
-  const int lane = threadIdx.x & 63;
-  for (int b = threadIdx.x >> 6; b < batch; b += kTermThreads / 64) {
-    int n = 0;
-    for (int t0 = 0; t0 < seq; t0 += 64)
-      n += __popcll(__ballot(t0 + lane < seq && labels[static_cast<int64_t>(b) * seq + t0 + lane] >= 0));
-    if (lane == 0) counts[b] = n;
-  }
-  __syncthreads();
-}
+__device__ __forceinline__ float word_max(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w)); }
+__device__ __forceinline__ float word_sum(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w >> 32)); }
 
 // max(a, b) that hands a NaN on, as the formula does.
 __device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
@@ -389,207 +326,360 @@ __device__ __forceinline__ TokenTerms policy_token(const PolicyArgs& a, int t, i
   return o;
 }
 
-__device__ __forceinline__ void write_policy(const PolicyArgs& a, double pg, double kl, double clipped) {
-  double loss = pg;
-  if (a.p.kl_coef != 0.0f) loss += static_cast<double>(a.p.kl_coef) * kl;
-  a.out[0] = static_cast<float>(static_cast<double>(a.p.weight) * loss);
-  a.out[1] = static_cast<float>(pg);
-  a.out[2] = static_cast<float>(kl);
-  a.out[3] = static_cast<float>(clipped);
-}
+// What a slice is read for.
+enum SliceUse : int {
+  USE_STATS = 0,   // the row's pair alone
+  USE_POLICY = 1   // the policy loss and its gradient
+};
 
-__global__ __launch_bounds__(kTermThreads) void policy_terms_kernel(PolicyArgs a) {
-  const int rows = a.batch * a.seq;
-  count_tokens(a.labels, a.batch, a.seq, a.counts);
-  double n = 0.0;
-  for (int b = threadIdx.x; b < a.batch; b += kTermThreads) n += a.counts[b];
-  n = block_total(n);
-  double sum_pg = 0.0, sum_kl = 0.0, sum_clip = 0.0;
-  for (int t = threadIdx.x; t < rows; t += kTermThreads) {
-    if (a.labels[t] < 0) {
-      if (a.g) a.g[t] = 0.0f;
-      continue;
-    }
-    const int b = t / a.seq;
-    const double w = a.p.reduce == MUON_REDUCE_TOKEN      ? 1.0 / n
-                     : a.p.reduce == MUON_REDUCE_SEQUENCE ? 1.0 / (static_cast<double>(a.counts[b]) * a.batch)
-                                                          : 1.0;
-    const TokenTerms o = policy_token(a, t, b, a.lp[t]);
-    sum_pg += w * static_cast<double>(o.pg);
-    sum_kl += w * static_cast<double>(o.kl);
-    sum_clip += w * static_cast<double>(o.clipped);
-    if (a.g) a.g[t] = static_cast<float>(static_cast<double>(a.p.weight) * w * static_cast<double>(o.g));
-  }
-  const double pg = block_total(sum_pg), kl = block_total(sum_kl), clipped = block_total(sum_clip);
-  if (threadIdx.x == 0) write_policy(a, pg, kl, clipped);
-}
-
-// ---------------------------------------------------------------------------
-// rows held in registers
-// ---------------------------------------------------------------------------
-// One workgroup holds a whole row (NV pieces a thread: 304 KB of the 512 KB of
-// a compute unit's registers at 151936 bf16 scores), so the policy loss, whose
-// gradient of a token needs nothing of other rows but their number, reads
-// every score once and writes every gradient once.  The workgroup walks rows
-// blockIdx, + gridDim, ...; as soon as a piece's gradient has gone out, the
-// same registers receive the next row's piece, so loads are in flight through
-// the whole second half of a row.
-template <typename T, int NT, int NV>
-__global__ __launch_bounds__(NT, 4) void policy_rows_kernel(LossArgs a, RowsRef grad, PolicyArgs p) {
-  constexpr int W = NT / 64;
-  const int t = static_cast<int>(threadIdx.x), lane = t & 63, wave = t >> 6;
-  const int stride = static_cast<int>(gridDim.x);
+// Workgroup: slice blockIdx % slices of row blockIdx / slices, NV pieces a
+// thread.
+//
+// USE_STATS leaves the slice's pair in a.part (whole rows: finishes the token).
+//
+// USE_POLICY reads every score once and writes every gradient once, which is
+// all the traffic the loss needs: a token's gradient depends on nothing of
+// other rows but their number, so a slice only lacks the pairs of its row's
+// other slices.  It publishes its own as one 64-bit word (an agent-scope
+// atomic store: no other data has to be made visible with it) and waits for
+// theirs, its scores staying in registers.  The slices of a row are
+// neighbours in the order in which workgroups start, so the wait is that of a
+// few microseconds' skew, and other workgroups of the compute unit run
+// meanwhile.  It is bounded: after a.spin polls the workgroup computes the
+// missing pairs itself from memory, so it ends whether or not its neighbours
+// ever run beside it.  (In place, a neighbour overwrites its slice only after
+// it has published: a pair computed here is used only if the neighbour's is
+// still missing afterwards.)
+// Against a workgroup per row with the row in its registers (1024 threads of 19
+// pieces): 2048 tokens x 151936 bf16 scores took 267 us there.
+template <typename T, int NV, int USE>
+__global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef grad, PolicyArgs p) {
+  const int t = static_cast<int>(threadIdx.x), lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int r = a.row0 + static_cast<int>(blockIdx.x) / a.slices, j = static_cast<int>(blockIdx.x) % a.slices;
+  const int64_t y = a.labels[r];
+  const T* row = row_at<const T>(a.x, r, a.seq);
+  const RowShape sh = row_shape(row, a.vocab);
+  const Slice sl = slice_of(sh, a.slices, j);
+  const bool edge = j == 0 && t < sh.edges;
   const float k = kLog2e / a.temperature;
-  const u32x4 masked = {Scores<T>::kMasked, Scores<T>::kMasked, Scores<T>::kMasked, Scores<T>::kMasked};
-  __shared__ float2 part[2][W];
-  __shared__ int found[2][W];
-  __shared__ float coef[2][3];
-  __shared__ double weight, sums[3];  // of wave 0
-
-  // The next row from r on that counts; rows left out on the way get their zeros.
-  auto next_row = [&](int r) {
-    for (; r < a.rows && a.labels[r] < 0; r += stride) {
-      if (t == 0 && a.logps) a.logps[r] = 0.0f;
-      if (grad.base == nullptr) continue;
-      T* out = row_at<T>(grad, r, a.seq);
-      const RowShape sh = row_shape(row_at<const T>(a.x, r, a.seq), a.vocab);
-      u32x4_any* body = reinterpret_cast<u32x4_any*>(out + sh.head);
-      for (int q = t; q < sh.full; q += NT) body[q] = u32x4{0, 0, 0, 0};
-      if (t < sh.edges) muon::Elem<T>::store(out + edge_score<T>(sh, t), 0.0f);
-    }
-    return r;
-  };
-
-  u32x4 w[NV];
-  float we = -INFINITY;  // this thread's edge
-  int r = next_row(static_cast<int>(blockIdx.x));
-  const T* row = row_at<const T>(a.x, r < a.rows ? r : 0, a.seq);
-  RowShape sh = row_shape(row, a.vocab);
-  if (r < a.rows) {
+  T* out = USE == USE_POLICY ? row_at<T>(grad, r, a.seq) : nullptr;
+  // the gradient's rows have an alignment of their own
+  u32x4_any* obody = USE == USE_POLICY ? reinterpret_cast<u32x4_any*>(out + sh.head) + sl.first : nullptr;
+  if (y < 0 || (USE == USE_STATS && y >= a.vocab)) {  // left out; or names no score, and its row is not needed
+    if (USE == USE_POLICY && grad.base) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      w[i] = masked;
-      if (i * NT + t < sh.full) w[i] = reinterpret_cast<const u32x4*>(row + sh.head)[i * NT + t];
+      for (int i = 0; i < NV; ++i)
+        if (t < sl.count - i * kThreads) *piece_at(obody, i * kThreads, t) = u32x4{0, 0, 0, 0};
+      if (edge) muon::Elem<T>::store(out + edge_score<T>(sh, t), 0.0f);
     }
-    if (t < sh.edges) we = muon::Elem<T>::load(row + edge_score<T>(sh, t));
+    if (j == 0 && t == 0) {
+      if (USE == USE_POLICY && a.logps) a.logps[r] = 0.0f;
+      if (USE == USE_STATS && a.slices == 1) finish_row<T>(a, r, y, 0.0f, 1.0f);
+    }
+    return;
   }
-  int counted = -1;  // the sequence (or 0: all) whose tokens the weight goes by
-  if (t == 0) sums[0] = sums[1] = sums[2] = 0.0;
-  const double inv_t = 1.0 / static_cast<double>(a.temperature);
-  for (int parity = 0; r < a.rows; parity ^= 1) {
-    const int b = r / a.seq;
-    const int64_t y = a.labels[r];
-    const bool named = y < a.vocab;
-    const float xy = muon::Elem<T>::load(row + (named ? y : 0));
-    // tokens that share the loss's mean with this one
-    const int set = p.p.reduce == MUON_REDUCE_SEQUENCE ? b : 0;
-    const bool count = set != counted;
-    if (count && p.p.reduce != MUON_REDUCE_SUM) {
-      const int lo = p.p.reduce == MUON_REDUCE_SEQUENCE ? b * a.seq : 0;
-      const int hi = p.p.reduce == MUON_REDUCE_SEQUENCE ? lo + a.seq : a.rows;
-      int n = 0;
-      for (int j = lo + t; j - t < hi; j += NT) n += __popcll(__ballot(j < hi && a.labels[j < hi ? j : lo] >= 0));
-      if (lane == 0) found[parity][wave] = n;
-    }
-    counted = set;
-    float m = kLowest, s = 0.0f;
+  u32x4 w[NV];
+  {
+    const u32x4* body = reinterpret_cast<const u32x4*>(row + sh.head) + sl.first;
+    const uint32_t none = Scores<T>::kMasked;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      take_piece<T>(w[i], m, s, k);
-      __builtin_amdgcn_sched_barrier(0);
+      w[i] = u32x4{none, none, none, none};
+      if (t < sl.count - i * kThreads) w[i] = *piece_at(body, i * kThreads, t);
     }
-    if (t < sh.edges) take_score(we, m, s, k);
-    wave_join(m, s, k);
-    if (lane == 0) part[parity][wave] = make_float2(m, s);
-    const int rn = next_row(r + stride);
-    __syncthreads();
-    if (wave == 0) {
-      const float2 q = part[parity][lane % W];
-      m = q.x;
-      s = q.y;
-      wave_join<W>(m, s, k);
-      if (count && lane == 0) {
-        double n = 0.0;
-        for (int i = 0; i < W; ++i) n += found[parity][i];
-        weight = p.p.reduce == MUON_REDUCE_TOKEN      ? 1.0 / n
-                 : p.p.reduce == MUON_REDUCE_SEQUENCE ? 1.0 / (n * p.batch)
-                                                      : 1.0;
-      }
-      double lp = token_lp(xy - m, s, inv_t);
-      if (!named) lp = __longlong_as_double(0x7ff8000000000000ll);
-      const TokenTerms o = policy_token(p, r, b, lp);
-      if (lane == 0) {
-        const double wt = weight;
-        sums[0] += wt * static_cast<double>(o.pg);
-        sums[1] += wt * static_cast<double>(o.kl);
-        sums[2] += wt * static_cast<double>(o.clipped);
-        const float G = static_cast<float>(static_cast<double>(p.p.weight) * wt * static_cast<double>(o.g)) / a.temperature;
-        coef[parity][0] = m;
-        coef[parity][1] = -G / s;
-        coef[parity][2] = G;
+  }
+  const float we = edge ? muon::Elem<T>::load(row + edge_score<T>(sh, t)) : -INFINITY;
+  const bool named = y < a.vocab;
+  float xy = 0.0f;
+  if (USE == USE_POLICY) xy = muon::Elem<T>::load(row + (named ? y : 0));
+  float m = -kFar, c = m * k, s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    // A piece is unpacked where it is used and never earlier, and its
+    // exponentials are summed there and never later: as far as the compiler
+    // knows the piece may have changed just before and the sum is read just
+    // after, so it keeps 4 registers a piece and not 8 more of widened scores.
+    asm volatile("" : "+v"(w[i]));
+    take_piece<T>(w[i], m, c, s, k);
+    asm volatile("" : "+v"(s));
+  }
+  if (wave == 0) {  // threads without an edge hold -infinity
+    const float v[1] = {we};
+    take_scores(v, m, c, s, k);
+  }
+  if (USE == USE_POLICY) asm volatile("" : "+v"(xy));  // read before this slice is published
+  block_join<kThreads>(m, s, k);
+  if (far_row(m, k)) far_slice(row, sh, sl, j == 0, k, m, s);
+  if (USE == USE_STATS) {
+    if (t == 0) {
+      if (a.slices == 1) finish_row<T>(a, r, y, m, s);
+      else a.part[static_cast<int64_t>(r) * a.slices + j] = pair_word(m, s);
+    }
+    return;
+  }
+  __shared__ float coef[4];
+  __shared__ uint64_t missing, own[64];
+  const int b = r / a.seq;
+  // wave 0: the row's pair from a slice's word in each lane, and what follows
+  auto settle = [&](uint64_t word) {
+    m = lane < a.slices ? word_max(word) : -kFar;
+    s = lane < a.slices ? word_sum(word) : 0.0f;
+    join_slices<64>(m, s, k);
+    double lp = token_lp(xy, m, s, k);
+    if (!named) lp = __longlong_as_double(0x7ff8000000000000ll);
+    const TokenTerms o = policy_token(p, r, b, lp);
+    const double wt = p.weights[p.p.reduce == MUON_REDUCE_SEQUENCE ? b : 0];
+    const float G = static_cast<float>(static_cast<double>(p.p.weight) * wt * static_cast<double>(o.g)) / a.temperature;
+    if (lane == 0) {
+      coef[0] = m;
+      coef[1] = -G / s;
+      coef[2] = G;
+      if (j == 0) {
         if (a.logps) a.logps[r] = static_cast<float>(lp);
+        p.terms[3 * static_cast<int64_t>(r)] = o.pg;
+        p.terms[3 * static_cast<int64_t>(r) + 1] = o.kl;
+        p.terms[3 * static_cast<int64_t>(r) + 2] = o.clipped;
+      }
+    }
+  };
+  uint64_t* slot = a.part + static_cast<int64_t>(r) * a.slices;
+  const uint64_t word = pair_word(m, s);
+  if (a.slices > 1 && t == 0) __hip_atomic_store(slot + j, word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (grad.base == nullptr && j > 0) return;  // evaluation: slice 0 has it all
+  if (wave == 0) {
+    uint64_t v = word;
+    bool ready = true;
+    if (a.slices > 1) {
+      for (int n = 0;; ++n) {
+        if (lane < a.slices) v = __hip_atomic_load(slot + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        ready = __all(v != 0);
+        if (ready || n >= a.spin) break;
+        __builtin_amdgcn_s_sleep(1);
+      }
+    }
+    const uint64_t lack = __ballot(v == 0);
+    if (lane == 0) missing = lack;
+    own[lane] = v;
+    if (ready) settle(v);
+  }
+  __syncthreads();
+  if (const uint64_t lack = missing) {
+    for (int i = 0; i < a.slices; ++i) {
+      if (!((lack >> i) & 1)) continue;
+      float mi, si;
+      slice_pair(row, sh, a.slices, i, k, mi, si);
+      if (t == 0) {
+        const uint64_t v = __hip_atomic_load(slot + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        own[i] = v ? v : pair_word(mi, si);
       }
     }
     __syncthreads();
-    const float M = coef[parity][0], scale = coef[parity][1], G = coef[parity][2];
-    // The pieces are unpacked again: as far as the compiler knows they may
-    // have changed, so it keeps 4 registers a piece across the join, not 8
-    // more of widened scores.
+    if (wave == 0) settle(own[lane]);
+    __syncthreads();
+  }
+  if (grad.base == nullptr) return;
+  const float M = coef[0], scale = coef[1], G = coef[2], C = M * k;
+  const bool far = far_row(M, k);
 #pragma unroll
-    for (int i = 0; i < NV; ++i) asm volatile("" : "+v"(w[i]));
-    const T* nrow = row_at<const T>(a.x, rn < a.rows ? rn : r, a.seq);
-    const RowShape nsh = row_shape(nrow, a.vocab);
-    const u32x4* nbody = reinterpret_cast<const u32x4*>(nrow + nsh.head);
-    const int nfull = rn < a.rows ? nsh.full : 0;
-    if (grad.base) {
-      T* out = row_at<T>(grad, r, a.seq);
-      u32x4_any* obody = reinterpret_cast<u32x4_any*>(out + sh.head);
+  for (int i = 0; i < NV; ++i) {
+    float v[kVec<T>];
+    asm volatile("" : "+v"(w[i]));
+    Scores<T>::unpack(w[i], v);
+    if (far) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        float v[kVec<T>];
-        Scores<T>::unpack(w[i], v);
-#pragma unroll
-        for (int e = 0; e < kVec<T>; ++e) v[e] = scale * exp2_fast((v[e] - M) * k);
-        if (i * NT + t < sh.full) obody[i * NT + t] = Scores<T>::pack(v);
-        w[i] = masked;
-        if (i * NT + t < nfull) w[i] = nbody[i * NT + t];
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (t < sh.edges) muon::Elem<T>::store(out + edge_score<T>(sh, t), scale * exp2_fast((we - M) * k));
-      // the label's score, by the thread whose piece or edge has just gone out
-      if (named) {
-        const int ly = static_cast<int>(y) - sh.head;
-        const bool in_piece = ly >= 0 && ly < sh.full * kVec<T>;
-        const int owner = in_piece ? (ly / kVec<T>) % NT : ly < 0 ? static_cast<int>(y) : ly - sh.full * kVec<T> + sh.head;
-        if (t == owner) muon::Elem<T>::store(out + y, scale * exp2_fast((xy - M) * k) + G);
-      }
+      for (int e = 0; e < kVec<T>; ++e) v[e] = scale * exp2_fast((v[e] - M) * k);
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        w[i] = masked;
-        if (i * NT + t < nfull) w[i] = nbody[i * NT + t];
-      }
+      for (int e = 0; e < kVec<T>; ++e) v[e] = scale * exp_at(v[e], k, C);
     }
-    if (rn < a.rows && t < nsh.edges) we = muon::Elem<T>::load(nrow + edge_score<T>(nsh, t));
-    r = rn;
-    row = nrow;
-    sh = nsh;
+    if (t < sl.count - i * kThreads)
+      __builtin_nontemporal_store(Scores<T>::pack(v), piece_at(obody, i * kThreads, t));
   }
-  if (t == 0) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) p.sums[static_cast<int64_t>(blockIdx.x) * 3 + i] = sums[i];
+  auto probability = [&](float x) { return far ? exp2_fast((x - M) * k) : exp_at(x, k, C); };
+  if (edge) muon::Elem<T>::store(out + edge_score<T>(sh, t), scale * probability(we));
+  // the label's score, by the thread whose piece or edge has just gone out
+  if (named) {
+    const int ly = static_cast<int>(y) - sh.head, q = ly >= 0 ? ly / kVec<T> : -1;
+    bool mine = q >= sl.first && q < sl.first + sl.count && (q - sl.first) % kThreads == t;
+    if (edge) mine = mine || edge_score<T>(sh, t) == y;
+    if (mine) muon::Elem<T>::store(out + y, scale * probability(xy) + G);
   }
 }
 
-// The losses of `n` workgroups, in index order per thread.
-__global__ __launch_bounds__(kTermThreads) void policy_sums_kernel(PolicyArgs p, int n) {
+// Joins the slices of each row; one wave per row.
+template <typename T> __global__ __launch_bounds__(kThreads) void row_join_kernel(LossArgs a) {
+  const int r = static_cast<int>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  if (r >= a.rows) return;
+  const int64_t y = a.labels[r];
+  float m = 0.0f, s = 1.0f;
+  if (y >= 0 && y < a.vocab) {
+    m = -kFar;
+    s = 0.0f;
+    if (lane < a.slices) {
+      const uint64_t v = a.part[static_cast<int64_t>(r) * a.slices + lane];
+      m = word_max(v);
+      s = word_sum(v);
+    }
+    join_slices<64>(m, s, kLog2e / a.temperature);
+  }
+  if (lane == 0) finish_row<T>(a, r, y, m, s);
+}
+
+constexpr int kGradUnroll = 4;
+
+// Gradient of row blockIdx / chunks, pieces of chunk blockIdx % chunks (the
+// first chunk takes the edges).
+template <typename T>
+__global__ __launch_bounds__(kThreads) void logits_grad_kernel(LossArgs a, RowsRef grad,
+                                                                   const float* __restrict__ g, int per_sequence,
+                                                                   int chunks) {
+  const int r = a.row0 + static_cast<int>(blockIdx.x) / chunks, c = static_cast<int>(blockIdx.x) % chunks;
+  const int64_t y = a.labels[r];
+  const T* row = row_at<const T>(a.x, r, a.seq);
+  T* out = row_at<T>(grad, r, a.seq);
+  const RowShape sh = row_shape(row, a.vocab);
+  const u32x4* body = reinterpret_cast<const u32x4*>(row + sh.head);
+  // the gradient's rows have an alignment of their own
+  u32x4_any* obody = reinterpret_cast<u32x4_any*>(out + sh.head);
+  const int t = static_cast<int>(threadIdx.x), p0 = c * kThreads * kGradUnroll + t;
+  const bool edge = c == 0 && t < sh.edges;
+  if (y < 0) {
+#pragma unroll
+    for (int u = 0; u < kGradUnroll; ++u) {
+      const int p = p0 + u * kThreads;
+      if (p < sh.full) obody[p] = u32x4{0, 0, 0, 0};
+    }
+    if (edge) muon::Elem<T>::store(out + edge_score<T>(sh, t), 0.0f);
+    return;
+  }
+  const float k = kLog2e / a.temperature;
+  const float2 st = a.stats[r];
+  float G = g[per_sequence ? r / a.seq : r] / a.temperature;
+  if (y >= a.vocab) G = __uint_as_float(0x7fc00000u);  // the label names no score
+  const float scale = -G / st.y, c0 = st.x * k;
+  const bool far = far_row(st.x, k);
+  u32x4 w[kGradUnroll];
+#pragma unroll
+  for (int u = 0; u < kGradUnroll; ++u) {
+    const int p = p0 + u * kThreads;
+    if (p < sh.full) w[u] = body[p];
+  }
+  // the label's place: piece py, score iy of it (no piece when it is an edge)
+  const int ly = static_cast<int>(y < a.vocab ? y : 0) - sh.head;
+  const int py = ly >= 0 ? ly / kVec<T> : -1, iy = ly - py * kVec<T>;
+#pragma unroll
+  for (int u = 0; u < kGradUnroll; ++u) {
+    const int p = p0 + u * kThreads;
+    if (p >= sh.full) continue;
+    float v[kVec<T>];
+    Scores<T>::unpack(w[u], v);
+    if (far) {
+#pragma unroll
+      for (int i = 0; i < kVec<T>; ++i) v[i] = scale * exp2_fast((v[i] - st.x) * k);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec<T>; ++i) v[i] = scale * exp_at(v[i], k, c0);
+    }
+    if (p == py) {
+#pragma unroll
+      for (int i = 0; i < kVec<T>; ++i)
+        if (i == iy) v[i] += G;
+    }
+    obody[p] = Scores<T>::pack(v);
+  }
+  if (edge) {
+    const int e = edge_score<T>(sh, t);
+    const float x = muon::Elem<T>::load(row + e);
+    float v = scale * (far ? exp2_fast((x - st.x) * k) : exp_at(x, k, c0));
+    if (e == y) v += G;
+    muon::Elem<T>::store(out + e, v);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// sums over tokens
+// ---------------------------------------------------------------------------
+constexpr int kTermThreads = 1024;
+
+// Sum over the workgroup in a fixed order, in every thread.
+template <int NT> __device__ __forceinline__ double block_total(double v) {
+  __shared__ double wave[NT / 64];
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  __syncthreads();  // an earlier call's values have been read
+  if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) t += wave[w];
+  return t;
+}
+
+// Before the slices of a policy loss: the weight of a token in the mean (of
+// each sequence, or one for all), and empty slots for the slices' pairs.
+// Workgroup b counts sequence b (workgroup 0 all tokens); all clear.
+__global__ __launch_bounds__(kTermThreads) void policy_prepare_kernel(PolicyArgs p, uint64_t* slots, int64_t n) {
+  const int t = static_cast<int>(threadIdx.x), b = static_cast<int>(blockIdx.x);
+  for (int64_t i = static_cast<int64_t>(b) * kTermThreads + t; i < n; i += static_cast<int64_t>(gridDim.x) * kTermThreads)
+    slots[i] = 0;
+  const bool each = p.p.reduce == MUON_REDUCE_SEQUENCE;
+  if (b >= (each ? p.batch : 1)) return;
+  double weight = 1.0;
+  if (p.p.reduce != MUON_REDUCE_SUM) {
+    const int64_t lo = each ? static_cast<int64_t>(b) * p.seq : 0;
+    const int64_t hi = lo + (each ? p.seq : static_cast<int64_t>(p.batch) * p.seq);
+    int count = 0;
+    constexpr int U = 4;
+    for (int64_t i = lo + t; i < hi; i += U * kTermThreads) {
+      int64_t y[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) y[u] = i + u * kTermThreads < hi ? p.labels[i + u * kTermThreads] : -1;
+#pragma unroll
+      for (int u = 0; u < U; ++u) count += y[u] >= 0;
+    }
+    const double total = block_total<kTermThreads>(count);  // whole numbers: exact
+    weight = 1.0 / (each ? total * p.batch : total);
+  }
+  if (t == 0) p.weights[b] = weight;
+}
+
+__device__ __forceinline__ void write_policy(const PolicyArgs& p, double pg, double kl, double clipped) {
+  double loss = pg;
+  if (p.p.kl_coef != 0.0f) loss += static_cast<double>(p.p.kl_coef) * kl;
+  p.out[0] = static_cast<float>(static_cast<double>(p.p.weight) * loss);
+  p.out[1] = static_cast<float>(pg);
+  p.out[2] = static_cast<float>(kl);
+  p.out[3] = static_cast<float>(clipped);
+}
+
+// The weighted sums of the tokens' terms: workgroup b of n adds the b-th run of
+// tokens.  One workgroup writes the losses, several leave their sums.
+__global__ __launch_bounds__(kTermThreads) void policy_sums_kernel(PolicyArgs p, int64_t rows) {
+  const int64_t per = (rows + gridDim.x - 1) / gridDim.x, lo = static_cast<int64_t>(blockIdx.x) * per;
+  const int64_t hi = lo + per < rows ? lo + per : rows;
   double v[3] = {0.0, 0.0, 0.0};
-  for (int i = threadIdx.x; i < n; i += kTermThreads)
+  for (int64_t i = lo + threadIdx.x; i < hi; i += kTermThreads) {
+    if (p.labels[i] < 0) continue;
+    const double w = p.weights[p.p.reduce == MUON_REDUCE_SEQUENCE ? i / p.seq : 0];
 #pragma unroll
-    for (int j = 0; j < 3; ++j) v[j] += p.sums[static_cast<int64_t>(i) * 3 + j];
+    for (int j = 0; j < 3; ++j) v[j] += w * static_cast<double>(p.terms[3 * i + j]);
+  }
 #pragma unroll
-  for (int j = 0; j < 3; ++j) v[j] = block_total(v[j]);
-  if (threadIdx.x == 0) write_policy(p, v[0], v[1], v[2]);
+  for (int j = 0; j < 3; ++j) v[j] = block_total<kTermThreads>(v[j]);
+  if (threadIdx.x != 0) return;
+  if (gridDim.x == 1) {
+    write_policy(p, v[0], v[1], v[2]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 3; ++j) p.sums[3 * blockIdx.x + j] = v[j];
+  }
+}
+__global__ void policy_total_kernel(PolicyArgs p, int n) {
+  double v[3] = {0.0, 0.0, 0.0};
+  for (int i = 0; i < n; ++i)
+#pragma unroll
+    for (int j = 0; j < 3; ++j) v[j] += p.sums[3 * i + j];
+  write_policy(p, v[0], v[1], v[2]);
 }
 
 // -log sigma(h) and sigma(h), without overflow.
@@ -601,77 +691,99 @@ __device__ __forceinline__ double sigmoid(double h) {
   return (h < 0.0 ? q : 1.0) / (1.0 + q);
 }
 
-__global__ __launch_bounds__(kTermThreads) void preference_terms_kernel(PreferenceArgs a) {
-  const int lane = threadIdx.x & 63;
-  // one wave per sequence in turn
-  for (int b = threadIdx.x >> 6; b < a.batch; b += kTermThreads / 64) {
+// Workgroup i: pair i.  Joins its tokens' slices, adds the two sequences'
+// scores, and leaves the gradient that every token of each sequence has.
+template <typename T> __global__ __launch_bounds__(kTermThreads) void preference_pairs_kernel(LossArgs a, PreferenceArgs p) {
+  const int i = static_cast<int>(blockIdx.x), pairs = p.batch / 2, t = static_cast<int>(threadIdx.x);
+  const float k = kLog2e / a.temperature;
+  double score[2];
+  int tokens[2];
+  for (int side = 0; side < 2; ++side) {
+    const int b = i + side * pairs;
     double sum = 0.0;
     int n = 0;
-    for (int t0 = 0; t0 < a.seq; t0 += 64) {
-      const int64_t t = static_cast<int64_t>(b) * a.seq + t0 + lane;
-      const bool counts = t0 + lane < a.seq && a.labels[t] >= 0;
-      n += __popcll(__ballot(counts));
-      if (counts) sum += a.lp[t] - (a.ref_lp ? static_cast<double>(a.ref_lp[t]) : 0.0);
+    for (int q = t; q < p.seq; q += kTermThreads) {
+      const int r = b * p.seq + q;
+      const int64_t y = a.labels[r];
+      float m = 0.0f, s = 1.0f;
+      if (a.slices > 1) {
+        if (y >= 0 && y < a.vocab) {
+          const uint64_t* v = a.part + static_cast<int64_t>(r) * a.slices;
+          // all slices of a far maximum are joined in the exact form
+          float top = -kFar;
+          for (int x = 0; x < a.slices; ++x) top = fmaxf(top, word_max(v[x]));
+          const bool far = far_row(top, k);
+          m = far ? kLowest : -kFar;
+          s = 0.0f;
+          for (int x = 0; x < a.slices; ++x) {
+            if (far) join<true>(m, s, word_max(v[x]), word_sum(v[x]), k);
+            else join(m, s, word_max(v[x]), word_sum(v[x]), k);
+          }
+        }
+        finish_row<T>(a, r, y, m, s);
+      }
+      if (y < 0) continue;
+      sum += a.lp[r] - (p.ref_lp ? static_cast<double>(p.ref_lp[r]) : 0.0);
+      ++n;
     }
+    sum = block_total<kTermThreads>(sum);
+    n = static_cast<int>(block_total<kTermThreads>(n));
+    score[side] = p.p.average ? (n ? sum / n : 0.0) : sum;
+    tokens[side] = n;
+  }
+  if (t != 0) return;
+  const double beta = p.p.beta, eps = p.p.label_smoothing, margin = score[0] - score[1], h = beta * margin;
+  double loss, d;
+  if (p.p.kind == MUON_PREFERENCE_SIGMOID) {
+    loss = (1.0 - eps) * neg_log_sigmoid(h) + eps * neg_log_sigmoid(-h);
+    d = beta * (eps * sigmoid(h) - (1.0 - eps) * sigmoid(-h));
+  } else {
+    const double off = margin - 0.5 / beta;
+    loss = off * off;
+    d = 2.0 * off;
+  }
+  p.terms[3 * static_cast<int64_t>(i)] = loss;
+  p.terms[3 * static_cast<int64_t>(i) + 1] = h;
+  p.terms[3 * static_cast<int64_t>(i) + 2] = margin > 0.0 ? 1.0 : 0.0;
+  d *= static_cast<double>(p.p.weight) / pairs;
+  for (int side = 0; side < 2; ++side) {
+    const int b = i + side * pairs;
+    if (p.rewards) p.rewards[b] = static_cast<float>(beta * score[side]);
+    const double g = side ? -d : d;
+    p.g[b] = static_cast<float>(p.p.average && tokens[side] ? g / tokens[side] : g);
+  }
+}
+
+__global__ __launch_bounds__(kTermThreads) void preference_sums_kernel(PreferenceArgs p) {
+  const int pairs = p.batch / 2;
+  double v[3] = {0.0, 0.0, 0.0};
+  for (int64_t i = threadIdx.x; i < pairs; i += kTermThreads)
 #pragma unroll
-    for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d, 64);
-    if (lane == 0) {
-      a.counts[b] = n;
-      const double s = a.p.average ? (n ? sum / n : 0.0) : sum;
-      a.score[b] = s;
-      if (a.rewards) a.rewards[b] = static_cast<float>(static_cast<double>(a.p.beta) * s);
-    }
-  }
-  __syncthreads();
-  const int pairs = a.batch / 2;
-  const double beta = a.p.beta, eps = a.p.label_smoothing;
-  double loss = 0.0, margin = 0.0, won = 0.0;
-  for (int i = threadIdx.x; i < pairs; i += kTermThreads) {
-    const double m = a.score[i] - a.score[i + pairs], h = beta * m;
-    if (a.p.kind == MUON_PREFERENCE_SIGMOID) {
-      loss += (1.0 - eps) * neg_log_sigmoid(h) + eps * neg_log_sigmoid(-h);
-    } else {
-      const double d = m - 0.5 / beta;
-      loss += d * d;
-    }
-    margin += h;
-    won += m > 0.0 ? 1.0 : 0.0;
-  }
-  loss = block_total(loss);
-  margin = block_total(margin);
-  won = block_total(won);
-  if (threadIdx.x == 0) {
-    const double n = pairs > 0 ? pairs : 1;
-    a.out[0] = static_cast<float>(static_cast<double>(a.p.weight) * loss / n);
-    a.out[1] = static_cast<float>(margin / n);
-    a.out[2] = static_cast<float>(won / n);
-  }
-  if (a.g == nullptr) return;
-  for (int t = threadIdx.x; t < a.batch * a.seq; t += kTermThreads) {
-    float g = 0.0f;
-    if (a.labels[t] >= 0) {
-      const int b = t / a.seq, i = b < pairs ? b : b - pairs;
-      const double m = a.score[i] - a.score[i + pairs], h = beta * m;
-      double d = a.p.kind == MUON_PREFERENCE_SIGMOID ? beta * (eps * sigmoid(h) - (1.0 - eps) * sigmoid(-h))
-                                                     : 2.0 * (m - 0.5 / beta);
-      if (b >= pairs) d = -d;
-      if (a.p.average) d /= a.counts[b];
-      g = static_cast<float>(static_cast<double>(a.p.weight) * d / pairs);
-    }
-    a.g[t] = g;
-  }
+    for (int j = 0; j < 3; ++j) v[j] += p.terms[3 * i + j];
+#pragma unroll
+  for (int j = 0; j < 3; ++j) v[j] = block_total<kTermThreads>(v[j]);
+  if (threadIdx.x != 0) return;
+  const double n = pairs > 0 ? pairs : 1;
+  p.out[0] = static_cast<float>(static_cast<double>(p.p.weight) * v[0] / n);
+  p.out[1] = static_cast<float>(v[1] / n);
+  p.out[2] = static_cast<float>(v[2] / n);
 }
 
 }  // namespace
 
-int loss_splits(int64_t rows, int64_t vocab, int bf16, int cus) {
-  // Rows that leave compute units idle are split, down to one trip of a
-  // workgroup's loads per split.
-  const int64_t trip = static_cast<int64_t>(kStatsThreads) * kStatsUnroll * (bf16 ? 8 : 4);
-  int64_t want = (2 * static_cast<int64_t>(cus) + rows - 1) / (rows > 0 ? rows : 1);
-  const int64_t most = (vocab + trip - 1) / trip;
-  if (want > most) want = most;
-  return static_cast<int>(want < 1 ? 1 : want > 32 ? 32 : want);
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
+#ifndef MAXNV
+#define MAXNV 10
+#endif
+int loss_slices(int64_t rows, int64_t vocab, int bf16, int cus) {
+  const int64_t pieces = vocab / (bf16 ? 8 : 4);
+  const int64_t least = (pieces + kThreads * MAXNV - 1) / (kThreads * MAXNV);
+  // rows that leave compute units idle are cut finer, down to one piece a thread
+  const int64_t idle = rows > 0 ? 2 * static_cast<int64_t>(cus) / rows : 1;
+  const int64_t most = std::min<int64_t>(64, (pieces + kThreads - 1) / kThreads);
+  return static_cast<int>(std::max<int64_t>(1, std::max(least, std::min(idle, most))));
 }
 
 // Rows of one launch when each takes `per` workgroups: a grid holds fewer than
@@ -681,81 +793,96 @@ static int rows_per_launch(int64_t per) {
   return static_cast<int>(n > 1 ? n : 1);
 }
 
-hipError_t launch_row_stats(hipStream_t s, const LossArgs& a) {
-  LossArgs c = a;
-  const int step = rows_per_launch(a.splits);
-  for (c.row0 = 0; c.row0 < a.rows; c.row0 += step) {
-    const int n = a.rows - c.row0 < step ? a.rows - c.row0 : step;
-    const unsigned grid = static_cast<unsigned>(n) * static_cast<unsigned>(a.splits);
-    if (a.bf16) row_stats_kernel<bf16_t><<<grid, kStatsThreads, 0, s>>>(c);
-    else row_stats_kernel<float><<<grid, kStatsThreads, 0, s>>>(c);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (a.splits > 1 && a.rows > 0) {
-    const unsigned blocks = static_cast<unsigned>((a.rows + 63) / 64);
-    if (a.bf16) row_join_kernel<bf16_t><<<blocks, 64, 0, s>>>(a);
-    else row_join_kernel<float><<<blocks, 64, 0, s>>>(a);
-  }
-  return hipGetLastError();
-}
+namespace {
 
-hipError_t launch_logits_grad(hipStream_t s, const LossArgs& a, RowsRef grad, const float* g) {
-  const int vec = a.bf16 ? 8 : 4;
-  const int pieces = a.vocab / vec;  // the most a row can have
-  const int chunks = std::max(1, (pieces + kGradThreads * kGradUnroll - 1) / (kGradThreads * kGradUnroll));
+template <typename T, int NV, int USE>
+hipError_t run_slices(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p) {
   LossArgs c = a;
-  const int step = rows_per_launch(chunks);
+  const int step = rows_per_launch(a.slices);
   for (c.row0 = 0; c.row0 < a.rows; c.row0 += step) {
     const int n = a.rows - c.row0 < step ? a.rows - c.row0 : step;
-    const unsigned grid = static_cast<unsigned>(n) * static_cast<unsigned>(chunks);
-    if (a.bf16) logits_grad_kernel<bf16_t><<<grid, kGradThreads, 0, s>>>(c, grad, g, chunks);
-    else logits_grad_kernel<float><<<grid, kGradThreads, 0, s>>>(c, grad, g, chunks);
+    slice_kernel<T, NV, USE><<<static_cast<unsigned>(n) * static_cast<unsigned>(a.slices), kThreads, 0, s>>>(c, grad, p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-hipError_t launch_policy_terms(hipStream_t s, const PolicyArgs& a) {
-  policy_terms_kernel<<<1, kTermThreads, 0, s>>>(a);
-  return hipGetLastError();
-}
-
-namespace {
-
-template <typename T, int NT, int NV>
-hipError_t run_policy_rows(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p, int cus) {
-  const int grid = std::min(a.rows, cus * (1024 / NT));
-  policy_rows_kernel<T, NT, NV><<<static_cast<unsigned>(grid), NT, 0, s>>>(a, grad, p);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  policy_sums_kernel<<<1, kTermThreads, 0, s>>>(p, grid);
-  return hipGetLastError();
-}
-
-template <typename T>
-hipError_t policy_rows(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p, int cus) {
-  const int pieces = a.vocab / kVec<T>;
-  if (pieces <= 256 * 5) return run_policy_rows<T, 256, 5>(s, a, grad, p, cus);
-  if (pieces <= 256 * 10) return run_policy_rows<T, 256, 10>(s, a, grad, p, cus);
-  if (pieces <= 256 * 15) return run_policy_rows<T, 256, 15>(s, a, grad, p, cus);
-  if (pieces <= 256 * 19) return run_policy_rows<T, 256, 19>(s, a, grad, p, cus);
-  if (pieces <= 512 * 15) return run_policy_rows<T, 512, 15>(s, a, grad, p, cus);
-  if (pieces <= 512 * 19) return run_policy_rows<T, 512, 19>(s, a, grad, p, cus);
-  if (pieces <= 1024 * 15) return run_policy_rows<T, 1024, 15>(s, a, grad, p, cus);
-  return run_policy_rows<T, 1024, 19>(s, a, grad, p, cus);
+template <typename T, int USE>
+hipError_t slices(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p) {
+  const int per = (a.vocab / kVec<T> + a.slices - 1) / a.slices;
+  if (per <= 1 * kThreads) return run_slices<T, 1, USE>(s, a, grad, p);
+  if (per <= 2 * kThreads) return run_slices<T, 2, USE>(s, a, grad, p);
+  if (per <= 4 * kThreads) return run_slices<T, 4, USE>(s, a, grad, p);
+  if (per <= 6 * kThreads) return run_slices<T, 6, USE>(s, a, grad, p);
+  if (per <= 8 * kThreads) return run_slices<T, 8, USE>(s, a, grad, p);
+  return run_slices<T, 10, USE>(s, a, grad, p);
 }
 
 }  // namespace
 
-bool policy_rows_fit(const LossArgs& a) { return a.vocab / (a.bf16 ? 8 : 4) <= 1024 * 19; }
-
-hipError_t launch_policy_rows(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p, int cus) {
-  return a.bf16 ? policy_rows<bf16_t>(s, a, grad, p, cus) : policy_rows<float>(s, a, grad, p, cus);
+hipError_t launch_slice_stats(hipStream_t s, const LossArgs& a) {
+  return a.bf16 ? slices<bf16_t, USE_STATS>(s, a, RowsRef{}, PolicyArgs{})
+                : slices<float, USE_STATS>(s, a, RowsRef{}, PolicyArgs{});
 }
 
-hipError_t launch_preference_terms(hipStream_t s, const PreferenceArgs& a) {
-  preference_terms_kernel<<<1, kTermThreads, 0, s>>>(a);
+hipError_t launch_row_stats(hipStream_t s, const LossArgs& a) {
+  const hipError_t e = launch_slice_stats(s, a);
+  if (e != hipSuccess || a.slices == 1 || a.rows == 0) return e;
+  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.rows) + kThreads / 64 - 1) / (kThreads / 64));
+  if (a.bf16) row_join_kernel<bf16_t><<<blocks, kThreads, 0, s>>>(a);
+  else row_join_kernel<float><<<blocks, kThreads, 0, s>>>(a);
   return hipGetLastError();
+}
+
+hipError_t launch_logits_grad(hipStream_t s, const LossArgs& a, RowsRef grad, const float* g, bool per_sequence) {
+  const int vec = a.bf16 ? 8 : 4;
+  const int pieces = a.vocab / vec;  // the most a row can have
+  const int chunks = std::max(1, (pieces + kThreads * kGradUnroll - 1) / (kThreads * kGradUnroll));
+  LossArgs c = a;
+  const int step = rows_per_launch(chunks);
+  const int each = per_sequence ? 1 : 0;
+  for (c.row0 = 0; c.row0 < a.rows; c.row0 += step) {
+    const int n = a.rows - c.row0 < step ? a.rows - c.row0 : step;
+    const unsigned grid = static_cast<unsigned>(n) * static_cast<unsigned>(chunks);
+    if (a.bf16) logits_grad_kernel<bf16_t><<<grid, kThreads, 0, s>>>(c, grad, g, each, chunks);
+    else logits_grad_kernel<float><<<grid, kThreads, 0, s>>>(c, grad, g, each, chunks);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+hipError_t launch_policy(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p) {
+  const int64_t slots = a.slices > 1 ? static_cast<int64_t>(a.rows) * a.slices : 0;
+  const int64_t clear = std::min<int64_t>(128, (slots + kTermThreads - 1) / kTermThreads);
+  const int64_t count = p.p.reduce == MUON_REDUCE_SEQUENCE ? p.batch : 1;
+  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::max(clear, count)));
+  policy_prepare_kernel<<<grid, kTermThreads, 0, s>>>(p, a.part, slots);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  e = a.bf16 ? slices<bf16_t, USE_POLICY>(s, a, grad, p) : slices<float, USE_POLICY>(s, a, grad, p);
+  if (e != hipSuccess) return e;
+  const int n = std::min(kPolicySums, std::max(1, a.rows / 8192));
+  policy_sums_kernel<<<static_cast<unsigned>(n), kTermThreads, 0, s>>>(p, a.rows);
+  e = hipGetLastError();
+  if (e != hipSuccess || n == 1) return e;
+  policy_total_kernel<<<1, 1, 0, s>>>(p, n);
+  return hipGetLastError();
+}
+
+hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, const PreferenceArgs& p) {
+  hipError_t e = launch_slice_stats(s, a);
+  if (e != hipSuccess) return e;
+  if (p.batch > 0) {
+    const unsigned pairs = static_cast<unsigned>(p.batch / 2);
+    if (a.bf16) preference_pairs_kernel<bf16_t><<<pairs, kTermThreads, 0, s>>>(a, p);
+    else preference_pairs_kernel<float><<<pairs, kTermThreads, 0, s>>>(a, p);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  preference_sums_kernel<<<1, kTermThreads, 0, s>>>(p);
+  e = hipGetLastError();
+  if (e != hipSuccess || grad.base == nullptr) return e;
+  return launch_logits_grad(s, a, grad, p.g, true);
 }

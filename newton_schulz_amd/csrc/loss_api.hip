@@ -14,18 +14,16 @@
 namespace {
 
 constexpr int64_t kMostTokens = int64_t{1} << 30;
-constexpr int64_t kMostVocab = int64_t{1} << 30;
-constexpr int kMostSplitRows = 8192;  // partial pairs of rows that are split: rows * splits stays under this
-constexpr int kMostRowGroups = 4096;  // workgroups that hold rows: four on each of at most 1024 compute units
 
 inline size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// What the kernels of one loss call hand each other.
+// What the kernels of one loss call hand each other, for the finest slicing
+// that `cus` compute units can ask for.
 struct LossLayout {
-  size_t part, sums, stats, lp, g, counts, score, total;
+  size_t part, stats, lp, terms, weights, sums, total;
 };
 
-LossLayout loss_layout(int64_t batch, int64_t seq) {
+LossLayout loss_layout(int64_t batch, int64_t seq, int slices) {
   const size_t rows = static_cast<size_t>(batch * seq), b = static_cast<size_t>(batch);
   LossLayout l;
   size_t at = 0;
@@ -34,13 +32,12 @@ LossLayout loss_layout(int64_t batch, int64_t seq) {
     at += up256(bytes);
     return p;
   };
-  l.part = take(sizeof(float2) * kMostSplitRows);
-  l.sums = take(sizeof(double) * 3 * kMostRowGroups);
+  l.part = take(sizeof(uint64_t) * rows * static_cast<size_t>(slices));
   l.stats = take(sizeof(float2) * rows);
   l.lp = take(sizeof(double) * rows);
-  l.g = take(sizeof(float) * rows);
-  l.counts = take(sizeof(int) * b);
-  l.score = take(sizeof(double) * b);
+  l.terms = take(std::max(sizeof(float) * 3 * rows, sizeof(double) * 3 * ((b + 1) / 2)));
+  l.weights = take(sizeof(double) * (b + 1));
+  l.sums = take(sizeof(double) * 3 * kPolicySums);
   l.total = at;
   return l;
 }
@@ -59,7 +56,7 @@ bool extent(const muon_logits_t& x, size_t* bytes) {
 muon_status_t check_logits(muon_ctx* c, const muon_logits_t* x, size_t* bytes) {
   if (x == nullptr) return fail(c, MUON_EINVAL, "logits NULL");
   if (!is_dtype(x->dtype)) return fail(c, MUON_EDTYPE, "logits dtype");
-  if (x->batch < 0 || x->seq < 0 || x->vocab < 1 || x->vocab > kMostVocab || x->batch > kMostTokens ||
+  if (x->batch < 0 || x->seq < 0 || x->vocab < 1 || x->vocab > MUON_MAX_VOCAB || x->batch > kMostTokens ||
       x->seq > kMostTokens || x->batch * x->seq > kMostTokens)
     return fail(c, MUON_ESHAPE, "batch, seq or vocab out of range");
   if ((x->batch > 1 && x->batch_stride < 0) || (x->seq > 1 && x->row_stride < 0))
@@ -137,6 +134,10 @@ RowsRef rows_ref(const muon_logits_t& x) {
   return RowsRef{static_cast<char*>(x.data), x.batch > 1 ? x.batch_stride * e : 0, x.seq > 1 ? x.row_stride * e : 0};
 }
 
+int slices_of(const muon_ctx* c, const muon_logits_t& x) {
+  return loss_slices(x.batch * x.seq, x.vocab, x.dtype == MUON_BF16, c ? c->cus : 256);
+}
+
 LossArgs loss_args(const muon_ctx* c, const LossLayout& l, const muon_logits_t& x, const int64_t* labels,
                    float temperature) {
   LossArgs a = {};
@@ -147,9 +148,9 @@ LossArgs loss_args(const muon_ctx* c, const LossLayout& l, const muon_logits_t& 
   a.vocab = static_cast<int>(x.vocab);
   a.labels = labels;
   a.temperature = temperature;
-  a.splits = loss_splits(a.rows, a.vocab, a.bf16, c->cus);
-  if (static_cast<int64_t>(a.rows) * a.splits > kMostSplitRows) a.splits = 1;
-  a.part = reinterpret_cast<float2*>(c->ws + l.part);
+  a.slices = slices_of(c, x);
+  a.spin = c->loss_spin;
+  a.part = reinterpret_cast<uint64_t*>(c->ws + l.part);
   a.lp = reinterpret_cast<double*>(c->ws + l.lp);
   a.stats = reinterpret_cast<float2*>(c->ws + l.stats);
   return a;
@@ -167,9 +168,20 @@ template <typename F> muon_status_t timed(muon_ctx* c, hipStream_t s, int cls, c
 
 extern "C" {
 
-size_t muon_loss_workspace_bytes(int64_t batch, int64_t seq) {
-  if (batch < 0 || seq < 0 || batch > kMostTokens || seq > kMostTokens || batch * seq > kMostTokens) return 0;
-  return loss_layout(batch, seq).total;
+size_t muon_loss_workspace_bytes(int64_t batch, int64_t seq, int64_t vocab, int32_t dtype) {
+  const muon_logits_t x = {nullptr, dtype, batch, seq, vocab, 0, 0};
+  size_t bytes = 0;
+  // (an address is no part of the size; every other argument is checked)
+  const muon_status_t st = check_logits(nullptr, &x, &bytes);
+  if (st != MUON_OK && !(st == MUON_EINVAL && bytes)) return 0;
+  return loss_layout(batch, seq, slices_of(nullptr, x)).total;
+}
+
+muon_status_t muon_loss_set_polls(muon_ctx_t* c, int32_t polls) {
+  if (polls < 0) return fail(c, MUON_EINVAL, "polls < 0");
+  if (c == nullptr) return fail(c, MUON_EINVAL, "context NULL");
+  c->loss_spin = polls;
+  return MUON_OK;
 }
 
 muon_status_t muon_token_logps(muon_ctx_t* c, void* stream, const muon_logits_t* logits,
@@ -186,7 +198,7 @@ muon_status_t muon_token_logps(muon_ctx_t* c, void* stream, const muon_logits_t*
                         {row_stats, rows * 8, 8, true, false, "row_stats"}};
   st = check_spans(c, spans, 4, false);
   if (st != MUON_OK) return st;
-  const LossLayout l = loss_layout(logits->batch, logits->seq);
+  const LossLayout l = loss_layout(logits->batch, logits->seq, slices_of(c, *logits));
   st = check_ctx(c, l.total);
   if (st != MUON_OK || rows == 0) return st;
   DeviceGuard g(c->device);
@@ -224,7 +236,7 @@ muon_status_t muon_token_logps_backward(muon_ctx_t* c, void* stream, const muon_
   a.stats = reinterpret_cast<float2*>(const_cast<float*>(row_stats));
   hipStream_t s = static_cast<hipStream_t>(stream);
   return timed(c, s, MUON_K_LOSS, "gradient launch",
-               [&] { return launch_logits_grad(s, a, rows_ref(*grad_logits), grad_logps); });
+               [&] { return launch_logits_grad(s, a, rows_ref(*grad_logits), grad_logps, false); });
 }
 
 muon_status_t muon_policy_loss(muon_ctx_t* c, void* stream, const muon_logits_t* logits,
@@ -256,7 +268,7 @@ muon_status_t muon_policy_loss(muon_ctx_t* c, void* stream, const muon_logits_t*
                         {logps, rows * 4, 4, true, false, "logps"}};
   st = check_spans(c, spans, 8, grad_logits && same_place(*logits, *grad_logits));
   if (st != MUON_OK) return st;
-  const LossLayout l = loss_layout(logits->batch, logits->seq);
+  const LossLayout l = loss_layout(logits->batch, logits->seq, slices_of(c, *logits));
   st = check_ctx(c, l.total);
   if (st != MUON_OK) return st;
   DeviceGuard dg(c->device);
@@ -267,23 +279,16 @@ muon_status_t muon_policy_loss(muon_ctx_t* c, void* stream, const muon_logits_t*
   t.batch = static_cast<int>(logits->batch);
   t.seq = static_cast<int>(logits->seq);
   t.labels = labels;
-  t.lp = a.lp;
   t.adv = advantages;
   t.old_lp = old_logps;
   t.ref_lp = ref_logps;
   t.out = out;
-  t.g = grad_logits ? reinterpret_cast<float*>(c->ws + l.g) : nullptr;
-  t.counts = reinterpret_cast<int*>(c->ws + l.counts);
+  t.weights = reinterpret_cast<double*>(c->ws + l.weights);
+  t.terms = reinterpret_cast<float*>(c->ws + l.terms);
   t.sums = reinterpret_cast<double*>(c->ws + l.sums);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return timed(c, s, MUON_K_LOSS, "policy loss launch", [&] {
-    if (a.rows > 64 && policy_rows_fit(a))
-      return launch_policy_rows(s, a, grad_logits ? rows_ref(*grad_logits) : RowsRef{}, t, std::min(c->cus, kMostRowGroups / 4));
-    hipError_t e = launch_row_stats(s, a);
-    if (e == hipSuccess) e = launch_policy_terms(s, t);
-    if (e == hipSuccess && grad_logits) e = launch_logits_grad(s, a, rows_ref(*grad_logits), t.g);
-    return e;
-  });
+  return timed(c, s, MUON_K_LOSS, "policy loss launch",
+               [&] { return launch_policy(s, a, grad_logits && rows ? rows_ref(*grad_logits) : RowsRef{}, t); });
 }
 
 muon_status_t muon_preference_loss(muon_ctx_t* c, void* stream, const muon_logits_t* logits,
@@ -314,7 +319,7 @@ muon_status_t muon_preference_loss(muon_ctx_t* c, void* stream, const muon_logit
                         {logps, rows * 4, 4, true, false, "logps"}};
   st = check_spans(c, spans, 7, grad_logits && same_place(*logits, *grad_logits));
   if (st != MUON_OK) return st;
-  const LossLayout l = loss_layout(logits->batch, logits->seq);
+  const LossLayout l = loss_layout(logits->batch, logits->seq, slices_of(c, *logits));
   st = check_ctx(c, l.total);
   if (st != MUON_OK) return st;
   DeviceGuard dg(c->device);
@@ -324,21 +329,14 @@ muon_status_t muon_preference_loss(muon_ctx_t* c, void* stream, const muon_logit
   t.p = *p;
   t.batch = static_cast<int>(logits->batch);
   t.seq = static_cast<int>(logits->seq);
-  t.labels = labels;
-  t.lp = a.lp;
   t.ref_lp = ref_logps;
   t.out = out;
   t.rewards = rewards;
-  t.g = grad_logits ? reinterpret_cast<float*>(c->ws + l.g) : nullptr;
-  t.score = reinterpret_cast<double*>(c->ws + l.score);
-  t.counts = reinterpret_cast<int*>(c->ws + l.counts);
+  t.g = reinterpret_cast<float*>(c->ws + l.weights);
+  t.terms = reinterpret_cast<double*>(c->ws + l.terms);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return timed(c, s, MUON_K_LOSS, "preference loss launch", [&] {
-    hipError_t e = launch_row_stats(s, a);
-    if (e == hipSuccess) e = launch_preference_terms(s, t);
-    if (e == hipSuccess && grad_logits) e = launch_logits_grad(s, a, rows_ref(*grad_logits), t.g);
-    return e;
-  });
+  return timed(c, s, MUON_K_LOSS, "preference loss launch",
+               [&] { return launch_preference(s, a, grad_logits && rows ? rows_ref(*grad_logits) : RowsRef{}, t); });
 }
 
 }  // extern "C"

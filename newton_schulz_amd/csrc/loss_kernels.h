@@ -1,4 +1,4 @@
-// Host-side declarations of the loss kernels' launchers (loss.hip).
+// Host-side declarations of the launchers of loss.hip and grad_clip.hip.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -19,56 +19,50 @@ struct LossArgs {
   int row0;          // first row of this launch (set by the launchers)
   const int64_t* labels;
   float temperature;
-  int splits;        // workgroups a row's statistics are split over
-  float2* part;      // [rows][splits] (maximum, sum around it) of each split
-  double* lp;        // [rows]
+  int slices;        // workgroups that a row is cut over
+  int spin;          // polls before a slice computes its neighbours' pairs itself
+  uint64_t* part;    // [rows][slices] pairs of the slices
+  double* lp;        // [rows] or nullptr
   float* logps;      // [rows] or nullptr
-  float2* stats;     // [rows] (maximum, sum) of the whole row
+  float2* stats;     // [rows] (maximum, sum) of the whole row, or nullptr
 };
 
-// Workgroups to split each row's statistics over.
-int loss_splits(int64_t rows, int64_t vocab, int bf16, int cus);
+// Slices of each row (at most 64 within MUON_MAX_VOCAB).
+int loss_slices(int64_t rows, int64_t vocab, int bf16, int cus);
 
 // stats, lp and logps of every row (logps of tokens left out: 0).
 hipError_t launch_row_stats(hipStream_t s, const LossArgs& a);
 
-// grad row r = g[r] / temperature * ([v = y] - softmax); zeros for tokens left out.
-hipError_t launch_logits_grad(hipStream_t s, const LossArgs& a, RowsRef grad, const float* g);
+// grad row r = g / temperature * ([v = y] - softmax), g[r] or g[sequence];
+// zeros for tokens left out.  Needs a.stats.
+hipError_t launch_logits_grad(hipStream_t s, const LossArgs& a, RowsRef grad, const float* g, bool per_sequence);
 
-// The policy loss of given log-probabilities: out[4] and (g not null) the
-// gradient of weight * loss in each of them.
+constexpr int kPolicySums = 64;  // workgroups that add up a policy loss's tokens
 struct PolicyArgs {
   muon_policy_params_t p;
   int batch, seq;
   const int64_t* labels;
-  const double* lp;
   const float* adv;
   const float* old_lp;
   const float* ref_lp;
   float* out;
-  float* g;
-  int* counts;   // [batch]
-  double* sums;  // three per workgroup of launch_policy_rows
+  double* weights;  // [batch] weight of a sequence's tokens, or one for all
+  float* terms;     // [rows][3] pg, kl, clipped
+  double* sums;     // [kPolicySums][3]
 };
-hipError_t launch_policy_terms(hipStream_t s, const PolicyArgs& a);
-
-// Loss and gradient in one pass over rows that a workgroup's registers hold.
-bool policy_rows_fit(const LossArgs& a);
-hipError_t launch_policy_rows(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p, int cus);
+// Loss, and gradient where grad.base is set, in one pass over the scores.
+hipError_t launch_policy(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p);
 
 struct PreferenceArgs {
   muon_preference_params_t p;
   int batch, seq;
-  const int64_t* labels;
-  const double* lp;
   const float* ref_lp;
   float* out;
   float* rewards;
-  float* g;
-  double* score;  // [batch]
-  int* counts;    // [batch]
+  float* g;       // [batch] gradient in each log-probability of a sequence
+  double* terms;  // [pairs][3] loss, margin, won
 };
-hipError_t launch_preference_terms(hipStream_t s, const PreferenceArgs& a);
+hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, const PreferenceArgs& p);
 
 // ---------------------------------------------------------------------------
 // gradient norm and scaling (grad_clip.hip)

@@ -36,6 +36,9 @@ struct muon_ctx {
   hipEvent_t tab_ev[kTabSlots] = {};
   bool tab_used[kTabSlots] = {};
   int tab_next = 0;
+  // polls (a microsecond or so each) before a slice of a row stops waiting for
+  // its neighbours and computes their pairs itself (loss.hip)
+  int loss_spin = 1 << 14;
   // timing
   bool timing = false;
   uint32_t tmask = (1u << MUON_K_COUNT) - 1;  // classes that record events

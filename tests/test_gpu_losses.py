@@ -248,6 +248,27 @@ def test_policy_loss(ctx, case):
     assert torch.equal(again, out) and torch.equal(own, grad)
 
 
+@pytest.mark.parametrize("case", [c for c in POLICY if c[2] > 4000])
+def test_policy_loss_without_waiting(case):
+    """No poll at all: workgroups compute what their row's others have not
+    published yet, in place too, and nothing changes."""
+    batch, seq, vocab, dtype, pad, reduce, per_token, kl, has_ref, has_old, t = case
+    x, y, xn, yn, lp, adv, old, ref, t32 = policy_inputs(case)
+    kw = dict(old_logps=old, ref_logps=ref, clip_low=0.2, clip_high=0.28, kl_coef=kl, reduce=reduce, temperature=t)
+    c = Context(DEV, 8 << 20)
+    got = []
+    for polls in (1 << 14, 0):
+        c.set_loss_polls(polls)
+        out, logps, own = torch.empty(4, device=DEV), torch.empty(batch, seq, device=DEV), placed_like(x)
+        c.policy_loss(own, y, adv, out, logps=logps, grad_logits=own, **kw)
+        got.append((out, logps, own))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    with pytest.raises(MuonError):
+        c.set_loss_polls(-1)
+    c.close()
+
+
 PREFERENCE = [
     # pairs, seq, vocab, dtype, pad, kind, smoothing, average, reference
     (1, 1, 9, F32, 0, "sigmoid", 0.0, False, True),
@@ -406,7 +427,7 @@ def test_refusals_of_the_binding(ctx):
     small = Context(DEV, 256)
     with pytest.raises(MuonError) as e:
         small.policy_loss(x, y, adv, out)
-    assert e.value.status == 4 and loss_workspace_bytes(2, 3) > 256
+    assert e.value.status == 4 and loss_workspace_bytes(2, 3, 64) > 256
     small.close()
 
 

@@ -4,6 +4,7 @@ that are never read.  No compute call is made here."""
 import ctypes
 
 import pytest
+import torch
 
 from newton_schulz_amd import _lib, loss_workspace_bytes
 from newton_schulz_amd._lib import (
@@ -56,6 +57,7 @@ def test_only_the_context_is_missing():
 def test_logits_are_checked():
     refused(policy(x=logits(dtype=7), grad=None), MUON_EDTYPE, "dtype")
     refused(policy(x=logits(vocab=0), grad=None), MUON_ESHAPE, "vocab")
+    refused(policy(x=logits(vocab=(1 << 19) + 1, rs=1 << 20), grad=None), MUON_ESHAPE, "vocab")
     refused(policy(x=logits(vocab=(1 << 30) + 1), grad=None), MUON_ESHAPE, "vocab")
     refused(policy(x=logits(batch=-1), grad=None), MUON_ESHAPE, "batch")
     refused(policy(x=logits(batch=1 << 20, seq=1 << 20), grad=None), MUON_ESHAPE, "batch")
@@ -175,6 +177,12 @@ def test_scaled_outputs_are_checked():
     refused(lib.muon_scale_grads(None, None, twice, None, 2, NORM), MUON_EINVAL, "overlap")
 
 
+def test_polls():
+    lib = _lib.load()
+    refused(lib.muon_loss_set_polls(None, 5), MUON_EINVAL, "context NULL")
+    refused(lib.muon_loss_set_polls(None, -1), MUON_EINVAL, "polls")
+
+
 def test_clipped_momentum_without_context():
     assert _lib.load().muon_momentum_update_clipped(None, None, None, 1, None, None, 1, 8, 0.9, 1, NORM,
                                                     None) == MUON_EINVAL
@@ -182,10 +190,15 @@ def test_clipped_momentum_without_context():
 
 def test_workspace_sizes():
     lib = _lib.load()
-    assert loss_workspace_bytes(-1, 4) == 0 and loss_workspace_bytes(1 << 20, 1 << 20) == 0
-    # two floats, a double and a float per token, beside fixed parts
-    assert 20 * 4096 <= loss_workspace_bytes(4, 1024) <= 20 * 4096 + 12 * 4 + 8 * 8192 + 6 * 256
-    assert loss_workspace_bytes(0, 0) > 0
+    bf, f32 = torch.bfloat16, torch.float32
+    assert loss_workspace_bytes(-1, 4, 100) == 0 and loss_workspace_bytes(1 << 20, 1 << 20, 100) == 0
+    assert loss_workspace_bytes(2, 4, 0) == 0 and loss_workspace_bytes(2, 4, 100, torch.float16) == 0
+    # per token two floats, a double and three floats, a word for each slice of
+    # at most 2560 pieces of 16 bytes; per sequence a double
+    for dtype, slices in ((bf, 8), (f32, 15)):
+        need = 4096 * (8 + 8 + 12 + 8 * slices) + 8 * 5 + 24 * 64
+        assert need <= loss_workspace_bytes(4, 1024, 151936, dtype) <= need + 6 * 256
+    assert loss_workspace_bytes(0, 0, 100) > 0
     # one double per chunk of at most 65536 elements
     t, n = tensors((0x10000, 1 << 30, MUON_BF16))
     assert lib.muon_grad_norm_workspace_bytes(t, n) == 8 * (1 << 14) + 256
