@@ -36,10 +36,10 @@ def _dtype(t: torch.Tensor) -> int:
     return _DT[t.dtype]
 
 
-def _stream(device: torch.device, stream) -> ctypes.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+def _stream(device: torch.device, stream) -> int:
+    # the raw handle of the current stream: building a torch.cuda.Stream for it
+    # costs 2 us a call
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _check(t: torch.Tensor, name: str, device: torch.device):

@@ -54,23 +54,27 @@ template <typename T> __device__ __forceinline__ int tensor_lead(const char* p) 
   return static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / sizeof(T));
 }
 
+template <typename T> __device__ __forceinline__ void load_whole(const T* p, float* v) {
+  if (sizeof(T) == 2) {
+    const u32x4 w = *reinterpret_cast<const u32x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  } else {
+    const u32x4 a = *reinterpret_cast<const u32x4*>(p), b = *reinterpret_cast<const u32x4*>(p + 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = __uint_as_float(a[i]);
+      v[4 + i] = __uint_as_float(b[i]);
+    }
+  }
+}
+
 template <typename T> __device__ __forceinline__ void load_group(const T* p, int64_t e0, int64_t n, float* v) {
   if (e0 >= 0 && e0 + kGroup <= n) {
-    if (sizeof(T) == 2) {
-      const u32x4 w = *reinterpret_cast<const u32x4*>(p + e0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-      }
-    } else {
-      const u32x4 a = *reinterpret_cast<const u32x4*>(p + e0), b = *reinterpret_cast<const u32x4*>(p + e0 + 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[i] = __uint_as_float(a[i]);
-        v[4 + i] = __uint_as_float(b[i]);
-      }
-    }
+    load_whole(p + e0, v);
     return;
   }
 #pragma unroll
@@ -81,14 +85,16 @@ template <typename T> __device__ __forceinline__ void store_group(T* p, int64_t 
   if (e0 >= 0 && e0 + kGroup <= n) {
     // the output may lie at another alignment than the input
     if (sizeof(T) == 2) {
-      *reinterpret_cast<u32x4_any*>(p + e0) = u32x4{muon::pack_bf16x2(v[0], v[1]), muon::pack_bf16x2(v[2], v[3]),
-                                                    muon::pack_bf16x2(v[4], v[5]), muon::pack_bf16x2(v[6], v[7])};
+      const u32x4 w = {muon::pack_bf16x2(v[0], v[1]), muon::pack_bf16x2(v[2], v[3]), muon::pack_bf16x2(v[4], v[5]),
+                       muon::pack_bf16x2(v[6], v[7])};
+      __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any*>(p + e0));
     } else {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<u32x4_any*>(p + e0 + 4 * h) =
-            u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
-                  __float_as_uint(v[4 * h + 3])};
+      for (int h = 0; h < 2; ++h) {
+        const u32x4 w = {__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]),
+                         __float_as_uint(v[4 * h + 3])};
+        __builtin_nontemporal_store(w, reinterpret_cast<u32x4_any*>(p + e0 + 4 * h));
+      }
     }
     return;
   }
@@ -110,26 +116,35 @@ template <int NT> __device__ __forceinline__ double block_sum(double v) {
   return t;
 }
 
+// Sum of the squares of groups q0 .. q0 + groups - 1 of a tensor (this thread's
+// part): at most kTrips groups a thread, all loads issued before the first use.
+constexpr int kTrips = 4;
 template <typename T>
 __device__ __forceinline__ double chunk_squares(const char* data, int64_t numel, int64_t q0, int groups) {
   const T* p = reinterpret_cast<const T*>(data);
-  const int lead = tensor_lead<T>(data);
-  double acc[kGroup] = {};
-  constexpr int U = 4;
-  for (int q = threadIdx.x; q < groups; q += kThreads * U) {
-    float v[U][kGroup];
+  const int lead = tensor_lead<T>(data), t = static_cast<int>(threadIdx.x);
+  float v[kTrips][kGroup];
+  const int64_t e0 = q0 * kGroup - lead;
+  if (e0 >= 0 && e0 + kThreads * kTrips * kGroup <= numel && groups == kThreads * kTrips) {
+    // a whole chunk inside the tensor: no bounds to look at
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      load_group<T>(p, q + u * kThreads < groups ? (q0 + q + u * kThreads) * kGroup - lead : numel, numel, v[u]);
+    for (int u = 0; u < kTrips; ++u) load_whole<T>(p + e0 + (u * kThreads + t) * kGroup, v[u]);
+  } else {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
-        const double d = static_cast<double>(v[u][i]);
-        acc[i] = fma(d, d, acc[i]);
-      }
+    for (int u = 0; u < kTrips; ++u) {
+      const int q = u * kThreads + t;
+      load_group<T>(p, q < groups ? e0 + static_cast<int64_t>(q) * kGroup : numel, numel, v[u]);
+    }
   }
-  return ((acc[0] + acc[1]) + (acc[2] + acc[3])) + ((acc[4] + acc[5]) + (acc[6] + acc[7]));
+  double acc[2] = {0.0, 0.0};
+#pragma unroll
+  for (int u = 0; u < kTrips; ++u)
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) {
+      const double d = static_cast<double>(v[u][i]);
+      acc[i & 1] = fma(d, d, acc[i & 1]);
+    }
+  return acc[0] + acc[1];
 }
 
 __global__ __launch_bounds__(kThreads) void sum_squares_kernel(NormTab t, int groups, double* __restrict__ partial) {
@@ -150,20 +165,27 @@ __device__ __forceinline__ void write_norm(double s, double max_norm, double eps
   norm[2] = c;
 }
 
+// Workgroup b of n adds the b-th run of the partials; the only one makes the
+// norm of it, several leave their sums for another such launch.
 constexpr int kJoinThreads = 1024;
 __global__ __launch_bounds__(kJoinThreads) void sum_partials_kernel(const double* __restrict__ partial, int64_t n,
-                                                                double max_norm, double eps, double* norm) {
+                                                                    double* __restrict__ sums, double max_norm,
+                                                                    double eps, double* norm) {
+  const int64_t per = (n + gridDim.x - 1) / gridDim.x, lo = static_cast<int64_t>(blockIdx.x) * per;
+  const int64_t hi = lo + per < n ? lo + per : n;
   double acc = 0.0;
   constexpr int U = 8;
-  for (int64_t p = threadIdx.x; p < n; p += U * kJoinThreads) {
+  for (int64_t p = lo + threadIdx.x; p < hi; p += U * kJoinThreads) {
     double v[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = p + u * kJoinThreads < n ? partial[p + u * kJoinThreads] : 0.0;
+    for (int u = 0; u < U; ++u) v[u] = p + u * kJoinThreads < hi ? partial[p + u * kJoinThreads] : 0.0;
 #pragma unroll
     for (int u = 0; u < U; ++u) acc += v[u];
   }
   const double s = block_sum<kJoinThreads>(acc);
-  if (threadIdx.x == 0) write_norm(s, max_norm, eps, norm);
+  if (threadIdx.x != 0) return;
+  if (gridDim.x == 1) write_norm(s, max_norm, eps, norm);
+  else sums[blockIdx.x] = s;
 }
 
 __global__ void clip_coef_kernel(double max_norm, double eps, double* norm) {
@@ -193,7 +215,7 @@ __device__ __forceinline__ void chunk_scale(const char* data, char* out, int64_t
 }
 
 __global__ __launch_bounds__(kThreads) void scale_kernel(ScaleTab t, int groups, const double* __restrict__ norm) {
-  const int b = static_cast<int>(blockIdx.x), i = find_tensor(t.in, b);
+  const int b = static_cast<int>(gridDim.x - 1 - blockIdx.x), i = find_tensor(t.in, b);
   const float c = static_cast<float>(norm[2]);
   const char* src = t.in.data[i];
   char* dst = t.out[i];
@@ -213,10 +235,11 @@ constexpr int64_t kMaxChunks = 1 << 23;
 }  // namespace
 
 int64_t clip_chunk(int64_t total) {
-  // small lists in small chunks, so that they still fill the device; large
-  // ones in chunks that keep the partial sums few
-  int64_t c = 4096;
-  while (c < 65536 && total / c > 16384) c *= 2;
+  // One group of 8 elements per thread and trip.  Four trips (16 KB of bf16 a
+  // workgroup) read 2.4 GB at 6.0 TB/s where 64 KB or more a workgroup read it at
+  // 5.5; lists too small to fill the device that way take one or two.
+  int64_t c = kThreads * kGroup;
+  while (c < kThreads * kGroup * kTrips && total / c > 2048) c *= 2;
   return c;
 }
 
@@ -274,7 +297,14 @@ hipError_t launch_grad_norm(hipStream_t s, const muon_tensor_t* t, int64_t count
     return hipGetLastError();
   });
   if (e != hipSuccess) return e;
-  sum_partials_kernel<<<1, kJoinThreads, 0, s>>>(partial, total, max_norm, eps, norm);
+  // the sums of several workgroups follow the partials (clip_partials)
+  const int join = total > 16384 ? kClipJoin : 1;
+  sum_partials_kernel<<<join, kJoinThreads, 0, s>>>(partial, total, partial + total, max_norm, eps, norm);
+  if (join > 1) {
+    const hipError_t j = hipGetLastError();
+    if (j != hipSuccess) return j;
+    sum_partials_kernel<<<1, kJoinThreads, 0, s>>>(partial + total, join, nullptr, max_norm, eps, norm);
+  }
   return hipGetLastError();
 }
 

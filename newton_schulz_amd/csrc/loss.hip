@@ -27,8 +27,7 @@
 // 6.1-6.3 TB/s on MI355X, one that reads and writes alike 5.7-6.0), and HBM is
 // fastest when the workgroups in flight cover a compact, moving window of
 // addresses: copying in 16 KB pieces per workgroup reaches 6.0 TB/s, in 300 KB
-// rows per workgroup 4.9.  So a row is cut into slices of at most kSlicePieces
-// pieces, one workgroup of 256 threads each, in address order; a slice is held
+// rows per workgroup 4.9.  So a row is cut into slices, one workgroup of 256 threads each, in address order; a slice is held
 // in registers.
 #include <algorithm>
 #include <cfloat>
@@ -212,6 +211,10 @@ __device__ __forceinline__ void finish_row(const LossArgs& a, int r, int64_t y, 
 // slices of a row
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 256;
+// Pieces a thread may hold.  Finer slices read in a tighter window but exchange
+// more pairs: 2048 x 151936 bf16 policy loss with at most 4, 6, 8, 10, 12, 16
+// pieces a thread: 307, 252, 228, 220, 223, 223 us; 512 threads of 10: 242 us.
+constexpr int kMostPieces = 10;
 
 // Slice j of a row: pieces [first, first + count), and with slice 0 the edges.
 struct Slice {
@@ -533,7 +536,8 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void logits_grad_kernel(LossArgs a, RowsRef grad,
                                                                    const float* __restrict__ g, int per_sequence,
                                                                    int chunks) {
-  const int r = a.row0 + static_cast<int>(blockIdx.x) / chunks, c = static_cast<int>(blockIdx.x) % chunks;
+  const int block = static_cast<int>(gridDim.x - 1 - blockIdx.x);
+  const int r = a.row0 + block / chunks, c = block % chunks;
   const int64_t y = a.labels[r];
   const T* row = row_at<const T>(a.x, r, a.seq);
   T* out = row_at<T>(grad, r, a.seq);
@@ -585,7 +589,7 @@ __global__ __launch_bounds__(kThreads) void logits_grad_kernel(LossArgs a, RowsR
       for (int i = 0; i < kVec<T>; ++i)
         if (i == iy) v[i] += G;
     }
-    obody[p] = Scores<T>::pack(v);
+    __builtin_nontemporal_store(Scores<T>::pack(v), obody + p);
   }
   if (edge) {
     const int e = edge_score<T>(sh, t);
@@ -691,82 +695,125 @@ __device__ __forceinline__ double sigmoid(double h) {
   return (h < 0.0 ? q : 1.0) / (1.0 + q);
 }
 
-// Workgroup i: pair i.  Joins its tokens' slices, adds the two sequences'
-// scores, and leaves the gradient that every token of each sequence has.
+__device__ __forceinline__ void write_preference(const PreferenceArgs& p, double loss, double margin, double won) {
+  const double n = p.batch > 1 ? p.batch / 2 : 1;
+  p.out[0] = static_cast<float>(static_cast<double>(p.p.weight) * loss / n);
+  p.out[1] = static_cast<float>(margin / n);
+  p.out[2] = static_cast<float>(won / n);
+}
+
+constexpr int kFewPairs = 8;  // handled by one workgroup, which then needs no launch to add them up
+
+// The score of token q of sequence b (0 for tokens left out), its row finished.
+template <typename T>
+__device__ __forceinline__ double token_score(const LossArgs& a, const PreferenceArgs& p, int b, int q, bool* counts) {
+  const int r = b * p.seq + q;
+  const int64_t y = a.labels[r];
+  *counts = y >= 0;
+  const float ref = *counts && p.ref_lp ? p.ref_lp[r] : 0.0f;
+  if (a.slices > 1) {
+    const float k = kLog2e / a.temperature;
+    float m = 0.0f, s = 1.0f;
+    if (y >= 0 && y < a.vocab) {
+      const uint64_t* v = a.part + static_cast<int64_t>(r) * a.slices;
+      m = -kFar;
+      s = 0.0f;
+      bool far = false;
+      constexpr int U = 8;  // words in flight
+      for (int x0 = 0; x0 < a.slices; x0 += U) {
+        uint64_t w[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) w[u] = x0 + u < a.slices ? v[x0 + u] : pair_word(-kFar, 0.0f);
+#pragma unroll
+        for (int u = 0; u < U; ++u) join(m, s, word_max(w[u]), word_sum(w[u]), k);
+      }
+      far = far_row(m, k);
+      if (far) {
+        m = kLowest;
+        s = 0.0f;
+        for (int x = 0; x < a.slices; ++x) join<true>(m, s, word_max(v[x]), word_sum(v[x]), k);
+      }
+    }
+    finish_row<T>(a, r, y, m, s);
+  }
+  return *counts ? a.lp[r] - static_cast<double>(ref) : 0.0;
+}
+
+// Pair i = blockIdx, + gridDim, ...: the two sequences' scores (half of the
+// workgroup each), its loss, and the gradient that every token of each
+// sequence has.  One workgroup (at most kFewPairs pairs) writes the losses;
+// more leave their pairs' terms.
 template <typename T> __global__ __launch_bounds__(kTermThreads) void preference_pairs_kernel(LossArgs a, PreferenceArgs p) {
-  const int i = static_cast<int>(blockIdx.x), pairs = p.batch / 2, t = static_cast<int>(threadIdx.x);
-  const float k = kLog2e / a.temperature;
-  double score[2];
-  int tokens[2];
-  for (int side = 0; side < 2; ++side) {
-    const int b = i + side * pairs;
+  constexpr int kHalf = kTermThreads / 2;
+  const int pairs = p.batch / 2, side = __builtin_amdgcn_readfirstlane(threadIdx.x / kHalf);
+  const int t = static_cast<int>(threadIdx.x) % kHalf, wave = t >> 6;
+  const double beta = p.p.beta, eps = p.p.label_smoothing;
+  __shared__ double scores[2][kHalf / 64];
+  __shared__ int tokens[2][kHalf / 64];
+  double total[3] = {0.0, 0.0, 0.0};
+  for (int i = static_cast<int>(blockIdx.x); i < pairs; i += static_cast<int>(gridDim.x)) {
     double sum = 0.0;
     int n = 0;
-    for (int q = t; q < p.seq; q += kTermThreads) {
-      const int r = b * p.seq + q;
-      const int64_t y = a.labels[r];
-      float m = 0.0f, s = 1.0f;
-      if (a.slices > 1) {
-        if (y >= 0 && y < a.vocab) {
-          const uint64_t* v = a.part + static_cast<int64_t>(r) * a.slices;
-          // all slices of a far maximum are joined in the exact form
-          float top = -kFar;
-          for (int x = 0; x < a.slices; ++x) top = fmaxf(top, word_max(v[x]));
-          const bool far = far_row(top, k);
-          m = far ? kLowest : -kFar;
-          s = 0.0f;
-          for (int x = 0; x < a.slices; ++x) {
-            if (far) join<true>(m, s, word_max(v[x]), word_sum(v[x]), k);
-            else join(m, s, word_max(v[x]), word_sum(v[x]), k);
-          }
-        }
-        finish_row<T>(a, r, y, m, s);
-      }
-      if (y < 0) continue;
-      sum += a.lp[r] - (p.ref_lp ? static_cast<double>(p.ref_lp[r]) : 0.0);
-      ++n;
+    for (int q = t; q < p.seq; q += kHalf) {
+      bool counts;
+      sum += token_score<T>(a, p, i + side * pairs, q, &counts);
+      n += counts;
     }
-    sum = block_total<kTermThreads>(sum);
-    n = static_cast<int>(block_total<kTermThreads>(n));
-    score[side] = p.p.average ? (n ? sum / n : 0.0) : sum;
-    tokens[side] = n;
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      sum += __shfl_xor(sum, d, 64);
+      n += __shfl_xor(n, d, 64);
+    }
+    __syncthreads();  // the last pair's sums have been read
+    if ((t & 63) == 0) {
+      scores[side][wave] = sum;
+      tokens[side][wave] = n;
+    }
+    __syncthreads();
+    if (threadIdx.x != 0) continue;
+    double score[2] = {0.0, 0.0};
+    int count[2] = {0, 0};
+    for (int k = 0; k < 2; ++k) {
+      for (int w = 0; w < kHalf / 64; ++w) {
+        score[k] += scores[k][w];
+        count[k] += tokens[k][w];
+      }
+      if (p.p.average) score[k] = count[k] ? score[k] / count[k] : 0.0;
+    }
+    const double margin = score[0] - score[1], h = beta * margin;
+    double loss, d;
+    if (p.p.kind == MUON_PREFERENCE_SIGMOID) {
+      loss = (1.0 - eps) * neg_log_sigmoid(h) + eps * neg_log_sigmoid(-h);
+      d = beta * (eps * sigmoid(h) - (1.0 - eps) * sigmoid(-h));
+    } else {
+      const double off = margin - 0.5 / beta;
+      loss = off * off;
+      d = 2.0 * off;
+    }
+    const double term[3] = {loss, h, margin > 0.0 ? 1.0 : 0.0};
+    for (int k = 0; k < 3; ++k) {
+      total[k] += term[k];
+      p.terms[3 * static_cast<int64_t>(i) + k] = term[k];
+    }
+    d *= static_cast<double>(p.p.weight) / pairs;
+    for (int k = 0; k < 2; ++k) {
+      const int b = i + k * pairs;
+      if (p.rewards) p.rewards[b] = static_cast<float>(beta * score[k]);
+      const double g = k ? -d : d;
+      p.g[b] = static_cast<float>(p.p.average && count[k] ? g / count[k] : g);
+    }
   }
-  if (t != 0) return;
-  const double beta = p.p.beta, eps = p.p.label_smoothing, margin = score[0] - score[1], h = beta * margin;
-  double loss, d;
-  if (p.p.kind == MUON_PREFERENCE_SIGMOID) {
-    loss = (1.0 - eps) * neg_log_sigmoid(h) + eps * neg_log_sigmoid(-h);
-    d = beta * (eps * sigmoid(h) - (1.0 - eps) * sigmoid(-h));
-  } else {
-    const double off = margin - 0.5 / beta;
-    loss = off * off;
-    d = 2.0 * off;
-  }
-  p.terms[3 * static_cast<int64_t>(i)] = loss;
-  p.terms[3 * static_cast<int64_t>(i) + 1] = h;
-  p.terms[3 * static_cast<int64_t>(i) + 2] = margin > 0.0 ? 1.0 : 0.0;
-  d *= static_cast<double>(p.p.weight) / pairs;
-  for (int side = 0; side < 2; ++side) {
-    const int b = i + side * pairs;
-    if (p.rewards) p.rewards[b] = static_cast<float>(beta * score[side]);
-    const double g = side ? -d : d;
-    p.g[b] = static_cast<float>(p.p.average && tokens[side] ? g / tokens[side] : g);
-  }
+  if (gridDim.x == 1 && threadIdx.x == 0) write_preference(p, total[0], total[1], total[2]);
 }
 
 __global__ __launch_bounds__(kTermThreads) void preference_sums_kernel(PreferenceArgs p) {
-  const int pairs = p.batch / 2;
   double v[3] = {0.0, 0.0, 0.0};
-  for (int64_t i = threadIdx.x; i < pairs; i += kTermThreads)
+  for (int64_t i = threadIdx.x; i < p.batch / 2; i += kTermThreads)
 #pragma unroll
     for (int j = 0; j < 3; ++j) v[j] += p.terms[3 * i + j];
 #pragma unroll
   for (int j = 0; j < 3; ++j) v[j] = block_total<kTermThreads>(v[j]);
-  if (threadIdx.x != 0) return;
-  const double n = pairs > 0 ? pairs : 1;
-  p.out[0] = static_cast<float>(static_cast<double>(p.p.weight) * v[0] / n);
-  p.out[1] = static_cast<float>(v[1] / n);
-  p.out[2] = static_cast<float>(v[2] / n);
+  if (threadIdx.x == 0) write_preference(p, v[0], v[1], v[2]);
 }
 
 }  // namespace
@@ -774,12 +821,9 @@ __global__ __launch_bounds__(kTermThreads) void preference_sums_kernel(Preferenc
 // ---------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------
-#ifndef MAXNV
-#define MAXNV 10
-#endif
 int loss_slices(int64_t rows, int64_t vocab, int bf16, int cus) {
   const int64_t pieces = vocab / (bf16 ? 8 : 4);
-  const int64_t least = (pieces + kThreads * MAXNV - 1) / (kThreads * MAXNV);
+  const int64_t least = (pieces + kThreads * kMostPieces - 1) / (kThreads * kMostPieces);
   // rows that leave compute units idle are cut finer, down to one piece a thread
   const int64_t idle = rows > 0 ? 2 * static_cast<int64_t>(cus) / rows : 1;
   const int64_t most = std::min<int64_t>(64, (pieces + kThreads - 1) / kThreads);
@@ -816,7 +860,7 @@ hipError_t slices(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyAr
   if (per <= 4 * kThreads) return run_slices<T, 4, USE>(s, a, grad, p);
   if (per <= 6 * kThreads) return run_slices<T, 6, USE>(s, a, grad, p);
   if (per <= 8 * kThreads) return run_slices<T, 8, USE>(s, a, grad, p);
-  return run_slices<T, 10, USE>(s, a, grad, p);
+  return run_slices<T, kMostPieces, USE>(s, a, grad, p);
 }
 
 }  // namespace
@@ -874,15 +918,15 @@ hipError_t launch_policy(hipStream_t s, const LossArgs& a, RowsRef grad, const P
 hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, const PreferenceArgs& p) {
   hipError_t e = launch_slice_stats(s, a);
   if (e != hipSuccess) return e;
-  if (p.batch > 0) {
-    const unsigned pairs = static_cast<unsigned>(p.batch / 2);
-    if (a.bf16) preference_pairs_kernel<bf16_t><<<pairs, kTermThreads, 0, s>>>(a, p);
-    else preference_pairs_kernel<float><<<pairs, kTermThreads, 0, s>>>(a, p);
-    e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  preference_sums_kernel<<<1, kTermThreads, 0, s>>>(p);
+  const int pairs = p.batch / 2;
+  const unsigned grid = pairs <= kFewPairs ? 1 : static_cast<unsigned>(pairs);
+  if (a.bf16) preference_pairs_kernel<bf16_t><<<grid, kTermThreads, 0, s>>>(a, p);
+  else preference_pairs_kernel<float><<<grid, kTermThreads, 0, s>>>(a, p);
   e = hipGetLastError();
+  if (e == hipSuccess && grid > 1) {
+    preference_sums_kernel<<<1, kTermThreads, 0, s>>>(p);
+    e = hipGetLastError();
+  }
   if (e != hipSuccess || grad.base == nullptr) return e;
   return launch_logits_grad(s, a, grad, p.g, true);
 }

@@ -366,9 +366,9 @@ muon_status_t check_list(muon_ctx* c, const muon_tensor_t* t, int64_t count, int
 
 size_t norm_bytes(const muon_tensor_t* t, int64_t count, int64_t total) {
   const int64_t chunk = clip_chunk(total);
-  size_t n = 0;
+  size_t n = kClipJoin;
   for (int64_t i = 0; i < count; ++i) n += static_cast<size_t>(clip_chunks(t[i], chunk));
-  return up256(n * 8) + 256;
+  return up256(n * 8);
 }
 
 muon_status_t check_norm(muon_ctx* c, const double* norm) {

@@ -72,6 +72,8 @@ hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, con
 // elements together, and the chunks that one tensor takes.
 int64_t clip_chunk(int64_t total);
 int64_t clip_chunks(const muon_tensor_t& t, int64_t chunk);
+constexpr int kClipJoin = 32;  // workgroups that add up many partials; room for their sums follows the partials
+
 
 hipError_t launch_grad_norm(hipStream_t s, const muon_tensor_t* t, int64_t count, int64_t chunk,
                             double* partial, double max_norm, double eps, double* norm);

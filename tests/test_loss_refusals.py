@@ -199,7 +199,7 @@ def test_workspace_sizes():
         need = 4096 * (8 + 8 + 12 + 8 * slices) + 8 * 5 + 24 * 64
         assert need <= loss_workspace_bytes(4, 1024, 151936, dtype) <= need + 6 * 256
     assert loss_workspace_bytes(0, 0, 100) > 0
-    # one double per chunk of at most 65536 elements
+    # one double per chunk of 8192 elements, and 32 more
     t, n = tensors((0x10000, 1 << 30, MUON_BF16))
-    assert lib.muon_grad_norm_workspace_bytes(t, n) == 8 * (1 << 14) + 256
+    assert lib.muon_grad_norm_workspace_bytes(t, n) == 8 * ((1 << 17) + 32)
     assert lib.muon_grad_norm_workspace_bytes(None, 0) == 0
