@@ -438,7 +438,7 @@ typedef struct {
 
 /* Workspace in bytes of any one of the loss calls on batch x seq rows of
  * `vocab` scores of `dtype` (pure host function; 0 for arguments out of
- * range).  8 bytes per row and slice of a row, about 28 per row beside. */
+ * range).  8 bytes per row and slice of a row, 32 per row beside. */
 size_t muon_loss_workspace_bytes(int64_t batch, int64_t seq, int64_t vocab, int32_t dtype);
 
 /* Log-probability of every token: logps[t] = z[y] - log sum_v exp(z[v]).

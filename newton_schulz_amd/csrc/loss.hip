@@ -193,18 +193,15 @@ __device__ __forceinline__ double token_lp(float xy, float m, float s, float k) 
   return (z - log2s) * 0.69314718055994530942;
 }
 
-// What the row's pair makes of token r (one thread).
-template <typename T>
-__device__ __forceinline__ void finish_row(const LossArgs& a, int r, int64_t y, float m, float s) {
+// What the row's pair and the label's score make of token r (one thread).
+__device__ __forceinline__ double finish_row(const LossArgs& a, int r, int64_t y, float xy, float m, float s) {
   double lp = 0.0;
-  if (y >= a.vocab) {
-    lp = __longlong_as_double(0x7ff8000000000000ll);
-  } else if (y >= 0) {
-    lp = token_lp(muon::Elem<T>::load(row_at<const T>(a.x, r, a.seq) + y), m, s, kLog2e / a.temperature);
-  }
+  if (y >= a.vocab) lp = __longlong_as_double(0x7ff8000000000000ll);
+  else if (y >= 0) lp = token_lp(xy, m, s, kLog2e / a.temperature);
   if (a.lp) a.lp[r] = lp;
   if (a.logps) a.logps[r] = static_cast<float>(lp);
   if (a.stats) a.stats[r] = make_float2(m, s);
+  return lp;
 }
 
 // ---------------------------------------------------------------------------
@@ -270,7 +267,27 @@ template <int N> __device__ __forceinline__ void join_slices(float& m, float& s,
   else wave_join<N>(m, s, k);
 }
 
-// A slice's pair as one 64-bit word, never 0 (S is 0 only where m is far).
+// Exchange between the workgroups of one launch.  What is exchanged goes
+// through agent-scope atomics, which do not stay in the L2 of one of the eight
+// XCDs; a workgroup waits for its stores to have arrived and then counts
+// itself.  (A release at that point would write back the whole L2 for stores
+// that nobody in the launch reads: with it, scoring 2044 x 151936 scores took 1109 us
+// instead of 90.)
+__device__ __forceinline__ void publish(uint64_t* to, uint64_t v) {
+  __hip_atomic_store(to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t published(const uint64_t* from) {
+  return __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Those that counted themselves before; called by the thread that published.
+__device__ __forceinline__ unsigned arrive(unsigned* count) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  const unsigned before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  asm volatile("" ::: "memory");
+  return before;
+}
+
+// Two numbers as one 64-bit word; of a slice's pair never 0 (S is 0 only where m is far).
 __device__ __forceinline__ uint64_t pair_word(float m, float s) {
   return (static_cast<uint64_t>(__float_as_uint(s)) << 32) | __float_as_uint(m);
 }
@@ -329,6 +346,89 @@ __device__ __forceinline__ TokenTerms policy_token(const PolicyArgs& a, int t, i
   return o;
 }
 
+// Sum over the workgroup in a fixed order, in every thread.
+template <int NT> __device__ __forceinline__ double block_total(double v) {
+  __shared__ double wave[NT / 64];
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
+  __syncthreads();  // an earlier call's values have been read
+  if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double t = 0.0;
+#pragma unroll
+  for (int w = 0; w < NT / 64; ++w) t += wave[w];
+  return t;
+}
+
+__device__ __forceinline__ void write_policy(const PolicyArgs& p, double pg, double kl, double clipped) {
+  double loss = pg;
+  if (p.p.kl_coef != 0.0f) loss += static_cast<double>(p.p.kl_coef) * kl;
+  p.out[0] = static_cast<float>(static_cast<double>(p.p.weight) * loss);
+  p.out[1] = static_cast<float>(pg);
+  p.out[2] = static_cast<float>(kl);
+  p.out[3] = static_cast<float>(clipped);
+}
+
+// The same of three values at once.
+template <int NT> __device__ __forceinline__ void block_totals(double (&v)[3]) {
+  __shared__ double wave[3][NT / 64];
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) v[j] += __shfl_xor(v[j], d, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0)
+#pragma unroll
+    for (int j = 0; j < 3; ++j) wave[j][threadIdx.x >> 6] = v[j];
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < 3; ++j) {
+    v[j] = 0.0;
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) v[j] += wave[j][w];
+  }
+}
+
+// The token weight that a word of the weights holds.
+__device__ __forceinline__ double word_weight(uint64_t w) { return __longlong_as_double(static_cast<long long>(w)); }
+
+// Labels in [lo, hi) that count, in every thread of the workgroup.
+template <int NT> __device__ __forceinline__ double count_labels(const int64_t* labels, int64_t lo, int64_t hi) {
+  int count = 0;
+  constexpr int U = 8;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += U * NT) {
+    int64_t y[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) y[u] = i + u * NT < hi ? labels[i + u * NT] : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) count += y[u] >= 0;
+  }
+  return block_total<NT>(count);  // whole numbers: exact
+}
+
+// Weight of a token of sequence b in the loss.
+template <int NT> __device__ __forceinline__ double token_weight(const PolicyArgs& p, int b) {
+  if (p.p.reduce == MUON_REDUCE_SUM) return 1.0;
+  if (p.p.reduce == MUON_REDUCE_TOKEN)
+    return 1.0 / count_labels<NT>(p.labels, 0, static_cast<int64_t>(p.batch) * p.seq);
+  const int64_t lo = static_cast<int64_t>(b) * p.seq;
+  return 1.0 / (count_labels<NT>(p.labels, lo, lo + p.seq) * p.batch);
+}
+
+// The weighted sums of the terms of tokens [lo, hi), in every thread.
+template <int NT> __device__ __forceinline__ void sum_terms(const PolicyArgs& p, int64_t lo, int64_t hi, double (&v)[3]) {
+  v[0] = v[1] = v[2] = 0.0;
+  for (int64_t i = lo + threadIdx.x; i < hi; i += NT) {
+    if (p.labels[i] < 0) continue;
+    const double w = word_weight(published(p.weights + (p.p.reduce == MUON_REDUCE_SEQUENCE ? i / p.seq : 0)));
+    const uint64_t term = published(p.terms + 2 * i), clipped = published(p.terms + 2 * i + 1);
+    v[0] += w * static_cast<double>(word_max(term));
+    v[1] += w * static_cast<double>(word_sum(term));
+    v[2] += w * static_cast<double>(word_max(clipped));
+  }
+  block_totals<NT>(v);
+}
+
 // What a slice is read for.
 enum SliceUse : int {
   USE_STATS = 0,   // the row's pair alone
@@ -356,9 +456,19 @@ enum SliceUse : int {
 // Against a workgroup per row with the row in its registers (1024 threads of 19
 // pieces): 2048 tokens x 151936 bf16 scores took 267 us there.
 template <typename T, int NV, int USE>
-__global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef grad, PolicyArgs p) {
+__device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& grad, const PolicyArgs& p) {
   const int t = static_cast<int>(threadIdx.x), lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int r = a.row0 + static_cast<int>(blockIdx.x) / a.slices, j = static_cast<int>(blockIdx.x) % a.slices;
+  const int b = r / a.seq;
+  if (USE == USE_POLICY && p.count_here && j == 0) {
+    // the first workgroup of those that share a mean publishes its weight
+    if (p.p.reduce == MUON_REDUCE_SEQUENCE ? r == b * a.seq : r == 0) {
+      const double weight = token_weight<kThreads>(p, b);
+      if (t == 0)
+        publish(p.weights + (p.p.reduce == MUON_REDUCE_SEQUENCE ? b : 0),
+                static_cast<uint64_t>(__double_as_longlong(weight)));
+    }
+  }
   const int64_t y = a.labels[r];
   const T* row = row_at<const T>(a.x, r, a.seq);
   const RowShape sh = row_shape(row, a.vocab);
@@ -377,7 +487,7 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef gra
     }
     if (j == 0 && t == 0) {
       if (USE == USE_POLICY && a.logps) a.logps[r] = 0.0f;
-      if (USE == USE_STATS && a.slices == 1) finish_row<T>(a, r, y, 0.0f, 1.0f);
+      if (USE == USE_STATS && a.slices == 1) finish_row(a, r, y, 0.0f, 0.0f, 1.0f);
     }
     return;
   }
@@ -394,7 +504,7 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef gra
   const float we = edge ? muon::Elem<T>::load(row + edge_score<T>(sh, t)) : -INFINITY;
   const bool named = y < a.vocab;
   float xy = 0.0f;
-  if (USE == USE_POLICY) xy = muon::Elem<T>::load(row + (named ? y : 0));
+  if (USE == USE_POLICY || j == 0) xy = muon::Elem<T>::load(row + (named ? y : 0));
   float m = -kFar, c = m * k, s = 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -415,23 +525,24 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef gra
   if (far_row(m, k)) far_slice(row, sh, sl, j == 0, k, m, s);
   if (USE == USE_STATS) {
     if (t == 0) {
-      if (a.slices == 1) finish_row<T>(a, r, y, m, s);
+      if (a.slices == 1) finish_row(a, r, y, xy, m, s);
       else a.part[static_cast<int64_t>(r) * a.slices + j] = pair_word(m, s);
+      if (a.slices > 1 && j == 0) a.chosen[r] = xy;
     }
     return;
   }
   __shared__ float coef[4];
   __shared__ uint64_t missing, own[64];
-  const int b = r / a.seq;
+  constexpr int kWeightLane = 63;  // (a row has at most 60 slices)
   // wave 0: the row's pair from a slice's word in each lane, and what follows
   auto settle = [&](uint64_t word) {
+    const double wt = word_weight(__shfl(word, kWeightLane, 64));
     m = lane < a.slices ? word_max(word) : -kFar;
     s = lane < a.slices ? word_sum(word) : 0.0f;
     join_slices<64>(m, s, k);
     double lp = token_lp(xy, m, s, k);
     if (!named) lp = __longlong_as_double(0x7ff8000000000000ll);
     const TokenTerms o = policy_token(p, r, b, lp);
-    const double wt = p.weights[p.p.reduce == MUON_REDUCE_SEQUENCE ? b : 0];
     const float G = static_cast<float>(static_cast<double>(p.p.weight) * wt * static_cast<double>(o.g)) / a.temperature;
     if (lane == 0) {
       coef[0] = m;
@@ -439,26 +550,26 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef gra
       coef[2] = G;
       if (j == 0) {
         if (a.logps) a.logps[r] = static_cast<float>(lp);
-        p.terms[3 * static_cast<int64_t>(r)] = o.pg;
-        p.terms[3 * static_cast<int64_t>(r) + 1] = o.kl;
-        p.terms[3 * static_cast<int64_t>(r) + 2] = o.clipped;
+        publish(p.terms + 2 * static_cast<int64_t>(r), pair_word(o.pg, o.kl));
+        publish(p.terms + 2 * static_cast<int64_t>(r) + 1, __float_as_uint(o.clipped));
       }
     }
   };
   uint64_t* slot = a.part + static_cast<int64_t>(r) * a.slices;
   const uint64_t word = pair_word(m, s);
-  if (a.slices > 1 && t == 0) __hip_atomic_store(slot + j, word, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  if (a.slices > 1 && t == 0) publish(slot + j, word);
   if (grad.base == nullptr && j > 0) return;  // evaluation: slice 0 has it all
   if (wave == 0) {
+    // lanes 0 .. slices - 1: the slices' pairs, the last lane: the weight
+    const uint64_t* from = lane == kWeightLane ? p.weights + (p.p.reduce == MUON_REDUCE_SEQUENCE ? b : 0) : slot + lane;
+    const bool asks = lane == kWeightLane || (a.slices > 1 && lane < a.slices);
     uint64_t v = word;
     bool ready = true;
-    if (a.slices > 1) {
-      for (int n = 0;; ++n) {
-        if (lane < a.slices) v = __hip_atomic_load(slot + lane, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        ready = __all(v != 0);
-        if (ready || n >= a.spin) break;
-        __builtin_amdgcn_s_sleep(1);
-      }
+    for (int n = 0;; ++n) {
+      if (asks) v = published(from);
+      ready = __all(v != 0);
+      if (ready || n >= a.spin) break;
+      __builtin_amdgcn_s_sleep(1);
     }
     const uint64_t lack = __ballot(v == 0);
     if (lane == 0) missing = lack;
@@ -472,9 +583,13 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef gra
       float mi, si;
       slice_pair(row, sh, a.slices, i, k, mi, si);
       if (t == 0) {
-        const uint64_t v = __hip_atomic_load(slot + i, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const uint64_t v = published(slot + i);
         own[i] = v ? v : pair_word(mi, si);
       }
+    }
+    if ((lack >> kWeightLane) & 1) {
+      const double weight = token_weight<kThreads>(p, b);
+      if (t == 0) own[kWeightLane] = static_cast<uint64_t>(__double_as_longlong(weight));
     }
     __syncthreads();
     if (wave == 0) settle(own[lane]);
@@ -509,8 +624,27 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef gra
   }
 }
 
+template <typename T, int NV, int USE>
+__global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef grad, PolicyArgs p) {
+  slice_work<T, NV, USE>(a, grad, p);
+  if (USE != USE_POLICY || p.arrived == nullptr) return;
+  // A small call is one launch: the last workgroup to get here adds up the
+  // tokens and leaves the exchange words as it found them, all zero.
+  __shared__ int last;
+  if (threadIdx.x == 0) last = arrive(p.arrived) == gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  double v[3];
+  sum_terms<kThreads>(p, 0, a.rows, v);
+  if (threadIdx.x == 0) {
+    write_policy(p, v[0], v[1], v[2]);
+    *p.arrived = 0;
+  }
+  for (int i = threadIdx.x; i < p.clear; i += kThreads) a.part[i] = 0;
+}
+
 // Joins the slices of each row; one wave per row.
-template <typename T> __global__ __launch_bounds__(kThreads) void row_join_kernel(LossArgs a) {
+__global__ __launch_bounds__(kThreads) void row_join_kernel(LossArgs a) {
   const int r = static_cast<int>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (r >= a.rows) return;
   const int64_t y = a.labels[r];
@@ -525,7 +659,7 @@ template <typename T> __global__ __launch_bounds__(kThreads) void row_join_kerne
     }
     join_slices<64>(m, s, kLog2e / a.temperature);
   }
-  if (lane == 0) finish_row<T>(a, r, y, m, s);
+  if (lane == 0) finish_row(a, r, y, a.chosen[r], m, s);
 }
 
 constexpr int kGradUnroll = 4;
@@ -605,78 +739,35 @@ __global__ __launch_bounds__(kThreads) void logits_grad_kernel(LossArgs a, RowsR
 // ---------------------------------------------------------------------------
 constexpr int kTermThreads = 1024;
 
-// Sum over the workgroup in a fixed order, in every thread.
-template <int NT> __device__ __forceinline__ double block_total(double v) {
-  __shared__ double wave[NT / 64];
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-  __syncthreads();  // an earlier call's values have been read
-  if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double t = 0.0;
-#pragma unroll
-  for (int w = 0; w < NT / 64; ++w) t += wave[w];
-  return t;
-}
-
-// Before the slices of a policy loss: the weight of a token in the mean (of
-// each sequence, or one for all), and empty slots for the slices' pairs.
-// Workgroup b counts sequence b (workgroup 0 all tokens); all clear.
+// Before the slices of a policy loss too large for the exchange words: the
+// weights (workgroup b: sequence b, workgroup 0: all tokens), and empty slots
+// for the slices' pairs.
 __global__ __launch_bounds__(kTermThreads) void policy_prepare_kernel(PolicyArgs p, uint64_t* slots, int64_t n) {
   const int t = static_cast<int>(threadIdx.x), b = static_cast<int>(blockIdx.x);
   for (int64_t i = static_cast<int64_t>(b) * kTermThreads + t; i < n; i += static_cast<int64_t>(gridDim.x) * kTermThreads)
     slots[i] = 0;
-  const bool each = p.p.reduce == MUON_REDUCE_SEQUENCE;
-  if (b >= (each ? p.batch : 1)) return;
-  double weight = 1.0;
-  if (p.p.reduce != MUON_REDUCE_SUM) {
-    const int64_t lo = each ? static_cast<int64_t>(b) * p.seq : 0;
-    const int64_t hi = lo + (each ? p.seq : static_cast<int64_t>(p.batch) * p.seq);
-    int count = 0;
-    constexpr int U = 4;
-    for (int64_t i = lo + t; i < hi; i += U * kTermThreads) {
-      int64_t y[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) y[u] = i + u * kTermThreads < hi ? p.labels[i + u * kTermThreads] : -1;
-#pragma unroll
-      for (int u = 0; u < U; ++u) count += y[u] >= 0;
-    }
-    const double total = block_total<kTermThreads>(count);  // whole numbers: exact
-    weight = 1.0 / (each ? total * p.batch : total);
-  }
-  if (t == 0) p.weights[b] = weight;
+  if (b >= (p.p.reduce == MUON_REDUCE_SEQUENCE ? p.batch : 1)) return;
+  const double weight = token_weight<kTermThreads>(p, b);
+  if (t == 0) p.weights[b] = static_cast<uint64_t>(__double_as_longlong(weight));
 }
 
-__device__ __forceinline__ void write_policy(const PolicyArgs& p, double pg, double kl, double clipped) {
-  double loss = pg;
-  if (p.p.kl_coef != 0.0f) loss += static_cast<double>(p.p.kl_coef) * kl;
-  p.out[0] = static_cast<float>(static_cast<double>(p.p.weight) * loss);
-  p.out[1] = static_cast<float>(pg);
-  p.out[2] = static_cast<float>(kl);
-  p.out[3] = static_cast<float>(clipped);
-}
-
-// The weighted sums of the tokens' terms: workgroup b of n adds the b-th run of
-// tokens.  One workgroup writes the losses, several leave their sums.
-__global__ __launch_bounds__(kTermThreads) void policy_sums_kernel(PolicyArgs p, int64_t rows) {
+// After the slices: workgroup b of n adds the b-th run of tokens.  One
+// workgroup writes the losses, and empties the exchange words (`clear` of
+// them from `words`) for the next call; several leave their sums.
+__global__ __launch_bounds__(kTermThreads) void policy_sums_kernel(PolicyArgs p, int64_t rows, uint64_t* words) {
   const int64_t per = (rows + gridDim.x - 1) / gridDim.x, lo = static_cast<int64_t>(blockIdx.x) * per;
-  const int64_t hi = lo + per < rows ? lo + per : rows;
-  double v[3] = {0.0, 0.0, 0.0};
-  for (int64_t i = lo + threadIdx.x; i < hi; i += kTermThreads) {
-    if (p.labels[i] < 0) continue;
-    const double w = p.weights[p.p.reduce == MUON_REDUCE_SEQUENCE ? i / p.seq : 0];
-#pragma unroll
-    for (int j = 0; j < 3; ++j) v[j] += w * static_cast<double>(p.terms[3 * i + j]);
-  }
-#pragma unroll
-  for (int j = 0; j < 3; ++j) v[j] = block_total<kTermThreads>(v[j]);
-  if (threadIdx.x != 0) return;
-  if (gridDim.x == 1) {
-    write_policy(p, v[0], v[1], v[2]);
-  } else {
+  double v[3];
+  sum_terms<kTermThreads>(p, lo, lo + per < rows ? lo + per : rows, v);
+  if (gridDim.x == 1) {  // (the sums' barriers lie after every read of the weights)
+    for (int i = threadIdx.x; i < p.clear; i += kTermThreads) words[i] = 0;
+    if (threadIdx.x == 0) write_policy(p, v[0], v[1], v[2]);
+  } else if (threadIdx.x == 0) {
 #pragma unroll
     for (int j = 0; j < 3; ++j) p.sums[3 * blockIdx.x + j] = v[j];
   }
+}
+__global__ __launch_bounds__(kTermThreads) void clear_words_kernel(uint64_t* words, int n) {
+  for (int i = static_cast<int>(blockIdx.x) * kTermThreads + threadIdx.x; i < n; i += gridDim.x * kTermThreads) words[i] = 0;
 }
 __global__ void policy_total_kernel(PolicyArgs p, int n) {
   double v[3] = {0.0, 0.0, 0.0};
@@ -705,20 +796,21 @@ __device__ __forceinline__ void write_preference(const PreferenceArgs& p, double
 constexpr int kFewPairs = 8;  // handled by one workgroup, which then needs no launch to add them up
 
 // The score of token q of sequence b (0 for tokens left out), its row finished.
-template <typename T>
 __device__ __forceinline__ double token_score(const LossArgs& a, const PreferenceArgs& p, int b, int q, bool* counts) {
   const int r = b * p.seq + q;
   const int64_t y = a.labels[r];
   *counts = y >= 0;
-  const float ref = *counts && p.ref_lp ? p.ref_lp[r] : 0.0f;
-  if (a.slices > 1) {
-    const float k = kLog2e / a.temperature;
+  const float ref = p.ref_lp ? p.ref_lp[r] : 0.0f;  // (anything where the token is left out)
+  double lp;
+  if (a.slices == 1) {
+    lp = a.lp[r];
+  } else {
+    const float k = kLog2e / a.temperature, xy = a.chosen[r];
     float m = 0.0f, s = 1.0f;
     if (y >= 0 && y < a.vocab) {
       const uint64_t* v = a.part + static_cast<int64_t>(r) * a.slices;
       m = -kFar;
       s = 0.0f;
-      bool far = false;
       constexpr int U = 8;  // words in flight
       for (int x0 = 0; x0 < a.slices; x0 += U) {
         uint64_t w[U];
@@ -727,56 +819,58 @@ __device__ __forceinline__ double token_score(const LossArgs& a, const Preferenc
 #pragma unroll
         for (int u = 0; u < U; ++u) join(m, s, word_max(w[u]), word_sum(w[u]), k);
       }
-      far = far_row(m, k);
-      if (far) {
+      if (far_row(m, k)) {  // joined again in the exact form
         m = kLowest;
         s = 0.0f;
         for (int x = 0; x < a.slices; ++x) join<true>(m, s, word_max(v[x]), word_sum(v[x]), k);
       }
     }
-    finish_row<T>(a, r, y, m, s);
+    lp = finish_row(a, r, y, xy, m, s);
   }
-  return *counts ? a.lp[r] - static_cast<double>(ref) : 0.0;
+  return *counts ? lp - static_cast<double>(ref) : 0.0;
 }
 
-// Pair i = blockIdx, + gridDim, ...: the two sequences' scores (half of the
-// workgroup each), its loss, and the gradient that every token of each
-// sequence has.  One workgroup (at most kFewPairs pairs) writes the losses;
-// more leave their pairs' terms.
-template <typename T> __global__ __launch_bounds__(kTermThreads) void preference_pairs_kernel(LossArgs a, PreferenceArgs p) {
-  constexpr int kHalf = kTermThreads / 2;
-  const int pairs = p.batch / 2, side = __builtin_amdgcn_readfirstlane(threadIdx.x / kHalf);
+// Scores of pairs blockIdx * n ... (n = 1, or all of at most kFewPairs): half of
+// the workgroup per sequence; then a thread per pair: its loss, and the gradient
+// that every token of each sequence has.  The only workgroup writes the losses;
+// several leave their pairs' terms.
+__global__ __launch_bounds__(kTermThreads) void preference_pairs_kernel(LossArgs a, PreferenceArgs p, int n) {
+  constexpr int kHalf = kTermThreads / 2, W = kHalf / 64;
+  const int pairs = p.batch / 2, first = static_cast<int>(blockIdx.x) * n;
+  const int side = __builtin_amdgcn_readfirstlane(threadIdx.x / kHalf);
   const int t = static_cast<int>(threadIdx.x) % kHalf, wave = t >> 6;
-  const double beta = p.p.beta, eps = p.p.label_smoothing;
-  __shared__ double scores[2][kHalf / 64];
-  __shared__ int tokens[2][kHalf / 64];
-  double total[3] = {0.0, 0.0, 0.0};
-  for (int i = static_cast<int>(blockIdx.x); i < pairs; i += static_cast<int>(gridDim.x)) {
+  __shared__ double scores[kFewPairs][2][W], terms[kFewPairs][3];
+  __shared__ int tokens[kFewPairs][2][W];
+  for (int i = 0; i < n; ++i) {
     double sum = 0.0;
-    int n = 0;
+    int count = 0;
     for (int q = t; q < p.seq; q += kHalf) {
       bool counts;
-      sum += token_score<T>(a, p, i + side * pairs, q, &counts);
-      n += counts;
+      sum += token_score(a, p, first + i + side * pairs, q, &counts);
+      count += counts;
     }
 #pragma unroll
     for (int d = 32; d > 0; d >>= 1) {
       sum += __shfl_xor(sum, d, 64);
-      n += __shfl_xor(n, d, 64);
+      count += __shfl_xor(count, d, 64);
     }
-    __syncthreads();  // the last pair's sums have been read
     if ((t & 63) == 0) {
-      scores[side][wave] = sum;
-      tokens[side][wave] = n;
+      scores[i][side][wave] = sum;
+      tokens[i][side][wave] = count;
     }
-    __syncthreads();
-    if (threadIdx.x != 0) continue;
+  }
+  __syncthreads();
+  if (static_cast<int>(threadIdx.x) < n) {
+    const int l = static_cast<int>(threadIdx.x), i = first + l;
+    const double beta = p.p.beta, eps = p.p.label_smoothing;
     double score[2] = {0.0, 0.0};
     int count[2] = {0, 0};
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
-      for (int w = 0; w < kHalf / 64; ++w) {
-        score[k] += scores[k][w];
-        count[k] += tokens[k][w];
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        score[k] += scores[l][k][w];
+        count[k] += tokens[l][k][w];
       }
       if (p.p.average) score[k] = count[k] ? score[k] / count[k] : 0.0;
     }
@@ -790,12 +884,13 @@ template <typename T> __global__ __launch_bounds__(kTermThreads) void preference
       loss = off * off;
       d = 2.0 * off;
     }
-    const double term[3] = {loss, h, margin > 0.0 ? 1.0 : 0.0};
-    for (int k = 0; k < 3; ++k) {
-      total[k] += term[k];
-      p.terms[3 * static_cast<int64_t>(i) + k] = term[k];
-    }
+    terms[l][0] = loss;
+    terms[l][1] = h;
+    terms[l][2] = margin > 0.0 ? 1.0 : 0.0;
+#pragma unroll
+    for (int k = 0; k < 3; ++k) p.terms[3 * static_cast<int64_t>(i) + k] = terms[l][k];
     d *= static_cast<double>(p.p.weight) / pairs;
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int b = i + k * pairs;
       if (p.rewards) p.rewards[b] = static_cast<float>(beta * score[k]);
@@ -803,7 +898,15 @@ template <typename T> __global__ __launch_bounds__(kTermThreads) void preference
       p.g[b] = static_cast<float>(p.p.average && count[k] ? g / count[k] : g);
     }
   }
-  if (gridDim.x == 1 && threadIdx.x == 0) write_preference(p, total[0], total[1], total[2]);
+  if (gridDim.x > 1) return;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double total[3] = {0.0, 0.0, 0.0};
+    for (int i = 0; i < n; ++i)
+#pragma unroll
+      for (int k = 0; k < 3; ++k) total[k] += terms[i][k];
+    write_preference(p, total[0], total[1], total[2]);
+  }
 }
 
 __global__ __launch_bounds__(kTermThreads) void preference_sums_kernel(PreferenceArgs p) {
@@ -811,8 +914,7 @@ __global__ __launch_bounds__(kTermThreads) void preference_sums_kernel(Preferenc
   for (int64_t i = threadIdx.x; i < p.batch / 2; i += kTermThreads)
 #pragma unroll
     for (int j = 0; j < 3; ++j) v[j] += p.terms[3 * i + j];
-#pragma unroll
-  for (int j = 0; j < 3; ++j) v[j] = block_total<kTermThreads>(v[j]);
+  block_totals<kTermThreads>(v);
   if (threadIdx.x == 0) write_preference(p, v[0], v[1], v[2]);
 }
 
@@ -826,7 +928,7 @@ int loss_slices(int64_t rows, int64_t vocab, int bf16, int cus) {
   const int64_t least = (pieces + kThreads * kMostPieces - 1) / (kThreads * kMostPieces);
   // rows that leave compute units idle are cut finer, down to one piece a thread
   const int64_t idle = rows > 0 ? 2 * static_cast<int64_t>(cus) / rows : 1;
-  const int64_t most = std::min<int64_t>(64, (pieces + kThreads - 1) / kThreads);
+  const int64_t most = std::min<int64_t>(60, (pieces + kThreads - 1) / kThreads);
   return static_cast<int>(std::max<int64_t>(1, std::max(least, std::min(idle, most))));
 }
 
@@ -865,7 +967,14 @@ hipError_t slices(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyAr
 
 }  // namespace
 
-hipError_t launch_slice_stats(hipStream_t s, const LossArgs& a) {
+// Empties the exchange words if a call failed half way.
+static hipError_t clear_exchange(hipStream_t s, Exchange& x) {
+  if (!x.dirty) return hipSuccess;
+  clear_words_kernel<<<8, kTermThreads, 0, s>>>(x.words, kExchangeWords + 1);
+  return hipGetLastError();
+}
+
+static hipError_t launch_slice_stats(hipStream_t s, const LossArgs& a) {
   return a.bf16 ? slices<bf16_t, USE_STATS>(s, a, RowsRef{}, PolicyArgs{})
                 : slices<float, USE_STATS>(s, a, RowsRef{}, PolicyArgs{});
 }
@@ -874,8 +983,7 @@ hipError_t launch_row_stats(hipStream_t s, const LossArgs& a) {
   const hipError_t e = launch_slice_stats(s, a);
   if (e != hipSuccess || a.slices == 1 || a.rows == 0) return e;
   const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.rows) + kThreads / 64 - 1) / (kThreads / 64));
-  if (a.bf16) row_join_kernel<bf16_t><<<blocks, kThreads, 0, s>>>(a);
-  else row_join_kernel<float><<<blocks, kThreads, 0, s>>>(a);
+  row_join_kernel<<<blocks, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -897,22 +1005,41 @@ hipError_t launch_logits_grad(hipStream_t s, const LossArgs& a, RowsRef grad, co
   return hipSuccess;
 }
 
-hipError_t launch_policy(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p) {
-  const int64_t slots = a.slices > 1 ? static_cast<int64_t>(a.rows) * a.slices : 0;
-  const int64_t clear = std::min<int64_t>(128, (slots + kTermThreads - 1) / kTermThreads);
-  const int64_t count = p.p.reduce == MUON_REDUCE_SEQUENCE ? p.batch : 1;
-  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, std::max(clear, count)));
-  policy_prepare_kernel<<<grid, kTermThreads, 0, s>>>(p, a.part, slots);
-  hipError_t e = hipGetLastError();
+hipError_t launch_policy(hipStream_t s, const LossArgs& args, RowsRef grad, const PolicyArgs& policy,
+                         Exchange& x) {
+  LossArgs a = args;
+  PolicyArgs p = policy;
+  const int64_t slots = static_cast<int64_t>(a.rows) * a.slices;
+  const int64_t sets = p.p.reduce == MUON_REDUCE_SEQUENCE ? p.batch : 1;
+  const bool kept = slots + sets <= kExchangeWords;
+  hipError_t e = hipSuccess;
+  if (kept) {
+    e = clear_exchange(s, x);
+    if (e != hipSuccess) return e;
+    a.part = x.words;
+    p.weights = x.words + slots;
+    p.count_here = 1;
+    p.clear = static_cast<int>(slots + sets);
+    if (a.rows > 0 && slots <= kArriveGroups) p.arrived = reinterpret_cast<unsigned*>(x.words + kExchangeWords);
+    x.dirty = true;  // until every launch below is in the stream
+  } else {
+    const int64_t clear = std::min<int64_t>(128, (slots + kTermThreads - 1) / kTermThreads);
+    policy_prepare_kernel<<<static_cast<unsigned>(std::max(clear, sets)), kTermThreads, 0, s>>>(p, a.part, slots);
+    e = hipGetLastError();
+  }
+  if (e == hipSuccess) e = a.bf16 ? slices<bf16_t, USE_POLICY>(s, a, grad, p) : slices<float, USE_POLICY>(s, a, grad, p);
   if (e != hipSuccess) return e;
-  e = a.bf16 ? slices<bf16_t, USE_POLICY>(s, a, grad, p) : slices<float, USE_POLICY>(s, a, grad, p);
-  if (e != hipSuccess) return e;
-  const int n = std::min(kPolicySums, std::max(1, a.rows / 8192));
-  policy_sums_kernel<<<static_cast<unsigned>(n), kTermThreads, 0, s>>>(p, a.rows);
-  e = hipGetLastError();
-  if (e != hipSuccess || n == 1) return e;
-  policy_total_kernel<<<1, 1, 0, s>>>(p, n);
-  return hipGetLastError();
+  if (p.arrived == nullptr) {
+    const int n = kept ? 1 : std::min(kPolicySums, std::max(1, a.rows / 8192));
+    policy_sums_kernel<<<static_cast<unsigned>(n), kTermThreads, 0, s>>>(p, a.rows, a.part);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (n > 1) policy_total_kernel<<<1, 1, 0, s>>>(p, n);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (kept) x.dirty = false;
+  return hipSuccess;
 }
 
 hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, const PreferenceArgs& p) {
@@ -920,8 +1047,7 @@ hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, con
   if (e != hipSuccess) return e;
   const int pairs = p.batch / 2;
   const unsigned grid = pairs <= kFewPairs ? 1 : static_cast<unsigned>(pairs);
-  if (a.bf16) preference_pairs_kernel<bf16_t><<<grid, kTermThreads, 0, s>>>(a, p);
-  else preference_pairs_kernel<float><<<grid, kTermThreads, 0, s>>>(a, p);
+  preference_pairs_kernel<<<grid, kTermThreads, 0, s>>>(a, p, grid == 1 ? pairs : 1);
   e = hipGetLastError();
   if (e == hipSuccess && grid > 1) {
     preference_sums_kernel<<<1, kTermThreads, 0, s>>>(p);

@@ -20,7 +20,7 @@ inline size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 // What the kernels of one loss call hand each other, for the finest slicing
 // that `cus` compute units can ask for.
 struct LossLayout {
-  size_t part, stats, lp, terms, weights, sums, total;
+  size_t part, stats, lp, terms, weights, pairs, sums, total;
 };
 
 LossLayout loss_layout(int64_t batch, int64_t seq, int slices) {
@@ -35,8 +35,9 @@ LossLayout loss_layout(int64_t batch, int64_t seq, int slices) {
   l.part = take(sizeof(uint64_t) * rows * static_cast<size_t>(slices));
   l.stats = take(sizeof(float2) * rows);
   l.lp = take(sizeof(double) * rows);
-  l.terms = take(std::max(sizeof(float) * 3 * rows, sizeof(double) * 3 * ((b + 1) / 2)));
+  l.terms = take(sizeof(uint64_t) * 2 * rows);
   l.weights = take(sizeof(double) * (b + 1));
+  l.pairs = take(sizeof(double) * 3 * (b / 2));
   l.sums = take(sizeof(double) * 3 * kPolicySums);
   l.total = at;
   return l;
@@ -151,6 +152,7 @@ LossArgs loss_args(const muon_ctx* c, const LossLayout& l, const muon_logits_t& 
   a.slices = slices_of(c, x);
   a.spin = c->loss_spin;
   a.part = reinterpret_cast<uint64_t*>(c->ws + l.part);
+  a.chosen = reinterpret_cast<float*>(c->ws + l.terms);
   a.lp = reinterpret_cast<double*>(c->ws + l.lp);
   a.stats = reinterpret_cast<float2*>(c->ws + l.stats);
   return a;
@@ -283,12 +285,12 @@ muon_status_t muon_policy_loss(muon_ctx_t* c, void* stream, const muon_logits_t*
   t.old_lp = old_logps;
   t.ref_lp = ref_logps;
   t.out = out;
-  t.weights = reinterpret_cast<double*>(c->ws + l.weights);
-  t.terms = reinterpret_cast<float*>(c->ws + l.terms);
+  t.weights = reinterpret_cast<uint64_t*>(c->ws + l.weights);
+  t.terms = reinterpret_cast<uint64_t*>(c->ws + l.terms);
   t.sums = reinterpret_cast<double*>(c->ws + l.sums);
   hipStream_t s = static_cast<hipStream_t>(stream);
   return timed(c, s, MUON_K_LOSS, "policy loss launch",
-               [&] { return launch_policy(s, a, grad_logits && rows ? rows_ref(*grad_logits) : RowsRef{}, t); });
+               [&] { return launch_policy(s, a, grad_logits && rows ? rows_ref(*grad_logits) : RowsRef{}, t, c->exchange); });
 }
 
 muon_status_t muon_preference_loss(muon_ctx_t* c, void* stream, const muon_logits_t* logits,
@@ -333,7 +335,7 @@ muon_status_t muon_preference_loss(muon_ctx_t* c, void* stream, const muon_logit
   t.out = out;
   t.rewards = rewards;
   t.g = reinterpret_cast<float*>(c->ws + l.weights);
-  t.terms = reinterpret_cast<double*>(c->ws + l.terms);
+  t.terms = reinterpret_cast<double*>(c->ws + l.pairs);
   hipStream_t s = static_cast<hipStream_t>(stream);
   return timed(c, s, MUON_K_LOSS, "preference loss launch",
                [&] { return launch_preference(s, a, grad_logits && rows ? rows_ref(*grad_logits) : RowsRef{}, t); });

@@ -22,12 +22,13 @@ struct LossArgs {
   int slices;        // workgroups that a row is cut over
   int spin;          // polls before a slice computes its neighbours' pairs itself
   uint64_t* part;    // [rows][slices] pairs of the slices
+  float* chosen;     // [rows] the labels' scores, of rows in several slices
   double* lp;        // [rows] or nullptr
   float* logps;      // [rows] or nullptr
   float2* stats;     // [rows] (maximum, sum) of the whole row, or nullptr
 };
 
-// Slices of each row (at most 64 within MUON_MAX_VOCAB).
+// Slices of each row (at most 60 within MUON_MAX_VOCAB).
 int loss_slices(int64_t rows, int64_t vocab, int bf16, int cus);
 
 // stats, lp and logps of every row (logps of tokens left out: 0).
@@ -46,12 +47,32 @@ struct PolicyArgs {
   const float* old_lp;
   const float* ref_lp;
   float* out;
-  double* weights;  // [batch] weight of a sequence's tokens, or one for all
-  float* terms;     // [rows][3] pg, kl, clipped
-  double* sums;     // [kPolicySums][3]
+  uint64_t* weights;  // [batch] weight of a sequence's tokens (binary64), or one for all
+  uint64_t* terms;    // [rows][2] words of pg and kl, and of clipped
+  double* sums;       // [kPolicySums][3]
+  // set by the launcher
+  int count_here;     // the slices count the tokens and publish the weights
+  int clear;          // exchange words to empty afterwards
+  unsigned* arrived;  // workgroups that are through (calls of one launch)
+};
+
+// Words of a context through which workgroups of one launch exchange what they
+// found (pairs of slices, weights of tokens, counts of those that are through).
+// They are zero between calls: each call leaves them so, so none has to clear
+// them first.  Calls that need more take their workspace and a launch more.
+// One word behind them counts a whole call's workgroups.
+constexpr int kExchangeWords = 32768;
+// Calls of so few workgroups are one launch, whose last workgroup adds up the
+// tokens.  All count themselves at one address, so many take longer than a
+// second launch: 36, 128, 256, 1024 workgroups 8.8, 8.9, 9.1, 12.7 us against 12.2
+// with two.
+constexpr int kArriveGroups = 256;
+struct Exchange {
+  uint64_t* words = nullptr;
+  bool dirty = false;  // a call failed between its launches
 };
 // Loss, and gradient where grad.base is set, in one pass over the scores.
-hipError_t launch_policy(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p);
+hipError_t launch_policy(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p, Exchange& x);
 
 struct PreferenceArgs {
   muon_preference_params_t p;

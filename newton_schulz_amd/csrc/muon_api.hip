@@ -98,6 +98,9 @@ muon_status_t muon_create(int device, size_t workspace_bytes, muon_ctx_t** out) 
             hipSuccess;
   ok = ok && hipMalloc(reinterpret_cast<void**>(&c->dev_tab), tab_bytes) == hipSuccess;
   ok = ok && hipHostMalloc(reinterpret_cast<void**>(&c->host_tab), tab_bytes, 0) == hipSuccess;
+  const size_t words = sizeof(uint64_t) * (kExchangeWords + 1);
+  ok = ok && hipMalloc(reinterpret_cast<void**>(&c->exchange.words), words) == hipSuccess;
+  ok = ok && hipMemset(c->exchange.words, 0, words) == hipSuccess;
   for (int i = 0; ok && i < kTabSlots; ++i)
     ok = hipEventCreateWithFlags(&c->tab_ev[i], hipEventDisableTiming) == hipSuccess;
   if (!ok) {
@@ -119,6 +122,7 @@ muon_status_t muon_destroy(muon_ctx_t* c) {
     if (c->tab_ev[i]) (void)hipEventDestroy(c->tab_ev[i]);
   if (c->host_tab) (void)hipHostFree(c->host_tab);
   if (c->dev_tab) (void)hipFree(c->dev_tab);
+  if (c->exchange.words) (void)hipFree(c->exchange.words);
   if (c->ws) (void)hipFree(c->ws);
   delete c;
   return MUON_OK;

@@ -8,6 +8,7 @@
 #include <string>
 #include <vector>
 
+#include "loss_kernels.h"
 #include "muon.h"
 #include "muon_internal.h"
 
@@ -39,6 +40,7 @@ struct muon_ctx {
   // polls (a microsecond or so each) before a slice of a row stops waiting for
   // its neighbours and computes their pairs itself (loss.hip)
   int loss_spin = 1 << 14;
+  Exchange exchange;
   // timing
   bool timing = false;
   uint32_t tmask = (1u << MUON_K_COUNT) - 1;  // classes that record events

@@ -193,11 +193,11 @@ def test_workspace_sizes():
     bf, f32 = torch.bfloat16, torch.float32
     assert loss_workspace_bytes(-1, 4, 100) == 0 and loss_workspace_bytes(1 << 20, 1 << 20, 100) == 0
     assert loss_workspace_bytes(2, 4, 0) == 0 and loss_workspace_bytes(2, 4, 100, torch.float16) == 0
-    # per token two floats, a double and three floats, a word for each slice of
-    # at most 2560 pieces of 16 bytes; per sequence a double
+    # per token two floats, a double and two words, a word for each slice of
+    # at most 2560 pieces of 16 bytes; per sequence a double, per pair three
     for dtype, slices in ((bf, 8), (f32, 15)):
-        need = 4096 * (8 + 8 + 12 + 8 * slices) + 8 * 5 + 24 * 64
-        assert need <= loss_workspace_bytes(4, 1024, 151936, dtype) <= need + 6 * 256
+        need = 4096 * (8 + 8 + 16 + 8 * slices) + 8 * 5 + 24 * 2 + 24 * 64
+        assert need <= loss_workspace_bytes(4, 1024, 151936, dtype) <= need + 7 * 256
     assert loss_workspace_bytes(0, 0, 100) > 0
     # one double per chunk of 8192 elements, and 32 more
     t, n = tensors((0x10000, 1 << 30, MUON_BF16))
