@@ -44,7 +44,12 @@ class MuonStep:
                  cap_kind: str = "full", ns_steps: int = 5, keep_bf16_weights: bool = False,
                  weight_decay: float = 0.0, scale: float = 1.0, ns_method: str = "quintic",
                  ns_coeffs=None, norms_from_momentum: bool = True, ns_fuse: str = "auto",
-                 inflight: int = 1):
+                 inflight: int = 1, max_grad_norm: Optional[float] = None):
+        """max_grad_norm: clip the gradient to this global norm (None: not at
+        all).  The norm is taken at the start of a step, over the flat gradient
+        and what step() is given beside it, and its coefficient multiplies the
+        gradient inside the momentum pass; `grad_norm` (float64 {sum of
+        squares, norm, coefficient} on the device) holds the last step's."""
         if inflight < 1:
             raise ValueError("inflight must be >= 1")
         self.inflight = inflight
@@ -70,7 +75,14 @@ class MuonStep:
         self.numel = self.plan.total_elems
         self.max_bucket = max((b.numel for b in self.plan.buckets), default=0)
         self.norms_from_momentum = norms_from_momentum
-        self.ctx = Context(self.device, self.plan.max_workspace)
+        self.max_grad_norm, self.grad_norm = max_grad_norm, None
+        workspace = self.plan.max_workspace
+        if max_grad_norm is not None:
+            # partial sums of the norm: 8 bytes per 2048 elements at most, and
+            # as much again (and 64 KB) for gradients that are not the step's own
+            workspace = max(workspace, 16 * (self.numel // 2048 + 64) + (1 << 16))
+            self.grad_norm = torch.zeros(3, dtype=torch.float64, device=self.device)
+        self.ctx = Context(self.device, workspace)
         self._alloc_state(grad_dtype, keep_bf16_weights)
 
     def _alloc_state(self, grad_dtype: torch.dtype, keep_bf16_weights: bool):
@@ -88,6 +100,7 @@ class MuonStep:
             sq = torch.empty(max(sq_blocks(self.max_bucket), 1), dtype=torch.float64, device=dev)
             self.lanes.append((ctx, upd, sq, self._bucket_work(upd)))
         _, self.update, self.sq, self._work = self.lanes[0]
+        self._grad_list = self.ctx.tensor_list([self.grad]) if self.grad_norm is not None else None
         self._side = [torch.cuda.Stream(dev) for _ in range(self.inflight - 1)]
         self._ev_start = torch.cuda.Event()
         self._ev_end = [torch.cuda.Event() for _ in self._side]
@@ -146,7 +159,8 @@ class MuonStep:
 
     def momentum_only(self, stream=None):
         """Momentum update of every matrix, without Newton-Schulz or apply
-        (used to pre-fill momentum); the update output is discarded."""
+        (used to pre-fill momentum; no clipping); the update output is
+        discarded."""
         for lo, hi, _, _ in self._work:
             self.ctx.momentum_update(self.grad[lo:hi], self.momentum[lo:hi], self.update[:hi - lo],
                                      self.beta, self.nesterov, stream)
@@ -156,7 +170,7 @@ class MuonStep:
         micro-bucket whose update buffer `upd` is laid out as in _bucket_work."""
         ctx = ctx if ctx is not None else self.ctx
         ctx.momentum_update(grad, momentum, upd, self.beta, self.nesterov, stream,
-                            sq_partials=sq if want_sq else None)
+                            sq_partials=sq if want_sq else None, grad_scale=self.grad_norm)
         self._run_nsa(upd, sq, groups, master, wb, stream, flag, ctx)
 
     def _run_nsa(self, upd, sq, groups, master, wb, stream, flag, ctx=None):
@@ -167,7 +181,7 @@ class MuonStep:
                               sq=(sq, upd) if whole else None)
         ctx.apply(master, upd, self.lr, self.scale, self.weight_decay, wb, stream)
 
-    def capture(self, nonfinite_flag: Optional[torch.Tensor] = None) -> "torch.cuda.CUDAGraph":
+    def capture(self, nonfinite_flag: Optional[torch.Tensor] = None, other_grads=None) -> "torch.cuda.CUDAGraph":
         """Record one whole step, every lane's launches included, into a HIP
         graph (stream capture through torch.cuda.CUDAGraph); replay() then
         runs it with no host work per launch.  Recording runs nothing.  The
@@ -180,7 +194,7 @@ class MuonStep:
         side = torch.cuda.Stream(self.device)
         side.wait_stream(cur)
         with torch.cuda.graph(g, stream=side):
-            self.step(stream=side, nonfinite_flag=nonfinite_flag)
+            self.step(stream=side, nonfinite_flag=nonfinite_flag, other_grads=other_grads)
         cur.wait_stream(side)
         self._graph = g
         return g
@@ -196,8 +210,20 @@ class MuonStep:
         """The lanes' contexts (per-kernel timing is kept per context)."""
         return [lane[0] for lane in self.lanes]
 
-    def step(self, stream=None, nonfinite_flag: Optional[torch.Tensor] = None):
+    def step(self, stream=None, nonfinite_flag: Optional[torch.Tensor] = None, other_grads=None):
+        """One step.  With max_grad_norm, `other_grads` (a sequence of tensors
+        or a TensorList) are gradients of parameters that another optimizer
+        steps: they enter the norm and are scaled in place."""
         main = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if self.grad_norm is not None:
+            if other_grads is None:
+                self.ctx.grad_norm(self._grad_list, self.grad_norm, self.max_grad_norm, stream=main)
+            else:
+                others = getattr(other_grads, "tensors", other_grads)
+                self.ctx.grad_norm([self.grad, *others], self.grad_norm, self.max_grad_norm, stream=main)
+                self.ctx.scale_grads(other_grads, self.grad_norm, stream=main)
+        elif other_grads is not None:
+            raise ValueError("other_grads needs max_grad_norm")
         if self._side:
             self._ev_start.record(main)
             for sd in self._side:

@@ -121,6 +121,8 @@ class MuonOffloadStep(MuonStep):
         self.pin = pin
         self.grads_on_host, self.update_to_host = grads_on_host, update_to_host
         self.timing = timing
+        if kw.get("max_grad_norm") is not None:
+            raise ValueError("clipping needs the whole gradient on the device before the step (use MuonStep)")
         super().__init__(shapes, device, inflight=inflight, **kw)
 
     def _alloc_state(self, grad_dtype: torch.dtype, keep_bf16_weights: bool):
