@@ -415,12 +415,14 @@ typedef struct {
  *     log-probability is 0 and its gradient row is zeros.  A label >= vocab
  *     names no score: the token's log-probability and gradient are NaN.
  *   - z = x / temperature are the scores that the softmax sees; temperature
- *     > 0 and finite.  Scores of -infinity have probability 0; a row of
+ *     in (1e-30, 1e30).  Scores of -infinity have probability 0; a row of
  *     nothing else, or with NaN or +infinity in it, gives NaN, as the formula
  *     does.
- *   - Sums over a vocabulary run in fp32 in a fixed order around the row's
- *     maximum; log-probabilities are formed, and everything per token or
- *     sequence summed, in binary64 and rounded to fp32 once when stored.
+ *   - Sums over a vocabulary run in a fixed order around the row's maximum:
+ *     fp32 exponentials, added in fp32 by fours (fp32 scores) or eights (bf16)
+ *     and in binary64 beyond, so that small log-probabilities keep their
+ *     relative accuracy too.  Log-probabilities are formed, and everything per
+ *     token or sequence summed, in binary64 and rounded to fp32 when stored.
  *     Two calls on identical inputs, rows at the same alignment to 16 bytes,
  *     give identical bits.
  *   - Gradients are of `weight` times the loss with respect to x and have
@@ -443,17 +445,17 @@ size_t muon_loss_workspace_bytes(int64_t batch, int64_t seq, int64_t vocab, int3
 
 /* Log-probability of every token: logps[t] = z[y] - log sum_v exp(z[v]).
  * logps: fp32 per token.  row_stats (may be NULL): two floats per token, the
- * row's maximum score and its sum of exponentials around it, which
+ * row's maximum score and its sum of exponentials around it less 1, which
  * muon_token_logps_backward takes. */
 muon_status_t muon_token_logps(muon_ctx_t* ctx, void* stream, const muon_logits_t* logits,
-                               const int64_t* labels, float temperature, float* logps,
+                               const int64_t* labels, double temperature, float* logps,
                                float* row_stats);
 
 /* Its gradient: grad_logits[t][v] = grad_logps[t] / temperature *
  * ([v = y] - exp(z[v]) / sum).  logits, labels, temperature as given to
  * muon_token_logps, row_stats as it left them. */
 muon_status_t muon_token_logps_backward(muon_ctx_t* ctx, void* stream, const muon_logits_t* logits,
-                                        const int64_t* labels, float temperature,
+                                        const int64_t* labels, double temperature,
                                         const float* row_stats, const float* grad_logps,
                                         const muon_logits_t* grad_logits);
 
@@ -469,9 +471,9 @@ typedef enum {
 } muon_reduce_t;
 
 typedef struct {
+  double temperature;
   float clip_low, clip_high;     /* ratio range [1 - clip_low, 1 + clip_high]; in [0, 1], >= 0 */
   float kl_coef;                 /* >= 0; > 0 needs ref_logps */
-  float temperature;
   float weight;                  /* factor of loss and gradient, e.g. 1 / accumulation steps */
   int32_t reduce;                /* muon_reduce_t */
   int32_t advantage_per_token;   /* advantages: 0 = [batch], 1 = per token */
@@ -499,9 +501,9 @@ muon_status_t muon_policy_loss(muon_ctx_t* ctx, void* stream, const muon_logits_
 typedef enum { MUON_PREFERENCE_SIGMOID = 0, MUON_PREFERENCE_IPO = 1 } muon_preference_t;
 
 typedef struct {
+  double temperature;
   float beta;             /* > 0 */
   float label_smoothing;  /* s, in [0, 0.5]; sigmoid only (else 0) */
-  float temperature;
   float weight;           /* factor of loss and gradient */
   int32_t kind;           /* muon_preference_t */
   int32_t average;        /* 0: a sequence's score is the sum over its tokens, 1: the mean */

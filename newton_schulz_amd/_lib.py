@@ -58,13 +58,13 @@ class Logits(ctypes.Structure):
 
 
 class PolicyParams(ctypes.Structure):
-    _fields_ = [("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float), ("kl_coef", ctypes.c_float),
-                ("temperature", ctypes.c_float), ("weight", ctypes.c_float), ("reduce", ctypes.c_int32),
+    _fields_ = [("temperature", ctypes.c_double), ("clip_low", ctypes.c_float), ("clip_high", ctypes.c_float),
+                ("kl_coef", ctypes.c_float), ("weight", ctypes.c_float), ("reduce", ctypes.c_int32),
                 ("advantage_per_token", ctypes.c_int32)]
 
 
 class PreferenceParams(ctypes.Structure):
-    _fields_ = [("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float), ("temperature", ctypes.c_float),
+    _fields_ = [("temperature", ctypes.c_double), ("beta", ctypes.c_float), ("label_smoothing", ctypes.c_float),
                 ("weight", ctypes.c_float), ("kind", ctypes.c_int32), ("average", ctypes.c_int32)]
 
 
@@ -118,8 +118,8 @@ def load() -> ctypes.CDLL:
         "muon_noalloc_last_error": (ctypes.c_char_p, []),
         "muon_loss_workspace_bytes": (sz, [i64, i64, i64, i32]),
         "muon_loss_set_polls": (i32, [vp, i32]),
-        "muon_token_logps": (i32, [vp, vp, P(Logits), vp, f32, vp, vp]),
-        "muon_token_logps_backward": (i32, [vp, vp, P(Logits), vp, f32, vp, vp, P(Logits)]),
+        "muon_token_logps": (i32, [vp, vp, P(Logits), vp, f64, vp, vp]),
+        "muon_token_logps_backward": (i32, [vp, vp, P(Logits), vp, f64, vp, vp, P(Logits)]),
         "muon_policy_loss": (i32, [vp, vp, P(Logits), vp, P(PolicyParams), vp, vp, vp, vp, vp, P(Logits)]),
         "muon_preference_loss": (i32, [vp, vp, P(Logits), vp, P(PreferenceParams), vp, vp, vp, vp, P(Logits)]),
         "muon_grad_norm_workspace_bytes": (sz, [P(Tensor), i64]),

@@ -381,7 +381,7 @@ class Context:
         # 2-D logits are one sequence of rows
         sequences = (x.batch,)
         per_token = advantages.shape != sequences
-        p = PolicyParams(clip_low, clip_high, kl_coef, temperature, weight, LOSS_REDUCE[reduce], 1 if per_token else 0)
+        p = PolicyParams(temperature, clip_low, clip_high, kl_coef, weight, LOSS_REDUCE[reduce], 1 if per_token else 0)
         st = self.lib.muon_policy_loss(
             self.handle, _stream(self.device, stream), ctypes.byref(x),
             _tokens(labels, "labels", shape, torch.int64, self.device), ctypes.byref(p),
@@ -409,7 +409,7 @@ class Context:
         gx = self._grad(logits, grad_logits)
         if kind not in PREFERENCE_KINDS:
             raise ValueError(f"unknown preference loss {kind!r}; one of {list(PREFERENCE_KINDS)}")
-        p = PreferenceParams(beta, label_smoothing, temperature, weight, PREFERENCE_KINDS[kind], 1 if average else 0)
+        p = PreferenceParams(temperature, beta, label_smoothing, weight, PREFERENCE_KINDS[kind], 1 if average else 0)
         st = self.lib.muon_preference_loss(
             self.handle, _stream(self.device, stream), ctypes.byref(x),
             _tokens(labels, "labels", shape, torch.int64, self.device), ctypes.byref(p),

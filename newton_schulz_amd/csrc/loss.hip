@@ -8,27 +8,34 @@
 // has seen, and a larger maximum m' turns s into s exp(m - m').  Partial pairs
 // join the same way, in a fixed order.
 //
-// Arithmetic.  Scores are widened to fp32; with k = log2 e / T and a reference
-// m, exp(z - m / T) is exp2(x k - c), c = m k rounded: one fused multiply-add
-// and one exponential.  The rounding of c is the same in S, in the gradient
-// and in the log-probability (x_y k - c - log2 S, in binary64: what follows
-// takes differences of two of them), so it cancels.  The reference is a
-// running maximum; it is raised, and s scaled, only when some lane of the wave
-// has met a larger score (rescaling at every piece took 10% more VALU cycles).
+// Arithmetic.  Scores are widened to fp32; with k = log2 e / T rounded,
+// exp(z - m / T) is exp2((x - m) k): the subtraction is exact for bf16, nothing
+// large cancels at any magnitude of x, and the largest score gives exactly 1.
+// (The rounding of k moves every log-probability by up to 1e-7, the same way.  A
+// second multiply-add with the rest of k would take that away; it costs scoring
+// 6%: 2044 x 151936 bf16 in 97 us, 91 without.)
+// m is a running maximum; it is raised, and s scaled, only when some lane of
+// the wave has met a larger score (rescaling at every piece took 10% more VALU
+// cycles).  It starts at the lowest finite number, so that a masked score
+// (-infinity) gives 0 and a row of nothing but the lowest number is uniform.
 //
-// c has to stay finite and -infinity (a masked score) must give 0, so the
-// reference starts at -1e30 instead of -infinity.  Rows whose maximum is not
-// inside (-1e30, 1e30) -- nothing but masks of the type's lowest value or of
-// -infinity, +infinity, values near the type's limit -- are done again as
-// exp2((x - m) k) with the exact maximum (far_row), where no large terms
-// cancel at any magnitude.
+// A token that the policy is sure of has S = 1 + u with a small u, and lp = -u
+// to first order: rounding S to fp32 would leave lp with an error of 2^-24
+// whatever its size.  So the 8 exponentials of a piece are added pairwise in
+// fp32 and everything beyond in binary64, and what is stored of S is u = S - 1.
+// The label's own gradient is G (1 - p) = -G expm1(lp).
+//
+// The gradient takes p as exp2(x k - c) / S with c = m k rounded, one fused
+// multiply-add a score; the rounding of c (far below 1 where |c| < 2^16) goes
+// into the factor that p is multiplied by anyway.  Rows of larger |c| take
+// exp2((x - m) k) there too.
 //
 // Shape of the kernels.  All are bound by HBM (a pass that only reads reaches
 // 6.1-6.3 TB/s on MI355X, one that reads and writes alike 5.7-6.0), and HBM is
 // fastest when the workgroups in flight cover a compact, moving window of
 // addresses: copying in 16 KB pieces per workgroup reaches 6.0 TB/s, in 300 KB
-// rows per workgroup 4.9.  So a row is cut into slices, one workgroup of 256 threads each, in address order; a slice is held
-// in registers.
+// rows per workgroup 4.9.  So a row is cut into slices, one workgroup of 256
+// threads each, in address order; a slice is held in registers.
 #include <algorithm>
 #include <cfloat>
 
@@ -39,9 +46,7 @@ using muon::bf16_t;
 
 namespace {
 
-constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLowest = -FLT_MAX;
-constexpr float kFar = 1e30f;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef u32x4 u32x4_any __attribute__((aligned(2)));  // 16 bytes at an element's alignment
@@ -116,93 +121,127 @@ template <typename T> __device__ __forceinline__ T* row_at(const RowsRef& x, int
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-// exp2(x k - c), c = m k.
-__device__ __forceinline__ float exp_at(float x, float k, float c) { return exp2_fast(__builtin_fmaf(x, k, -c)); }
-
-// Whether a row of maximum m takes the exact form, exp2((x - m) k).
-__device__ __forceinline__ bool far_row(float m, float k) { return !(fabsf(m) < kFar) || k > 1e6f; }
-
 // (m, s) joined with (mo, so).
-template <bool EXACT = false>
-__device__ __forceinline__ void join(float& m, float& s, float mo, float so, float k) {
+__device__ __forceinline__ void join(float& m, double& s, float mo, double so, float k) {
   const float mn = fmaxf(m, mo);
-  if (EXACT) s = s * exp2_fast((m - mn) * k) + so * exp2_fast((mo - mn) * k);
-  else s = s * exp2_fast(m * k - mn * k) + so * exp2_fast(mo * k - mn * k);
+  s = s * static_cast<double>(exp2_fast((m - mn) * k)) + so * static_cast<double>(exp2_fast((mo - mn) * k));
   m = mn;
 }
 
 // The pair of N neighbouring lanes, in each of them (the two terms of a join
 // commute, so both partners form the same sum).
-template <int N = 64, bool EXACT = false> __device__ __forceinline__ void wave_join(float& m, float& s, float k) {
+template <int N = 64> __device__ __forceinline__ void wave_join(float& m, double& s, float k) {
 #pragma unroll
-  for (int d = N / 2; d > 0; d >>= 1) join<EXACT>(m, s, __shfl_xor(m, d, 64), __shfl_xor(s, d, 64), k);
+  for (int d = N / 2; d > 0; d >>= 1) join(m, s, __shfl_xor(m, d, 64), __shfl_xor(s, d, 64), k);
 }
 
 // The pair of all threads of the workgroup, in every thread.
-template <int NT, bool EXACT = false> __device__ __forceinline__ void block_join(float& m, float& s, float k) {
+template <int NT> __device__ __forceinline__ void block_join(float& m, double& s, float k) {
   constexpr int W = NT / 64;
-  __shared__ float2 wave[W];
-  wave_join<64, EXACT>(m, s, k);
+  __shared__ float wave_m[W];
+  __shared__ double wave_s[W];
+  wave_join(m, s, k);
   __syncthreads();  // an earlier call's values have been read
-  if ((threadIdx.x & 63) == 0) wave[threadIdx.x >> 6] = make_float2(m, s);
+  if ((threadIdx.x & 63) == 0) {
+    wave_m[threadIdx.x >> 6] = m;
+    wave_s[threadIdx.x >> 6] = s;
+  }
   __syncthreads();
-  const float2 q = wave[threadIdx.x & (W - 1)];
-  m = q.x;
-  s = q.y;
-  wave_join<W, EXACT>(m, s, k);
+  m = wave_m[threadIdx.x & (W - 1)];
+  s = wave_s[threadIdx.x & (W - 1)];
+  wave_join<W>(m, s, k);
 }
 
-// (m, s) with one more score, in the exact form.
-__device__ __forceinline__ void take_exact(float v, float& m, float& s, float k) {
-  const float mn = fmaxf(m, v);
-  s = s * exp2_fast((m - mn) * k) + exp2_fast((v - mn) * k);
-  m = mn;
-}
-
-// (m, s) with more scores; c = m k.
-template <int N> __device__ __forceinline__ void take_scores(const float (&v)[N], float& m, float& c, float& s, float k) {
+// (m, s) with N = 1, 4 or 8 more scores.
+template <int N> __device__ __forceinline__ void take_scores(const float (&v)[N], float& m, double& s, float k) {
   float mn = m;
 #pragma unroll
   for (int i = 0; i < N; ++i) mn = fmaxf(mn, v[i]);
   if (__any(mn > m)) {
-    const float cn = mn * k;
-    s *= exp2_fast(c - cn);
+    s *= static_cast<double>(exp2_fast((m - mn) * k));
     m = mn;
-    c = cn;
     asm volatile("" : "+v"(s));  // stays a branch
   }
+  float e[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) s += exp_at(v[i], k, c);
+  for (int i = 0; i < N; ++i) e[i] = exp2_fast((v[i] - m) * k);
+#pragma unroll
+  for (int w = N / 2; w > 0; w /= 2)
+#pragma unroll
+    for (int i = 0; i < w; ++i) e[i] += e[i + w];
+  s += static_cast<double>(e[0]);
 }
-template <typename T> __device__ __forceinline__ void take_piece(u32x4 w, float& m, float& c, float& s, float k) {
+template <typename T> __device__ __forceinline__ void take_piece(u32x4 w, float& m, double& s, float k) {
   float v[kVec<T>];
   Scores<T>::unpack(w, v);
-  take_scores(v, m, c, s, k);
+  take_scores(v, m, s, k);
 }
 
-// lp of score xy in a row of pair (m, s).  log2 S = e + log2 f, S = 2^e f
-// with f in [1/2, 1): the large part is exact, so the absolute error is that
-// of log2 f, below 2^-23, at any S.
-__device__ __forceinline__ double token_lp(float xy, float m, float s, float k) {
+// log s to a few units of binary64, also next to 1: s = 2^e f with f in [3/4,
+// 3/2), log f = 2 (t + t^3 / 3 + ...), t = (f - 1) / (f + 1), |t| <= 1/5.
+__device__ __forceinline__ double log_sum(double s) {
+  if (!(s > 0.0)) return s == 0.0 ? -static_cast<double>(INFINITY) : s;  // no score left, or NaN
   int e = 0;
-  const float f = frexpf(s, &e);
-  const double log2s = static_cast<double>(e) + static_cast<double>(__builtin_amdgcn_logf(f));
-  const double kd = static_cast<double>(k);
-  const double z = far_row(m, k) ? static_cast<double>(xy - m) * kd
-                                 : static_cast<double>(xy) * kd - static_cast<double>(m * k);
-  return (z - log2s) * 0.69314718055994530942;
+  double f = frexp(s, &e);
+  if (f < 0.75) {
+    f *= 2.0;
+    --e;
+  }
+  const double t = (f - 1.0) / (f + 1.0), q = t * t;
+  double r = 1.0 / 19.0;
+  r = r * q + 1.0 / 17.0;
+  r = r * q + 1.0 / 15.0;
+  r = r * q + 1.0 / 13.0;
+  r = r * q + 1.0 / 11.0;
+  r = r * q + 1.0 / 9.0;
+  r = r * q + 1.0 / 7.0;
+  r = r * q + 1.0 / 5.0;
+  r = r * q + 1.0 / 3.0;
+  r = r * q + 1.0;
+  return static_cast<double>(e) * 0.69314718055994530942 + 2.0 * t * r;
+}
+
+// lp of score xy in a row of pair (m, s).
+__device__ __forceinline__ double token_lp(const LossArgs& a, float xy, float m, double s) {
+  return (static_cast<double>(xy) - static_cast<double>(m)) * a.inv_t - log_sum(s);
 }
 
 // What the row's pair and the label's score make of token r (one thread).
-__device__ __forceinline__ double finish_row(const LossArgs& a, int r, int64_t y, float xy, float m, float s) {
+__device__ __forceinline__ double finish_row(const LossArgs& a, int r, int64_t y, float xy, float m, double s) {
   double lp = 0.0;
   if (y >= a.vocab) lp = __longlong_as_double(0x7ff8000000000000ll);
-  else if (y >= 0) lp = token_lp(xy, m, s, kLog2e / a.temperature);
+  else if (y >= 0) lp = token_lp(a, xy, m, s);
   if (a.lp) a.lp[r] = lp;
   if (a.logps) a.logps[r] = static_cast<float>(lp);
-  if (a.stats) a.stats[r] = make_float2(m, s);
+  if (a.stats) a.stats[r] = make_float2(m, static_cast<float>(s - 1.0));
   return lp;
 }
+
+// The gradient of a row's scores: scale * p for every score, p = exp2(x k - c)
+// or, far, exp2((x - m) k).
+struct RowGrad {
+  float scale, c, m;
+  bool far;
+  __device__ __forceinline__ float at(float x, float k) const {
+    return scale * exp2_fast(far ? (x - m) * k : __builtin_fmaf(x, k, -c));
+  }
+};
+__device__ __forceinline__ RowGrad row_grad(float G, float m, float u, float k) {
+  RowGrad g;
+  g.m = m;
+  g.c = m * k;
+  g.far = !(fabsf(g.c) < 65536.0f);
+  g.scale = -G / (1.0f + u);
+  if (!g.far) {
+    // exp2(x k - c) is 2^d times what it should be, d = m k - c (exact, below
+    // 2^-8): 2^-d = 1 - h + h^2 / 2, h = d log 2
+    const float h = __builtin_fmaf(m, k, -g.c) * 0.69314718f;
+    g.scale *= 1.0f - h * (1.0f - 0.5f * h);
+  }
+  return g;
+}
+// The label's own gradient.
+__device__ __forceinline__ float label_grad(float G, double lp) { return -G * expm1f(static_cast<float>(lp)); }
 
 // ---------------------------------------------------------------------------
 // slices of a row
@@ -222,49 +261,23 @@ __device__ __forceinline__ Slice slice_of(const RowShape& sh, int slices, int j)
   return {first, min(per, sh.full - first)};
 }
 
-// The pair of one slice of a far row, in every thread.
-template <typename T>
-__device__ __forceinline__ void far_slice(const T* row, const RowShape& sh, Slice sl, bool edges, float k, float& m,
-                                          float& s) {
-  m = kLowest;
-  s = 0.0f;
-  const T* x = row + sh.head + static_cast<int64_t>(sl.first) * kVec<T>;
-#pragma unroll 1
-  for (int e = threadIdx.x; e < sl.count * kVec<T>; e += kThreads) take_exact(muon::Elem<T>::load(x + e), m, s, k);
-  if (edges && static_cast<int>(threadIdx.x) < sh.edges)
-    take_exact(muon::Elem<T>::load(row + edge_score<T>(sh, threadIdx.x)), m, s, k);
-  block_join<kThreads, true>(m, s, k);
-}
-
 // The pair of slice j read from memory, in every thread: the sums of
 // slice_kernel in its order, so the same bits.
 template <typename T>
 __device__ __forceinline__ void slice_pair(const T* row, const RowShape& sh, int slices, int j, float k, float& m,
-                                           float& s) {
+                                           double& s) {
   const Slice sl = slice_of(sh, slices, j);
   const u32x4* body = reinterpret_cast<const u32x4*>(row + sh.head) + sl.first;
   const int t = static_cast<int>(threadIdx.x);
-  float c = -kFar * k;
-  m = -kFar;
-  s = 0.0f;
+  m = kLowest;
+  s = 0.0;
 #pragma unroll 1
-  for (int q = t; q < sl.count; q += kThreads) take_piece<T>(body[q], m, c, s, k);
+  for (int q = t; q < sl.count; q += kThreads) take_piece<T>(body[q], m, s, k);
   if (j == 0 && t < sh.edges) {
     const float v[1] = {muon::Elem<T>::load(row + edge_score<T>(sh, t))};
-    take_scores(v, m, c, s, k);
+    take_scores(v, m, s, k);
   }
   block_join<kThreads>(m, s, k);
-  if (far_row(m, k)) far_slice(row, sh, sl, j == 0, k, m, s);
-}
-
-// The pair of a row from those of its slices, one in each of N lanes (lanes
-// without one hold (-kFar, 0)), in each of them.
-template <int N> __device__ __forceinline__ void join_slices(float& m, float& s, float k) {
-  float top = m;
-#pragma unroll
-  for (int d = N / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, 64));
-  if (far_row(top, k)) wave_join<N, true>(m, s, k);
-  else wave_join<N>(m, s, k);
 }
 
 // Exchange between the workgroups of one launch.  What is exchanged goes
@@ -287,12 +300,19 @@ __device__ __forceinline__ unsigned arrive(unsigned* count) {
   return before;
 }
 
-// Two numbers as one 64-bit word; of a slice's pair never 0 (S is 0 only where m is far).
-__device__ __forceinline__ uint64_t pair_word(float m, float s) {
-  return (static_cast<uint64_t>(__float_as_uint(s)) << 32) | __float_as_uint(m);
+// Two numbers as one 64-bit word.
+__device__ __forceinline__ uint64_t word_of(float lo, float hi) {
+  return (static_cast<uint64_t>(__float_as_uint(hi)) << 32) | __float_as_uint(lo);
 }
-__device__ __forceinline__ float word_max(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w)); }
-__device__ __forceinline__ float word_sum(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w >> 32)); }
+__device__ __forceinline__ float word_lo(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w)); }
+__device__ __forceinline__ float word_hi(uint64_t w) { return __uint_as_float(static_cast<uint32_t>(w >> 32)); }
+
+// A pair as a word that is never 0: m (a zero with its sign set) and s - 1.
+__device__ __forceinline__ uint64_t pair_word(float m, double s) {
+  return word_of(m == 0.0f ? -0.0f : m, static_cast<float>(s - 1.0));
+}
+__device__ __forceinline__ float word_max(uint64_t w) { return word_lo(w); }
+__device__ __forceinline__ double word_sum(uint64_t w) { return 1.0 + static_cast<double>(word_hi(w)); }
 
 // max(a, b) that hands a NaN on, as the formula does.
 __device__ __forceinline__ float max_nan(float a, float b) { return (a > b || a != a) ? a : b; }
@@ -422,9 +442,9 @@ template <int NT> __device__ __forceinline__ void sum_terms(const PolicyArgs& p,
     if (p.labels[i] < 0) continue;
     const double w = word_weight(published(p.weights + (p.p.reduce == MUON_REDUCE_SEQUENCE ? i / p.seq : 0)));
     const uint64_t term = published(p.terms + 2 * i), clipped = published(p.terms + 2 * i + 1);
-    v[0] += w * static_cast<double>(word_max(term));
-    v[1] += w * static_cast<double>(word_sum(term));
-    v[2] += w * static_cast<double>(word_max(clipped));
+    v[0] += w * static_cast<double>(word_lo(term));
+    v[1] += w * static_cast<double>(word_hi(term));
+    v[2] += w * static_cast<double>(word_lo(clipped));
   }
   block_totals<NT>(v);
 }
@@ -474,7 +494,7 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
   const RowShape sh = row_shape(row, a.vocab);
   const Slice sl = slice_of(sh, a.slices, j);
   const bool edge = j == 0 && t < sh.edges;
-  const float k = kLog2e / a.temperature;
+  const float k = a.k;
   T* out = USE == USE_POLICY ? row_at<T>(grad, r, a.seq) : nullptr;
   // the gradient's rows have an alignment of their own
   u32x4_any* obody = USE == USE_POLICY ? reinterpret_cast<u32x4_any*>(out + sh.head) + sl.first : nullptr;
@@ -487,7 +507,7 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
     }
     if (j == 0 && t == 0) {
       if (USE == USE_POLICY && a.logps) a.logps[r] = 0.0f;
-      if (USE == USE_STATS && a.slices == 1) finish_row(a, r, y, 0.0f, 0.0f, 1.0f);
+      if (USE == USE_STATS && a.slices == 1) finish_row(a, r, y, 0.0f, 0.0f, 1.0);
     }
     return;
   }
@@ -505,7 +525,8 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
   const bool named = y < a.vocab;
   float xy = 0.0f;
   if (USE == USE_POLICY || j == 0) xy = muon::Elem<T>::load(row + (named ? y : 0));
-  float m = -kFar, c = m * k, s = 0.0f;
+  float m = kLowest;
+  double s = 0.0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     // A piece is unpacked where it is used and never earlier, and its
@@ -513,16 +534,15 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
     // knows the piece may have changed just before and the sum is read just
     // after, so it keeps 4 registers a piece and not 8 more of widened scores.
     asm volatile("" : "+v"(w[i]));
-    take_piece<T>(w[i], m, c, s, k);
+    take_piece<T>(w[i], m, s, k);
     asm volatile("" : "+v"(s));
   }
   if (wave == 0) {  // threads without an edge hold -infinity
     const float v[1] = {we};
-    take_scores(v, m, c, s, k);
+    take_scores(v, m, s, k);
   }
   if (USE == USE_POLICY) asm volatile("" : "+v"(xy));  // read before this slice is published
   block_join<kThreads>(m, s, k);
-  if (far_row(m, k)) far_slice(row, sh, sl, j == 0, k, m, s);
   if (USE == USE_STATS) {
     if (t == 0) {
       if (a.slices == 1) finish_row(a, r, y, xy, m, s);
@@ -531,26 +551,26 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
     }
     return;
   }
-  __shared__ float coef[4];
+  __shared__ RowGrad coef;
+  __shared__ float own_grad;
   __shared__ uint64_t missing, own[64];
   constexpr int kWeightLane = 63;  // (a row has at most 60 slices)
   // wave 0: the row's pair from a slice's word in each lane, and what follows
   auto settle = [&](uint64_t word) {
     const double wt = word_weight(__shfl(word, kWeightLane, 64));
-    m = lane < a.slices ? word_max(word) : -kFar;
-    s = lane < a.slices ? word_sum(word) : 0.0f;
-    join_slices<64>(m, s, k);
-    double lp = token_lp(xy, m, s, k);
+    m = lane < a.slices ? word_max(word) : kLowest;
+    s = lane < a.slices ? word_sum(word) : 0.0;
+    wave_join(m, s, k);
+    double lp = token_lp(a, xy, m, s);
     if (!named) lp = __longlong_as_double(0x7ff8000000000000ll);
     const TokenTerms o = policy_token(p, r, b, lp);
-    const float G = static_cast<float>(static_cast<double>(p.p.weight) * wt * static_cast<double>(o.g)) / a.temperature;
+    const float G = static_cast<float>(static_cast<double>(p.p.weight) * wt * static_cast<double>(o.g) * a.inv_t);
     if (lane == 0) {
-      coef[0] = m;
-      coef[1] = -G / s;
-      coef[2] = G;
+      coef = row_grad(G, m, static_cast<float>(s - 1.0), k);
+      own_grad = label_grad(G, lp);
       if (j == 0) {
         if (a.logps) a.logps[r] = static_cast<float>(lp);
-        publish(p.terms + 2 * static_cast<int64_t>(r), pair_word(o.pg, o.kl));
+        publish(p.terms + 2 * static_cast<int64_t>(r), word_of(o.pg, o.kl));
         publish(p.terms + 2 * static_cast<int64_t>(r) + 1, __float_as_uint(o.clipped));
       }
     }
@@ -580,7 +600,8 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
   if (const uint64_t lack = missing) {
     for (int i = 0; i < a.slices; ++i) {
       if (!((lack >> i) & 1)) continue;
-      float mi, si;
+      float mi;
+      double si;
       slice_pair(row, sh, a.slices, i, k, mi, si);
       if (t == 0) {
         const uint64_t v = published(slot + i);
@@ -596,31 +617,29 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
     __syncthreads();
   }
   if (grad.base == nullptr) return;
-  const float M = coef[0], scale = coef[1], G = coef[2], C = M * k;
-  const bool far = far_row(M, k);
+  const RowGrad g = coef;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     float v[kVec<T>];
     asm volatile("" : "+v"(w[i]));
     Scores<T>::unpack(w[i], v);
-    if (far) {
+    if (g.far) {
 #pragma unroll
-      for (int e = 0; e < kVec<T>; ++e) v[e] = scale * exp2_fast((v[e] - M) * k);
+      for (int e = 0; e < kVec<T>; ++e) v[e] = g.scale * exp2_fast((v[e] - g.m) * k);
     } else {
 #pragma unroll
-      for (int e = 0; e < kVec<T>; ++e) v[e] = scale * exp_at(v[e], k, C);
+      for (int e = 0; e < kVec<T>; ++e) v[e] = g.scale * exp2_fast(__builtin_fmaf(v[e], k, -g.c));
     }
     if (t < sl.count - i * kThreads)
       __builtin_nontemporal_store(Scores<T>::pack(v), piece_at(obody, i * kThreads, t));
   }
-  auto probability = [&](float x) { return far ? exp2_fast((x - M) * k) : exp_at(x, k, C); };
-  if (edge) muon::Elem<T>::store(out + edge_score<T>(sh, t), scale * probability(we));
+  if (edge) muon::Elem<T>::store(out + edge_score<T>(sh, t), g.at(we, k));
   // the label's score, by the thread whose piece or edge has just gone out
   if (named) {
     const int ly = static_cast<int>(y) - sh.head, q = ly >= 0 ? ly / kVec<T> : -1;
     bool mine = q >= sl.first && q < sl.first + sl.count && (q - sl.first) % kThreads == t;
     if (edge) mine = mine || edge_score<T>(sh, t) == y;
-    if (mine) muon::Elem<T>::store(out + y, scale * probability(xy) + G);
+    if (mine) muon::Elem<T>::store(out + y, own_grad);
   }
 }
 
@@ -648,16 +667,17 @@ __global__ __launch_bounds__(kThreads) void row_join_kernel(LossArgs a) {
   const int r = static_cast<int>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (r >= a.rows) return;
   const int64_t y = a.labels[r];
-  float m = 0.0f, s = 1.0f;
+  float m = 0.0f;
+  double s = 1.0;
   if (y >= 0 && y < a.vocab) {
-    m = -kFar;
-    s = 0.0f;
+    m = kLowest;
+    s = 0.0;
     if (lane < a.slices) {
       const uint64_t v = a.part[static_cast<int64_t>(r) * a.slices + lane];
       m = word_max(v);
       s = word_sum(v);
     }
-    join_slices<64>(m, s, kLog2e / a.temperature);
+    wave_join(m, s, a.k);
   }
   if (lane == 0) finish_row(a, r, y, a.chosen[r], m, s);
 }
@@ -690,12 +710,11 @@ __global__ __launch_bounds__(kThreads) void logits_grad_kernel(LossArgs a, RowsR
     if (edge) muon::Elem<T>::store(out + edge_score<T>(sh, t), 0.0f);
     return;
   }
-  const float k = kLog2e / a.temperature;
+  const float k = a.k;
   const float2 st = a.stats[r];
-  float G = g[per_sequence ? r / a.seq : r] / a.temperature;
+  float G = static_cast<float>(static_cast<double>(g[per_sequence ? r / a.seq : r]) * a.inv_t);
   if (y >= a.vocab) G = __uint_as_float(0x7fc00000u);  // the label names no score
-  const float scale = -G / st.y, c0 = st.x * k;
-  const bool far = far_row(st.x, k);
+  const RowGrad rg = row_grad(G, st.x, st.y, k);
   u32x4 w[kGradUnroll];
 #pragma unroll
   for (int u = 0; u < kGradUnroll; ++u) {
@@ -705,32 +724,34 @@ __global__ __launch_bounds__(kThreads) void logits_grad_kernel(LossArgs a, RowsR
   // the label's place: piece py, score iy of it (no piece when it is an edge)
   const int ly = static_cast<int>(y < a.vocab ? y : 0) - sh.head;
   const int py = ly >= 0 ? ly / kVec<T> : -1, iy = ly - py * kVec<T>;
+  auto own = [&](float xy) {
+    return label_grad(G, token_lp(a, xy, st.x, 1.0 + static_cast<double>(st.y)));
+  };
 #pragma unroll
   for (int u = 0; u < kGradUnroll; ++u) {
     const int p = p0 + u * kThreads;
     if (p >= sh.full) continue;
     float v[kVec<T>];
     Scores<T>::unpack(w[u], v);
-    if (far) {
-#pragma unroll
-      for (int i = 0; i < kVec<T>; ++i) v[i] = scale * exp2_fast((v[i] - st.x) * k);
-    } else {
-#pragma unroll
-      for (int i = 0; i < kVec<T>; ++i) v[i] = scale * exp_at(v[i], k, c0);
-    }
+    float xy = 0.0f;
     if (p == py) {
 #pragma unroll
-      for (int i = 0; i < kVec<T>; ++i)
-        if (i == iy) v[i] += G;
+      for (int i = 0; i < kVec<T>; ++i) xy = i == iy ? v[i] : xy;
+    }
+    if (rg.far) {
+#pragma unroll
+      for (int i = 0; i < kVec<T>; ++i) v[i] = rg.scale * exp2_fast((v[i] - rg.m) * k);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec<T>; ++i) v[i] = rg.scale * exp2_fast(__builtin_fmaf(v[i], k, -rg.c));
     }
     __builtin_nontemporal_store(Scores<T>::pack(v), obody + p);
+    if (p == py && y < a.vocab) muon::Elem<T>::store(out + y, own(xy));
   }
   if (edge) {
     const int e = edge_score<T>(sh, t);
     const float x = muon::Elem<T>::load(row + e);
-    float v = scale * (far ? exp2_fast((x - st.x) * k) : exp_at(x, k, c0));
-    if (e == y) v += G;
-    muon::Elem<T>::store(out + e, v);
+    muon::Elem<T>::store(out + e, e == y ? own(x) : rg.at(x, k));
   }
 }
 
@@ -805,24 +826,20 @@ __device__ __forceinline__ double token_score(const LossArgs& a, const Preferenc
   if (a.slices == 1) {
     lp = a.lp[r];
   } else {
-    const float k = kLog2e / a.temperature, xy = a.chosen[r];
-    float m = 0.0f, s = 1.0f;
+    const float xy = a.chosen[r];
+    float m = 0.0f;
+    double s = 1.0;
     if (y >= 0 && y < a.vocab) {
       const uint64_t* v = a.part + static_cast<int64_t>(r) * a.slices;
-      m = -kFar;
-      s = 0.0f;
+      m = kLowest;
+      s = 0.0;
       constexpr int U = 8;  // words in flight
       for (int x0 = 0; x0 < a.slices; x0 += U) {
         uint64_t w[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) w[u] = x0 + u < a.slices ? v[x0 + u] : pair_word(-kFar, 0.0f);
+        for (int u = 0; u < U; ++u) w[u] = x0 + u < a.slices ? v[x0 + u] : pair_word(kLowest, 0.0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) join(m, s, word_max(w[u]), word_sum(w[u]), k);
-      }
-      if (far_row(m, k)) {  // joined again in the exact form
-        m = kLowest;
-        s = 0.0f;
-        for (int x = 0; x < a.slices; ++x) join<true>(m, s, word_max(v[x]), word_sum(v[x]), k);
+        for (int u = 0; u < U; ++u) join(m, s, word_max(w[u]), word_sum(w[u]), a.k);
       }
     }
     lp = finish_row(a, r, y, xy, m, s);

@@ -122,7 +122,9 @@ muon_status_t check_spans(muon_ctx* c, const Span* s, int n, bool in_place) {
   return MUON_OK;
 }
 
-bool good_temperature(float t) { return t > 0.0f && std::isfinite(t) && std::isfinite(1.0f / t); }
+constexpr double kLog2e = 1.44269504088896340736;
+// also 1 / t and log2 e / t, which the kernels take in fp32, have to be finite
+bool good_temperature(double t) { return t > 1e-30 && t < 1e30; }
 
 muon_status_t check_ctx(muon_ctx* c, size_t need) {
   if (c == nullptr) return fail(c, MUON_EINVAL, "context NULL");
@@ -140,7 +142,7 @@ int slices_of(const muon_ctx* c, const muon_logits_t& x) {
 }
 
 LossArgs loss_args(const muon_ctx* c, const LossLayout& l, const muon_logits_t& x, const int64_t* labels,
-                   float temperature) {
+                   double temperature) {
   LossArgs a = {};
   a.x = rows_ref(x);
   a.bf16 = x.dtype == MUON_BF16;
@@ -148,7 +150,8 @@ LossArgs loss_args(const muon_ctx* c, const LossLayout& l, const muon_logits_t& 
   a.seq = static_cast<int>(x.seq > 0 ? x.seq : 1);
   a.vocab = static_cast<int>(x.vocab);
   a.labels = labels;
-  a.temperature = temperature;
+  a.k = static_cast<float>(kLog2e / temperature);
+  a.inv_t = 1.0 / temperature;
   a.slices = slices_of(c, x);
   a.spin = c->loss_spin;
   a.part = reinterpret_cast<uint64_t*>(c->ws + l.part);
@@ -187,7 +190,7 @@ muon_status_t muon_loss_set_polls(muon_ctx_t* c, int32_t polls) {
 }
 
 muon_status_t muon_token_logps(muon_ctx_t* c, void* stream, const muon_logits_t* logits,
-                               const int64_t* labels, float temperature, float* logps,
+                               const int64_t* labels, double temperature, float* logps,
                                float* row_stats) {
   size_t xb = 0;
   muon_status_t st = check_logits(c, logits, &xb);
@@ -213,7 +216,7 @@ muon_status_t muon_token_logps(muon_ctx_t* c, void* stream, const muon_logits_t*
 }
 
 muon_status_t muon_token_logps_backward(muon_ctx_t* c, void* stream, const muon_logits_t* logits,
-                                        const int64_t* labels, float temperature,
+                                        const int64_t* labels, double temperature,
                                         const float* row_stats, const float* grad_logps,
                                         const muon_logits_t* grad_logits) {
   size_t xb = 0, gb = 0;

@@ -18,14 +18,15 @@ struct LossArgs {
   int rows, seq, vocab;
   int row0;          // first row of this launch (set by the launchers)
   const int64_t* labels;
-  float temperature;
+  float k;           // log2 e / temperature
+  double inv_t;      // 1 / temperature
   int slices;        // workgroups that a row is cut over
   int spin;          // polls before a slice computes its neighbours' pairs itself
   uint64_t* part;    // [rows][slices] pairs of the slices
   float* chosen;     // [rows] the labels' scores, of rows in several slices
   double* lp;        // [rows] or nullptr
   float* logps;      // [rows] or nullptr
-  float2* stats;     // [rows] (maximum, sum) of the whole row, or nullptr
+  float2* stats;     // [rows] (maximum, sum - 1) of the whole row, or nullptr
 };
 
 // Slices of each row (at most 60 within MUON_MAX_VOCAB).

@@ -99,7 +99,7 @@ SHAPES = [
 def test_logps_and_their_gradient(ctx, shape, dtype, t):
     batch, seq, vocab, pad, shift = shape
     x, y, xn, yn = make(batch, seq, vocab, dtype, seed=vocab, pad=pad, shift=shift)
-    t32 = float(np.float32(t))
+    t32 = t
     logps = torch.full((batch, seq), 7.0, device=DEV)
     stats = torch.empty(batch, seq, 2, device=DEV)
     ctx.token_logps(x, y, logps, row_stats=stats, temperature=t)
@@ -163,6 +163,59 @@ def test_special_rows(ctx, dtype):
     same(grad.float().cpu().numpy(), gw, tol, "gradient")
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("vocab", [700, 4099, 50257])
+def test_tokens_the_policy_is_sure_of(ctx, vocab, dtype):
+    """lp close to 0: S = 1 + u.  The largest score gives exactly 1; in its
+    piece of 8 (4) scores, three (two) additions round by at most u = 2^-24
+    each, and everything else is relative to u: the terms' arguments, the
+    exponentials, S - 1 stored once per slice and once per row."""
+    x, y, _, _ = make(1, 24, vocab, dtype, empty=0.0, seed=11, scale=1.0)
+    x = x.clone()
+    lift = torch.linspace(9, 30, 24, device=DEV)
+    x[0, torch.arange(24), y[0]] = lift.to(dtype)
+    xn, yn = x.double().cpu().numpy(), y.cpu().numpy()
+    want = lo.token_logps_ref(xn, yn)
+    assert (want < 0).all() and want.min() > -4 and want.max() > -1e-6
+    logps, stats = torch.empty(1, 24, device=DEV), torch.empty(1, 24, 2, device=DEV)
+    ctx.token_logps(x, y, logps, row_stats=stats)
+    tol = 3.5 * U + np.abs(want) * U * (3 * 32 + 20)
+    same(logps.cpu().numpy(), want, tol, "logps")
+    # the label's gradient, G (1 - p), keeps that too
+    grad, coef = torch.empty_like(x), torch.ones(1, 24, device=DEV)
+    ctx.token_logps_backward(x, y, stats, coef, grad)
+    got = grad[0, torch.arange(24), y[0]].double().cpu().numpy()
+    one_minus_p = -np.expm1(want[0])
+    assert (np.abs(got - one_minus_p) <= tol[0] * 1.01 + one_minus_p * (torch.finfo(dtype).eps / 2 + 4 * U)).all()
+    out, g2 = torch.empty(4, device=DEV), torch.empty_like(x)
+    ctx.policy_loss(x, y, torch.full((1,), -1.0, device=DEV), out, grad_logits=g2, reduce="sum")
+    got = g2[0, torch.arange(24), y[0]].double().cpu().numpy()
+    assert (np.abs(got - one_minus_p) <= tol[0] * 1.01 + one_minus_p * (torch.finfo(dtype).eps / 2 + 4 * U)).all()
+
+
+@pytest.mark.parametrize("base,step,t", [(1e10, 1024.0, 2000.0), (-3e12, 262144.0, 1e6), (4.5e4, 0.0625, 1.0), (2e4, 0.03125, 0.5)])
+def test_scores_of_large_magnitude(ctx, base, step, t):
+    """Differences of a few units on top of scores whose product with log2 e / T
+    is far from (and close to) the range the gradient's multiply-add takes."""
+    rng = np.random.default_rng(8)
+    xn = (np.float32(base) + np.float32(step) * rng.integers(-60, 60, (2, 5, 3001)).astype(np.float32)).astype(np.float32)
+    x, xn = torch.from_numpy(xn).to(DEV), xn.astype(np.float64)
+    y = torch.from_numpy(rng.integers(0, 3001, (2, 5))).to(DEV)
+    yn = y.cpu().numpy()
+    logps, stats = torch.empty(2, 5, device=DEV), torch.empty(2, 5, 2, device=DEV)
+    ctx.token_logps(x, y, logps, row_stats=stats, temperature=t)
+    want = lo.token_logps_ref(xn, yn, t)
+    same(logps.cpu().numpy(), want, lp_tolerance(xn, yn, want, t) + U * np.abs(want), "logps")
+    coef, grad, g2, out = (torch.ones(2, 5, device=DEV), torch.empty_like(x), torch.empty_like(x),
+                           torch.empty(4, device=DEV))
+    ctx.token_logps_backward(x, y, stats, coef, grad, temperature=t)
+    gw = lo.logits_grad_ref(xn, yn, np.ones((2, 5)), t)
+    tol = grad_tolerance(xn, yn, np.ones((2, 5)), t, gw, torch.finfo(F32).eps)
+    same(grad.cpu().numpy(), gw, tol, "gradient")
+    ctx.policy_loss(x, y, torch.full((2,), -1.0, device=DEV), out, grad_logits=g2, reduce="sum", temperature=t)
+    same(g2.cpu().numpy(), gw, tol, "policy gradient")
+
+
 def placed_like(x):
     """A copy of x with its strides and alignment (the order of a row's sum
     goes by where the row starts)."""
@@ -193,7 +246,7 @@ def policy_inputs(case, seed=3):
     if batch > 2:
         y[1] = -1  # a sequence with no token
         yn[1] = -1
-    t32 = float(np.float32(t))
+    t32 = t
     lp = lo.token_logps_ref(xn, yn, t32)
     rng = np.random.default_rng(seed)
 

@@ -24,7 +24,7 @@ def logits(data=LOGITS, dtype=MUON_BF16, batch=B, seq=S, vocab=V, bs=S * V, rs=V
 
 
 def policy(x=None, labels=LABELS, params=(), adv=ADV, old=OLD, ref=REF, out=OUT, logps=LOGPS, grad="own"):
-    p = dict(clip_low=0.2, clip_high=0.2, kl_coef=0.1, temperature=1.0, weight=1.0, reduce=0, advantage_per_token=0)
+    p = dict(temperature=1.0, clip_low=0.2, clip_high=0.2, kl_coef=0.1, weight=1.0, reduce=0, advantage_per_token=0)
     p.update(params)
     x = x if x is not None else logits()
     g = logits(GRAD, x.dtype, x.batch, x.seq, x.vocab, x.batch_stride, x.row_stride) if grad == "own" else grad
@@ -83,7 +83,7 @@ def test_gradient_is_checked():
 
 @pytest.mark.parametrize("params", [
     dict(temperature=0.0), dict(temperature=-1.0), dict(temperature=float("inf")), dict(temperature=float("nan")),
-    dict(temperature=1e-45), dict(clip_low=-0.1), dict(clip_low=1.5), dict(clip_high=-0.1), dict(clip_high=float("nan")),
+    dict(temperature=1e-45), dict(temperature=1e31), dict(clip_low=-0.1), dict(clip_low=1.5), dict(clip_high=-0.1), dict(clip_high=float("nan")),
     dict(kl_coef=-1.0), dict(kl_coef=float("inf")), dict(weight=float("nan")), dict(reduce=3), dict(reduce=-1)])
 def test_policy_parameters(params):
     st = policy(params=params)
