@@ -8,12 +8,14 @@
 // has seen, and a larger maximum m' turns s into s exp(m - m').  Partial pairs
 // join the same way, in a fixed order.
 //
-// Arithmetic.  Scores are widened to fp32; with k = log2 e / T rounded,
-// exp(z - m / T) is exp2((x - m) k): the subtraction is exact for bf16, nothing
-// large cancels at any magnitude of x, and the largest score gives exactly 1.
-// (The rounding of k moves every log-probability by up to 1e-7, the same way.  A
-// second multiply-add with the rest of k would take that away; it costs scoring
-// 6%: 2044 x 151936 bf16 in 97 us, 91 without.)
+// Arithmetic.  Scores are widened to fp32; with k = log2 e / T rounded to fp32
+// and k' what that leaves, exp(z - m / T) is exp2((x - m) k): the subtraction is
+// exact for bf16, nothing large cancels at any magnitude of x, and the largest
+// score gives exactly 1.  Factors between two maxima, which lie further apart
+// and move whole sums, are exp2((m - m') k + (m - m') k'): without k' there the
+// log-probabilities over a vocabulary of 151936 were off by up to 1.2e-7 on
+// average, all the same way (it adds up over a sequence), and by 6e-8 with it,
+// which costs scoring 1-2%.  With k' at every score it would be another 6%.
 // m is a running maximum; it is raised, and s scaled, only when some lane of
 // the wave has met a larger score (rescaling at every piece took 10% more VALU
 // cycles).  It starts at the lowest finite number, so that a masked score
@@ -121,26 +123,36 @@ template <typename T> __device__ __forceinline__ T* row_at(const RowsRef& x, int
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
+// log2 e / T = k + rest; exp(d / T) for d <= 0.  (-infinity is taken as the
+// lowest finite number, whose product with a rest below 0 is finite too.)
+struct Scale {
+  float k, rest;
+  __device__ __forceinline__ float exp(float d) const {
+    const float f = fmaxf(d, kLowest);
+    return exp2_fast(__builtin_fmaf(f, k, f * rest));
+  }
+};
+
 // (m, s) joined with (mo, so).
-__device__ __forceinline__ void join(float& m, double& s, float mo, double so, float k) {
+__device__ __forceinline__ void join(float& m, double& s, float mo, double so, Scale q) {
   const float mn = fmaxf(m, mo);
-  s = s * static_cast<double>(exp2_fast((m - mn) * k)) + so * static_cast<double>(exp2_fast((mo - mn) * k));
+  s = s * static_cast<double>(q.exp(m - mn)) + so * static_cast<double>(q.exp(mo - mn));
   m = mn;
 }
 
 // The pair of N neighbouring lanes, in each of them (the two terms of a join
 // commute, so both partners form the same sum).
-template <int N = 64> __device__ __forceinline__ void wave_join(float& m, double& s, float k) {
+template <int N = 64> __device__ __forceinline__ void wave_join(float& m, double& s, Scale q) {
 #pragma unroll
-  for (int d = N / 2; d > 0; d >>= 1) join(m, s, __shfl_xor(m, d, 64), __shfl_xor(s, d, 64), k);
+  for (int d = N / 2; d > 0; d >>= 1) join(m, s, __shfl_xor(m, d, 64), __shfl_xor(s, d, 64), q);
 }
 
 // The pair of all threads of the workgroup, in every thread.
-template <int NT> __device__ __forceinline__ void block_join(float& m, double& s, float k) {
+template <int NT> __device__ __forceinline__ void block_join(float& m, double& s, Scale q) {
   constexpr int W = NT / 64;
   __shared__ float wave_m[W];
   __shared__ double wave_s[W];
-  wave_join(m, s, k);
+  wave_join(m, s, q);
   __syncthreads();  // an earlier call's values have been read
   if ((threadIdx.x & 63) == 0) {
     wave_m[threadIdx.x >> 6] = m;
@@ -149,32 +161,32 @@ template <int NT> __device__ __forceinline__ void block_join(float& m, double& s
   __syncthreads();
   m = wave_m[threadIdx.x & (W - 1)];
   s = wave_s[threadIdx.x & (W - 1)];
-  wave_join<W>(m, s, k);
+  wave_join<W>(m, s, q);
 }
 
 // (m, s) with N = 1, 4 or 8 more scores.
-template <int N> __device__ __forceinline__ void take_scores(const float (&v)[N], float& m, double& s, float k) {
+template <int N> __device__ __forceinline__ void take_scores(const float (&v)[N], float& m, double& s, Scale q) {
   float mn = m;
 #pragma unroll
   for (int i = 0; i < N; ++i) mn = fmaxf(mn, v[i]);
   if (__any(mn > m)) {
-    s *= static_cast<double>(exp2_fast((m - mn) * k));
+    s *= static_cast<double>(q.exp(m - mn));
     m = mn;
     asm volatile("" : "+v"(s));  // stays a branch
   }
   float e[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) e[i] = exp2_fast((v[i] - m) * k);
+  for (int i = 0; i < N; ++i) e[i] = exp2_fast((v[i] - m) * q.k);
 #pragma unroll
   for (int w = N / 2; w > 0; w /= 2)
 #pragma unroll
     for (int i = 0; i < w; ++i) e[i] += e[i + w];
   s += static_cast<double>(e[0]);
 }
-template <typename T> __device__ __forceinline__ void take_piece(u32x4 w, float& m, double& s, float k) {
+template <typename T> __device__ __forceinline__ void take_piece(u32x4 w, float& m, double& s, Scale q) {
   float v[kVec<T>];
   Scores<T>::unpack(w, v);
-  take_scores(v, m, s, k);
+  take_scores(v, m, s, q);
 }
 
 // log s to a few units of binary64, also next to 1: s = 2^e f with f in [3/4,
@@ -264,7 +276,7 @@ __device__ __forceinline__ Slice slice_of(const RowShape& sh, int slices, int j)
 // The pair of slice j read from memory, in every thread: the sums of
 // slice_kernel in its order, so the same bits.
 template <typename T>
-__device__ __forceinline__ void slice_pair(const T* row, const RowShape& sh, int slices, int j, float k, float& m,
+__device__ __forceinline__ void slice_pair(const T* row, const RowShape& sh, int slices, int j, Scale scale, float& m,
                                            double& s) {
   const Slice sl = slice_of(sh, slices, j);
   const u32x4* body = reinterpret_cast<const u32x4*>(row + sh.head) + sl.first;
@@ -272,12 +284,12 @@ __device__ __forceinline__ void slice_pair(const T* row, const RowShape& sh, int
   m = kLowest;
   s = 0.0;
 #pragma unroll 1
-  for (int q = t; q < sl.count; q += kThreads) take_piece<T>(body[q], m, s, k);
+  for (int q = t; q < sl.count; q += kThreads) take_piece<T>(body[q], m, s, scale);
   if (j == 0 && t < sh.edges) {
     const float v[1] = {muon::Elem<T>::load(row + edge_score<T>(sh, t))};
-    take_scores(v, m, s, k);
+    take_scores(v, m, s, scale);
   }
-  block_join<kThreads>(m, s, k);
+  block_join<kThreads>(m, s, scale);
 }
 
 // Exchange between the workgroups of one launch.  What is exchanged goes
@@ -435,13 +447,18 @@ template <int NT> __device__ __forceinline__ double token_weight(const PolicyArg
   return 1.0 / (count_labels<NT>(p.labels, lo, lo + p.seq) * p.batch);
 }
 
-// The weighted sums of the terms of tokens [lo, hi), in every thread.
-template <int NT> __device__ __forceinline__ void sum_terms(const PolicyArgs& p, int64_t lo, int64_t hi, double (&v)[3]) {
+// The weighted sums of the terms of tokens [lo, hi), in every thread; SAME: by
+// the launch that formed them.
+template <int NT, bool SAME>
+__device__ __forceinline__ void sum_terms(const PolicyArgs& p, int64_t lo, int64_t hi, double (&v)[3]) {
   v[0] = v[1] = v[2] = 0.0;
+  auto word = [](const uint64_t* from) { return SAME ? published(from) : *from; };
   for (int64_t i = lo + threadIdx.x; i < hi; i += NT) {
-    if (p.labels[i] < 0) continue;
-    const double w = word_weight(published(p.weights + (p.p.reduce == MUON_REDUCE_SEQUENCE ? i / p.seq : 0)));
-    const uint64_t term = published(p.terms + 2 * i), clipped = published(p.terms + 2 * i + 1);
+    const int64_t y = p.labels[i];
+    const uint64_t weight = word(p.weights + (p.p.reduce == MUON_REDUCE_SEQUENCE ? i / p.seq : 0));
+    const uint64_t term = word(p.terms + 2 * i), clipped = word(p.terms + 2 * i + 1);
+    if (y < 0) continue;  // (nothing was formed)
+    const double w = word_weight(weight);
     v[0] += w * static_cast<double>(word_lo(term));
     v[1] += w * static_cast<double>(word_hi(term));
     v[2] += w * static_cast<double>(word_lo(clipped));
@@ -495,6 +512,7 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
   const Slice sl = slice_of(sh, a.slices, j);
   const bool edge = j == 0 && t < sh.edges;
   const float k = a.k;
+  const Scale scale = {a.k, a.k_rest};
   T* out = USE == USE_POLICY ? row_at<T>(grad, r, a.seq) : nullptr;
   // the gradient's rows have an alignment of their own
   u32x4_any* obody = USE == USE_POLICY ? reinterpret_cast<u32x4_any*>(out + sh.head) + sl.first : nullptr;
@@ -534,15 +552,15 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
     // knows the piece may have changed just before and the sum is read just
     // after, so it keeps 4 registers a piece and not 8 more of widened scores.
     asm volatile("" : "+v"(w[i]));
-    take_piece<T>(w[i], m, s, k);
+    take_piece<T>(w[i], m, s, scale);
     asm volatile("" : "+v"(s));
   }
   if (wave == 0) {  // threads without an edge hold -infinity
     const float v[1] = {we};
-    take_scores(v, m, s, k);
+    take_scores(v, m, s, scale);
   }
   if (USE == USE_POLICY) asm volatile("" : "+v"(xy));  // read before this slice is published
-  block_join<kThreads>(m, s, k);
+  block_join<kThreads>(m, s, scale);
   if (USE == USE_STATS) {
     if (t == 0) {
       if (a.slices == 1) finish_row(a, r, y, xy, m, s);
@@ -560,7 +578,7 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
     const double wt = word_weight(__shfl(word, kWeightLane, 64));
     m = lane < a.slices ? word_max(word) : kLowest;
     s = lane < a.slices ? word_sum(word) : 0.0;
-    wave_join(m, s, k);
+    wave_join(m, s, scale);
     double lp = token_lp(a, xy, m, s);
     if (!named) lp = __longlong_as_double(0x7ff8000000000000ll);
     const TokenTerms o = policy_token(p, r, b, lp);
@@ -602,7 +620,7 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
       if (!((lack >> i) & 1)) continue;
       float mi;
       double si;
-      slice_pair(row, sh, a.slices, i, k, mi, si);
+      slice_pair(row, sh, a.slices, i, scale, mi, si);
       if (t == 0) {
         const uint64_t v = published(slot + i);
         own[i] = v ? v : pair_word(mi, si);
@@ -654,7 +672,7 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef gra
   __syncthreads();
   if (!last) return;
   double v[3];
-  sum_terms<kThreads>(p, 0, a.rows, v);
+  sum_terms<kThreads, true>(p, 0, a.rows, v);
   if (threadIdx.x == 0) {
     write_policy(p, v[0], v[1], v[2]);
     *p.arrived = 0;
@@ -677,7 +695,7 @@ __global__ __launch_bounds__(kThreads) void row_join_kernel(LossArgs a) {
       m = word_max(v);
       s = word_sum(v);
     }
-    wave_join(m, s, a.k);
+    wave_join(m, s, Scale{a.k, a.k_rest});
   }
   if (lane == 0) finish_row(a, r, y, a.chosen[r], m, s);
 }
@@ -778,7 +796,7 @@ __global__ __launch_bounds__(kTermThreads) void policy_prepare_kernel(PolicyArgs
 __global__ __launch_bounds__(kTermThreads) void policy_sums_kernel(PolicyArgs p, int64_t rows, uint64_t* words) {
   const int64_t per = (rows + gridDim.x - 1) / gridDim.x, lo = static_cast<int64_t>(blockIdx.x) * per;
   double v[3];
-  sum_terms<kTermThreads>(p, lo, lo + per < rows ? lo + per : rows, v);
+  sum_terms<kTermThreads, false>(p, lo, lo + per < rows ? lo + per : rows, v);
   if (gridDim.x == 1) {  // (the sums' barriers lie after every read of the weights)
     for (int i = threadIdx.x; i < p.clear; i += kTermThreads) words[i] = 0;
     if (threadIdx.x == 0) write_policy(p, v[0], v[1], v[2]);
@@ -839,7 +857,7 @@ __device__ __forceinline__ double token_score(const LossArgs& a, const Preferenc
 #pragma unroll
         for (int u = 0; u < U; ++u) w[u] = x0 + u < a.slices ? v[x0 + u] : pair_word(kLowest, 0.0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) join(m, s, word_max(w[u]), word_sum(w[u]), a.k);
+        for (int u = 0; u < U; ++u) join(m, s, word_max(w[u]), word_sum(w[u]), Scale{a.k, a.k_rest});
       }
     }
     lp = finish_row(a, r, y, xy, m, s);

@@ -150,7 +150,9 @@ LossArgs loss_args(const muon_ctx* c, const LossLayout& l, const muon_logits_t& 
   a.seq = static_cast<int>(x.seq > 0 ? x.seq : 1);
   a.vocab = static_cast<int>(x.vocab);
   a.labels = labels;
-  a.k = static_cast<float>(kLog2e / temperature);
+  const double k = kLog2e / temperature;
+  a.k = static_cast<float>(k);
+  a.k_rest = static_cast<float>(k - static_cast<double>(a.k));
   a.inv_t = 1.0 / temperature;
   a.slices = slices_of(c, x);
   a.spin = c->loss_spin;

@@ -18,7 +18,7 @@ struct LossArgs {
   int rows, seq, vocab;
   int row0;          // first row of this launch (set by the launchers)
   const int64_t* labels;
-  float k;           // log2 e / temperature
+  float k, k_rest;   // log2 e / temperature = k + k_rest, k rounded to fp32
   double inv_t;      // 1 / temperature
   int slices;        // workgroups that a row is cut over
   int spin;          // polls before a slice computes its neighbours' pairs itself
