@@ -8,17 +8,21 @@
 // has seen, and a larger maximum m' turns s into s exp(m - m').  Partial pairs
 // join the same way, in a fixed order.
 //
-// Arithmetic.  Scores are widened to fp32; with k = log2 e / T rounded to fp32
-// and k' what that leaves, exp(z - m / T) is exp2((x - m) k): the subtraction is
-// exact for bf16, nothing large cancels at any magnitude of x, and the largest
-// score gives exactly 1.  Factors between two maxima, which lie further apart
-// and move whole sums, are exp2((m - m') k + (m - m') k'): without k' there the
-// log-probabilities over a vocabulary of 151936 were off by up to 1.2e-7 on
-// average, all the same way (it adds up over a sequence), and by 6e-8 with it,
-// which costs scoring 1-2%.  With k' at every score it would be another 6%.
-// m is a running maximum; it is raised, and s scaled, only when some lane of
-// the wave has met a larger score (rescaling at every piece took 10% more VALU
-// cycles).  It starts at the lowest finite number, so that a masked score
+// Arithmetic.  Scores are widened to fp32; with k = log2 e / T, exp(z - m / T) is
+// exp2((x - m) k): the subtraction is exact for bf16, nothing large cancels at
+// any magnitude of x, and the largest score gives exactly 1.  k rounded to fp32
+// is another temperature: every log-probability over a vocabulary of 151936
+// would be off the same way, by up to 1.2e-7 on average, and the sum over a
+// sequence by as much as there are tokens.  So k is rounded up for some of the
+// scores of a piece and down for the others, as many as make its mean right to
+// 2^-28 (fp32 scores, 4 a piece: 2^-27), which leaves at most 3e-8 and costs
+// nothing (a second multiply-add with the rest at every score took scoring 6%).
+// Factors between two maxima take the rest along.
+// m is the running maximum of a wave; it is raised, and s scaled, only when some
+// lane has met a larger score, and the lanes' sums then join without further
+// exponentials.  (With a maximum per lane nearly every piece raised some lane's,
+// and joins of pairs made 3/10 of the VALU instructions, which bound scoring: 2044
+// rows of 151936 bf16 took 95 us, 88.5 so.)  It starts at the lowest finite number, so that a masked score
 // (-infinity) gives 0 and a row of nothing but the lowest number is uniform.
 //
 // A token that the policy is sure of has S = 1 + u with a small u, and lp = -u
@@ -127,6 +131,8 @@ __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_ex
 // lowest finite number, whose product with a rest below 0 is finite too.)
 struct Scale {
   float k, rest;
+  const float (&each)[8];  // for the scores of a piece
+  __device__ __forceinline__ explicit Scale(const LossArgs& a) : k(a.k), rest(a.k_rest), each(a.k_each) {}
   __device__ __forceinline__ float exp(float d) const {
     const float f = fmaxf(d, kLowest);
     return exp2_fast(__builtin_fmaf(f, k, f * rest));
@@ -134,56 +140,94 @@ struct Scale {
 };
 
 // (m, s) joined with (mo, so).
-__device__ __forceinline__ void join(float& m, double& s, float mo, double so, Scale q) {
+__device__ __forceinline__ void join(float& m, double& s, float mo, double so, const Scale& q) {
   const float mn = fmaxf(m, mo);
   s = s * static_cast<double>(q.exp(m - mn)) + so * static_cast<double>(q.exp(mo - mn));
   m = mn;
 }
 
-// The pair of N neighbouring lanes, in each of them (the two terms of a join
-// commute, so both partners form the same sum).
-template <int N = 64> __device__ __forceinline__ void wave_join(float& m, double& s, Scale q) {
-#pragma unroll
-  for (int d = N / 2; d > 0; d >>= 1) join(m, s, __shfl_xor(m, d, 64), __shfl_xor(s, d, 64), q);
+// The maximum and the sum over a wave, in every lane; all lanes take part.
+// Quads, then halves and mirrors of 16 lanes, then the rows of 16 into the last
+// one: no LDS, and a fixed order.
+template <int CTRL, int ROWS> __device__ __forceinline__ int dpp(int old, int v) {
+  return __builtin_amdgcn_update_dpp(old, v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS> __device__ __forceinline__ float max_step(float v) {
+  const int w = __float_as_int(v);
+  return fmaxf(v, __int_as_float(dpp<CTRL, ROWS>(w, w)));
+}
+template <int CTRL, int ROWS> __device__ __forceinline__ double sum_step(double v) {
+  return v + __hiloint2double(dpp<CTRL, ROWS>(0, __double2hiint(v)), dpp<CTRL, ROWS>(0, __double2loint(v)));
+}
+constexpr int kQuad1 = 0xb1, kQuad2 = 0x4e, kHalfMirror = 0x141, kMirror = 0x140, kLane15 = 0x142, kLane31 = 0x143;
+__device__ __forceinline__ float wave_max(float v) {
+  v = max_step<kQuad1, 0xf>(v);
+  v = max_step<kQuad2, 0xf>(v);
+  v = max_step<kHalfMirror, 0xf>(v);
+  v = max_step<kMirror, 0xf>(v);
+  v = max_step<kLane15, 0xa>(v);
+  v = max_step<kLane31, 0xc>(v);
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v = sum_step<kQuad1, 0xf>(v);
+  v = sum_step<kQuad2, 0xf>(v);
+  v = sum_step<kHalfMirror, 0xf>(v);
+  v = sum_step<kMirror, 0xf>(v);
+  v = sum_step<kLane15, 0xa>(v);
+  v = sum_step<kLane31, 0xc>(v);
+  return __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(v), 63),
+                          __builtin_amdgcn_readlane(__double2loint(v), 63));
 }
 
-// The pair of all threads of the workgroup, in every thread.
-template <int NT> __device__ __forceinline__ void block_join(float& m, double& s, Scale q) {
+// The pair of a wave's lanes, in each of them.
+__device__ __forceinline__ void wave_join(float& m, double& s, const Scale& q) {
+  const float mn = wave_max(m);
+  s = wave_sum(s * static_cast<double>(q.exp(m - mn)));
+  m = mn;
+}
+
+// The pair of a workgroup whose waves have one maximum each, in wave 0.
+template <int NT> __device__ __forceinline__ void block_join(float& m, double& s, const Scale& q) {
   constexpr int W = NT / 64;
   __shared__ float wave_m[W];
   __shared__ double wave_s[W];
-  wave_join(m, s, q);
+  const int lane = static_cast<int>(threadIdx.x) & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  s = wave_sum(s);
   __syncthreads();  // an earlier call's values have been read
-  if ((threadIdx.x & 63) == 0) {
-    wave_m[threadIdx.x >> 6] = m;
-    wave_s[threadIdx.x >> 6] = s;
+  if (lane == 0) {
+    wave_m[wave] = m;
+    wave_s[wave] = s;
   }
   __syncthreads();
-  m = wave_m[threadIdx.x & (W - 1)];
-  s = wave_s[threadIdx.x & (W - 1)];
-  wave_join<W>(m, s, q);
+  if (wave) return;
+  m = wave_m[lane & (W - 1)];
+  s = lane < W ? wave_s[lane] : 0.0;
+  wave_join(m, s, q);
 }
 
-// (m, s) with N = 1, 4 or 8 more scores.
-template <int N> __device__ __forceinline__ void take_scores(const float (&v)[N], float& m, double& s, Scale q) {
+// (m, s) with N = 1, 4 or 8 more scores from every lane; m is the wave's, s the
+// lane's.
+template <int N> __device__ __forceinline__ void take_scores(const float (&v)[N], float& m, double& s, const Scale& q) {
   float mn = m;
 #pragma unroll
   for (int i = 0; i < N; ++i) mn = fmaxf(mn, v[i]);
   if (__any(mn > m)) {
+    mn = wave_max(mn);
     s *= static_cast<double>(q.exp(m - mn));
     m = mn;
     asm volatile("" : "+v"(s));  // stays a branch
   }
   float e[N];
 #pragma unroll
-  for (int i = 0; i < N; ++i) e[i] = exp2_fast((v[i] - m) * q.k);
+  for (int i = 0; i < N; ++i) e[i] = exp2_fast((v[i] - m) * (N == 1 ? q.k : q.each[i]));
 #pragma unroll
   for (int w = N / 2; w > 0; w /= 2)
 #pragma unroll
     for (int i = 0; i < w; ++i) e[i] += e[i + w];
   s += static_cast<double>(e[0]);
 }
-template <typename T> __device__ __forceinline__ void take_piece(u32x4 w, float& m, double& s, Scale q) {
+template <typename T> __device__ __forceinline__ void take_piece(u32x4 w, float& m, double& s, const Scale& q) {
   float v[kVec<T>];
   Scores<T>::unpack(w, v);
   take_scores(v, m, s, q);
@@ -273,10 +317,10 @@ __device__ __forceinline__ Slice slice_of(const RowShape& sh, int slices, int j)
   return {first, min(per, sh.full - first)};
 }
 
-// The pair of slice j read from memory, in every thread: the sums of
-// slice_kernel in its order, so the same bits.
+// The pair of slice j read from memory, in wave 0: the sums of slice_kernel in
+// its order, so the same bits.
 template <typename T>
-__device__ __forceinline__ void slice_pair(const T* row, const RowShape& sh, int slices, int j, Scale scale, float& m,
+__device__ __forceinline__ void slice_pair(const T* row, const RowShape& sh, int slices, int j, const Scale& scale, float& m,
                                            double& s) {
   const Slice sl = slice_of(sh, slices, j);
   const u32x4* body = reinterpret_cast<const u32x4*>(row + sh.head) + sl.first;
@@ -284,9 +328,14 @@ __device__ __forceinline__ void slice_pair(const T* row, const RowShape& sh, int
   m = kLowest;
   s = 0.0;
 #pragma unroll 1
-  for (int q = t; q < sl.count; q += kThreads) take_piece<T>(body[q], m, s, scale);
-  if (j == 0 && t < sh.edges) {
-    const float v[1] = {muon::Elem<T>::load(row + edge_score<T>(sh, t))};
+  for (int q = 0; q < sl.count; q += kThreads) {
+    const uint32_t none = Scores<T>::kMasked;
+    u32x4 w = {none, none, none, none};
+    if (q + t < sl.count) w = body[q + t];
+    take_piece<T>(w, m, s, scale);
+  }
+  if (j == 0 && t < 64) {
+    const float v[1] = {t < sh.edges ? muon::Elem<T>::load(row + edge_score<T>(sh, t)) : -INFINITY};
     take_scores(v, m, s, scale);
   }
   block_join<kThreads>(m, s, scale);
@@ -512,7 +561,7 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
   const Slice sl = slice_of(sh, a.slices, j);
   const bool edge = j == 0 && t < sh.edges;
   const float k = a.k;
-  const Scale scale = {a.k, a.k_rest};
+  const Scale scale(a);
   T* out = USE == USE_POLICY ? row_at<T>(grad, r, a.seq) : nullptr;
   // the gradient's rows have an alignment of their own
   u32x4_any* obody = USE == USE_POLICY ? reinterpret_cast<u32x4_any*>(out + sh.head) + sl.first : nullptr;
@@ -695,7 +744,7 @@ __global__ __launch_bounds__(kThreads) void row_join_kernel(LossArgs a) {
       m = word_max(v);
       s = word_sum(v);
     }
-    wave_join(m, s, Scale{a.k, a.k_rest});
+    wave_join(m, s, Scale(a));
   }
   if (lane == 0) finish_row(a, r, y, a.chosen[r], m, s);
 }
@@ -857,7 +906,7 @@ __device__ __forceinline__ double token_score(const LossArgs& a, const Preferenc
 #pragma unroll
         for (int u = 0; u < U; ++u) w[u] = x0 + u < a.slices ? v[x0 + u] : pair_word(kLowest, 0.0);
 #pragma unroll
-        for (int u = 0; u < U; ++u) join(m, s, word_max(w[u]), word_sum(w[u]), Scale{a.k, a.k_rest});
+        for (int u = 0; u < U; ++u) join(m, s, word_max(w[u]), word_sum(w[u]), Scale(a));
       }
     }
     lp = finish_row(a, r, y, xy, m, s);
