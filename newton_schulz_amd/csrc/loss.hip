@@ -4,9 +4,9 @@
 // Mathematics.  With z = x / T, M = max z and S = sum_v exp(z_v - M):
 //   lp = z_y - M - log S,   d lp / d x_v = ([v = y] - exp(z_v - M) / S) / T,
 // so a row needs two numbers, (max x, S), beyond itself.  They are found in
-// one pass: each thread keeps the maximum m and the sum s around it of what it
-// has seen, and a larger maximum m' turns s into s exp(m - m').  Partial pairs
-// join the same way, in a fixed order.
+// one pass: a maximum m and sums s around it of what has been seen; a larger
+// maximum m' turns s into s exp(m - m').  Partial pairs join the same way, in a
+// fixed order.
 //
 // Arithmetic.  Scores are widened to fp32; with k = log2 e / T, exp(z - m / T) is
 // exp2((x - m) k): the subtraction is exact for bf16, nothing large cancels at
@@ -21,9 +21,10 @@
 // m is the running maximum of a wave; it is raised, and s scaled, only when some
 // lane has met a larger score, and the lanes' sums then join without further
 // exponentials.  (With a maximum per lane nearly every piece raised some lane's,
-// and joins of pairs made 3/10 of the VALU instructions, which bound scoring: 2044
-// rows of 151936 bf16 took 95 us, 88.5 so.)  It starts at the lowest finite number, so that a masked score
-// (-infinity) gives 0 and a row of nothing but the lowest number is uniform.
+// and joins of pairs made 3/10 of the VALU instructions, which bound scoring:
+// 2044 rows of 151936 bf16 took 95 us, 88.5 so.)  It starts at the lowest finite
+// number, so that a masked score (-infinity) gives 0 and a row of nothing but
+// the lowest number is uniform.
 //
 // A token that the policy is sure of has S = 1 + u with a small u, and lp = -u
 // to first order: rounding S to fp32 would leave lp with an error of 2^-24
@@ -36,7 +37,8 @@
 // into the factor that p is multiplied by anyway.  Rows of larger |c| take
 // exp2((x - m) k) there too.
 //
-// Shape of the kernels.  All are bound by HBM (a pass that only reads reaches
+// Shape of the kernels.  The statistics issue VALU instructions most of the time
+// they read; the gradients are bound by HBM (a pass that only reads reaches
 // 6.1-6.3 TB/s on MI355X, one that reads and writes alike 5.7-6.0), and HBM is
 // fastest when the workgroups in flight cover a compact, moving window of
 // addresses: copying in 16 KB pieces per workgroup reaches 6.0 TB/s, in 300 KB
@@ -592,6 +594,12 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
   const bool named = y < a.vocab;
   float xy = 0.0f;
   if (USE == USE_POLICY || j == 0) xy = muon::Elem<T>::load(row + (named ? y : 0));
+  // From the wave's first lane on.  Slices seldom fill the last pieces, and the
+  // statistics alone are bound by VALU: skipping what a wave has nothing of took
+  // 2048 rows of 50257 bf16 scores and their gradient from 107.2 to 105.4 us; in
+  // the policy loss, which waits for memory, the branches cost more (32000
+  // scores: 50.5, 50.1 us without).
+  const int own_pieces = sl.count - wave * 64;
   float m = kLowest;
   double s = 0.0;
 #pragma unroll
@@ -601,7 +609,7 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
     // knows the piece may have changed just before and the sum is read just
     // after, so it keeps 4 registers a piece and not 8 more of widened scores.
     asm volatile("" : "+v"(w[i]));
-    take_piece<T>(w[i], m, s, scale);
+    if (USE == USE_POLICY || i * kThreads < own_pieces) take_piece<T>(w[i], m, s, scale);
     asm volatile("" : "+v"(s));
   }
   if (wave == 0) {  // threads without an edge hold -infinity
