@@ -355,12 +355,26 @@ __device__ __forceinline__ void publish(uint64_t* to, uint64_t v) {
 __device__ __forceinline__ uint64_t published(const uint64_t* from) {
   return __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
-// Those that counted themselves before; called by the thread that published.
-__device__ __forceinline__ unsigned arrive(unsigned* count) {
+// Whether all other workgroups of the launch have counted themselves; called by
+// the thread that published.  kCountedTogether workgroups share a counter, and
+// the last of them counts for all in the first: at one address 480 workgroups
+// wait 5 us for each other, in this way 1.
+__device__ __forceinline__ unsigned count_one(uint64_t* at) {
+  return __hip_atomic_fetch_add(reinterpret_cast<unsigned*>(at), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ bool arrive_last(uint64_t* counters) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  const unsigned before = __hip_atomic_fetch_add(count, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const unsigned g = blockIdx.x / kCountedTogether, groups = (gridDim.x - 1) / kCountedTogether + 1;
+  const unsigned in_group = min(gridDim.x - g * kCountedTogether, static_cast<unsigned>(kCountedTogether));
+  uint64_t* mine = counters + (1 + g) * kCounterWords;
+  bool last = count_one(mine) == in_group - 1;
+  if (last) {
+    *mine = 0;
+    last = count_one(counters) == groups - 1;
+    if (last) *counters = 0;
+  }
   asm volatile("" ::: "memory");
-  return before;
+  return last;
 }
 
 // Two numbers as one 64-bit word.
@@ -576,7 +590,7 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
     }
     if (j == 0 && t == 0) {
       if (USE == USE_POLICY && a.logps) a.logps[r] = 0.0f;
-      if (USE == USE_STATS && a.slices == 1) finish_row(a, r, y, 0.0f, 0.0f, 1.0);
+      if (USE == USE_STATS && a.slices == 1 && a.arrived == nullptr) finish_row(a, r, y, 0.0f, 0.0f, 1.0);
     }
     return;
   }
@@ -620,9 +634,9 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
   block_join<kThreads>(m, s, scale);
   if (USE == USE_STATS) {
     if (t == 0) {
-      if (a.slices == 1) finish_row(a, r, y, xy, m, s);
-      else a.part[static_cast<int64_t>(r) * a.slices + j] = pair_word(m, s);
-      if (a.slices > 1 && j == 0) a.chosen[r] = xy;
+      if (a.slices == 1 && a.arrived == nullptr) finish_row(a, r, y, xy, m, s);
+      else publish(a.part + static_cast<int64_t>(r) * a.slices + j, pair_word(m, s));
+      if (a.slices > 1 && j == 0 && a.arrived == nullptr) a.chosen[r] = xy;
     }
     return;
   }
@@ -718,22 +732,55 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
   }
 }
 
+// Whether this workgroup is the last one of the launch to get here.
+__device__ __forceinline__ bool last_to_arrive(const LossArgs& a) {
+  __shared__ int last;
+  if (threadIdx.x == 0) last = arrive_last(a.arrived);
+  __syncthreads();
+  return last;
+}
+
+// Every row of a small call joined by its last workgroup, a thread per row, and
+// the exchange words left as they were found, all zero.
+template <typename T> __device__ __forceinline__ void join_rows(const LossArgs& a) {
+  __shared__ uint64_t words[kArriveGroups];
+  const int t = static_cast<int>(threadIdx.x), slots = a.rows * a.slices;
+  for (int i = t; i < slots; i += kThreads) {
+    words[i] = published(a.part + i);
+    a.part[i] = 0;
+  }
+  __syncthreads();
+  const Scale scale(a);
+  for (int r = t; r < a.rows; r += kThreads) {
+    const int64_t y = a.labels[r];
+    float m = 0.0f, xy = 0.0f;
+    double s = 1.0;
+    if (y >= 0 && y < a.vocab) {
+      xy = muon::Elem<T>::load(row_at<const T>(a.x, r, a.seq) + y);
+      const uint64_t* w = words + r * a.slices;
+      m = kLowest;
+      s = 0.0;
+#pragma unroll 4
+      for (int i = 0; i < a.slices; ++i) m = fmaxf(m, word_max(w[i]));
+#pragma unroll 4
+      for (int i = 0; i < a.slices; ++i) s += word_sum(w[i]) * static_cast<double>(scale.exp(word_max(w[i]) - m));
+    }
+    finish_row(a, r, y, xy, m, s);
+  }
+}
+
 template <typename T, int NV, int USE>
 __global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef grad, PolicyArgs p) {
   slice_work<T, NV, USE>(a, grad, p);
-  if (USE != USE_POLICY || p.arrived == nullptr) return;
-  // A small call is one launch: the last workgroup to get here adds up the
-  // tokens and leaves the exchange words as it found them, all zero.
-  __shared__ int last;
-  if (threadIdx.x == 0) last = arrive(p.arrived) == gridDim.x - 1;
-  __syncthreads();
-  if (!last) return;
+  // A small call is one launch: its last workgroup does the rest.
+  if (a.arrived == nullptr || !last_to_arrive(a)) return;
+  if (USE == USE_STATS) {
+    join_rows<T>(a);
+    return;
+  }
   double v[3];
   sum_terms<kThreads, true>(p, 0, a.rows, v);
-  if (threadIdx.x == 0) {
-    write_policy(p, v[0], v[1], v[2]);
-    *p.arrived = 0;
-  }
+  if (threadIdx.x == 0) write_policy(p, v[0], v[1], v[2]);
   for (int i = threadIdx.x; i < p.clear; i += kThreads) a.part[i] = 0;
 }
 
@@ -922,13 +969,14 @@ __device__ __forceinline__ double token_score(const LossArgs& a, const Preferenc
   return *counts ? lp - static_cast<double>(ref) : 0.0;
 }
 
-// Scores of pairs blockIdx * n ... (n = 1, or all of at most kFewPairs): half of
-// the workgroup per sequence; then a thread per pair: its loss, and the gradient
-// that every token of each sequence has.  The only workgroup writes the losses;
-// several leave their pairs' terms.
-__global__ __launch_bounds__(kTermThreads) void preference_pairs_kernel(LossArgs a, PreferenceArgs p, int n) {
-  constexpr int kHalf = kTermThreads / 2, W = kHalf / 64;
-  const int pairs = p.batch / 2, first = static_cast<int>(blockIdx.x) * n;
+// Scores of the pairs [first, first + n) (n = 1, or all of at most kFewPairs):
+// half of the workgroup per sequence; then a thread per pair: its loss, and the
+// gradient that every token of each sequence has.  Who has all pairs writes the
+// losses; others leave their pairs' terms.
+template <int NT>
+__device__ __forceinline__ void pairs_work(const LossArgs& a, const PreferenceArgs& p, int first, int n) {
+  constexpr int kHalf = NT / 2, W = kHalf / 64;
+  const int pairs = p.batch / 2;
   const int side = __builtin_amdgcn_readfirstlane(threadIdx.x / kHalf);
   const int t = static_cast<int>(threadIdx.x) % kHalf, wave = t >> 6;
   __shared__ double scores[kFewPairs][2][W], terms[kFewPairs][3];
@@ -990,7 +1038,7 @@ __global__ __launch_bounds__(kTermThreads) void preference_pairs_kernel(LossArgs
       p.g[b] = static_cast<float>(p.p.average && count[k] ? g / count[k] : g);
     }
   }
-  if (gridDim.x > 1) return;
+  if (n < pairs) return;
   __syncthreads();
   if (threadIdx.x == 0) {
     double total[3] = {0.0, 0.0, 0.0};
@@ -999,6 +1047,21 @@ __global__ __launch_bounds__(kTermThreads) void preference_pairs_kernel(LossArgs
       for (int k = 0; k < 3; ++k) total[k] += terms[i][k];
     write_preference(p, total[0], total[1], total[2]);
   }
+}
+
+__global__ __launch_bounds__(kTermThreads) void preference_pairs_kernel(LossArgs a, PreferenceArgs p, int n) {
+  pairs_work<kTermThreads>(a, p, static_cast<int>(blockIdx.x) * n, n);
+}
+
+// A small call of few pairs: its last workgroup joins the rows and scores them.
+template <typename T, int NV>
+__global__ __launch_bounds__(kThreads) void slice_pairs_kernel(LossArgs a, PreferenceArgs p) {
+  slice_work<T, NV, USE_STATS>(a, RowsRef{}, PolicyArgs{});
+  if (!last_to_arrive(a)) return;
+  join_rows<T>(a);
+  __syncthreads();
+  a.slices = 1;  // (the rows' log-probabilities are whole)
+  pairs_work<kThreads>(a, p, 0, p.batch / 2);
 }
 
 __global__ __launch_bounds__(kTermThreads) void preference_sums_kernel(PreferenceArgs p) {
@@ -1033,6 +1096,17 @@ static int rows_per_launch(int64_t per) {
 
 namespace {
 
+// Every pair's loss by the same launch as the rows' statistics.
+struct PairsRef {
+  const PreferenceArgs* p;
+};
+
+template <typename T, int NV, int USE>
+hipError_t run_slices(hipStream_t s, const LossArgs& a, RowsRef, const PairsRef& pairs) {
+  slice_pairs_kernel<T, NV><<<static_cast<unsigned>(a.rows * a.slices), kThreads, 0, s>>>(a, *pairs.p);
+  return hipGetLastError();
+}
+
 template <typename T, int NV, int USE>
 hipError_t run_slices(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p) {
   LossArgs c = a;
@@ -1046,8 +1120,8 @@ hipError_t run_slices(hipStream_t s, const LossArgs& a, RowsRef grad, const Poli
   return hipSuccess;
 }
 
-template <typename T, int USE>
-hipError_t slices(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p) {
+template <typename T, int USE, typename P>
+hipError_t slices(hipStream_t s, const LossArgs& a, RowsRef grad, const P& p) {
   const int per = (a.vocab / kVec<T> + a.slices - 1) / a.slices;
   if (per <= 1 * kThreads) return run_slices<T, 1, USE>(s, a, grad, p);
   if (per <= 2 * kThreads) return run_slices<T, 2, USE>(s, a, grad, p);
@@ -1062,8 +1136,10 @@ hipError_t slices(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyAr
 // Empties the exchange words if a call failed half way.
 static hipError_t clear_exchange(hipStream_t s, Exchange& x) {
   if (!x.dirty) return hipSuccess;
-  clear_words_kernel<<<8, kTermThreads, 0, s>>>(x.words, kExchangeWords + 1);
-  return hipGetLastError();
+  clear_words_kernel<<<8, kTermThreads, 0, s>>>(x.words, kExchangeWords + kCounters * kCounterWords);
+  const hipError_t e = hipGetLastError();
+  if (e == hipSuccess) x.dirty = false;
+  return e;
 }
 
 static hipError_t launch_slice_stats(hipStream_t s, const LossArgs& a) {
@@ -1071,9 +1147,22 @@ static hipError_t launch_slice_stats(hipStream_t s, const LossArgs& a) {
                 : slices<float, USE_STATS>(s, a, RowsRef{}, PolicyArgs{});
 }
 
-hipError_t launch_row_stats(hipStream_t s, const LossArgs& a) {
+// `a` with its pairs in the exchange words, to be joined by the last workgroup.
+static LossArgs in_one_launch(const LossArgs& a, const Exchange& x) {
+  LossArgs c = a;
+  c.part = x.words;
+  c.arrived = x.words + kExchangeWords;
+  return c;
+}
+
+hipError_t launch_row_stats(hipStream_t s, const LossArgs& a, Exchange& x) {
+  if (a.rows == 0 || a.slices == 1) return launch_slice_stats(s, a);
+  if (static_cast<int64_t>(a.rows) * a.slices <= kArriveGroups) {
+    const hipError_t e = clear_exchange(s, x);
+    return e == hipSuccess ? launch_slice_stats(s, in_one_launch(a, x)) : e;
+  }
   const hipError_t e = launch_slice_stats(s, a);
-  if (e != hipSuccess || a.slices == 1 || a.rows == 0) return e;
+  if (e != hipSuccess) return e;
   const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.rows) + kThreads / 64 - 1) / (kThreads / 64));
   row_join_kernel<<<blocks, kThreads, 0, s>>>(a);
   return hipGetLastError();
@@ -1112,7 +1201,7 @@ hipError_t launch_policy(hipStream_t s, const LossArgs& args, RowsRef grad, cons
     p.weights = x.words + slots;
     p.count_here = 1;
     p.clear = static_cast<int>(slots + sets);
-    if (a.rows > 0 && slots <= kArriveGroups) p.arrived = reinterpret_cast<unsigned*>(x.words + kExchangeWords);
+    if (a.rows > 0 && slots <= kArriveGroups) a = in_one_launch(a, x);
     x.dirty = true;  // until every launch below is in the stream
   } else {
     const int64_t clear = std::min<int64_t>(128, (slots + kTermThreads - 1) / kTermThreads);
@@ -1121,7 +1210,7 @@ hipError_t launch_policy(hipStream_t s, const LossArgs& args, RowsRef grad, cons
   }
   if (e == hipSuccess) e = a.bf16 ? slices<bf16_t, USE_POLICY>(s, a, grad, p) : slices<float, USE_POLICY>(s, a, grad, p);
   if (e != hipSuccess) return e;
-  if (p.arrived == nullptr) {
+  if (a.arrived == nullptr) {
     const int n = kept ? 1 : std::min(kPolicySums, std::max(1, a.rows / 8192));
     policy_sums_kernel<<<static_cast<unsigned>(n), kTermThreads, 0, s>>>(p, a.rows, a.part);
     e = hipGetLastError();
@@ -1134,16 +1223,25 @@ hipError_t launch_policy(hipStream_t s, const LossArgs& args, RowsRef grad, cons
   return hipSuccess;
 }
 
-hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, const PreferenceArgs& p) {
-  hipError_t e = launch_slice_stats(s, a);
-  if (e != hipSuccess) return e;
+hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, const PreferenceArgs& p, Exchange& x) {
   const int pairs = p.batch / 2;
-  const unsigned grid = pairs <= kFewPairs ? 1 : static_cast<unsigned>(pairs);
-  preference_pairs_kernel<<<grid, kTermThreads, 0, s>>>(a, p, grid == 1 ? pairs : 1);
-  e = hipGetLastError();
-  if (e == hipSuccess && grid > 1) {
-    preference_sums_kernel<<<1, kTermThreads, 0, s>>>(p);
+  hipError_t e;
+  if (a.rows > 0 && pairs <= kFewPairs && static_cast<int64_t>(a.rows) * a.slices <= kArriveGroups) {
+    e = clear_exchange(s, x);
+    if (e != hipSuccess) return e;
+    const LossArgs c = in_one_launch(a, x);
+    e = a.bf16 ? slices<bf16_t, USE_STATS>(s, c, RowsRef{}, PairsRef{&p})
+               : slices<float, USE_STATS>(s, c, RowsRef{}, PairsRef{&p});
+  } else {
+    e = launch_slice_stats(s, a);
+    if (e != hipSuccess) return e;
+    const unsigned grid = pairs <= kFewPairs ? 1 : static_cast<unsigned>(pairs);
+    preference_pairs_kernel<<<grid, kTermThreads, 0, s>>>(a, p, grid == 1 ? pairs : 1);
     e = hipGetLastError();
+    if (e == hipSuccess && grid > 1) {
+      preference_sums_kernel<<<1, kTermThreads, 0, s>>>(p);
+      e = hipGetLastError();
+    }
   }
   if (e != hipSuccess || grad.base == nullptr) return e;
   return launch_logits_grad(s, a, grad, p.g, true);

@@ -220,7 +220,7 @@ muon_status_t muon_token_logps(muon_ctx_t* c, void* stream, const muon_logits_t*
   a.logps = logps;
   a.stats = reinterpret_cast<float2*>(row_stats);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return timed(c, s, MUON_K_LOSS, "row statistics launch", [&] { return launch_row_stats(s, a); });
+  return timed(c, s, MUON_K_LOSS, "row statistics launch", [&] { return launch_row_stats(s, a, c->exchange); });
 }
 
 muon_status_t muon_token_logps_backward(muon_ctx_t* c, void* stream, const muon_logits_t* logits,
@@ -349,7 +349,7 @@ muon_status_t muon_preference_loss(muon_ctx_t* c, void* stream, const muon_logit
   t.terms = reinterpret_cast<double*>(c->ws + l.pairs);
   hipStream_t s = static_cast<hipStream_t>(stream);
   return timed(c, s, MUON_K_LOSS, "preference loss launch",
-               [&] { return launch_preference(s, a, grad_logits && rows ? rows_ref(*grad_logits) : RowsRef{}, t); });
+               [&] { return launch_preference(s, a, grad_logits && rows ? rows_ref(*grad_logits) : RowsRef{}, t, c->exchange); });
 }
 
 }  // extern "C"

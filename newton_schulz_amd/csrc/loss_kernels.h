@@ -12,6 +12,23 @@ struct RowsRef {
   int64_t bs, rs;
 };
 
+// Words of a context through which workgroups of one launch exchange what they
+// found (pairs of slices, weights of tokens, counts of those that are through).
+// They are zero between calls: each call leaves them so, so none has to clear
+// them first.  Calls that need more take their workspace and a launch more.
+// Counters of a call's workgroups lie behind them, in different channels.
+constexpr int kExchangeWords = 32768;
+// Calls of so few workgroups are one launch, whose last workgroup does what is
+// left.  Against a launch more: 480 workgroups of log-probabilities 8.9 and 10.3 us
+// (12.7 if all count themselves at one address), 564 of the policy loss 10.4 and
+// 13.6, 198 of the preference loss 14.0 and 16.9, 536 of it 16.8 and 16.9.
+constexpr int kArriveGroups = 1024;
+constexpr int kCountedTogether = 32, kCounters = 1 + kArriveGroups / kCountedTogether, kCounterWords = 32;
+struct Exchange {
+  uint64_t* words = nullptr;
+  bool dirty = false;  // a call failed between its launches
+};
+
 struct LossArgs {
   RowsRef x;
   int bf16;
@@ -28,13 +45,14 @@ struct LossArgs {
   double* lp;        // [rows] or nullptr
   float* logps;      // [rows] or nullptr
   float2* stats;     // [rows] (maximum, sum - 1) of the whole row, or nullptr
+  uint64_t* arrived; // a call's counters if it is one launch, else nullptr
 };
 
 // Slices of each row (at most 60 within MUON_MAX_VOCAB).
 int loss_slices(int64_t rows, int64_t vocab, int bf16, int cus);
 
 // stats, lp and logps of every row (logps of tokens left out: 0).
-hipError_t launch_row_stats(hipStream_t s, const LossArgs& a);
+hipError_t launch_row_stats(hipStream_t s, const LossArgs& a, Exchange& x);
 
 // grad row r = g / temperature * ([v = y] - softmax), g[r] or g[sequence];
 // zeros for tokens left out.  Needs a.stats.
@@ -55,24 +73,8 @@ struct PolicyArgs {
   // set by the launcher
   int count_here;     // the slices count the tokens and publish the weights
   int clear;          // exchange words to empty afterwards
-  unsigned* arrived;  // workgroups that are through (calls of one launch)
 };
 
-// Words of a context through which workgroups of one launch exchange what they
-// found (pairs of slices, weights of tokens, counts of those that are through).
-// They are zero between calls: each call leaves them so, so none has to clear
-// them first.  Calls that need more take their workspace and a launch more.
-// One word behind them counts a whole call's workgroups.
-constexpr int kExchangeWords = 32768;
-// Calls of so few workgroups are one launch, whose last workgroup adds up the
-// tokens.  All count themselves at one address, so many take longer than a
-// second launch: 36, 128, 256, 1024 workgroups 8.8, 8.9, 9.1, 12.7 us against 12.2
-// with two.
-constexpr int kArriveGroups = 256;
-struct Exchange {
-  uint64_t* words = nullptr;
-  bool dirty = false;  // a call failed between its launches
-};
 // Loss, and gradient where grad.base is set, in one pass over the scores.
 hipError_t launch_policy(hipStream_t s, const LossArgs& a, RowsRef grad, const PolicyArgs& p, Exchange& x);
 
@@ -85,7 +87,7 @@ struct PreferenceArgs {
   float* g;       // [batch] gradient in each log-probability of a sequence
   double* terms;  // [pairs][3] loss, margin, won
 };
-hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, const PreferenceArgs& p);
+hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, const PreferenceArgs& p, Exchange& x);
 
 // ---------------------------------------------------------------------------
 // gradient norm and scaling (grad_clip.hip)

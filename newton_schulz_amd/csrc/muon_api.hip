@@ -98,7 +98,7 @@ muon_status_t muon_create(int device, size_t workspace_bytes, muon_ctx_t** out) 
             hipSuccess;
   ok = ok && hipMalloc(reinterpret_cast<void**>(&c->dev_tab), tab_bytes) == hipSuccess;
   ok = ok && hipHostMalloc(reinterpret_cast<void**>(&c->host_tab), tab_bytes, 0) == hipSuccess;
-  const size_t words = sizeof(uint64_t) * (kExchangeWords + 1);
+  const size_t words = sizeof(uint64_t) * (kExchangeWords + kCounters * kCounterWords);
   ok = ok && hipMalloc(reinterpret_cast<void**>(&c->exchange.words), words) == hipSuccess;
   ok = ok && hipMemset(c->exchange.words, 0, words) == hipSuccess;
   for (int i = 0; ok && i < kTabSlots; ++i)

@@ -3,8 +3,9 @@ the binary64 oracle (needs a gfx950 GPU).
 
 Tolerances, with u = 2^-24 (half a binary32 step, relative):
   * S = sum_v exp(z_v - M).  A term's argument has at most three roundings
-    (subtraction, the constant log2 e / T, the product), so its relative error
-    is 3 u |z_v - M| and 2 u of the exponential; averaged with the softmax,
+    (subtraction, the constant log2 e / T, the product; the constant is rounded up
+    in some places of 16 bytes and down in others, with their mean within u / 4),
+    so its relative error on average is 3 u |z_v - M| and 2 u of the exponential; averaged with the softmax,
     E[M - z] <= entropy <= log V.  Sums of at most n terms per thread and the
     joins add at most (n + n / 4 * 3 + 40) u: a rescale (product, exponential)
     for every 16 bytes of scores, 40 for the joins across threads.
@@ -542,3 +543,41 @@ def test_timing_class(ctx):
     c.token_logps(x, y, torch.empty(1, 4, device=DEV))
     assert c.timing_read()["loss"][1] == 1
     c.close()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_calls_of_one_launch_and_of_several(ctx, dtype):
+    """Small calls leave the rest of the work to their last workgroup, which has
+    to leave the exchange words empty for the next call: sizes on both sides of
+    the limit, in turn, twice; every repeat gives the same bits, and the results
+    are the oracle's."""
+    shapes = [(2, 512, 300), (2, 513, 300), (2, 1, 151936), (4, 64, 50257), (2, 1, 5), (4, 100, 50257), (16, 64, 77),
+              (18, 5, 9001)]
+    first = {}
+    for turn in range(2):
+        for shape in shapes:
+            batch, seq, vocab = shape
+            x, y, xn, yn = make(batch, seq, vocab, dtype, seed=vocab + seq)
+            y[0, 0] = yn[0, 0] = vocab - 1
+            y[-1] = yn[-1] = -1  # a whole sequence left out
+            ref = torch.full((batch, seq), -9.0, device=DEV)
+            lps = [torch.full((batch, seq), 3.0, device=DEV) for _ in range(3)]
+            stats, rewards = torch.empty(batch, seq, 2, device=DEV), torch.empty(batch, device=DEV)
+            out, out3 = torch.empty(4, device=DEV), torch.empty(3, device=DEV)
+            ctx.token_logps(x, y, lps[0], row_stats=stats)
+            ctx.preference_loss(x, y, ref, out3, rewards=rewards, logps=lps[1])
+            ctx.policy_loss(x, y, torch.ones(batch, device=DEV), out, old_logps=ref, logps=lps[2])
+            stats[y < 0] = 0
+            got = [v.cpu().numpy() for v in (*lps, stats, rewards, out, out3)]
+            if turn:
+                for a, b in zip(first[shape], got):
+                    assert np.array_equal(a, b), shape
+                continue
+            first[shape] = got
+            lp = lo.token_logps_ref(xn, yn)
+            tol = lp_tolerance(xn, yn, lp, 1.0)
+            for v in got[:3]:
+                same(v, lp, tol + U * np.abs(lp), f"logps {shape}")
+            valid = yn >= 0
+            score = 0.1 * np.where(valid, lp + 9.0, 0.0).sum(1)
+            same(got[4], score, 0.1 * np.where(valid, tol, 0.0).sum(1) + 3 * U * np.abs(score) + 1e-12, f"rewards {shape}")
