@@ -8,6 +8,13 @@
  *                                                 squares for the norms)
  *   - orthogonalise it by Newton-Schulz        -> muon_newton_schulz_batched
  *   - move the weight by -lr times the result  -> muon_apply
+ * and, in front of it in a post-training step:
+ *   - log-probabilities of tokens from logits  -> muon_token_logps
+ *   - the loss with the gradient of the logits -> muon_policy_loss,
+ *                                                 muon_preference_loss
+ *   - the global gradient norm and clipping    -> muon_grad_norm,
+ *                                                 muon_scale_grads,
+ *                                                 muon_momentum_update_clipped
  *
  * Conventions shared by every entry point
  *   - Tensor arguments are DEVICE pointers to memory the caller owns and
@@ -143,9 +150,10 @@ typedef struct muon_plan_s muon_plan_t;
 
 /* Create a context on HIP device `device` holding one preallocated device
  * workspace slab of `workspace_bytes` (blog section "Memory control", item 2:
- * preallocate the workspace once and only take views of it per micro-bucket).
- * This is the only call that allocates device memory.  On success *out owns
- * the slab until muon_destroy.  Errors: MUON_EINVAL (out NULL),
+ * preallocate the workspace once and only take views of it per micro-bucket),
+ * and beside it 265 KiB through which the workgroups of one loss call exchange
+ * what they found.  This is the only call that allocates device memory.  On
+ * success *out owns the slab until muon_destroy.  Errors: MUON_EINVAL (out NULL),
  * MUON_EHIP (no such device / allocation failed), MUON_ENOMEM. */
 muon_status_t muon_create(int device, size_t workspace_bytes, muon_ctx_t** out);
 
