@@ -47,10 +47,14 @@
 #include <algorithm>
 #include <cfloat>
 
+#include "exchange.h"
 #include "loss_kernels.h"
 #include "muon_device.h"
 
 using muon::bf16_t;
+using muon::last_to_arrive;
+using muon::publish;
+using muon::published;
 
 namespace {
 
@@ -341,40 +345,6 @@ __device__ __forceinline__ void slice_pair(const T* row, const RowShape& sh, int
     take_scores(v, m, s, scale);
   }
   block_join<kThreads>(m, s, scale);
-}
-
-// Exchange between the workgroups of one launch.  What is exchanged goes
-// through agent-scope atomics, which do not stay in the L2 of one of the eight
-// XCDs; a workgroup waits for its stores to have arrived and then counts
-// itself.  (A release at that point would write back the whole L2 for stores
-// that nobody in the launch reads: with it, scoring 2044 x 151936 scores took 1109 us
-// instead of 90.)
-__device__ __forceinline__ void publish(uint64_t* to, uint64_t v) {
-  __hip_atomic_store(to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ uint64_t published(const uint64_t* from) {
-  return __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-// Whether all other workgroups of the launch have counted themselves; called by
-// the thread that published.  kCountedTogether workgroups share a counter, and
-// the last of them counts for all in the first: at one address 480 workgroups
-// wait 5 us for each other, in this way 1.
-__device__ __forceinline__ unsigned count_one(uint64_t* at) {
-  return __hip_atomic_fetch_add(reinterpret_cast<unsigned*>(at), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ bool arrive_last(uint64_t* counters) {
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  const unsigned g = blockIdx.x / kCountedTogether, groups = (gridDim.x - 1) / kCountedTogether + 1;
-  const unsigned in_group = min(gridDim.x - g * kCountedTogether, static_cast<unsigned>(kCountedTogether));
-  uint64_t* mine = counters + (1 + g) * kCounterWords;
-  bool last = count_one(mine) == in_group - 1;
-  if (last) {
-    *mine = 0;
-    last = count_one(counters) == groups - 1;
-    if (last) *counters = 0;
-  }
-  asm volatile("" ::: "memory");
-  return last;
 }
 
 // Two numbers as one 64-bit word.
@@ -732,14 +702,6 @@ __device__ __forceinline__ void slice_work(const LossArgs& a, const RowsRef& gra
   }
 }
 
-// Whether this workgroup is the last one of the launch to get here.
-__device__ __forceinline__ bool last_to_arrive(const LossArgs& a) {
-  __shared__ int last;
-  if (threadIdx.x == 0) last = arrive_last(a.arrived);
-  __syncthreads();
-  return last;
-}
-
 // Every row of a small call joined by its last workgroup, a thread per row, and
 // the exchange words left as they were found, all zero.
 template <typename T> __device__ __forceinline__ void join_rows(const LossArgs& a) {
@@ -773,7 +735,7 @@ template <typename T, int NV, int USE>
 __global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef grad, PolicyArgs p) {
   slice_work<T, NV, USE>(a, grad, p);
   // A small call is one launch: its last workgroup does the rest.
-  if (a.arrived == nullptr || !last_to_arrive(a)) return;
+  if (a.arrived == nullptr || !last_to_arrive(a.arrived)) return;
   if (USE == USE_STATS) {
     join_rows<T>(a);
     return;
@@ -1057,7 +1019,7 @@ __global__ __launch_bounds__(kTermThreads) void preference_pairs_kernel(LossArgs
 template <typename T, int NV>
 __global__ __launch_bounds__(kThreads) void slice_pairs_kernel(LossArgs a, PreferenceArgs p) {
   slice_work<T, NV, USE_STATS>(a, RowsRef{}, PolicyArgs{});
-  if (!last_to_arrive(a)) return;
+  if (!last_to_arrive(a.arrived)) return;
   join_rows<T>(a);
   __syncthreads();
   a.slices = 1;  // (the rows' log-probabilities are whole)
@@ -1134,7 +1096,7 @@ hipError_t slices(hipStream_t s, const LossArgs& a, RowsRef grad, const P& p) {
 }  // namespace
 
 // Empties the exchange words if a call failed half way.
-static hipError_t clear_exchange(hipStream_t s, Exchange& x) {
+hipError_t clear_exchange(hipStream_t s, Exchange& x) {
   if (!x.dirty) return hipSuccess;
   clear_words_kernel<<<8, kTermThreads, 0, s>>>(x.words, kExchangeWords + kCounters * kCounterWords);
   const hipError_t e = hipGetLastError();

@@ -422,7 +422,7 @@ muon_status_t muon_grad_norm(muon_ctx_t* c, void* stream, const muon_tensor_t* g
   hipStream_t s = static_cast<hipStream_t>(stream);
   return timed(c, s, MUON_K_CLIP, "gradient norm launch", [&] {
     return launch_grad_norm(s, grads, count, clip_chunk(total), reinterpret_cast<double*>(c->ws), max_norm, eps,
-                            norm);
+                            norm, c->exchange);
   });
 }
 

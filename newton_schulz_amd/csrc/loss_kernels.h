@@ -28,6 +28,8 @@ struct Exchange {
   uint64_t* words = nullptr;
   bool dirty = false;  // a call failed between its launches
 };
+// Empties the words if a call failed half way.
+hipError_t clear_exchange(hipStream_t s, Exchange& x);
 
 struct LossArgs {
   RowsRef x;
@@ -101,7 +103,7 @@ constexpr int kClipJoin = 32;  // workgroups that add up many partials; room for
 
 
 hipError_t launch_grad_norm(hipStream_t s, const muon_tensor_t* t, int64_t count, int64_t chunk,
-                            double* partial, double max_norm, double eps, double* norm);
+                            double* partial, double max_norm, double eps, double* norm, Exchange& x);
 hipError_t launch_clip_coef(hipStream_t s, double max_norm, double eps, double* norm);
 hipError_t launch_scale_grads(hipStream_t s, const muon_tensor_t* t, const muon_tensor_t* out,
                               int64_t count, int64_t chunk, const double* norm);

@@ -196,3 +196,26 @@ def test_clipping_in_a_recorded_graph(ctx):
         want, eager = torch.empty_like(norm), [torch.empty_like(t) for t in ts]
         ctx.clip_grads(ts, want, max_norm=0.5, out=eager)
         assert torch.equal(norm, want) and all(torch.equal(a, b) for a, b in zip(outs, eager)), k
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_lists_of_one_launch_and_of_several(ctx, dtype):
+    """Sizes on both sides of the limit of a single launch (1024 chunks of 2048
+    to 8192 elements, 128 tensors), in turn, twice, with a loss call between."""
+    lists = [[1 << 21], [(1 << 21) - 2048, 1, 1], [2049] * 127, [2049] * 129, [(1 << 23) - 4096], [1 << 23, 5], [3]]
+    first = {}
+    logits, labels = torch.randn(4, 9, 700, device=DEV), torch.zeros(4, 9, dtype=torch.int64, device=DEV)
+    logps = torch.empty(4, 9, device=DEV)
+    for turn in range(2):
+        for i, sizes in enumerate(lists):
+            ts = tensors(sizes, dtype, seed=i)
+            norm = torch.full((3,), -1.0, dtype=torch.float64, device=DEV)
+            ctx.grad_norm(ts, norm, max_norm=2.0)
+            ctx.token_logps(logits, labels, logps)
+            got = norm.cpu().numpy()
+            if turn:
+                assert np.array_equal(got, first[i]), sizes
+                continue
+            first[i] = got
+            want = lo.grad_norm_ref([t.double().cpu().numpy() for t in ts], 2.0)
+            assert np.abs(got - want).max() <= (sum(sizes) + 4) * 2.0 ** -53 * max(want[0], 1.0), sizes
