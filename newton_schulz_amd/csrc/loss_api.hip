@@ -20,7 +20,7 @@ inline size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 // What the kernels of one loss call hand each other, for the finest slicing
 // that `cus` compute units can ask for.
 struct LossLayout {
-  size_t part, stats, lp, terms, weights, pairs, sums, total;
+  size_t part, stats, lp, terms, weights, pairs, sums, total;  // (lp: in the policy loss the labels' scores)
 };
 
 LossLayout loss_layout(int64_t batch, int64_t seq, int slices) {
@@ -298,6 +298,7 @@ muon_status_t muon_policy_loss(muon_ctx_t* c, void* stream, const muon_logits_t*
   t.out = out;
   t.weights = reinterpret_cast<uint64_t*>(c->ws + l.weights);
   t.terms = reinterpret_cast<uint64_t*>(c->ws + l.terms);
+  t.scores = reinterpret_cast<uint64_t*>(c->ws + l.lp);
   t.sums = reinterpret_cast<double*>(c->ws + l.sums);
   hipStream_t s = static_cast<hipStream_t>(stream);
   return timed(c, s, MUON_K_LOSS, "policy loss launch",

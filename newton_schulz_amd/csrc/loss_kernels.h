@@ -71,6 +71,7 @@ struct PolicyArgs {
   float* out;
   uint64_t* weights;  // [batch] weight of a sequence's tokens (binary64), or one for all
   uint64_t* terms;    // [rows][2] words of pg and kl, and of clipped
+  uint64_t* scores;   // [rows] the label's score, where the workgroup of its slice stopped waiting
   double* sums;       // [kPolicySums][3]
   // set by the launcher
   int count_here;     // the slices count the tokens and publish the weights
