@@ -133,15 +133,16 @@ template <typename T> __device__ __forceinline__ T* row_at(const RowsRef& x, int
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-// log2 e / T = k + rest; exp(d / T) for d <= 0.  (-infinity is taken as the
-// lowest finite number, whose product with a rest below 0 is finite too.)
+// log2 e / T = k + rest; exp(d / T) for d <= 0.  -infinity is taken as the lowest
+// finite number, and its product with a rest below 0, which is infinite for k
+// above 2^24, as the largest: f k, 2^24 times that, decides.
 struct Scale {
   float k, rest;
   const float (&each)[8];  // for the scores of a piece
   __device__ __forceinline__ explicit Scale(const LossArgs& a) : k(a.k), rest(a.k_rest), each(a.k_each) {}
   __device__ __forceinline__ float exp(float d) const {
     const float f = fmaxf(d, kLowest);
-    return exp2_fast(__builtin_fmaf(f, k, f * rest));
+    return exp2_fast(__builtin_fmaf(f, k, fminf(f * rest, FLT_MAX)));
   }
 };
 
