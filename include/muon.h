@@ -152,8 +152,9 @@ typedef struct muon_plan_s muon_plan_t;
  * workspace slab of `workspace_bytes` (blog section "Memory control", item 2:
  * preallocate the workspace once and only take views of it per micro-bucket),
  * and beside it 265 KiB through which the workgroups of one loss call exchange
- * what they found.  This is the only call that allocates device memory.  On
- * success *out owns the slab until muon_destroy.  Errors: MUON_EINVAL (out NULL),
+ * what they found.  This is the only call that allocates device memory.  It
+ * waits for the device's null stream, so that the context is ready for every
+ * stream.  On success *out owns the slab until muon_destroy.  Errors: MUON_EINVAL (out NULL),
  * MUON_EHIP (no such device / allocation failed), MUON_ENOMEM. */
 muon_status_t muon_create(int device, size_t workspace_bytes, muon_ctx_t** out);
 

@@ -101,6 +101,9 @@ muon_status_t muon_create(int device, size_t workspace_bytes, muon_ctx_t** out) 
   const size_t words = sizeof(uint64_t) * (kExchangeWords + kCounters * kCounterWords);
   ok = ok && hipMalloc(reinterpret_cast<void**>(&c->exchange.words), words) == hipSuccess;
   ok = ok && hipMemset(c->exchange.words, 0, words) == hipSuccess;
+  // zeros before the first call, whatever its stream: the fill runs on the null
+  // stream, which non-blocking streams are not ordered behind, and may queue there
+  ok = ok && hipStreamSynchronize(nullptr) == hipSuccess;
   for (int i = 0; ok && i < kTabSlots; ++i)
     ok = hipEventCreateWithFlags(&c->tab_ev[i], hipEventDisableTiming) == hipSuccess;
   if (!ok) {
