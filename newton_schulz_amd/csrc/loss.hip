@@ -1125,12 +1125,13 @@ hipError_t slices(hipStream_t s, const LossArgs& a, RowsRef grad, const P& p) {
 
 }  // namespace
 
-// Empties the exchange words if a call failed half way.
 hipError_t clear_exchange(hipStream_t s, Exchange& x) {
   if (!x.dirty) return hipSuccess;
   clear_words_kernel<<<8, kTermThreads, 0, s>>>(x.words, kExchangeWords + kCounters * kCounterWords);
   const hipError_t e = hipGetLastError();
-  if (e == hipSuccess) x.dirty = false;
+  // a launch that only goes into a graph has emptied nothing yet
+  hipStreamCaptureStatus c = hipStreamCaptureStatusNone;
+  if (e == hipSuccess && hipStreamIsCapturing(s, &c) == hipSuccess && c == hipStreamCaptureStatusNone) x.dirty = false;
   return e;
 }
 
@@ -1186,6 +1187,14 @@ hipError_t launch_policy(hipStream_t s, const LossArgs& args, RowsRef grad, cons
   const int64_t sets = p.p.reduce == MUON_REDUCE_SEQUENCE ? p.batch : 1;
   const bool kept = slots + sets <= kExchangeWords;
   hipError_t e = hipSuccess;
+  // words that a launch has filled and none after it will empty
+  auto failed = [&](hipError_t why) {
+    if (kept) {
+      x.dirty = true;
+      (void)clear_exchange(s, x);  // now if that is possible: a recorded call would not ask
+    }
+    return why;
+  };
   if (kept) {
     e = clear_exchange(s, x);
     if (e != hipSuccess) return e;
@@ -1194,25 +1203,23 @@ hipError_t launch_policy(hipStream_t s, const LossArgs& args, RowsRef grad, cons
     p.count_here = 1;
     p.clear = static_cast<int>(slots + sets);
     if (a.rows > 0 && slots <= kArriveGroups) a = in_one_launch(a, x);
-    x.dirty = true;  // until every launch below is in the stream
   } else {
     const int64_t clear = std::min<int64_t>(128, (slots + kTermThreads - 1) / kTermThreads);
     policy_prepare_kernel<<<static_cast<unsigned>(std::max(clear, sets)), kTermThreads, 0, s>>>(p, a.part, slots);
     e = hipGetLastError();
   }
-  if (e == hipSuccess) e = a.bf16 ? slices<bf16_t, USE_POLICY>(s, a, grad, p) : slices<float, USE_POLICY>(s, a, grad, p);
   if (e != hipSuccess) return e;
+  e = a.bf16 ? slices<bf16_t, USE_POLICY>(s, a, grad, p) : slices<float, USE_POLICY>(s, a, grad, p);
+  if (e != hipSuccess) return failed(e);
   if (a.arrived == nullptr) {
     const int n = kept ? 1 : std::min(kPolicySums, std::max(1, a.rows / 8192));
     policy_sums_kernel<<<static_cast<unsigned>(n), kTermThreads, 0, s>>>(p, a.rows, a.part);
     e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess) return failed(e);
     if (n > 1) policy_total_kernel<<<1, 1, 0, s>>>(p, n);
     e = hipGetLastError();
-    if (e != hipSuccess) return e;
   }
-  if (kept) x.dirty = false;
-  return hipSuccess;
+  return e;
 }
 
 hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, const PreferenceArgs& p, Exchange& x) {

@@ -28,7 +28,8 @@ struct Exchange {
   uint64_t* words = nullptr;
   bool dirty = false;  // a call failed between its launches
 };
-// Empties the words if a call failed half way.
+// Empties the words if a call failed half way; recorded into a graph it leaves
+// `dirty` as it is, so that calls before the first replay empty them too.
 hipError_t clear_exchange(hipStream_t s, Exchange& x);
 
 struct LossArgs {
