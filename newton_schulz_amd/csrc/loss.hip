@@ -778,7 +778,7 @@ __global__ __launch_bounds__(kThreads) void slice_kernel(LossArgs a, RowsRef gra
 
 // Joins the slices of each row; one wave per row.
 __global__ __launch_bounds__(kThreads) void row_join_kernel(LossArgs a) {
-  const int r = static_cast<int>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int r = a.row0 + static_cast<int>(blockIdx.x) * (kThreads / 64) + (threadIdx.x >> 6), lane = threadIdx.x & 63;
   if (r >= a.rows) return;
   const int64_t y = a.labels[r];
   float m = 0.0f;
@@ -875,11 +875,11 @@ __global__ __launch_bounds__(kThreads) void logits_grad_kernel(LossArgs a, RowsR
 constexpr int kTermThreads = 1024;
 
 // Before the slices of a policy loss too large for the exchange words: the
-// weights (workgroup b: sequence b, workgroup 0: all tokens), and empty slots
-// for the slices' pairs.
-__global__ __launch_bounds__(kTermThreads) void policy_prepare_kernel(PolicyArgs p, uint64_t* slots, int64_t n) {
-  const int t = static_cast<int>(threadIdx.x), b = static_cast<int>(blockIdx.x);
-  for (int64_t i = static_cast<int64_t>(b) * kTermThreads + t; i < n; i += static_cast<int64_t>(gridDim.x) * kTermThreads)
+// weights (workgroup b: sequence first + b, or all tokens), and empty slots for
+// the slices' pairs.
+__global__ __launch_bounds__(kTermThreads) void policy_prepare_kernel(PolicyArgs p, uint64_t* slots, int64_t n, int first) {
+  const int t = static_cast<int>(threadIdx.x), b = first + static_cast<int>(blockIdx.x);
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kTermThreads + t; i < n; i += static_cast<int64_t>(gridDim.x) * kTermThreads)
     slots[i] = 0;
   if (b >= (p.p.reduce == MUON_REDUCE_SEQUENCE ? p.batch : 1)) return;
   const double weight = token_weight<kTermThreads>(p, b);
@@ -1041,8 +1041,8 @@ __device__ __forceinline__ void pairs_work(const LossArgs& a, const PreferenceAr
   }
 }
 
-__global__ __launch_bounds__(kTermThreads) void preference_pairs_kernel(LossArgs a, PreferenceArgs p, int n) {
-  pairs_work<kTermThreads>(a, p, static_cast<int>(blockIdx.x) * n, n);
+__global__ __launch_bounds__(kTermThreads) void preference_pairs_kernel(LossArgs a, PreferenceArgs p, int first, int n) {
+  pairs_work<kTermThreads>(a, p, first + static_cast<int>(blockIdx.x) * n, n);
 }
 
 // A small call of few pairs: its last workgroup joins the rows and scores them.
@@ -1079,8 +1079,11 @@ int loss_slices(int64_t rows, int64_t vocab, int bf16, int cus) {
   return static_cast<int>(std::max<int64_t>(1, std::max(least, std::min(idle, most))));
 }
 
-// Rows of one launch when each takes `per` workgroups: a grid holds fewer than
-// 2^32 threads.
+// A grid holds fewer than 2^32 threads; more rows, sequences or pairs are several
+// launches.
+constexpr int kMostTermGroups = 1 << 20;  // workgroups of kTermThreads in one launch
+
+// Rows of one launch when each takes `per` workgroups.
 static int rows_per_launch(int64_t per) {
   const int64_t n = 0xff0000 / per;  // of 256 threads
   return static_cast<int>(n > 1 ? n : 1);
@@ -1154,11 +1157,17 @@ hipError_t launch_row_stats(hipStream_t s, const LossArgs& a, Exchange& x) {
     const hipError_t e = clear_exchange(s, x);
     return e == hipSuccess ? launch_slice_stats(s, in_one_launch(a, x)) : e;
   }
-  const hipError_t e = launch_slice_stats(s, a);
+  hipError_t e = launch_slice_stats(s, a);
   if (e != hipSuccess) return e;
-  const unsigned blocks = static_cast<unsigned>((static_cast<int64_t>(a.rows) + kThreads / 64 - 1) / (kThreads / 64));
-  row_join_kernel<<<blocks, kThreads, 0, s>>>(a);
-  return hipGetLastError();
+  LossArgs c = a;
+  constexpr int kRows = kThreads / 64;  // of a workgroup
+  const int step = rows_per_launch(1) * kRows;
+  for (c.row0 = 0; c.row0 < a.rows; c.row0 += step) {
+    row_join_kernel<<<static_cast<unsigned>((std::min(step, a.rows - c.row0) + kRows - 1) / kRows), kThreads, 0, s>>>(c);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 hipError_t launch_logits_grad(hipStream_t s, const LossArgs& a, RowsRef grad, const float* g, bool per_sequence) {
@@ -1205,10 +1214,14 @@ hipError_t launch_policy(hipStream_t s, const LossArgs& args, RowsRef grad, cons
     if (a.rows > 0 && slots <= kArriveGroups) a = in_one_launch(a, x);
   } else {
     const int64_t clear = std::min<int64_t>(128, (slots + kTermThreads - 1) / kTermThreads);
-    policy_prepare_kernel<<<static_cast<unsigned>(std::max(clear, sets)), kTermThreads, 0, s>>>(p, a.part, slots);
-    e = hipGetLastError();
+    const int64_t groups = std::max(clear, sets);
+    for (int64_t first = 0; first < groups && e == hipSuccess; first += kMostTermGroups) {
+      const unsigned grid = static_cast<unsigned>(std::min<int64_t>(groups - first, kMostTermGroups));
+      policy_prepare_kernel<<<grid, kTermThreads, 0, s>>>(p, a.part, first ? 0 : slots, static_cast<int>(first));
+      e = hipGetLastError();
+    }
+    if (e != hipSuccess) return e;
   }
-  if (e != hipSuccess) return e;
   e = a.bf16 ? slices<bf16_t, USE_POLICY>(s, a, grad, p) : slices<float, USE_POLICY>(s, a, grad, p);
   if (e != hipSuccess) return failed(e);
   if (a.arrived == nullptr) {
@@ -1234,10 +1247,15 @@ hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, con
   } else {
     e = launch_slice_stats(s, a);
     if (e != hipSuccess) return e;
-    const unsigned grid = pairs <= kFewPairs ? 1 : static_cast<unsigned>(pairs);
-    preference_pairs_kernel<<<grid, kTermThreads, 0, s>>>(a, p, grid == 1 ? pairs : 1);
-    e = hipGetLastError();
-    if (e == hipSuccess && grid > 1) {
+    if (pairs <= kFewPairs) {
+      preference_pairs_kernel<<<1, kTermThreads, 0, s>>>(a, p, 0, pairs);
+      e = hipGetLastError();
+    }
+    for (int first = 0; pairs > kFewPairs && first < pairs && e == hipSuccess; first += kMostTermGroups) {
+      preference_pairs_kernel<<<static_cast<unsigned>(std::min(pairs - first, kMostTermGroups)), kTermThreads, 0, s>>>(a, p, first, 1);
+      e = hipGetLastError();
+    }
+    if (e == hipSuccess && pairs > kFewPairs) {
       preference_sums_kernel<<<1, kTermThreads, 0, s>>>(p);
       e = hipGetLastError();
     }
