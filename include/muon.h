@@ -539,7 +539,7 @@ muon_status_t muon_preference_loss(muon_ctx_t* ctx, void* stream, const muon_log
  * the element. */
 typedef struct {
   void* data;
-  int64_t numel;   /* >= 0 */
+  int64_t numel;   /* in [0, 1.37e11] (2^37 - 2^14); 2^40 in a whole list */
   int32_t dtype;   /* MUON_BF16 or MUON_F32 */
 } muon_tensor_t;
 

@@ -361,6 +361,10 @@ muon_status_t muon_preference_loss(muon_ctx_t* c, void* stream, const muon_logit
 namespace {
 
 constexpr int64_t kMostElements = int64_t{1} << 40;
+// Of one tensor, which is one launch: its chunks (8192 elements in lists that
+// large, and one more for where it starts) are workgroups of 256 threads, and a grid
+// holds fewer than 2^32 threads.
+constexpr int64_t kMostInTensor = ((int64_t{1} << 24) - 2) * 8192;
 
 // Each entry on its own; *total receives the elements of all.
 muon_status_t check_list(muon_ctx* c, const muon_tensor_t* t, int64_t count, int64_t* total) {
@@ -369,7 +373,7 @@ muon_status_t check_list(muon_ctx* c, const muon_tensor_t* t, int64_t count, int
   if (count > 0 && t == nullptr) return fail(c, MUON_EINVAL, "tensor list NULL");
   for (int64_t i = 0; i < count; ++i) {
     if (!is_dtype(t[i].dtype)) return fail(c, MUON_EDTYPE, "tensor dtype");
-    if (t[i].numel < 0 || t[i].numel > kMostElements) return fail(c, MUON_ESHAPE, "tensor numel");
+    if (t[i].numel < 0 || t[i].numel > kMostInTensor) return fail(c, MUON_ESHAPE, "tensor numel");
     if (t[i].numel && t[i].data == nullptr) return fail(c, MUON_EINVAL, "tensor data NULL");
     if (reinterpret_cast<uintptr_t>(t[i].data) % esize(t[i].dtype)) return fail(c, MUON_EINVAL, "misaligned tensor");
     *total += t[i].numel;
