@@ -570,7 +570,8 @@ muon_status_t muon_clip_coef(muon_ctx_t* ctx, void* stream, double max_norm, dou
  * out[i]'s dtype.  out NULL: in place; a coefficient of exactly 1 then writes
  * nothing.  Otherwise out[i] has grads[i]'s numel, any dtype, and is disjoint
  * from every other tensor of both lists (out[i] == grads[i], same dtype, is
- * in place).  Errors: as for muon_grad_norm. */
+ * in place); gradients that are only read may overlap each other.  Errors: as
+ * for muon_grad_norm. */
 muon_status_t muon_scale_grads(muon_ctx_t* ctx, void* stream, const muon_tensor_t* grads,
                                const muon_tensor_t* out, int64_t count, const double* norm);
 

@@ -455,23 +455,33 @@ muon_status_t muon_scale_grads(muon_ctx_t* c, void* stream, const muon_tensor_t*
     for (int64_t i = 0; i < count; ++i)
       if (out[i].numel != grads[i].numel) return fail(c, MUON_ESHAPE, "out and grads differ in numel");
   }
-  // Every byte of either list once, but for an output that is its own input.
+  // Nothing written that is read or written elsewhere (an output that is its own
+  // input counts once); what is only read may overlap.
   try {
-    std::vector<std::pair<uintptr_t, uintptr_t>> v;
-    v.reserve(static_cast<size_t>(2 * count + 1));
-    auto add = [&](const void* p, size_t bytes) {
-      if (bytes) v.emplace_back(reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes);
+    struct Range {
+      uintptr_t from, to;
+      bool written;
     };
-    add(norm, 24);
+    std::vector<Range> v;
+    v.reserve(static_cast<size_t>(2 * count + 1));
+    auto add = [&](const void* p, size_t bytes, bool written) {
+      const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+      if (bytes) v.push_back({at, at + bytes, written});
+    };
+    add(norm, 24, false);
     for (int64_t i = 0; i < count; ++i) {
       const size_t n = static_cast<size_t>(grads[i].numel);
-      add(grads[i].data, n * esize(grads[i].dtype));
-      if (out && !(out[i].data == grads[i].data && out[i].dtype == grads[i].dtype))
-        add(out[i].data, n * esize(out[i].dtype));
+      const bool in_place = !out || (out[i].data == grads[i].data && out[i].dtype == grads[i].dtype);
+      add(grads[i].data, n * esize(grads[i].dtype), in_place);
+      if (!in_place) add(out[i].data, n * esize(out[i].dtype), true);
     }
-    std::sort(v.begin(), v.end());
-    for (size_t i = 1; i < v.size(); ++i)
-      if (v[i].first < v[i - 1].second) return fail(c, MUON_EINVAL, "tensors overlap");
+    std::sort(v.begin(), v.end(), [](const Range& a, const Range& b) { return a.from < b.from; });
+    uintptr_t any = 0, written = 0;  // ends of what came before
+    for (const Range& r : v) {
+      if (r.from < (r.written ? any : written)) return fail(c, MUON_EINVAL, "tensors overlap");
+      any = std::max(any, r.to);
+      if (r.written) written = std::max(written, r.to);
+    }
   } catch (...) {
     return fail(c, MUON_ENOMEM, "host memory");
   }

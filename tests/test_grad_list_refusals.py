@@ -30,3 +30,31 @@ def test_a_tensor_fits_one_launch():
     # longer lists take more launches
     assert norm(*[(0x10000 + i * most * 2, most, MUON_BF16) for i in range(9)]) == (MUON_ESHAPE, "too many elements")
     assert norm(*[(0x10000 + i * most * 2, most, MUON_BF16) for i in range(8)]) == (MUON_EINVAL, "context NULL")
+
+
+def scale(grads, out):
+    return answer(_lib.load().muon_scale_grads(None, None, tensors(*grads), tensors(*out) if out else None, len(grads), NORM))
+
+
+FINE, OVERLAP = (MUON_EINVAL, "context NULL"), (MUON_EINVAL, "tensors overlap")
+
+
+def test_gradients_that_are_only_read_may_overlap():
+    """One gradient scaled into two buffers, views of one buffer: every output
+    has its own place, so the results do not depend on any order."""
+    a, part, b, c = (0x10000, 16, MUON_F32), (0x10010, 4, MUON_F32), (0x20000, 16, MUON_F32), (0x30000, 16, MUON_BF16)
+    small = (0x40000, 4, MUON_F32)
+    assert scale([a, a], [b, c]) == FINE
+    assert scale([a, part], [b, small]) == FINE
+    assert scale([part, a], [small, b]) == FINE
+    # but nothing that is written
+    assert scale([a, a], None) == OVERLAP
+    assert scale([a, part], None) == OVERLAP
+    assert scale([a, a], [a, b]) == OVERLAP
+    assert scale([a, a], [b, a]) == OVERLAP
+    assert scale([a, part], [b, part]) == OVERLAP
+    assert scale([a, part], [a, small]) == OVERLAP
+    assert scale([a, b], [c, (0x30010, 16, MUON_BF16)]) == OVERLAP
+    # one that lies inside another and ends first does not hide the overlap of the next
+    assert scale([a, part, b], [c, small, (0x1003c, 16, MUON_F32)]) == OVERLAP
+    assert scale([a], [(NORM + 8, 16, MUON_F32)]) == OVERLAP
