@@ -100,7 +100,6 @@ class MuonStep:
             sq = torch.empty(max(sq_blocks(self.max_bucket), 1), dtype=torch.float64, device=dev)
             self.lanes.append((ctx, upd, sq, self._bucket_work(upd)))
         _, self.update, self.sq, self._work = self.lanes[0]
-        self._grad_list = self.ctx.tensor_list([self.grad]) if self.grad_norm is not None else None
         self._side = [torch.cuda.Stream(dev) for _ in range(self.inflight - 1)]
         self._ev_start = torch.cuda.Event()
         self._ev_end = [torch.cuda.Event() for _ in self._side]
@@ -217,7 +216,7 @@ class MuonStep:
         main = stream if stream is not None else torch.cuda.current_stream(self.device)
         if self.grad_norm is not None:
             if other_grads is None:
-                self.ctx.grad_norm(self._grad_list, self.grad_norm, self.max_grad_norm, stream=main)
+                self.ctx.grad_norm([self.grad], self.grad_norm, self.max_grad_norm, stream=main)
             else:
                 others = getattr(other_grads, "tensors", other_grads)
                 self.ctx.grad_norm([self.grad, *others], self.grad_norm, self.max_grad_norm, stream=main)
