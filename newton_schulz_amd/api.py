@@ -196,6 +196,10 @@ class TensorList:
     def __len__(self):
         return len(self.tensors)
 
+    def norm_workspace_bytes(self) -> int:
+        """Workspace a context needs for grad_norm over the list."""
+        return int(_lib.load().muon_grad_norm_workspace_bytes(self.array, len(self)))
+
 
 class Context:
     """A libmuon context: one device and one preallocated workspace slab."""

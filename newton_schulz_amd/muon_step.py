@@ -34,7 +34,7 @@ from typing import List, Optional, Sequence, Tuple
 
 import torch
 
-from .api import SQ_BLOCK, Context, Plan, ns_params, sq_blocks
+from .api import SQ_BLOCK, Context, Plan, TensorList, ns_params, sq_blocks
 
 
 class MuonStep:
@@ -79,10 +79,12 @@ class MuonStep:
         workspace = self.plan.max_workspace
         if max_grad_norm is not None:
             # partial sums of the norm: 8 bytes per 2048 elements at most, and
-            # as much again (and 64 KB) for gradients that are not the step's own
+            # as much again (and 64 KB) for gradients that are not the step's own;
+            # more of those get a context of their own (_norm_context)
             workspace = max(workspace, 16 * (self.numel // 2048 + 64) + (1 << 16))
             self.grad_norm = torch.zeros(3, dtype=torch.float64, device=self.device)
         self.ctx = Context(self.device, workspace)
+        self._norm_ctx: List[Context] = []
         self._alloc_state(grad_dtype, keep_bf16_weights)
 
     def _alloc_state(self, grad_dtype: torch.dtype, keep_bf16_weights: bool):
@@ -192,6 +194,8 @@ class MuonStep:
         cur = torch.cuda.current_stream(self.device)
         side = torch.cuda.Stream(self.device)
         side.wait_stream(cur)
+        if self.grad_norm is not None and other_grads is not None:
+            self._norm_context(self._with_own(other_grads))  # what it allocates cannot be recorded
         with torch.cuda.graph(g, stream=side):
             self.step(stream=side, nonfinite_flag=nonfinite_flag, other_grads=other_grads)
         cur.wait_stream(side)
@@ -206,8 +210,26 @@ class MuonStep:
 
     @property
     def contexts(self) -> List[Context]:
-        """The lanes' contexts (per-kernel timing is kept per context)."""
-        return [lane[0] for lane in self.lanes]
+        """The lanes' contexts (per-kernel timing is kept per context), and
+        those that norms over many other gradients have needed."""
+        return [lane[0] for lane in self.lanes] + self._norm_ctx
+
+    def _with_own(self, other_grads) -> TensorList:
+        return self.ctx.tensor_list([self.grad, *getattr(other_grads, "tensors", other_grads)])
+
+    def _norm_context(self, grads: TensorList) -> Context:
+        """A context whose workspace holds the partial sums of `grads`: the
+        step's, or one made for the largest list so far (and kept: recorded
+        steps may use it), twice as large so that few are ever made."""
+        need = grads.norm_workspace_bytes()
+        for ctx in (self.ctx, *self._norm_ctx):
+            if need <= ctx.workspace_bytes:
+                return ctx
+        if torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("the norm of these gradients needs memory that cannot be allocated while a graph is "
+                               "recorded: run step() with them once before")
+        self._norm_ctx.append(Context(self.device, 2 * need))
+        return self._norm_ctx[-1]
 
     def step(self, stream=None, nonfinite_flag: Optional[torch.Tensor] = None, other_grads=None):
         """One step.  With max_grad_norm, `other_grads` (a sequence of tensors
@@ -218,8 +240,8 @@ class MuonStep:
             if other_grads is None:
                 self.ctx.grad_norm([self.grad], self.grad_norm, self.max_grad_norm, stream=main)
             else:
-                others = getattr(other_grads, "tensors", other_grads)
-                self.ctx.grad_norm([self.grad, *others], self.grad_norm, self.max_grad_norm, stream=main)
+                grads = self._with_own(other_grads)
+                self._norm_context(grads).grad_norm(grads, self.grad_norm, self.max_grad_norm, stream=main)
                 self.ctx.scale_grads(other_grads, self.grad_norm, stream=main)
         elif other_grads is not None:
             raise ValueError("other_grads needs max_grad_norm")
