@@ -187,8 +187,9 @@ class MuonStep:
         graph (stream capture through torch.cuda.CUDAGraph); replay() then
         runs it with no host work per launch.  Recording runs nothing.  The
         graph keeps what the step passed when it was recorded: lr, beta,
-        scale and weight decay, and the state buffers' addresses (their
-        contents are read at replay).  Per-kernel timing skips recorded
+        scale and weight decay, max_grad_norm, and the addresses of the state
+        buffers and of other_grads (their contents are read, and other_grads
+        scaled, at replay; the tensors are kept).  Per-kernel timing skips recorded
         launches.  Record again after changing a hyperparameter."""
         g = torch.cuda.CUDAGraph()
         cur = torch.cuda.current_stream(self.device)
@@ -200,6 +201,7 @@ class MuonStep:
             self.step(stream=side, nonfinite_flag=nonfinite_flag, other_grads=other_grads)
         cur.wait_stream(side)
         self._graph = g
+        self._graph_tensors = (self.grad, nonfinite_flag, list(getattr(other_grads, "tensors", other_grads) or ()))
         return g
 
     def replay(self):
@@ -234,7 +236,9 @@ class MuonStep:
     def step(self, stream=None, nonfinite_flag: Optional[torch.Tensor] = None, other_grads=None):
         """One step.  With max_grad_norm, `other_grads` (a sequence of tensors
         or a TensorList) are gradients of parameters that another optimizer
-        steps: they enter the norm and are scaled in place."""
+        steps: they enter the norm and are scaled in place.  Lists with more
+        partial sums than the step's workspace has room for allocate at their
+        first step."""
         main = stream if stream is not None else torch.cuda.current_stream(self.device)
         if self.grad_norm is not None:
             if other_grads is None:

@@ -1,4 +1,7 @@
 """MuonStep with clipping: whose gradients the norm is of (needs a gfx950 GPU)."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -90,4 +93,24 @@ def test_an_allocation_is_refused_while_a_graph_is_recorded():
     torch.cuda.synchronize()
     # 27000 ones and a gradient of zeros
     assert a.grad_norm[0].item() == 27000
+    close(a)
+
+
+def test_a_recorded_step_keeps_the_gradients_it_scales():
+    """Replays write to the other gradients' memory: it stays theirs although the
+    caller lets go of them, and of the step's own gradient buffer."""
+    a = make([(64, 64, 0)])
+    others = [torch.ones(1 << 20, device=DEV), torch.ones(77, device=DEV)]
+    a.capture(other_grads=others)
+    at = [t.data_ptr() for t in (a.grad, *others)]
+    kept = [weakref.ref(t) for t in (a.grad, *others)]
+    del others
+    a.grad = torch.zeros_like(a.grad)
+    gc.collect()
+    assert [t().data_ptr() for t in kept] == at
+    fresh = [torch.full((1 << 20,), 3.0, device=DEV) for _ in range(4)]
+    for _ in range(3):
+        a.replay()
+        torch.cuda.synchronize()
+        assert all((t == 3).all() for t in fresh)
     close(a)
