@@ -9,14 +9,17 @@
 // fixed order.
 //
 // Arithmetic.  Scores are widened to fp32; with k = log2 e / T, exp(z - m / T) is
-// exp2((x - m) k): the subtraction is exact for bf16, nothing large cancels at
-// any magnitude of x, and the largest score gives exactly 1.  k rounded to fp32
-// is another temperature: every log-probability over a vocabulary of 151936
-// would be off the same way, by up to 1.2e-7 on average, and the sum over a
-// sequence by as much as there are tokens.  So k is rounded up for some of the
-// scores of a piece and down for the others, as many as make its mean right to
-// 2^-28 (fp32 scores, 4 a piece: 2^-27), which leaves at most 3e-8 and costs
-// nothing (a second multiply-add with the rest at every score took scoring 6%).
+// exp2((x - m) k): the subtraction is exact for bf16 of like size, nothing large
+// cancels at any magnitude of x, and the largest score gives exactly 1.  k rounded
+// to fp32 is another temperature: every log-probability would be off the same way,
+// by up to 2^-24 of the scores' mean distance from their maximum (5 over 151936
+// normal ones: 3e-7), and the sum over a sequence by as much as there are tokens.
+// So k is rounded up for some of the scores of a piece and down for the others,
+// as many as make its mean right to 2^-27 (fp32 scores, 4 a piece: 2^-26), which
+// costs nothing (a second multiply-add with the rest at every score took scoring
+// 6%).  The mean over 1024 rows of 50257 or 151936 scores is then off by 1e-8
+// (bf16) and 3e-8 (fp32) at T = 0.83 and 1, and by 4.4e-8 and 6.6e-8 where k lies
+// half a step from fp32, next to 1.
 // Factors between two maxima take the rest along.
 // m is the running maximum of a wave; it is raised, and s scaled, only when some
 // lane has met a larger score, and the lanes' sums then join without further
