@@ -506,6 +506,7 @@ muon_status_t muon_policy_loss(muon_ctx_t* ctx, void* stream, const muon_logits_
                                const muon_logits_t* grad_logits);
 
 /* MUON_PREFERENCE_SIGMOID: -(1 - s) log sigma(h) - s log sigma(-h), h = beta m
+ *                          (s = 0: the first term alone, also where h is infinite)
  * MUON_PREFERENCE_IPO:     (m - 1 / (2 beta))^2 */
 typedef enum { MUON_PREFERENCE_SIGMOID = 0, MUON_PREFERENCE_IPO = 1 } muon_preference_t;
 

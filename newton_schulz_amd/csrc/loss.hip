@@ -1012,7 +1012,8 @@ __device__ __forceinline__ void pairs_work(const LossArgs& a, const PreferenceAr
     const double margin = score[0] - score[1], h = beta * margin;
     double loss, d;
     if (p.p.kind == MUON_PREFERENCE_SIGMOID) {
-      loss = (1.0 - eps) * neg_log_sigmoid(h) + eps * neg_log_sigmoid(-h);
+      loss = (1.0 - eps) * neg_log_sigmoid(h);
+      if (eps != 0.0) loss += eps * neg_log_sigmoid(-h);  // infinite where the rejected answer is impossible
       d = beta * (eps * sigmoid(h) - (1.0 - eps) * sigmoid(-h));
     } else {
       const double off = margin - 0.5 / beta;

@@ -116,7 +116,9 @@ def preference_ref(lp, y, ref=None, kind="sigmoid", beta=0.1, label_smoothing=0.
     m = score[:pairs] - score[pairs:]
     h = beta * m
     if kind == "sigmoid":
-        loss = (1 - label_smoothing) * np.logaddexp(0, -h) + label_smoothing * np.logaddexp(0, h)
+        loss = (1 - label_smoothing) * np.logaddexp(0, -h)
+        if label_smoothing:
+            loss = loss + label_smoothing * np.logaddexp(0, h)
         sig = np.exp(-np.logaddexp(0, -h))
         d = beta * (label_smoothing * sig - (1 - label_smoothing) * np.exp(-np.logaddexp(0, h)))
     else:
