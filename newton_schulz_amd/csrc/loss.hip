@@ -136,16 +136,16 @@ template <typename T> __device__ __forceinline__ T* row_at(const RowsRef& x, int
 
 __device__ __forceinline__ float exp2_fast(float v) { return __builtin_amdgcn_exp2f(v); }
 
-// log2 e / T = k + rest; exp(d / T) for d <= 0.  -infinity is taken as the lowest
-// finite number, and its product with a rest below 0, which is infinite for k
-// above 2^24, as the largest: f k, 2^24 times that, decides.
+// log2 e / T = k + rest; exp(d / T) for d <= 0.  What is below `none`, -infinity too,
+// is taken as that: exp2(none k) is 0, and the product with the rest, which exceeds
+// 1 for k above 2^24, is far from overflow.
 struct Scale {
-  float k, rest;
+  float k, rest, none;
   const float (&each)[8];  // for the scores of a piece
-  __device__ __forceinline__ explicit Scale(const LossArgs& a) : k(a.k), rest(a.k_rest), each(a.k_each) {}
+  __device__ __forceinline__ explicit Scale(const LossArgs& a) : k(a.k), rest(a.k_rest), none(a.none), each(a.k_each) {}
   __device__ __forceinline__ float exp(float d) const {
-    const float f = fmaxf(d, kLowest);
-    return exp2_fast(__builtin_fmaf(f, k, fminf(f * rest, FLT_MAX)));
+    const float f = fmaxf(d, none);
+    return exp2_fast(__builtin_fmaf(f, k, f * rest));
   }
 };
 

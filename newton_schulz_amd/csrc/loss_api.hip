@@ -153,6 +153,7 @@ LossArgs loss_args(const muon_ctx* c, const LossLayout& l, const muon_logits_t& 
   const double k = kLog2e / temperature;
   a.k = static_cast<float>(k);
   a.k_rest = static_cast<float>(k - static_cast<double>(a.k));
+  a.none = static_cast<float>(-256.0 / k);  // (finite: k is above 1e-30)
   // k lies between two fp32 numbers: the mean over a piece of the two is k
   const float down = static_cast<double>(a.k) <= k ? a.k : std::nextafterf(a.k, 0.0f);
   const float up = std::nextafterf(down, INFINITY);

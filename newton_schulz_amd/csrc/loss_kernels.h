@@ -39,6 +39,7 @@ struct LossArgs {
   int row0;          // first row of this launch (set by the launchers)
   const int64_t* labels;
   float k, k_rest;   // log2 e / temperature = k + k_rest, k rounded to fp32
+  float none;        // a difference of scores whose exponential is 0: 2^-256
   float k_each[8];   // its neighbours in fp32, of mean k over the 8 or 4 scores of 16 bytes
   double inv_t;      // 1 / temperature
   int slices;        // workgroups that a row is cut over
