@@ -343,7 +343,9 @@ class Context:
         """Log-probability of every row's label under softmax(logits /
         temperature) into `logps` (float32, the labels' shape; 0 where the
         label is negative).  `row_stats` (float32, [..., 2]) keeps what
-        token_logps_backward needs of each row."""
+        token_logps_backward needs of each row.  As every call here this one
+        is no autograd function: logits that require a gradient are read like
+        any others and nothing is recorded."""
         x, shape = _logits(logits, "logits", self.device), logits.shape[:-1]
         st = self.lib.muon_token_logps(
             self.handle, _stream(self.device, stream), ctypes.byref(x),
@@ -356,7 +358,8 @@ class Context:
                              grad_logps: torch.Tensor, grad_logits: torch.Tensor,
                              temperature: float = 1.0, stream=None):
         """Gradient of token_logps into `grad_logits` (the logits' dtype; may
-        be the logits themselves)."""
+        be the logits themselves, unless autograd saved them for a backward
+        pass of its own)."""
         x, shape = _logits(logits, "logits", self.device), logits.shape[:-1]
         gx = self._grad(logits, grad_logits)
         st = self.lib.muon_token_logps_backward(
@@ -374,7 +377,8 @@ class Context:
                     weight: float = 1.0, temperature: float = 1.0, stream=None):
         """Clipped policy loss with a KL term, and the gradient of weight *
         loss in the logits (`grad_logits`; None: none is formed; may be the
-        logits themselves).  advantages: float32, one per sequence ([batch])
+        logits themselves, as in token_logps_backward); hand it on with
+        logits.backward(grad_logits), no graph is recorded here.  advantages: float32, one per sequence ([batch])
         or per token.  old_logps None: the logits' own policy.  out: four
         float32 {weight * loss, policy term, KL, share clipped}.  reduce:
         "token", "sequence" or "sum"."""
@@ -406,7 +410,8 @@ class Context:
         """Preference loss over batch / 2 pairs (sequence i was preferred over
         sequence batch / 2 + i), and the gradient of weight * loss in the
         logits.  ref_logps None: no reference.  out: three float32 {weight *
-        loss, mean of beta * margin, share of pairs ranked right}.  rewards:
+        loss, mean of beta * margin, share of pairs ranked right}.
+        grad_logits: as for policy_loss.  rewards:
         float32 [batch], beta times each sequence's score.  kind: "sigmoid" or
         "ipo"; average: scores are means over a sequence's tokens."""
         x, shape = _logits(logits, "logits", self.device), logits.shape[:-1]

@@ -333,7 +333,7 @@ hipError_t launch_grad_norm(hipStream_t s, const muon_tensor_t* t, int64_t count
     return hipGetLastError();
   });
   if (e != hipSuccess || one) return e;
-  // the sums of several workgroups follow the partials (clip_partials)
+  // the sums of several workgroups follow the partials (kClipJoin of them at most)
   const int join = total > 16384 ? kClipJoin : 1;
   sum_partials_kernel<<<join, kJoinThreads, 0, s>>>(partial, total, partial + total, max_norm, eps, norm);
   if (join > 1) {

@@ -19,7 +19,7 @@ struct RowsRef {
 // Counters of a call's workgroups lie behind them, in different channels.
 constexpr int kExchangeWords = 32768;
 // Calls of so few workgroups are one launch, whose last workgroup does what is
-// left.  Against a launch more: 480 workgroups of log-probabilities 8.9 and 10.3 us
+// left.  Against a launch more: 480 workgroups of log-probabilities 8.5 and 10.3 us
 // (12.7 if all count themselves at one address), 564 of the policy loss 10.4 and
 // 13.6, 198 of the preference loss 14.0 and 16.9, 536 of it 16.8 and 16.9.
 constexpr int kArriveGroups = 1024;
@@ -103,7 +103,6 @@ hipError_t launch_preference(hipStream_t s, const LossArgs& a, RowsRef grad, con
 int64_t clip_chunk(int64_t total);
 int64_t clip_chunks(const muon_tensor_t& t, int64_t chunk);
 constexpr int kClipJoin = 32;  // workgroups that add up many partials; room for their sums follows the partials
-
 
 hipError_t launch_grad_norm(hipStream_t s, const muon_tensor_t* t, int64_t count, int64_t chunk,
                             double* partial, double max_norm, double eps, double* norm, Exchange& x);
