@@ -15,6 +15,13 @@
  *   - the global gradient norm and clipping    -> muon_grad_norm,
  *                                                 muon_scale_grads,
  *                                                 muon_momentum_update_clipped
+ * Around the layers whose weights it moves:
+ *   - 8-bit rows of activations and weights    -> muon_quantize_rows,
+ *                                                 muon_dequantize_rows
+ *   - products of them, and a layer's forward  -> muon_matmul8, muon_linear8
+ *   - gradients out of what was kept           -> muon_input_grad8,
+ *                                                 muon_weight_grad8
+ *   - verification of drafted tokens           -> muon_verify_draft
  *
  * Conventions shared by every entry point
  *   - Tensor arguments are DEVICE pointers to memory the caller owns and
@@ -589,6 +596,141 @@ muon_status_t muon_momentum_update_clipped(muon_ctx_t* ctx, void* stream, const 
                                            double* sq_partials);
 
 /* ------------------------------------------------------------------------ */
+/* Linear layers in 8 bits                                                   */
+/* ------------------------------------------------------------------------ */
+
+/* A linear layer is y = x w^T: x tokens x k, w n x k (a matrix that the step
+ * moves, one row per output channel), y tokens x n.  Its forward product runs
+ * in 8-bit integers with a scale for each token and each channel, the integers
+ * of x are what is kept for the backward pass (one byte an activation), and
+ * the gradients are formed out of them.
+ *
+ * Rows of values: element (r, c) at data + (r * row_stride + c) elements of
+ * `dtype`.  The stride (elements, >= 0; of a single row it is ignored) may
+ * exceed cols; rows that are written must be disjoint. */
+typedef struct {
+  void* data;
+  int32_t dtype;       /* MUON_BF16 or MUON_F32 */
+  int64_t rows, cols;  /* rows in [0, MUON_MAX_ROWS8], cols >= 1 */
+  int64_t row_stride;
+} muon_rows_t;
+
+/* 8-bit rows: element (r, c) is scale[r] * data[r * row_stride + c].  Rows
+ * start at multiples of 16 bytes (data and row_stride; the bytes between a
+ * row's end and the next multiple of 16 may be read, their values do not
+ * matter, and are never written; the last row's need not exist).  scale:
+ * `rows` floats.  Integers range over [-128, 127]. */
+#define MUON_MAX_ROWS8 (1 << 24)
+#define MUON_MAX_COLS8 131071 /* 128 * 128 * cols < 2^31: a product's sum fits 32 bits */
+typedef struct {
+  int8_t* data;
+  float* scale;
+  int64_t rows, cols;  /* cols in [1, MUON_MAX_COLS8] */
+  int64_t row_stride;  /* bytes */
+} muon_rows8_t;
+
+/* Errors of the calls below: MUON_EINVAL (ctx or another required pointer
+ * NULL, misaligned pointers, outputs that overlap another argument or their
+ * own rows), MUON_ESHAPE (sizes out of range or not matching), MUON_EDTYPE,
+ * MUON_EWORKSPACE, MUON_EHIP.  Arrays without elements may be NULL.  Two calls
+ * on identical inputs give identical bits; every call may be recorded into a
+ * HIP graph.  The workspace is the context's, so calls on one context are
+ * ordered. */
+
+/* q = x in 8 bits, a scale per row:
+ *     scale[r] = max_c |x[r][c]| / 127              (one binary32 rounding; at
+ *                most 0x1.020406p+121, so that 127 scale is finite)
+ *     q[r][c]  = x[r][c] / scale[r] to the nearest integer, ties to even, of
+ *                the exact quotient; in [-127, 127]
+ * A row of zeros, or one whose scale rounds to 0, has scale 0 and integers 0.
+ * A row with a NaN or an infinity has scale NaN and integers 0: its values are
+ * NaN, as is what is formed out of them. */
+muon_status_t muon_quantize_rows(muon_ctx_t* ctx, void* stream, const muon_rows_t* x,
+                                 const muon_rows8_t* q);
+
+/* out = scale * q, one binary32 rounding, then to out's dtype. */
+muon_status_t muon_dequantize_rows(muon_ctx_t* ctx, void* stream, const muon_rows8_t* q,
+                                   const muon_rows_t* out);
+
+/* Workspace in bytes of any of the calls below for a layer of n x k weights
+ * and up to `tokens` tokens (pure host function; 0 for arguments out of
+ * range). */
+size_t muon_linear8_workspace_bytes(int64_t tokens, int64_t n, int64_t k);
+
+/* out[m][n] = (sum_k a[m][k] b[n][k]) * (a.scale[m] * b.scale[n]): the integers'
+ * sum exact, rounded to binary32, each product one binary32 rounding, then to
+ * out's dtype. */
+muon_status_t muon_matmul8(muon_ctx_t* ctx, void* stream, const muon_rows8_t* a,
+                           const muon_rows8_t* b, const muon_rows_t* out);
+
+/* muon_quantize_rows of x, and muon_matmul8 of that with w.  x8 (tokens x k)
+ * receives the integers and scales, for the backward pass; NULL: they stay in
+ * the workspace (nothing is kept). */
+muon_status_t muon_linear8(muon_ctx_t* ctx, void* stream, const muon_rows_t* x,
+                           const muon_rows8_t* w, const muon_rows8_t* x8, const muon_rows_t* out);
+
+/* The layer's gradients, straight through the rounding of x and w:
+ *     grad_x[t][k] = sum_n grad_y[t][n] w[n][k]       w, x: the values that the
+ *     grad_w[n][k] = sum_t grad_y[t][n] x[t][k]       8-bit rows stand for
+ * grad_y: tokens x n, BF16.  bf16 matrix products accumulated in fp32.  For a
+ * BF16 output the values of w (x) may be rounded to bf16 (2^-8, what
+ * activations kept in bf16 would have); for an F32 output they enter with
+ * 2^-16 at least.  accumulate != 0: the sum is added to what the output
+ * holds (in fp32, one rounding), else it replaces it. */
+muon_status_t muon_input_grad8(muon_ctx_t* ctx, void* stream, const muon_rows_t* grad_y,
+                               const muon_rows8_t* w, const muon_rows_t* grad_x,
+                               int32_t accumulate);
+muon_status_t muon_weight_grad8(muon_ctx_t* ctx, void* stream, const muon_rows_t* grad_y,
+                                const muon_rows8_t* x, const muon_rows_t* grad_w,
+                                int32_t accumulate);
+
+/* ------------------------------------------------------------------------ */
+/* Verification of drafted tokens                                            */
+/* ------------------------------------------------------------------------ */
+
+/* Workspace in bytes of muon_verify_draft (pure host function; 0 for arguments
+ * out of range). */
+size_t muon_verify_workspace_bytes(int64_t batch, int64_t draft, int64_t vocab);
+
+/* Which of the tokens that a draft proposed the target keeps, and the token
+ * behind them, so that what comes out is distributed as if the target had
+ * been sampled token by token.
+ *   logits: batch x (draft + 1) rows of the target's scores, row i those of
+ *     the token at place i given all before it.
+ *   draft_tokens: [batch][draft]; a sequence's draft ends at its first
+ *     negative token (or after `draft`).  A token >= vocab has probability 0.
+ *   draft_logits: the scores that the drafted tokens were sampled from, batch x
+ *     draft rows (batch x 0 .. if draft is 0), any dtype; NULL: the draft was
+ *     deterministic, all of its probability at the token.
+ *   uniforms: [batch][draft + 1] in [0, 1).
+ * With p_i, q_i the softmax of row i's scores over the temperature, place
+ * i = 0, 1, ... keeps its drafted token x while
+ *     uniforms[i] * q_i(x) < p_i(x),
+ * and the first place r that does not, or that has no drafted token, takes the
+ * token v that is drawn by u = uniforms[draft] from the weights
+ *     w_v = max(p_r(v) - q_r(v), 0)     (no drafted token, or all of them 0: p_r(v)):
+ * the lowest v with w_v > 0 and sum_{j <= v} w_j > u sum_j w_j (if none: the
+ * last with w_v > 0).  Probabilities are compared, and the weights formed and
+ * added, in binary64.  temperature 0: a drafted token is kept while it is the
+ * row's largest score (ties: the lowest index), and that is the token taken
+ * at place r; uniforms and draft_logits are not read.
+ * A row with NaN or +infinity among its scores, or nothing but -infinity, has
+ * no distribution: the target's keeps no token and none can be taken (token
+ * -1, log-probability NaN); of the draft's rows such a one keeps no token and
+ * takes the next from p_r alone.
+ * accepted: [batch], how many drafted tokens were kept.  tokens: [batch]
+ * [draft + 1]: those, the token taken behind them, and -1 beyond.  logps (may
+ * be NULL): fp32 [batch][draft + 1], the log-probability of each under p_i
+ * (temperature 0: of the softmax of the scores), 0 beyond: the old_logps of
+ * muon_policy_loss.  Conventions and errors: those of the loss calls;
+ * temperature is 0 or in (1e-30, 1e30), draft at most 1024. */
+#define MUON_MAX_DRAFT 1024
+muon_status_t muon_verify_draft(muon_ctx_t* ctx, void* stream, const muon_logits_t* logits,
+                                const int64_t* draft_tokens, const muon_logits_t* draft_logits,
+                                const float* uniforms, double temperature, int64_t* tokens,
+                                int64_t* accepted, float* logps);
+
+/* ------------------------------------------------------------------------ */
 /* Diagnostics                                                               */
 /* ------------------------------------------------------------------------ */
 
@@ -617,7 +759,9 @@ typedef enum {
   MUON_K_FUSED = 7,  /* whole-iteration launches of small units (muon_fuse_t) */
   MUON_K_LOSS = 8,   /* token log-probabilities, the losses and their gradients */
   MUON_K_CLIP = 9,   /* global gradient norm and gradient scaling */
-  MUON_K_COUNT = 10
+  MUON_K_LINEAR8 = 10, /* 8-bit rows, their products and gradients */
+  MUON_K_VERIFY = 11,  /* verification of drafted tokens */
+  MUON_K_COUNT = 12
 } muon_kernel_class_t;
 
 muon_status_t muon_timing_enable(muon_ctx_t* ctx, int32_t enable, int32_t capacity);

@@ -12,7 +12,7 @@ MUON_F32, MUON_BF16 = 0, 1
 MUON_CAP_FULL_BYTES, MUON_CAP_WORKSPACE = 0, 1
 MUON_NOALLOC_SCRATCH_BYTES = 256 << 20
 KERNEL_CLASSES = ["momentum", "norm", "gram", "symsq", "update", "apply", "prod", "fused",
-                  "loss", "clip"]
+                  "loss", "clip", "linear8", "verify"]
 
 # every symbol include/muon.h declares
 EXPORTS = [
@@ -27,6 +27,9 @@ EXPORTS = [
     "muon_loss_workspace_bytes", "muon_loss_set_polls", "muon_token_logps", "muon_token_logps_backward",
     "muon_policy_loss", "muon_preference_loss", "muon_grad_norm_workspace_bytes",
     "muon_grad_norm", "muon_clip_coef", "muon_scale_grads", "muon_momentum_update_clipped",
+    "muon_quantize_rows", "muon_dequantize_rows", "muon_linear8_workspace_bytes", "muon_matmul8",
+    "muon_linear8", "muon_input_grad8", "muon_weight_grad8", "muon_verify_workspace_bytes",
+    "muon_verify_draft",
 ]
 
 
@@ -70,6 +73,16 @@ class PreferenceParams(ctypes.Structure):
 
 class Tensor(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
+class Rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
+class Rows8(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
 
 
 _LIB = None
@@ -126,6 +139,15 @@ def load() -> ctypes.CDLL:
         "muon_grad_norm": (i32, [vp, vp, P(Tensor), i64, f64, f64, vp]),
         "muon_clip_coef": (i32, [vp, vp, f64, f64, vp]),
         "muon_scale_grads": (i32, [vp, vp, P(Tensor), P(Tensor), i64, vp]),
+        "muon_quantize_rows": (i32, [vp, vp, P(Rows), P(Rows8)]),
+        "muon_dequantize_rows": (i32, [vp, vp, P(Rows8), P(Rows)]),
+        "muon_linear8_workspace_bytes": (sz, [i64, i64, i64]),
+        "muon_matmul8": (i32, [vp, vp, P(Rows8), P(Rows8), P(Rows)]),
+        "muon_linear8": (i32, [vp, vp, P(Rows), P(Rows8), P(Rows8), P(Rows)]),
+        "muon_input_grad8": (i32, [vp, vp, P(Rows), P(Rows8), P(Rows), i32]),
+        "muon_weight_grad8": (i32, [vp, vp, P(Rows), P(Rows8), P(Rows), i32]),
+        "muon_verify_workspace_bytes": (sz, [i64, i64, i64]),
+        "muon_verify_draft": (i32, [vp, vp, P(Logits), vp, P(Logits), vp, f64, vp, vp, vp]),
         "muon_momentum_update_clipped": (i32, [vp, vp, vp, i32, vp, vp, i32, i64, f32, i32, vp, vp]),
     }
     for name, (res, args) in sig.items():

@@ -15,7 +15,7 @@ import torch
 from . import _lib
 from ._lib import (
     MUON_BF16, MUON_CAP_FULL_BYTES, MUON_CAP_WORKSPACE, MUON_F32, Logits, NsParams, PolicyParams,
-    PreferenceParams, Shape, Tensor,
+    PreferenceParams, Rows, Shape, Tensor,
 )
 
 
@@ -199,6 +199,61 @@ class TensorList:
     def norm_workspace_bytes(self) -> int:
         """Workspace a context needs for grad_norm over the list."""
         return int(_lib.load().muon_grad_norm_workspace_bytes(self.array, len(self)))
+
+
+def linear8_workspace_bytes(tokens: int, n: int, k: int) -> int:
+    """Workspace a context needs for any call on a layer of n x k 8-bit weights
+    and up to `tokens` tokens."""
+    return int(_lib.load().muon_linear8_workspace_bytes(tokens, n, k))
+
+
+def verify_workspace_bytes(batch: int, draft: int, vocab: int) -> int:
+    """Workspace a context needs for verify_draft."""
+    return int(_lib.load().muon_verify_workspace_bytes(batch, draft, vocab))
+
+
+def _rows(t: torch.Tensor, name: str, device: torch.device) -> Rows:
+    """Values as [rows, cols], or [..., cols] whose leading dimensions are rows
+    at one stride; the columns contiguous."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a tensor on {device}")
+    if t.dim() < 2:
+        raise ValueError(f"{name} must be [rows, cols]")
+    if t.dim() > 2:
+        t = t.flatten(0, -2) if t.numel() == 0 else t.view(-1, t.shape[-1])  # (raises where the rows have no one stride)
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"the columns of {name} must be contiguous")
+    return Rows(t.data_ptr(), _dtype(t), t.shape[0], t.shape[1], t.stride(0))
+
+
+class Rows8:
+    """8-bit rows: values scale[r] * q[r, c].  q: int8 [rows, cols], rows at
+    multiples of 16 bytes (Context.rows8 makes such ones); scale: float32
+    [rows].  Made once for tensors that stay where they are, kept while they
+    live."""
+
+    def __init__(self, q: torch.Tensor, scale: torch.Tensor):
+        if q.dtype != torch.int8:
+            raise TypeError("q must be int8")
+        if q.dim() != 2 or (q.shape[1] > 1 and q.stride(1) != 1):
+            raise ValueError("q must be [rows, cols], the columns contiguous")
+        if scale.device != q.device or not scale.is_contiguous():
+            raise ValueError("scale must be contiguous and on q's device")
+        if scale.dtype != torch.float32:
+            raise TypeError("scale must be float32")
+        if scale.shape != q.shape[:1]:
+            raise ValueError("scale must hold one number per row")
+        self.q, self.scale = q, scale
+        self.struct = _lib.Rows8(q.data_ptr(), scale.data_ptr(), q.shape[0], q.shape[1], q.stride(0))
+        self.ref = ctypes.byref(self.struct)
+
+    @property
+    def shape(self):
+        return self.q.shape
+
+    def __getitem__(self, rows: slice) -> "Rows8":
+        """Some of the rows, in place."""
+        return Rows8(self.q[rows], self.scale[rows])
 
 
 class Context:
@@ -435,6 +490,92 @@ class Context:
         if grad_logits.shape != logits.shape or grad_logits.dtype != logits.dtype:
             raise ValueError("grad_logits must have the logits' shape and dtype")
         return _logits(grad_logits, "grad_logits", self.device)
+
+    # -- linear layers in 8 bits ------------------------------------------------
+    def rows8(self, rows: int, cols: int) -> Rows8:
+        """Room for 8-bit rows, each at a multiple of 16 bytes."""
+        q = torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.int8, device=self.device)
+        return Rows8(q[:, :cols], torch.empty(rows, dtype=torch.float32, device=self.device))
+
+    def _rows8(self, x: Rows8, name: str):
+        if x.q.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}")
+        return x.ref
+
+    def quantize_rows(self, x: torch.Tensor, x8: Rows8, stream=None):
+        """The rows of x (bf16 or float32, any row stride) in 8 bits with a scale
+        each: the largest magnitude becomes 127."""
+        r = _rows(x, "x", self.device)
+        self._raise(self.lib.muon_quantize_rows(self.handle, _stream(self.device, stream), ctypes.byref(r),
+                                                self._rows8(x8, "x8")), "muon_quantize_rows")
+
+    def dequantize_rows(self, x8: Rows8, out: torch.Tensor, stream=None):
+        """The values that 8-bit rows stand for (bf16 or float32)."""
+        r = _rows(out, "out", self.device)
+        self._raise(self.lib.muon_dequantize_rows(self.handle, _stream(self.device, stream), self._rows8(x8, "x8"),
+                                                  ctypes.byref(r)), "muon_dequantize_rows")
+
+    def matmul8(self, a: Rows8, b: Rows8, out: torch.Tensor, stream=None):
+        """out = a b^T, summed in integers (bf16 or float32)."""
+        r = _rows(out, "out", self.device)
+        self._raise(self.lib.muon_matmul8(self.handle, _stream(self.device, stream), self._rows8(a, "a"),
+                                          self._rows8(b, "b"), ctypes.byref(r)), "muon_matmul8")
+
+    def linear8(self, x: torch.Tensor, w: Rows8, out: torch.Tensor, x8: Optional[Rows8] = None, stream=None):
+        """out = x w^T in 8 bits: x [tokens, k] is quantised by token, w holds a
+        row per channel.  `x8` (tokens x k) keeps the quantised activations for
+        the backward pass (weight_grad8); None: they are not kept.  As every
+        call here no autograd function."""
+        r, o = _rows(x, "x", self.device), _rows(out, "out", self.device)
+        self._raise(self.lib.muon_linear8(self.handle, _stream(self.device, stream), ctypes.byref(r), self._rows8(w, "w"),
+                                          None if x8 is None else self._rows8(x8, "x8"), ctypes.byref(o)), "muon_linear8")
+
+    def input_grad8(self, grad_y: torch.Tensor, w: Rows8, grad_x: torch.Tensor, accumulate: bool = False, stream=None):
+        """Gradient of linear8 in x: grad_x (+)= grad_y w.  grad_y: bf16
+        [tokens, n]; grad_x: bf16 or float32."""
+        y, o = _rows(grad_y, "grad_y", self.device), _rows(grad_x, "grad_x", self.device)
+        self._raise(self.lib.muon_input_grad8(self.handle, _stream(self.device, stream), ctypes.byref(y), self._rows8(w, "w"),
+                                              ctypes.byref(o), 1 if accumulate else 0), "muon_input_grad8")
+
+    def weight_grad8(self, grad_y: torch.Tensor, x8: Rows8, grad_w: torch.Tensor, accumulate: bool = False, stream=None):
+        """Gradient of linear8 in the weights, out of the kept activations:
+        grad_w (+)= grad_y^T x8.  grad_w: bf16 or float32 [n, k], e.g. a view of
+        MuonStep.grad."""
+        y, o = _rows(grad_y, "grad_y", self.device), _rows(grad_w, "grad_w", self.device)
+        self._raise(self.lib.muon_weight_grad8(self.handle, _stream(self.device, stream), ctypes.byref(y),
+                                               self._rows8(x8, "x8"), ctypes.byref(o), 1 if accumulate else 0),
+                    "muon_weight_grad8")
+
+    # -- verification of drafted tokens -----------------------------------------
+    def verify_draft(self, logits: torch.Tensor, draft_tokens: torch.Tensor, tokens: torch.Tensor,
+                     accepted: torch.Tensor, draft_logits: Optional[torch.Tensor] = None,
+                     uniforms: Optional[torch.Tensor] = None, logps: Optional[torch.Tensor] = None,
+                     temperature: float = 1.0, stream=None):
+        """Keeps the drafted tokens that the target's scores allow and takes the
+        token behind them.  logits: [batch, draft + 1, vocab]; draft_tokens:
+        int64 [batch, draft], a negative one ends a sequence's draft;
+        draft_logits: [batch, draft, vocab] that the tokens were sampled from,
+        None: a deterministic draft; uniforms: float32 [batch, draft + 1] in
+        [0, 1).  tokens (int64 [batch, draft + 1]) receives the kept tokens, the
+        one taken, then -1; accepted (int64 [batch]) how many were kept; logps
+        (float32 like tokens) their log-probabilities under the target.
+        temperature 0: the most likely tokens, uniforms and draft_logits unused."""
+        if logits.dim() != 3:
+            raise ValueError("logits must be [batch, draft + 1, vocab]")
+        x, dev = _logits(logits, "logits", self.device), self.device
+        places = logits.shape[:2]
+        draft = (places[0], places[1] - 1)
+        d = None
+        if draft_logits is not None:
+            if draft_logits.shape != (*draft, logits.shape[2]):
+                raise ValueError("draft_logits must be [batch, draft, vocab]")
+            d = ctypes.byref(_logits(draft_logits, "draft_logits", dev))
+        st = self.lib.muon_verify_draft(
+            self.handle, _stream(dev, stream), ctypes.byref(x), _tokens(draft_tokens, "draft_tokens", draft, torch.int64, dev), d,
+            _tokens(uniforms, "uniforms", places, torch.float32, dev), temperature,
+            _tokens(tokens, "tokens", places, torch.int64, dev), _tokens(accepted, "accepted", places[:1], torch.int64, dev),
+            _tokens(logps, "logps", places, torch.float32, dev))
+        self._raise(st, "muon_verify_draft")
 
     # -- gradient norm and clipping -------------------------------------------
     def tensor_list(self, tensors: Sequence[torch.Tensor]) -> TensorList:

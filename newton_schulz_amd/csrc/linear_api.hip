@@ -1,0 +1,270 @@
+// C entry points of the 8-bit linear layers and of draft verification:
+// argument checks, workspace layout, launches.  Arguments are checked before
+// the context, as for the losses.
+#include <cmath>
+
+#include "api_checks.h"
+#include "linear8.h"
+
+namespace {
+
+constexpr int64_t kMostStride = int64_t{1} << 40;
+constexpr int64_t kMostOut = int64_t{1} << 39;  // elements of a product
+
+inline int64_t up16(int64_t n) { return (n + 15) & ~int64_t{15}; }
+
+// Rows of values; bytes receives their extent.
+muon_status_t check_rows(muon_ctx* c, const muon_rows_t* x, bool written, size_t* bytes) {
+  *bytes = 0;
+  if (x == nullptr) return fail(c, MUON_EINVAL, "rows NULL");
+  if (!is_dtype(x->dtype)) return fail(c, MUON_EDTYPE, "rows dtype");
+  if (x->rows < 0 || x->rows > MUON_MAX_ROWS8 || x->cols < 1 || x->cols > MUON_MAX_ROWS8)
+    return fail(c, MUON_ESHAPE, "rows or cols out of range");
+  if (x->rows == 0) return MUON_OK;
+  if (x->rows > 1 && (x->row_stride < 0 || x->row_stride > kMostStride)) return fail(c, MUON_ESHAPE, "row stride out of range");
+  if (written && x->rows > 1 && x->row_stride < x->cols) return fail(c, MUON_EINVAL, "rows of an output overlap");
+  if (x->data == nullptr) return fail(c, MUON_EINVAL, "rows data NULL");
+  if (reinterpret_cast<uintptr_t>(x->data) % esize(x->dtype)) return fail(c, MUON_EINVAL, "misaligned rows");
+  *bytes = static_cast<size_t>((x->rows - 1) * (x->rows > 1 ? x->row_stride : 0) + x->cols) * esize(x->dtype);
+  return MUON_OK;
+}
+
+muon_status_t check_rows8(muon_ctx* c, const muon_rows8_t* x, bool written, size_t* bytes) {
+  *bytes = 0;
+  if (x == nullptr) return fail(c, MUON_EINVAL, "8-bit rows NULL");
+  if (x->rows < 0 || x->rows > MUON_MAX_ROWS8 || x->cols < 1 || x->cols > MUON_MAX_COLS8)
+    return fail(c, MUON_ESHAPE, "rows or cols of 8-bit rows out of range");
+  if (x->rows == 0) return MUON_OK;
+  if (x->rows > 1 && (x->row_stride < 0 || x->row_stride > kMostStride))
+    return fail(c, MUON_ESHAPE, "row stride of 8-bit rows out of range");
+  if (x->data == nullptr || x->scale == nullptr) return fail(c, MUON_EINVAL, "8-bit rows data or scale NULL");
+  if (reinterpret_cast<uintptr_t>(x->data) % 16 || (x->rows > 1 && x->row_stride % 16))
+    return fail(c, MUON_EINVAL, "8-bit rows start at multiples of 16 bytes");
+  if (reinterpret_cast<uintptr_t>(x->scale) % 4) return fail(c, MUON_EINVAL, "misaligned scale");
+  if (written && x->rows > 1 && x->row_stride < x->cols) return fail(c, MUON_EINVAL, "rows of an output overlap");
+  *bytes = static_cast<size_t>((x->rows - 1) * (x->rows > 1 ? x->row_stride : 0) + x->cols);
+  return MUON_OK;
+}
+
+Values values(const muon_rows_t& x) {
+  return {static_cast<char*>(x.data), x.dtype == MUON_BF16, x.rows > 1 ? x.row_stride : 0};
+}
+Bytes bytes8(const muon_rows8_t& x) { return {x.data, x.scale, x.rows > 1 ? x.row_stride : 0}; }
+
+Span span(const muon_rows_t& x, size_t bytes, bool written) {
+  return {bytes ? x.data : nullptr, bytes, esize(x.dtype), written, false, "rows"};
+}
+// The two arrays of 8-bit rows.
+void spans8(Span* s, const muon_rows8_t& x, size_t bytes, bool written) {
+  s[0] = {bytes ? x.data : nullptr, bytes, 16, written, false, "8-bit rows"};
+  s[1] = {bytes ? x.scale : nullptr, bytes ? static_cast<size_t>(x.rows) * 4 : 0, 4, written, false, "scale"};
+}
+
+// What linear8 keeps in the workspace where nobody keeps the activations.
+struct LinearLayout {
+  size_t q, scale, total;
+};
+LinearLayout linear_layout(int64_t tokens, int64_t k) {
+  LinearLayout l;
+  l.q = 0;
+  l.scale = up256(static_cast<size_t>(tokens * up16(k)));
+  l.total = l.scale + up256(static_cast<size_t>(tokens) * 4);
+  return l;
+}
+
+muon_status_t matmul8(muon_ctx* c, hipStream_t s, const Bytes& a, int64_t m, const muon_rows8_t& b, const muon_rows_t& out) {
+  const Matmul8Args t = {a, bytes8(b), values(out), m, b.rows, static_cast<int>(b.cols)};
+  return timed(c, s, MUON_K_LINEAR8, "8-bit product launch", [&] { return launch_matmul8(s, t); });
+}
+
+muon_status_t grad8(muon_ctx* c, void* stream, const muon_rows_t* y, const muon_rows8_t* q, const muon_rows_t* out,
+                    bool of_columns, int32_t accumulate) {
+  size_t yb = 0, qb = 0, ob = 0;
+  muon_status_t st = check_rows(c, y, false, &yb);
+  if (st == MUON_OK) st = check_rows8(c, q, false, &qb);
+  if (st == MUON_OK) st = check_rows(c, out, true, &ob);
+  if (st != MUON_OK) return st;
+  if (y->dtype != MUON_BF16) return fail(c, MUON_EDTYPE, "grad_y is bf16");
+  const int64_t m = of_columns ? y->cols : y->rows, contraction = of_columns ? y->rows : y->cols;
+  if (contraction != q->rows || out->rows != m || out->cols != q->cols)
+    return fail(c, MUON_ESHAPE, "the gradient's shapes do not match");
+  if (m * q->cols > kMostOut) return fail(c, MUON_ESHAPE, "too many elements");
+  Span spans[4];
+  spans[0] = span(*y, yb, false);
+  spans[1] = span(*out, ob, true);
+  spans8(spans + 2, *q, qb, false);
+  st = check_spans(c, spans, 4, false);
+  if (st == MUON_OK) st = check_ctx(c, 0);
+  if (st != MUON_OK || m == 0) return st;
+  DeviceGuard g(c->device);
+  const Grad8Args t = {values(*y), of_columns, bytes8(*q), values(*out), m, q->cols, contraction, accumulate != 0};
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(c, s, MUON_K_LINEAR8, "8-bit gradient launch", [&] { return launch_grad8(s, t); });
+}
+
+}  // namespace
+
+extern "C" {
+
+muon_status_t muon_quantize_rows(muon_ctx_t* c, void* stream, const muon_rows_t* x, const muon_rows8_t* q) {
+  size_t xb = 0, qb = 0;
+  muon_status_t st = check_rows(c, x, false, &xb);
+  if (st == MUON_OK) st = check_rows8(c, q, true, &qb);
+  if (st != MUON_OK) return st;
+  if (x->rows != q->rows || x->cols != q->cols) return fail(c, MUON_ESHAPE, "values and 8-bit rows differ in shape");
+  Span spans[3];
+  spans[0] = span(*x, xb, false);
+  spans8(spans + 1, *q, qb, true);
+  st = check_spans(c, spans, 3, false);
+  if (st == MUON_OK) st = check_ctx(c, 0);
+  if (st != MUON_OK || x->rows == 0) return st;
+  DeviceGuard g(c->device);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(c, s, MUON_K_LINEAR8, "quantisation launch",
+               [&] { return launch_quantize_rows(s, values(*x), bytes8(*q), x->rows, static_cast<int>(x->cols)); });
+}
+
+muon_status_t muon_dequantize_rows(muon_ctx_t* c, void* stream, const muon_rows8_t* q, const muon_rows_t* out) {
+  size_t ob = 0, qb = 0;
+  muon_status_t st = check_rows8(c, q, false, &qb);
+  if (st == MUON_OK) st = check_rows(c, out, true, &ob);
+  if (st != MUON_OK) return st;
+  if (out->rows != q->rows || out->cols != q->cols) return fail(c, MUON_ESHAPE, "values and 8-bit rows differ in shape");
+  Span spans[3];
+  spans[0] = span(*out, ob, true);
+  spans8(spans + 1, *q, qb, false);
+  st = check_spans(c, spans, 3, false);
+  if (st == MUON_OK) st = check_ctx(c, 0);
+  if (st != MUON_OK || q->rows == 0) return st;
+  DeviceGuard g(c->device);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(c, s, MUON_K_LINEAR8, "8-bit rows read back", [&] {
+    return launch_dequantize_rows(s, bytes8(*q), values(*out), q->rows, static_cast<int>(q->cols));
+  });
+}
+
+size_t muon_linear8_workspace_bytes(int64_t tokens, int64_t n, int64_t k) {
+  if (tokens < 0 || tokens > MUON_MAX_ROWS8 || n < 0 || n > MUON_MAX_ROWS8 || k < 1 || k > MUON_MAX_COLS8) return 0;
+  return linear_layout(tokens, k).total;
+}
+
+muon_status_t muon_matmul8(muon_ctx_t* c, void* stream, const muon_rows8_t* a, const muon_rows8_t* b,
+                           const muon_rows_t* out) {
+  size_t ab = 0, bb = 0, ob = 0;
+  muon_status_t st = check_rows8(c, a, false, &ab);
+  if (st == MUON_OK) st = check_rows8(c, b, false, &bb);
+  if (st == MUON_OK && b->rows == 0) return fail(c, MUON_ESHAPE, "no columns");
+  if (st == MUON_OK) st = check_rows(c, out, true, &ob);
+  if (st != MUON_OK) return st;
+  if (a->cols != b->cols || out->rows != a->rows || out->cols != b->rows)
+    return fail(c, MUON_ESHAPE, "the product's shapes do not match");
+  if (out->rows * out->cols > kMostOut) return fail(c, MUON_ESHAPE, "too many elements");
+  Span spans[5];
+  spans[0] = span(*out, ob, true);
+  spans8(spans + 1, *a, ab, false);
+  spans8(spans + 3, *b, bb, false);
+  st = check_spans(c, spans, 5, false);
+  if (st == MUON_OK) st = check_ctx(c, 0);
+  if (st != MUON_OK || a->rows == 0) return st;
+  DeviceGuard g(c->device);
+  return matmul8(c, static_cast<hipStream_t>(stream), bytes8(*a), a->rows, *b, *out);
+}
+
+muon_status_t muon_linear8(muon_ctx_t* c, void* stream, const muon_rows_t* x, const muon_rows8_t* w,
+                           const muon_rows8_t* x8, const muon_rows_t* out) {
+  size_t xb = 0, wb = 0, qb = 0, ob = 0;
+  muon_status_t st = check_rows(c, x, false, &xb);
+  if (st == MUON_OK) st = check_rows8(c, w, false, &wb);
+  if (st == MUON_OK && w->rows == 0) return fail(c, MUON_ESHAPE, "no columns");
+  if (st == MUON_OK && x8) st = check_rows8(c, x8, true, &qb);
+  if (st == MUON_OK) st = check_rows(c, out, true, &ob);
+  if (st != MUON_OK) return st;
+  if (x->cols != w->cols || out->rows != x->rows || out->cols != w->rows)
+    return fail(c, MUON_ESHAPE, "the product's shapes do not match");
+  if (x8 && (x8->rows != x->rows || x8->cols != x->cols)) return fail(c, MUON_ESHAPE, "values and 8-bit rows differ in shape");
+  if (out->rows * out->cols > kMostOut) return fail(c, MUON_ESHAPE, "too many elements");
+  Span spans[6] = {};
+  spans[0] = span(*out, ob, true);
+  spans[1] = span(*x, xb, false);
+  spans8(spans + 2, *w, wb, false);
+  if (x8) spans8(spans + 4, *x8, qb, true);
+  st = check_spans(c, spans, x8 ? 6 : 4, false);
+  const LinearLayout l = linear_layout(x->rows, x->cols);
+  if (st == MUON_OK) st = check_ctx(c, l.total);
+  if (st != MUON_OK || x->rows == 0) return st;
+  DeviceGuard g(c->device);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const Bytes q = x8 ? bytes8(*x8)
+                     : Bytes{reinterpret_cast<int8_t*>(c->ws + l.q), reinterpret_cast<float*>(c->ws + l.scale), up16(x->cols)};
+  st = timed(c, s, MUON_K_LINEAR8, "quantisation launch",
+             [&] { return launch_quantize_rows(s, values(*x), q, x->rows, static_cast<int>(x->cols)); });
+  return st == MUON_OK ? matmul8(c, s, q, x->rows, *w, *out) : st;
+}
+
+muon_status_t muon_input_grad8(muon_ctx_t* c, void* stream, const muon_rows_t* grad_y, const muon_rows8_t* w,
+                               const muon_rows_t* grad_x, int32_t accumulate) {
+  return grad8(c, stream, grad_y, w, grad_x, false, accumulate);
+}
+
+muon_status_t muon_weight_grad8(muon_ctx_t* c, void* stream, const muon_rows_t* grad_y, const muon_rows8_t* x,
+                                const muon_rows_t* grad_w, int32_t accumulate) {
+  return grad8(c, stream, grad_y, x, grad_w, true, accumulate);
+}
+
+size_t muon_verify_workspace_bytes(int64_t batch, int64_t draft, int64_t vocab) {
+  if (batch < 0 || draft < 0 || draft > MUON_MAX_DRAFT || vocab < 1 || vocab > MUON_MAX_VOCAB || batch > kMostTokens ||
+      batch * (draft + 1) > kMostTokens)
+    return 0;
+  return 256;
+}
+
+muon_status_t muon_verify_draft(muon_ctx_t* c, void* stream, const muon_logits_t* logits, const int64_t* draft_tokens,
+                                const muon_logits_t* draft_logits, const float* uniforms, double temperature,
+                                int64_t* tokens, int64_t* accepted, float* logps) {
+  size_t xb = 0, db = 0;
+  muon_status_t st = check_logits(c, logits, &xb);
+  if (st != MUON_OK) return st;
+  if (logits->seq < 1) return fail(c, MUON_ESHAPE, "no row for the token behind the draft");
+  if (logits->seq - 1 > MUON_MAX_DRAFT) return fail(c, MUON_ESHAPE, "draft too long");
+  const bool greedy = temperature == 0.0;
+  if (!greedy && !good_temperature(temperature)) return fail(c, MUON_EINVAL, "temperature");
+  const int64_t draft = logits->seq - 1;
+  if (draft_logits) {
+    st = check_logits(c, draft_logits, &db);
+    if (st != MUON_OK) return st;
+    if (draft_logits->batch != logits->batch || draft_logits->seq != draft || draft_logits->vocab != logits->vocab)
+      return fail(c, MUON_ESHAPE, "draft_logits and logits differ in shape");
+  }
+  const size_t batch = static_cast<size_t>(logits->batch), places = batch * static_cast<size_t>(draft + 1);
+  const Span spans[] = {{logits->data, xb, 1, false, true, "logits"},
+                        {draft_logits && db ? draft_logits->data : nullptr, db, 1, false, false, "draft_logits"},
+                        {draft_tokens, batch * static_cast<size_t>(draft) * 8, 8, false, true, "draft_tokens"},
+                        {uniforms, places * 4, 4, false, !greedy, "uniforms"},
+                        {tokens, places * 8, 8, true, true, "tokens"},
+                        {accepted, batch * 8, 8, true, true, "accepted"},
+                        {logps, places * 4, 4, true, false, "logps"}};
+  st = check_spans(c, spans, 7, false);
+  if (st == MUON_OK) st = check_ctx(c, muon_verify_workspace_bytes(logits->batch, draft, logits->vocab));
+  if (st != MUON_OK || batch == 0) return st;
+  DeviceGuard g(c->device);
+  VerifyArgs a = {};
+  a.x = rows_ref(*logits);
+  a.x_bf16 = logits->dtype == MUON_BF16;
+  if (draft_logits && draft && !greedy) {
+    a.d = rows_ref(*draft_logits);
+    a.d_bf16 = draft_logits->dtype == MUON_BF16;
+  }
+  a.batch = static_cast<int>(batch);
+  a.draft = static_cast<int>(draft);
+  a.vocab = static_cast<int>(logits->vocab);
+  a.drafted = draft_tokens;
+  a.uniforms = uniforms;
+  a.inv_t = greedy ? 0.0 : 1.0 / temperature;
+  a.tokens = tokens;
+  a.accepted = accepted;
+  a.logps = logps;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(c, s, MUON_K_VERIFY, "draft verification launch", [&] { return launch_verify(s, a); });
+}
+
+}  // extern "C"

@@ -30,11 +30,11 @@ contractions).  Device memory beyond the state grows by (k - 1) lanes.
 """
 from __future__ import annotations
 
-from typing import List, Optional, Sequence, Tuple
+from typing import Dict, List, Optional, Sequence, Tuple
 
 import torch
 
-from .api import SQ_BLOCK, Context, Plan, TensorList, ns_params, sq_blocks
+from .api import SQ_BLOCK, Context, Plan, Rows8, TensorList, ns_params, sq_blocks
 
 
 class MuonStep:
@@ -44,8 +44,12 @@ class MuonStep:
                  cap_kind: str = "full", ns_steps: int = 5, keep_bf16_weights: bool = False,
                  weight_decay: float = 0.0, scale: float = 1.0, ns_method: str = "quintic",
                  ns_coeffs=None, norms_from_momentum: bool = True, ns_fuse: str = "auto",
-                 inflight: int = 1, max_grad_norm: Optional[float] = None):
-        """max_grad_norm: clip the gradient to this global norm (None: not at
+                 inflight: int = 1, max_grad_norm: Optional[float] = None,
+                 keep_int8_weights: bool = False):
+        """keep_int8_weights: also keep the weights as 8-bit rows with a scale
+        per row (weight8(i): what Context.linear8 and input_grad8 take), formed
+        anew from the master weights by every step, and by quantize_weights()
+        for weights that were set from outside.  max_grad_norm: clip the gradient to this global norm (None: not at
         all).  The norm is taken at the start of a step, over the flat gradient
         and what step() is given beside it, and its coefficient multiplies the
         gradient inside the momentum pass; `grad_norm` (float64 {sum of
@@ -86,6 +90,46 @@ class MuonStep:
         self.ctx = Context(self.device, workspace)
         self._norm_ctx: List[Context] = []
         self._alloc_state(grad_dtype, keep_bf16_weights)
+        self._weight8: List[Rows8] = []
+        # by micro-bucket (its offset): runs of matrices with as many columns,
+        # which follow each other in the flat layout and so are rows of one
+        self._runs8: Dict[int, List[Tuple[int, int, Rows8]]] = {}
+        if keep_int8_weights:
+            self._alloc_int8()
+
+    def _alloc_int8(self):
+        weight8 = [None] * len(self.shapes)
+        for b in self.plan.buckets:
+            runs = self._runs8.setdefault(b.elem_offset, [])
+            j = 0
+            while j < len(b.indices):
+                cols, k, rows = self.shapes[b.indices[j]][1], j, 0
+                while k < len(b.indices) and self.shapes[b.indices[k]][1] == cols:
+                    rows += self.shapes[b.indices[k]][0]
+                    k += 1
+                run, at, lo = self.ctx.rows8(rows, cols), 0, b.offsets[j]
+                for i in b.indices[j:k]:
+                    weight8[i] = run[at:at + self.shapes[i][0]]
+                    at += self.shapes[i][0]
+                runs.append((lo, lo + rows * cols, run))
+                j = k
+        self._weight8 = weight8
+        self.quantize_weights()
+
+    def weight8(self, i: int) -> Rows8:
+        """Matrix i in 8 bits, a scale per row (keep_int8_weights)."""
+        if not self._weight8:
+            raise ValueError("the step keeps no 8-bit weights (keep_int8_weights)")
+        return self._weight8[i]
+
+    def quantize_weights(self, stream=None):
+        """The 8-bit weights from the master weights, all of them."""
+        for lo in self._runs8:
+            self._quantize_bucket(lo, self.ctx, stream)
+
+    def _quantize_bucket(self, offset: int, ctx: Context, stream):
+        for lo, hi, run in self._runs8.get(offset, ()):
+            ctx.quantize_rows(self.master[lo:hi].view(run.shape), run, stream)
 
     def _alloc_state(self, grad_dtype: torch.dtype, keep_bf16_weights: bool):
         off, dev = self.numel, self.device
@@ -181,6 +225,7 @@ class MuonStep:
             ctx.newton_schulz(mats, None, h, self.params, flag, stream, _ptrs=ptrs,
                               sq=(sq, upd) if whole else None)
         ctx.apply(master, upd, self.lr, self.scale, self.weight_decay, wb, stream)
+        self._quantize_bucket(master.storage_offset(), ctx, stream)
 
     def capture(self, nonfinite_flag: Optional[torch.Tensor] = None, other_grads=None) -> "torch.cuda.CUDAGraph":
         """Record one whole step, every lane's launches included, into a HIP
