@@ -606,12 +606,12 @@ muon_status_t muon_momentum_update_clipped(muon_ctx_t* ctx, void* stream, const 
  * the gradients are formed out of them.
  *
  * Rows of values: element (r, c) at data + (r * row_stride + c) elements of
- * `dtype`.  The stride (elements, >= 0; of a single row it is ignored) may
- * exceed cols; rows that are written must be disjoint. */
+ * `dtype`.  The stride (elements, in [0, 2^22]; of a single row it is ignored)
+ * may exceed cols; rows that are written must be disjoint. */
 typedef struct {
   void* data;
   int32_t dtype;       /* MUON_BF16 or MUON_F32 */
-  int64_t rows, cols;  /* rows in [0, MUON_MAX_ROWS8], cols >= 1 */
+  int64_t rows, cols;  /* rows in [0, MUON_MAX_ROWS8], cols in [1, 2^22] */
   int64_t row_stride;
 } muon_rows_t;
 
@@ -626,7 +626,7 @@ typedef struct {
   int8_t* data;
   float* scale;
   int64_t rows, cols;  /* cols in [1, MUON_MAX_COLS8] */
-  int64_t row_stride;  /* bytes */
+  int64_t row_stride;  /* bytes, in [0, 2^22] */
 } muon_rows8_t;
 
 /* Errors of the calls below: MUON_EINVAL (ctx or another required pointer

@@ -3,64 +3,343 @@
 //   weights: sum over tokens of grad_y (columns) and the kept activations,
 //   inputs:  sum over channels of grad_y (rows) and the weights.
 #include "linear8.h"
-#include "muon_device.h"
-
-using muon::bf16_t;
+#include "ns_mfma_common.h"
 
 namespace {
 
-constexpr int kTile = 64, kStep = 16, kPitch = kTile + 4;
+// ---------------------------------------------------------------------------
+// tiles on the matrix cores
+// ---------------------------------------------------------------------------
+typedef u32x4_t u32x4_any __attribute__((aligned(2)));
 
-// Sums in fp32 of exact values, for any addresses and strides.
-template <typename T>
-__global__ __launch_bounds__(256) void grad8_simple_kernel(Grad8Args a) {
-  __shared__ float ty[kStep * kPitch], tq[kStep * kPitch];
-  const bf16_t* y = reinterpret_cast<const bf16_t*>(a.y.p);
-  const int64_t tiles_n = (a.n + kTile - 1) / kTile;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) / tiles_n * kTile, n0 = static_cast<int64_t>(blockIdx.x) % tiles_n * kTile;
-  const int jx = threadIdx.x & 15, ix = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int64_t c0 = 0; c0 < a.c; c0 += kStep) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < kTile * kStep; e += 256) {
-      const int i = a.of_columns ? e % kTile : e / kStep, ci = a.of_columns ? e / kTile : e % kStep;
-      float v = 0.0f;
-      if (m0 + i < a.m && c0 + ci < a.c)
-        v = muon::bf16_to_f32(a.of_columns ? y[(c0 + ci) * a.y.ld + m0 + i] : y[(m0 + i) * a.y.ld + c0 + ci]);
-      ty[ci * kPitch + i] = v;
-      const int j = e % kTile, cj = e / kTile;
-      v = 0.0f;
-      if (n0 + j < a.n && c0 + cj < a.c) v = a.q.scale[c0 + cj] * static_cast<float>(a.q.p[(c0 + cj) * a.q.ld + n0 + j]);
-      tq[cj * kPitch + j] = v;
+constexpr int kC = 64;  // of the contraction in a stage
+
+// LDS offset of element (k, col), col a multiple of 4, in a tile of 64 rows k
+// by R columns: 16-byte chunks, swizzled so that the four rows of a
+// transposed read lie on distinct banks.
+template <int R>
+__device__ __forceinline__ int km_off(int k, int col) {
+  return k * (2 * R) + (((col >> 3) ^ (((k & 3) << 2) & (R / 8 - 1))) << 4) + ((col & 7) << 1);
+}
+// Matrix core operand of 32 columns from cb on, k = 16 kk + 8 (lane / 32) + 0..7.
+template <int R>
+__device__ __forceinline__ bf16x8_t km_frag(const char* t, int cb, int kk, int lane) {
+  const int gq = lane >> 4, j = lane & 15;
+  const int col = cb + 16 * (gq & 1) + 4 * (j & 3);
+  const int k = 16 * kk + 8 * (gq >> 1) + (j >> 2);
+  const u32x2_t lo = __builtin_bit_cast(u32x2_t, ld_tr16(t + km_off<R>(k, col)));
+  const u32x2_t hi = __builtin_bit_cast(u32x2_t, ld_tr16(t + km_off<R>(k + 4, col)));
+  return __builtin_bit_cast(bf16x8_t, u32x4_t{lo.x, lo.y, hi.x, hi.y});
+}
+
+// 16 bytes of y through registers: TM rows of the output by 64 of the contraction.
+template <int TM, int NT, bool COLS>
+struct YStage {
+  static constexpr int NC = TM * kC / 8 / NT;
+  u32x4_t v[NC];
+  static __device__ __forceinline__ int row(int e) { return COLS ? e / (TM / 8) : e / (kC / 8); }  // of memory
+  static __device__ __forceinline__ int chunk(int e) { return COLS ? e % (TM / 8) : e % (kC / 8); }
+
+  // fast: every chunk is inside
+  __device__ __forceinline__ void load(const Grad8Args& a, int64_t m0, int64_t c0, int tid, bool fast) {
+    const bf16_t* y = reinterpret_cast<const bf16_t*>(a.y.p);
+    const int64_t r0 = COLS ? c0 : m0, k0 = COLS ? m0 : c0;
+    const int64_t rows = COLS ? a.c : a.m, cols = COLS ? a.m : a.c;
+    const char* base = reinterpret_cast<const char*>(uniform_ptr(y + r0 * a.y.ld + k0));
+    const uint32_t ld = static_cast<uint32_t>(a.y.ld) * 2u;
+    if (fast) {
+#pragma unroll
+      for (int q = 0; q < NC; ++q) {
+        const int e = tid + q * NT;
+        v[q] = *reinterpret_cast<const u32x4_any*>(base + (static_cast<uint32_t>(row(e)) * ld + static_cast<uint32_t>(chunk(e)) * 16u));
+      }
+      return;
     }
-    __syncthreads();
-    for (int c = 0; c < kStep; ++c) {
-      float vy[4], vq[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) vy[i] = ty[c * kPitch + ix + 16 * i];
+    for (int q = 0; q < NC; ++q) {
+      const int e = tid + q * NT;
+      const int64_t left = cols - (k0 + 8 * chunk(e));
+      v[q] = u32x4_t{0, 0, 0, 0};
+      if (r0 + row(e) >= rows || left <= 0) continue;
+      const char* at = base + (static_cast<uint32_t>(row(e)) * ld + static_cast<uint32_t>(chunk(e)) * 16u);
+      if (left >= 8) {
+        v[q] = *reinterpret_cast<const u32x4_any*>(at);
+      } else {
+        const bf16_t* h = reinterpret_cast<const bf16_t*>(at);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) vq[j] = tq[c * kPitch + jx + 16 * j];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_fmaf(vy[i], vq[j], acc[i][j]);
+        for (int i = 0; i < 7; ++i)
+          if (i < left) v[q][i / 2] |= static_cast<uint32_t>(h[i]) << (16 * (i & 1));
+      }
     }
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ix + 16 * i, n = n0 + jx + 16 * j;
-      if (m >= a.m || n >= a.n) continue;
-      T* at = reinterpret_cast<T*>(a.out.p) + m * a.out.ld + n;
-      muon::Elem<T>::store(at, a.accumulate ? muon::Elem<T>::load(at) + acc[i][j] : acc[i][j]);
+  __device__ __forceinline__ void store(char* lds, int tid, int q) const {
+    const int e = tid + q * NT;
+    const int off = COLS ? km_off<TM>(row(e), 8 * chunk(e)) : rt_off<64>(row(e), chunk(e));
+    *reinterpret_cast<u32x4_t*>(lds + off) = v[q];
+  }
+};
+
+// 16 integers a chunk through registers, stored as the bf16 values they stand
+// for: PARTS planes of 64 x TN, the second what the first one's rounding left.
+template <int TN, int NT, int PARTS>
+struct QStage {
+  static constexpr int NC = TN * kC / 16 / NT;
+  u32x4_t v[NC];
+  float s[NC];
+  static __device__ __forceinline__ int row(int e) { return e / (TN / 16); }
+  static __device__ __forceinline__ int chunk(int e) { return e % (TN / 16); }
+
+  __device__ __forceinline__ void load(const Grad8Args& a, int64_t n0, int64_t c0, int tid, bool fast) {
+    const char* base = reinterpret_cast<const char*>(uniform_ptr(a.q.p + c0 * a.q.ld + n0));
+    const float* scale = uniform_ptr(a.q.scale + c0);
+    const uint32_t ld = static_cast<uint32_t>(a.q.ld);
+    if (fast) {
+#pragma unroll
+      for (int q = 0; q < NC; ++q) {
+        const int e = tid + q * NT;
+        v[q] = *reinterpret_cast<const u32x4_t*>(base + (static_cast<uint32_t>(row(e)) * ld + static_cast<uint32_t>(chunk(e)) * 16u));
+        s[q] = scale[row(e)];
+      }
+      return;
     }
+#pragma unroll
+    for (int q = 0; q < NC; ++q) {
+      const int e = tid + q * NT;
+      const int64_t left = a.n - (n0 + 16 * chunk(e)), c = c0 + row(e);
+      v[q] = u32x4_t{0, 0, 0, 0};
+      s[q] = 0.0f;
+      if (c >= a.c) continue;
+      s[q] = scale[row(e)];
+      if (left <= 0) continue;
+      const char* at = base + (static_cast<uint32_t>(row(e)) * ld + static_cast<uint32_t>(chunk(e)) * 16u);
+      // (rows lie 16 bytes apart at least, so only the last one's end may be the memory's)
+      if (left >= 16 || (c + 1 < a.c && ld != 0)) {
+        v[q] = *reinterpret_cast<const u32x4_t*>(at);
+      } else {
+        const uint8_t* b = reinterpret_cast<const uint8_t*>(at);
+#pragma unroll
+        for (int i = 0; i < 15; ++i)
+          if (i < left) v[q][i / 4] |= static_cast<uint32_t>(b[i]) << (8 * (i & 3));
+      }
+    }
+  }
+  // half h (8 integers) of chunk q
+  __device__ __forceinline__ void store(char* lds, int tid, int q, int h) const {
+    const int e = tid + q * NT;
+    u32x4_t hi, lo;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int w = static_cast<int>(v[q][2 * h + i / 2]);
+      const int sh = 16 * (i & 1);
+      const float x0 = s[q] * static_cast<float>((w << (24 - sh)) >> 24), x1 = s[q] * static_cast<float>((w << (16 - sh)) >> 24);
+      hi[i] = muon::pack_bf16x2(x0, x1);
+      if constexpr (PARTS == 2)
+        lo[i] = muon::pack_bf16x2(x0 - __uint_as_float(hi[i] << 16), x1 - __uint_as_float(hi[i] & 0xffff0000u));
+    }
+    const int off = km_off<TN>(row(e), 16 * chunk(e) + 8 * h);
+    *reinterpret_cast<u32x4_t*>(lds + off) = hi;
+    if constexpr (PARTS == 2) *reinterpret_cast<u32x4_t*>(lds + kC * TN * 2 + off) = lo;
+  }
+};
+
+// LDS offset of an fp32 value of the staged output, rows of R values.
+template <int R>
+__device__ __forceinline__ int of_off(int r, int c) {
+  return r * (R * 4) + ((((c >> 2) ^ (r & 15)) & (R / 4 - 1)) << 4) + ((c & 3) << 2);
+}
+
+template <typename O, int TM, int TN, int NWN, int PARTS, bool COLS>
+__global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, int tiles_m, int tiles_n) {
+  constexpr int NW = 2 * NWN, NT = 64 * NW;
+  constexpr int WM = TM / 2, WN = TN / NWN, FM = WM / 32, FN = WN / 32;
+  constexpr int YB = TM * kC * 2, STAGE = YB + PARTS * TN * kC * 2;
+  __shared__ __attribute__((aligned(1024))) char st[2 * STAGE];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / NWN, wn = wave % NWN;
+  const int64_t total = static_cast<int64_t>(tiles_m) * tiles_n;
+  const int G = static_cast<int>(gridDim.x), hw = static_cast<int>(blockIdx.x);
+  const int64_t first = G % 8 == 0 ? static_cast<int64_t>(hw % 8) * (G / 8) + hw / 8 : hw;
+  const int KT = static_cast<int>((a.c + kC - 1) / kC);
+  for (int64_t l = first; l < total; l += G) {
+    // bands of four tile columns, row by row inside a band
+    constexpr int GN = 4;
+    const int64_t band = l / (static_cast<int64_t>(tiles_m) * GN);
+    const int w = static_cast<int>(min(static_cast<int64_t>(GN), tiles_n - band * GN));
+    const int64_t r = l - band * tiles_m * GN;
+    const int64_t m0 = r / w * TM, n0 = (band * GN + r % w) * TN;
+    const bool inside_m = m0 + TM <= a.m, inside_n = n0 + TN <= a.n;
+
+    f32x16_t acc[FM][FN];
+#pragma unroll
+    for (int mi = 0; mi < FM; ++mi)
+#pragma unroll
+      for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = (f32x16_t)(0.0f);
+
+    YStage<TM, NT, COLS> ys;
+    QStage<TN, NT, PARTS> qs;
+    auto load = [&](int kt) __attribute__((always_inline)) {
+      const int64_t c0 = static_cast<int64_t>(kt) * kC;
+      const bool full = c0 + kC <= a.c;
+      ys.load(a, m0, c0, tid, full && inside_m);
+      qs.load(a, n0, c0, tid, full && inside_n);
+    };
+    constexpr int NY = YStage<TM, NT, COLS>::NC, NQ = QStage<TN, NT, PARTS>::NC;
+    bf16x8_t fa[2][PARTS][FN], fb[2][FM];
+    auto frags = [&](const char* sm, int kk, auto BUF) __attribute__((always_inline)) {
+      constexpr int b = decltype(BUF)::value;
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p)
+#pragma unroll
+        for (int ni = 0; ni < FN; ++ni) fa[b][p][ni] = km_frag<TN>(sm + YB + p * (kC * TN * 2), wn * WN + ni * 32, kk, lane);
+#pragma unroll
+      for (int mi = 0; mi < FM; ++mi) {
+        if constexpr (COLS) fb[b][mi] = km_frag<TM>(sm, wm * WM + mi * 32, kk, lane);
+        else fb[b][mi] = *reinterpret_cast<const bf16x8_t*>(sm + rt_off<64>(wm * WM + mi * 32 + (lane & 31), 2 * kk + (lane >> 5)));
+      }
+    };
+    constexpr int NMF = FM * FN * PARTS, TAIL = NMF / 2, KK = kC / 16;
+    constexpr int NRD = (COLS ? 2 : 1) * FM + 2 * FN * PARTS;
+    auto mfmas = [&](auto BUF, auto BEGIN, auto END) __attribute__((always_inline)) {
+      constexpr int b = decltype(BUF)::value;
+      static_for<decltype(END)::value - decltype(BEGIN)::value>([&](auto P) {
+        constexpr int p = decltype(P)::value + decltype(BEGIN)::value;
+        constexpr int part = p / (FM * FN), mi = p % (FM * FN) / FN, ni = p % FN;
+        acc[mi][ni] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[b][part][ni], fb[b][mi], acc[mi][ni], 0, 0, 0);
+      });
+    };
+    // what a stage stores of the next one, in four parts
+    auto store_part = [&](char* to, int part) __attribute__((always_inline)) {
+#pragma unroll
+      for (int q = 0; q < NY; ++q)
+        if (q % 3 == part) ys.store(to, tid, q);
+#pragma unroll
+      for (int h = 0; h < 2 * NQ; ++h)
+        if (h % 3 == part) qs.store(to + YB, tid, h / 2, h % 2);
+    };
+    auto interleave = [&](auto NM) __attribute__((always_inline)) {
+      static_for<decltype(NM)::value>([&](auto I) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if constexpr (decltype(I)::value < NRD) __builtin_amdgcn_sched_group_barrier(0x100, NRD > NMF ? 2 : 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
+      });
+    };
+    auto stage = [&](auto S, int kt) __attribute__((always_inline)) {
+      char* cur = st + decltype(S)::value * STAGE;
+      char* nxt = st + (1 - decltype(S)::value) * STAGE;
+      static_for<KK>([&](auto KI) {
+        constexpr int kk = decltype(KI)::value;
+        constexpr int b = kk & 1;
+        if constexpr (kk + 1 < KK) {
+          frags(cur, kk + 1, ic<b ^ 1>{});
+          store_part(nxt, kk);
+          mfmas(ic<b>{}, ic<0>{}, ic<NMF>{});
+          interleave(ic<NMF>{});
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (kk + 2 == KK) load(kt + 2);
+        } else {
+          mfmas(ic<b>{}, ic<0>{}, ic<NMF - TAIL>{});
+          __builtin_amdgcn_sched_barrier(0);
+          // (a bare barrier: the loads of the stage after the next stay in flight)
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
+          frags(nxt, 0, ic<0>{});
+          mfmas(ic<b>{}, ic<NMF - TAIL>{}, ic<NMF>{});
+          interleave(ic<TAIL>{});
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      });
+    };
+    load(0);
+    static_for<3>([&](auto P) { store_part(st, decltype(P)::value); });
+    load(1);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    frags(st, 0, ic<0>{});
+    // whole rounds of two stages: past the end they hold zeros
+    for (int kt = 0; kt < KT; kt += 2) static_for<2>([&](auto S) { stage(S, kt + decltype(S)::value); });
+
+    // ---- epilogue: fp32 sums through LDS, row-contiguous stores
+    int el = lane;
+    asm volatile("" : "+v"(el));
+    __syncthreads();
+    constexpr int E = static_cast<int>(sizeof(O));
+    constexpr int ROUNDS = TM * TN * 4 > 2 * STAGE ? 2 : 1, RR = TM / ROUNDS;
+    static_assert(RR * TN * 4 <= 2 * STAGE, "output rows fit the stage buffers");
+    O* out = reinterpret_cast<O*>(a.out.p);
+    const bool wide = ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(a.out.ld * E)) & 15u) == 0;
+    static_for<ROUNDS>([&](auto R) {
+      constexpr int rd = decltype(R)::value;
+      if (ROUNDS == 1 || wm == rd) {
+        static_for<FM>([&](auto MI) {
+          constexpr int mi = decltype(MI)::value;
+          const int row = (ROUNDS == 1 ? wm * WM : 0) + mi * 32 + (el & 31);
+          static_for<FN>([&](auto NI) {
+            constexpr int ni = decltype(NI)::value;
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              *reinterpret_cast<float4*>(st + of_off<TN>(row, wn * WN + ni * 32 + 8 * g + 4 * (el >> 5))) =
+                  make_float4(acc[mi][ni][4 * g], acc[mi][ni][4 * g + 1], acc[mi][ni][4 * g + 2], acc[mi][ni][4 * g + 3]);
+            __builtin_amdgcn_sched_barrier(0);
+          });
+        });
+      }
+      __syncthreads();
+      constexpr int C = 16 / E, CH = TN / C;
+      const int et = wave * 64 + el;
+#pragma unroll 2
+      for (int it = 0; it < RR * CH / NT; ++it) {
+        const int e = et + it * NT, row = e / CH, c = C * (e % CH);
+        const int64_t m = m0 + rd * RR + row, n = n0 + c;
+        if (m >= a.m || n >= a.n) continue;
+        float v[C];
+#pragma unroll
+        for (int q = 0; q < C; q += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(st + of_off<TN>(row, c + q));
+          v[q] = f.x, v[q + 1] = f.y, v[q + 2] = f.z, v[q + 3] = f.w;
+        }
+        O* to = out + m * a.out.ld + n;
+        if (wide && n + C <= a.n) {
+          u32x4_t w4;
+          if (a.accumulate) {
+            w4 = *reinterpret_cast<const u32x4_t*>(to);
+#pragma unroll
+            for (int q = 0; q < C; ++q) v[q] += muon::Elem<O>::load(reinterpret_cast<const O*>(&w4) + q);
+          }
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if constexpr (E == 2) w4[q] = muon::pack_bf16x2(v[2 * q], v[2 * q + 1]);
+            else w4[q] = __float_as_uint(v[q]);
+          }
+          __builtin_nontemporal_store(w4, reinterpret_cast<u32x4_t*>(to));
+        } else {
+#pragma unroll
+          for (int q = 0; q < C; ++q)
+            if (n + q < a.n) muon::Elem<O>::store(to + q, a.accumulate ? muon::Elem<O>::load(to + q) + v[q] : v[q]);
+        }
+      }
+      __syncthreads();
+    });
+  }
+}
+
+template <typename O, int TM, int TN, int NWN, int PARTS>
+hipError_t go_tiles(hipStream_t s, const Grad8Args& a) {
+  const int tm = static_cast<int>((a.m + TM - 1) / TM), tn = static_cast<int>((a.n + TN - 1) / TN);
+  const int64_t tiles = static_cast<int64_t>(tm) * tn, cap = a.cus * (NWN == 4 ? 1 : 2);
+  const unsigned grid = static_cast<unsigned>(tiles < cap ? tiles : cap);
+  if (a.of_columns) grad8_tile_kernel<O, TM, TN, NWN, PARTS, true><<<grid, 128 * NWN, 0, s>>>(a, tm, tn);
+  else grad8_tile_kernel<O, TM, TN, NWN, PARTS, false><<<grid, 128 * NWN, 0, s>>>(a, tm, tn);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_grad8(hipStream_t s, const Grad8Args& a) {
   if (a.m == 0 || a.n == 0) return hipSuccess;
-  const unsigned grid = static_cast<unsigned>(((a.m + kTile - 1) / kTile) * ((a.n + kTile - 1) / kTile));
-  if (a.out.bf16) grad8_simple_kernel<bf16_t><<<grid, 256, 0, s>>>(a);
-  else grad8_simple_kernel<float><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError();
+  const int64_t t256 = ((a.m + 255) / 256) * ((a.n + 255) / 256);
+  const bool large = t256 * 2 >= a.cus;
+  if (a.out.bf16) return large ? go_tiles<bf16_t, 256, 256, 4, 1>(s, a) : go_tiles<bf16_t, 128, 128, 2, 1>(s, a);
+  return large ? go_tiles<float, 256, 128, 4, 2>(s, a) : go_tiles<float, 128, 64, 2, 2>(s, a);
 }

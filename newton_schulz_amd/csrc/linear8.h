@@ -29,6 +29,7 @@ struct Matmul8Args {
   Values out;
   int64_t m, n;
   int k;
+  int cus;
 };
 hipError_t launch_matmul8(hipStream_t s, const Matmul8Args& a);
 
@@ -40,6 +41,7 @@ struct Grad8Args {
   Values out;
   int64_t m, n, c;
   int accumulate;
+  int cus;
 };
 hipError_t launch_grad8(hipStream_t s, const Grad8Args& a);
 

@@ -8,7 +8,8 @@
 
 namespace {
 
-constexpr int64_t kMostStride = int64_t{1} << 40;
+// A tile's 256 rows lie within 2 GiB (offsets of its loads): strides up to 2^22.
+constexpr int64_t kMostStride = int64_t{1} << 22;
 constexpr int64_t kMostOut = int64_t{1} << 39;  // elements of a product
 
 inline int64_t up16(int64_t n) { return (n + 15) & ~int64_t{15}; }
@@ -18,7 +19,7 @@ muon_status_t check_rows(muon_ctx* c, const muon_rows_t* x, bool written, size_t
   *bytes = 0;
   if (x == nullptr) return fail(c, MUON_EINVAL, "rows NULL");
   if (!is_dtype(x->dtype)) return fail(c, MUON_EDTYPE, "rows dtype");
-  if (x->rows < 0 || x->rows > MUON_MAX_ROWS8 || x->cols < 1 || x->cols > MUON_MAX_ROWS8)
+  if (x->rows < 0 || x->rows > MUON_MAX_ROWS8 || x->cols < 1 || x->cols > kMostStride)
     return fail(c, MUON_ESHAPE, "rows or cols out of range");
   if (x->rows == 0) return MUON_OK;
   if (x->rows > 1 && (x->row_stride < 0 || x->row_stride > kMostStride)) return fail(c, MUON_ESHAPE, "row stride out of range");
@@ -73,7 +74,7 @@ LinearLayout linear_layout(int64_t tokens, int64_t k) {
 }
 
 muon_status_t matmul8(muon_ctx* c, hipStream_t s, const Bytes& a, int64_t m, const muon_rows8_t& b, const muon_rows_t& out) {
-  const Matmul8Args t = {a, bytes8(b), values(out), m, b.rows, static_cast<int>(b.cols)};
+  const Matmul8Args t = {a, bytes8(b), values(out), m, b.rows, static_cast<int>(b.cols), c->cus};
   return timed(c, s, MUON_K_LINEAR8, "8-bit product launch", [&] { return launch_matmul8(s, t); });
 }
 
@@ -97,7 +98,7 @@ muon_status_t grad8(muon_ctx* c, void* stream, const muon_rows_t* y, const muon_
   if (st == MUON_OK) st = check_ctx(c, 0);
   if (st != MUON_OK || m == 0) return st;
   DeviceGuard g(c->device);
-  const Grad8Args t = {values(*y), of_columns, bytes8(*q), values(*out), m, q->cols, contraction, accumulate != 0};
+  const Grad8Args t = {values(*y), of_columns, bytes8(*q), values(*out), m, q->cols, contraction, accumulate != 0, c->cus};
   hipStream_t s = static_cast<hipStream_t>(stream);
   return timed(c, s, MUON_K_LINEAR8, "8-bit gradient launch", [&] { return launch_grad8(s, t); });
 }
