@@ -1,6 +1,8 @@
 // Checks of arguments and helpers that the C entry points share.
 #pragma once
 
+#include <cmath>
+
 #include "loss_kernels.h"
 #include "muon_ctx.h"
 
@@ -72,6 +74,15 @@ inline muon_status_t check_spans(muon_ctx* c, const Span* s, int n, bool in_plac
 
 // also 1 / t and log2 e / t, which the kernels take in fp32, have to be finite
 inline bool good_temperature(double t) { return t > 1e-30 && t < 1e30; }
+
+// Neighbours of k in fp32 whose mean over `vec` scores is k to half a step / vec.
+inline void k_neighbours(double k, int vec, float (&each)[8]) {
+  const float near = static_cast<float>(k);
+  const float down = static_cast<double>(near) <= k ? near : std::nextafterf(near, 0.0f);
+  const float up = std::nextafterf(down, INFINITY);
+  const double ups = vec * (k - down) / (static_cast<double>(up) - down);
+  for (int i = 0; i < 8; ++i) each[i] = i % vec < static_cast<int>(ups + 0.5) ? up : down;
+}
 
 inline muon_status_t check_ctx(muon_ctx* c, size_t need) {
   if (c == nullptr) return fail(c, MUON_EINVAL, "context NULL");

@@ -32,36 +32,36 @@ __device__ __forceinline__ bf16x8_t km_frag(const char* t, int cb, int kk, int l
   return __builtin_bit_cast(bf16x8_t, u32x4_t{lo.x, lo.y, hi.x, hi.y});
 }
 
-// 16 bytes of y through registers: TM rows of the output by 64 of the contraction.
+// 16 bytes of y through registers: TM rows of the output by 64 of the
+// contraction.  A thread's chunks lie STEP rows (of memory) apart.
 template <int TM, int NT, bool COLS>
 struct YStage {
-  static constexpr int NC = TM * kC / 8 / NT;
+  static constexpr int CPR = COLS ? TM / 8 : kC / 8, STEP = NT / CPR, NC = TM * kC / 8 / NT;
   u32x4_t v[NC];
-  static __device__ __forceinline__ int row(int e) { return COLS ? e / (TM / 8) : e / (kC / 8); }  // of memory
-  static __device__ __forceinline__ int chunk(int e) { return COLS ? e % (TM / 8) : e % (kC / 8); }
-
+  uint32_t off;  // of the thread's first chunk, bytes
+  int row, chunk;
+  __device__ __forceinline__ void init(const Grad8Args& a, uint32_t tid) {
+    row = tid / CPR;
+    chunk = tid % CPR;
+    off = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.y.ld) * 2u + static_cast<uint32_t>(chunk) * 16u;
+  }
   // fast: every chunk is inside
-  __device__ __forceinline__ void load(const Grad8Args& a, int64_t m0, int64_t c0, int tid, bool fast) {
-    const bf16_t* y = reinterpret_cast<const bf16_t*>(a.y.p);
+  __device__ __forceinline__ void load(const Grad8Args& a, int64_t m0, int64_t c0, bool fast) {
     const int64_t r0 = COLS ? c0 : m0, k0 = COLS ? m0 : c0;
-    const int64_t rows = COLS ? a.c : a.m, cols = COLS ? a.m : a.c;
-    const char* base = reinterpret_cast<const char*>(uniform_ptr(y + r0 * a.y.ld + k0));
-    const uint32_t ld = static_cast<uint32_t>(a.y.ld) * 2u;
-    if (fast) {
+    const char* base = uniform_ptr(a.y.p + (r0 * a.y.ld + k0) * 2);
+    const int64_t step = a.y.ld * (2 * STEP);
+    if (__builtin_expect(fast, 1)) {
 #pragma unroll
-      for (int q = 0; q < NC; ++q) {
-        const int e = tid + q * NT;
-        v[q] = *reinterpret_cast<const u32x4_any*>(base + (static_cast<uint32_t>(row(e)) * ld + static_cast<uint32_t>(chunk(e)) * 16u));
-      }
+      for (int q = 0; q < NC; ++q) v[q] = *reinterpret_cast<const u32x4_any*>(base + q * step + off);
       return;
     }
+    const int left = static_cast<int>(min((COLS ? a.m : a.c) - k0, int64_t{1} << 20)) - 8 * chunk;
+    const int rows = static_cast<int>(min((COLS ? a.c : a.m) - r0, int64_t{1} << 20)) - row;
 #pragma unroll
     for (int q = 0; q < NC; ++q) {
-      const int e = tid + q * NT;
-      const int64_t left = cols - (k0 + 8 * chunk(e));
       v[q] = u32x4_t{0, 0, 0, 0};
-      if (r0 + row(e) >= rows || left <= 0) continue;
-      const char* at = base + (static_cast<uint32_t>(row(e)) * ld + static_cast<uint32_t>(chunk(e)) * 16u);
+      if (q * STEP >= rows || left <= 0) continue;
+      const char* at = base + q * step + off;
       if (left >= 8) {
         v[q] = *reinterpret_cast<const u32x4_any*>(at);
       } else {
@@ -72,10 +72,12 @@ struct YStage {
       }
     }
   }
-  __device__ __forceinline__ void store(char* lds, int tid, int q) const {
-    const int e = tid + q * NT;
-    const int off = COLS ? km_off<TM>(row(e), 8 * chunk(e)) : rt_off<64>(row(e), chunk(e));
-    *reinterpret_cast<u32x4_t*>(lds + off) = v[q];
+  // lds: from address()
+  __device__ __forceinline__ int address() const { return COLS ? km_off<TM>(row, 8 * chunk) : rt_off<64>(row, chunk); }
+  __device__ __forceinline__ void store(char* lds, int at, int q) const {
+    // (rows 64 apart share a swizzle of rt_off)
+    const int o = COLS ? at + q * STEP * 2 * TM : STEP % 64 == 0 ? at + q * STEP * 128 : rt_off<64>(row + q * STEP, chunk);
+    *reinterpret_cast<u32x4_t*>(lds + o) = v[q];
   }
 };
 
@@ -83,37 +85,41 @@ struct YStage {
 // for: PARTS planes of 64 x TN, the second what the first one's rounding left.
 template <int TN, int NT, int PARTS>
 struct QStage {
-  static constexpr int NC = TN * kC / 16 / NT;
+  static constexpr int CPR = TN / 16, STEP = NT / CPR, NC = TN * kC / 16 / NT;
+  static_assert(STEP % 4 == 0, "the rows of a thread's chunks share a swizzle");
   u32x4_t v[NC];
   float s[NC];
-  static __device__ __forceinline__ int row(int e) { return e / (TN / 16); }
-  static __device__ __forceinline__ int chunk(int e) { return e % (TN / 16); }
-
-  __device__ __forceinline__ void load(const Grad8Args& a, int64_t n0, int64_t c0, int tid, bool fast) {
-    const char* base = reinterpret_cast<const char*>(uniform_ptr(a.q.p + c0 * a.q.ld + n0));
+  uint32_t off;
+  int row, chunk;
+  __device__ __forceinline__ void init(const Grad8Args& a, uint32_t tid) {
+    row = tid / CPR;
+    chunk = tid % CPR;
+    off = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.q.ld) + static_cast<uint32_t>(chunk) * 16u;
+  }
+  __device__ __forceinline__ void load(const Grad8Args& a, int64_t n0, int64_t c0, bool fast) {
+    const char* base = uniform_ptr(reinterpret_cast<const char*>(a.q.p) + c0 * a.q.ld + n0);
     const float* scale = uniform_ptr(a.q.scale + c0);
-    const uint32_t ld = static_cast<uint32_t>(a.q.ld);
-    if (fast) {
+    const int64_t step = a.q.ld * STEP;
+    if (__builtin_expect(fast, 1)) {
 #pragma unroll
       for (int q = 0; q < NC; ++q) {
-        const int e = tid + q * NT;
-        v[q] = *reinterpret_cast<const u32x4_t*>(base + (static_cast<uint32_t>(row(e)) * ld + static_cast<uint32_t>(chunk(e)) * 16u));
-        s[q] = scale[row(e)];
+        v[q] = *reinterpret_cast<const u32x4_t*>(base + q * step + off);
+        s[q] = (scale + q * STEP)[static_cast<uint32_t>(row)];
       }
       return;
     }
+    const int left = static_cast<int>(min(a.n - n0, int64_t{1} << 20)) - 16 * chunk;
+    const int rows = static_cast<int>(min(a.c - c0, int64_t{1} << 20)) - row;
 #pragma unroll
     for (int q = 0; q < NC; ++q) {
-      const int e = tid + q * NT;
-      const int64_t left = a.n - (n0 + 16 * chunk(e)), c = c0 + row(e);
       v[q] = u32x4_t{0, 0, 0, 0};
       s[q] = 0.0f;
-      if (c >= a.c) continue;
-      s[q] = scale[row(e)];
+      if (q * STEP >= rows) continue;
+      s[q] = scale[row + q * STEP];
       if (left <= 0) continue;
-      const char* at = base + (static_cast<uint32_t>(row(e)) * ld + static_cast<uint32_t>(chunk(e)) * 16u);
+      const char* at = base + q * step + off;
       // (rows lie 16 bytes apart at least, so only the last one's end may be the memory's)
-      if (left >= 16 || (c + 1 < a.c && ld != 0)) {
+      if (left >= 16 || (q * STEP + 1 < rows && a.q.ld != 0)) {
         v[q] = *reinterpret_cast<const u32x4_t*>(at);
       } else {
         const uint8_t* b = reinterpret_cast<const uint8_t*>(at);
@@ -123,9 +129,9 @@ struct QStage {
       }
     }
   }
+  __device__ __forceinline__ int address() const { return km_off<TN>(row, 16 * chunk); }
   // half h (8 integers) of chunk q
-  __device__ __forceinline__ void store(char* lds, int tid, int q, int h) const {
-    const int e = tid + q * NT;
+  __device__ __forceinline__ void store(char* lds, int at, int q, int h) const {
     u32x4_t hi, lo;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -136,9 +142,9 @@ struct QStage {
       if constexpr (PARTS == 2)
         lo[i] = muon::pack_bf16x2(x0 - __uint_as_float(hi[i] << 16), x1 - __uint_as_float(hi[i] & 0xffff0000u));
     }
-    const int off = km_off<TN>(row(e), 16 * chunk(e) + 8 * h);
-    *reinterpret_cast<u32x4_t*>(lds + off) = hi;
-    if constexpr (PARTS == 2) *reinterpret_cast<u32x4_t*>(lds + kC * TN * 2 + off) = lo;
+    char* to = lds + at + q * STEP * 2 * TN + 16 * h;  // (the swizzle leaves a chunk's lowest bit)
+    *reinterpret_cast<u32x4_t*>(to) = hi;
+    if constexpr (PARTS == 2) *reinterpret_cast<u32x4_t*>(to + kC * TN * 2) = lo;
   }
 };
 
@@ -179,11 +185,14 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, i
 
     YStage<TM, NT, COLS> ys;
     QStage<TN, NT, PARTS> qs;
+    ys.init(a, tid);
+    qs.init(a, tid);
+    const int ya = ys.address(), qa = qs.address();
     auto load = [&](int kt) __attribute__((always_inline)) {
       const int64_t c0 = static_cast<int64_t>(kt) * kC;
       const bool full = c0 + kC <= a.c;
-      ys.load(a, m0, c0, tid, full && inside_m);
-      qs.load(a, n0, c0, tid, full && inside_n);
+      ys.load(a, m0, c0, full && inside_m);
+      qs.load(a, n0, c0, full && inside_n);
     };
     constexpr int NY = YStage<TM, NT, COLS>::NC, NQ = QStage<TN, NT, PARTS>::NC;
     bf16x8_t fa[2][PARTS][FN], fb[2][FM];
@@ -213,10 +222,10 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, i
     auto store_part = [&](char* to, int part) __attribute__((always_inline)) {
 #pragma unroll
       for (int q = 0; q < NY; ++q)
-        if (q % 3 == part) ys.store(to, tid, q);
+        if (q % 3 == part) ys.store(to, ya, q);
 #pragma unroll
       for (int h = 0; h < 2 * NQ; ++h)
-        if (h % 3 == part) qs.store(to + YB, tid, h / 2, h % 2);
+        if (h % 3 == part) qs.store(to + YB, qa, h / 2, h % 2);
     };
     auto interleave = [&](auto NM) __attribute__((always_inline)) {
       static_for<decltype(NM)::value>([&](auto I) {

@@ -45,17 +45,46 @@ struct Grad8Args {
 };
 hipError_t launch_grad8(hipStream_t s, const Grad8Args& a);
 
+// What the kernels of one verification hand each other.
+struct VerifyPart {  // of a slice: largest score, its lowest index, sum around it
+  float m;
+  int best;
+  double s;
+};
+struct VerifyEnd {  // of a sequence
+  int r, y, mode;
+  float mp, mq;
+  int best;
+  double sp;
+};
+// Slices of a row in the first reading and in the second, and where in the
+// workspace things lie; `bytes`: of the wider of the scores' types.
+struct VerifyPlan {
+  int slices, slice, cuts, cut, rows, launch;
+  size_t parts, ends, sums, weights, total;
+};
+VerifyPlan verify_plan(int64_t batch, int64_t draft, int64_t vocab, int bytes);
+
 struct VerifyArgs {
   RowsRef x;       // target: batch x (draft + 1) rows
   int x_bf16;
-  RowsRef d;       // draft: batch x draft rows; base nullptr: deterministic
+  RowsRef d;       // draft: batch x draft rows; base nullptr: deterministic, or greedy
   int d_bf16;
-  int batch, draft, vocab;
+  int draft, vocab;
   const int64_t* drafted;
   const float* uniforms;
   double inv_t;    // 1 / temperature; 0: greedy
+  float k, k_rest; // log2 e / temperature = k + k_rest = kd (greedy: of temperature 1)
+  double kd;
+  float k_each[8]; // for the scores of 16 bytes: neighbours of k with its mean
   int64_t* tokens;
   int64_t* accepted;
   float* logps;
+  // set by the launcher
+  int slices, slice, cuts, cut, rows;
+  VerifyPart* parts;
+  VerifyEnd* ends;
+  double2* sums;
+  double* weights;
 };
-hipError_t launch_verify(hipStream_t s, const VerifyArgs& a);
+hipError_t launch_verify(hipStream_t s, VerifyArgs a, int64_t batch, const VerifyPlan& p, char* ws);

@@ -216,7 +216,8 @@ size_t muon_verify_workspace_bytes(int64_t batch, int64_t draft, int64_t vocab) 
   if (batch < 0 || draft < 0 || draft > MUON_MAX_DRAFT || vocab < 1 || vocab > MUON_MAX_VOCAB || batch > kMostTokens ||
       batch * (draft + 1) > kMostTokens)
     return 0;
-  return 256;
+  // (the slices of fp32 scores are the finer ones)
+  return verify_plan(batch, draft, vocab, 4).total;
 }
 
 muon_status_t muon_verify_draft(muon_ctx_t* c, void* stream, const muon_logits_t* logits, const int64_t* draft_tokens,
@@ -245,7 +246,10 @@ muon_status_t muon_verify_draft(muon_ctx_t* c, void* stream, const muon_logits_t
                         {accepted, batch * 8, 8, true, true, "accepted"},
                         {logps, places * 4, 4, true, false, "logps"}};
   st = check_spans(c, spans, 7, false);
-  if (st == MUON_OK) st = check_ctx(c, muon_verify_workspace_bytes(logits->batch, draft, logits->vocab));
+  // (slices are counted in the wider of the two types)
+  const int bytes = logits->dtype == MUON_F32 || (draft_logits && draft_logits->dtype == MUON_F32) ? 4 : 2;
+  const VerifyPlan p = verify_plan(logits->batch, draft, logits->vocab, bytes);
+  if (st == MUON_OK) st = check_ctx(c, p.total);
   if (st != MUON_OK || batch == 0) return st;
   DeviceGuard g(c->device);
   VerifyArgs a = {};
@@ -255,17 +259,20 @@ muon_status_t muon_verify_draft(muon_ctx_t* c, void* stream, const muon_logits_t
     a.d = rows_ref(*draft_logits);
     a.d_bf16 = draft_logits->dtype == MUON_BF16;
   }
-  a.batch = static_cast<int>(batch);
   a.draft = static_cast<int>(draft);
   a.vocab = static_cast<int>(logits->vocab);
   a.drafted = draft_tokens;
   a.uniforms = uniforms;
   a.inv_t = greedy ? 0.0 : 1.0 / temperature;
+  a.kd = 1.44269504088896340736 * (greedy ? 1.0 : a.inv_t);
+  a.k = static_cast<float>(a.kd);
+  a.k_rest = static_cast<float>(a.kd - static_cast<double>(a.k));
+  k_neighbours(a.kd, bytes == 4 ? 4 : 8, a.k_each);
   a.tokens = tokens;
   a.accepted = accepted;
   a.logps = logps;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return timed(c, s, MUON_K_VERIFY, "draft verification launch", [&] { return launch_verify(s, a); });
+  return timed(c, s, MUON_K_VERIFY, "draft verification launch", [&] { return launch_verify(s, a, logits->batch, p, c->ws); });
 }
 
 }  // extern "C"

@@ -76,11 +76,7 @@ LossArgs loss_args(const muon_ctx* c, const LossLayout& l, const muon_logits_t& 
   a.k_rest = static_cast<float>(k - static_cast<double>(a.k));
   a.none = static_cast<float>(-256.0 / k);  // (finite: k is above 1e-30)
   // k lies between two fp32 numbers: the mean over a piece of the two is k
-  const float down = static_cast<double>(a.k) <= k ? a.k : std::nextafterf(a.k, 0.0f);
-  const float up = std::nextafterf(down, INFINITY);
-  const int vec = a.bf16 ? 8 : 4;
-  const double ups = vec * (k - down) / (static_cast<double>(up) - down);
-  for (int i = 0; i < 8; ++i) a.k_each[i] = i % vec < static_cast<int>(ups + 0.5) ? up : down;
+  k_neighbours(k, a.bf16 ? 8 : 4, a.k_each);
   a.inv_t = 1.0 / temperature;
   a.slices = slices_of(c, x);
   a.spin = c->loss_spin;
