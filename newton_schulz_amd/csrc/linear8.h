@@ -46,11 +46,6 @@ struct Grad8Args {
 hipError_t launch_grad8(hipStream_t s, const Grad8Args& a);
 
 // What the kernels of one verification hand each other.
-struct VerifyPart {  // of a slice: largest score, its lowest index, sum around it
-  float m;
-  int best;
-  double s;
-};
 struct VerifyEnd {  // of a sequence
   int r, y, mode;
   float mp, mq;
@@ -60,7 +55,7 @@ struct VerifyEnd {  // of a sequence
 // Slices of a row in the first reading and in the second, and where in the
 // workspace things lie; `bytes`: of the wider of the scores' types.
 struct VerifyPlan {
-  int slices, slice, cuts, cut, rows, launch;
+  int slices, slice, cuts, cut, rows, groups, launch;
   size_t parts, ends, sums, weights, total;
 };
 VerifyPlan verify_plan(int64_t batch, int64_t draft, int64_t vocab, int bytes);
@@ -81,10 +76,12 @@ struct VerifyArgs {
   int64_t* accepted;
   float* logps;
   // set by the launcher
-  int slices, slice, cuts, cut, rows;
-  VerifyPart* parts;
+  int slices, slice, cuts, cut, rows, groups;
+  uint64_t* counters;  // zero between launches
+  uint64_t* parts;     // [batch][rows][slices][2]: maximum and its index, sum
   VerifyEnd* ends;
-  double2* sums;
-  double* weights;
+  uint64_t* sums;      // [batch][cuts][2]
+  uint64_t* weights;   // [batch][cuts]
 };
-hipError_t launch_verify(hipStream_t s, VerifyArgs a, int64_t batch, const VerifyPlan& p, char* ws);
+hipError_t launch_verify(hipStream_t s, VerifyArgs a, int64_t batch, const VerifyPlan& p, char* ws,
+                         Exchange& x);

@@ -272,7 +272,7 @@ muon_status_t muon_verify_draft(muon_ctx_t* c, void* stream, const muon_logits_t
   a.accepted = accepted;
   a.logps = logps;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  return timed(c, s, MUON_K_VERIFY, "draft verification launch", [&] { return launch_verify(s, a, logits->batch, p, c->ws); });
+  return timed(c, s, MUON_K_VERIFY, "draft verification launch", [&] { return launch_verify(s, a, logits->batch, p, c->ws, c->exchange); });
 }
 
 }  // extern "C"

@@ -13,23 +13,34 @@
 // rows that are drawn from are therefore read again with exponentials good to
 // 2^-45 and everything in binary64.
 //
-// Shape.  Rows are cut into slices, a workgroup each.
+// Shape.  Rows are cut into slices, a workgroup each; the last workgroup of a
+// sequence to finish goes on with what needs all of them.
 //   verify_pairs_kernel: maximum and sum of every row that may be needed (the
-//     bound: HBM and the exponentials);
-//   verify_sums_kernel: which place ends the sequence, and that row's sums;
-//   verify_weights_kernel: the sums of max(p - q, 0) (with draft scores only);
-//   verify_take_kernel: the slice that u falls into, the token, the outputs.
+//     bound: HBM and the exponentials); last: which place ends the sequence;
+//   verify_sums_kernel: that row's sums; last, where there are no draft scores:
+//     the token;
+//   verify_weights_kernel: the sums of max(p - q, 0); last: the token.
 #include <cfloat>
+#include <type_traits>
 
+#include "exchange.h"
 #include "linear8.h"
 #include "muon_device.h"
+#include "wave_ops.h"
 
 using muon::bf16_t;
+using muon::publish;
+using muon::published;
+using muon::wave_max;
+using muon::wave_sum;
 
 namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kRun = 4, kMostCuts = 64 * kRun;  // slices of the second reading that a lane holds, and of a row
+constexpr int kN = 8, kMostCut = 2 * kThreads * kN;  // scores that a thread takes at a time, and of a slice of the second reading
+// Counters of a sequence: of 32 workgroups each, then one of those; in lines of their own.
+constexpr int kTogether = 32, kCounterStride = 8;
 constexpr float kLowest = -FLT_MAX;
 
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
@@ -57,14 +68,6 @@ __device__ __forceinline__ void piece(const T* row, int i, int end, float (&v)[k
   }
 }
 
-__device__ __forceinline__ float wave_max(float v) {
-  for (int d = 32; d > 0; d /= 2) v = fmaxf(v, __shfl_xor(v, d));
-  return v;
-}
-__device__ __forceinline__ double wave_sum(double v) {
-  for (int d = 32; d > 0; d /= 2) v += __shfl_xor(v, d);
-  return v;
-}
 __device__ __forceinline__ int wave_min(int v) {
   for (int d = 32; d > 0; d /= 2) v = min(v, __shfl_xor(v, d));
   return v;
@@ -91,25 +94,68 @@ struct Scale {
   }
 };
 
-// 2^t for t <= 0, to 2^-45: t = n / 32 + f with a table of 2^(j / 32), and a
-// polynomial of degree 5 in f log 2 (|f log 2| <= 0.0109: the rest is 2^-48).
-struct Exp2 {
-  const double* table;  // LDS
-  __device__ __forceinline__ double operator()(double t) const {
-    t = fmax(t, -1080.0);
-    const double n = rint(t * 32.0);
-    const double f = __builtin_fma(n, -1.0 / 32.0, t) * 0.69314718055994530942;
+// exp(x / T) around a maximum m in binary64, to 2^-44: (x - m) / T log2 e = n / 32
+// + f / 32 with |f| <= 1/2, from a table of 2^(j / 32) and the series of 2^(f /
+// 32) up to its fourth term (the fifth is below 2^-39 / 120).
+__device__ const double kRoots[32] = {
+    0x1.0000000000000p+0, 0x1.059b0d3158574p+0, 0x1.0b5586cf9890fp+0, 0x1.11301d0125b51p+0,
+    0x1.172b83c7d517bp+0, 0x1.1d4873168b9aap+0, 0x1.2387a6e756238p+0, 0x1.29e9df51fdee1p+0,
+    0x1.306fe0a31b715p+0, 0x1.371a7373aa9cbp+0, 0x1.3dea64c123422p+0, 0x1.44e086061892dp+0,
+    0x1.4bfdad5362a27p+0, 0x1.5342b569d4f82p+0, 0x1.5ab07dd485429p+0, 0x1.6247eb03a5585p+0,
+    0x1.6a09e667f3bcdp+0, 0x1.71f75e8ec5f74p+0, 0x1.7a11473eb0187p+0, 0x1.82589994cce13p+0,
+    0x1.8ace5422aa0dbp+0, 0x1.93737b0cdc5e5p+0, 0x1.9c49182a3f090p+0, 0x1.a5503b23e255dp+0,
+    0x1.ae89f995ad3adp+0, 0x1.b7f76f2fb5e47p+0, 0x1.c199bdd85529cp+0, 0x1.cb720dcef9069p+0,
+    0x1.d5818dcfba487p+0, 0x1.dfc97337b9b5fp+0, 0x1.ea4afa2a490dap+0, 0x1.f50765b6e4540p+0,
+};
+struct Exp {
+  const double* table;  // kRoots in LDS
+  double k, m;          // 32 log2 e / T, the maximum
+  __device__ __forceinline__ Exp(const double* t, double kd, float top) : table(t), k(32.0 * kd), m(static_cast<double>(top)) {}
+  __device__ __forceinline__ double operator()(float x) const {
+    // (the difference first: scores of any size, the type's lowest too, keep it exact)
+    const double t = fmax((static_cast<double>(x) - m) * k, -34000.0);  // (2^-1062)
+    const double n = rint(t), f = t - n;
     const int i = static_cast<int>(n);
-    double p = __builtin_fma(f, 1.0 / 120.0, 1.0 / 24.0);
-    p = __builtin_fma(f, p, 1.0 / 6.0);
-    p = __builtin_fma(f, p, 0.5);
-    p = __builtin_fma(f, p, 1.0);
+    double p = __builtin_fma(f, 0x1.3b2ab6fba4e77p-27, 0x1.c6b08d704a0c0p-20);  // (log 2 / 32)^j / j!
+    p = __builtin_fma(f, p, 0x1.ebfbdff82c58fp-13);
+    p = __builtin_fma(f, p, 0x1.62e42fefa39efp-6);
     p = __builtin_fma(f, p, 1.0);
     return ldexp(p * table[i & 31], i >> 5);
   }
 };
 __device__ __forceinline__ void fill_table(double* table) {
-  if (threadIdx.x < 32) table[threadIdx.x] = exp2(static_cast<double>(threadIdx.x) / 32.0);
+  if (threadIdx.x < 32) table[threadIdx.x] = kRoots[threadIdx.x];
+}
+
+__device__ __forceinline__ void publish_double(uint64_t* to, double v) {
+  publish(to, static_cast<uint64_t>(__double_as_longlong(v)));
+}
+__device__ __forceinline__ double published_double(const uint64_t* from) {
+  return __longlong_as_double(static_cast<long long>(published(from)));
+}
+
+// Whether this workgroup, the index-th of `count` of sequence b, is the last of
+// them to get here; thread 0 has published what it found.
+__device__ __forceinline__ bool last_of_sequence(const VerifyArgs& a, int b, int index, int count) {
+  __shared__ int last;
+  if (threadIdx.x == 0) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    const int g = index / kTogether, groups = (count - 1) / kTogether + 1, in_group = min(count - g * kTogether, kTogether);
+    uint64_t* mine = a.counters + (static_cast<int64_t>(b) * a.groups + 1 + g) * kCounterStride;
+    uint64_t* all = a.counters + static_cast<int64_t>(b) * a.groups * kCounterStride;
+    bool l = muon::count_one(mine) == static_cast<unsigned>(in_group - 1);
+    if (l) {
+      *mine = 0;
+      if (groups > 1) {
+        l = muon::count_one(all) == static_cast<unsigned>(groups - 1);
+        if (l) *all = 0;
+      }
+    }
+    asm volatile("" ::: "memory");
+    last = l;
+  }
+  __syncthreads();
+  return last;
 }
 
 template <typename T> __device__ __forceinline__ const T* row_of(const RowsRef& x, int b, int i) {
@@ -185,115 +231,89 @@ __device__ __forceinline__ Part slice_part(const T* row, int lo, int hi, const S
   return r;
 }
 
-template <typename TX, typename TD, bool GREEDY>
-__global__ __launch_bounds__(kThreads) void verify_pairs_kernel(VerifyArgs a) {
-  const int j = blockIdx.x, b = blockIdx.z, i = blockIdx.y;  // rows 0 .. draft: the target's, beyond: the draft's
-  const int len = drafted_places(a, b);
-  const bool target = i <= a.draft;
-  const int place = target ? i : i - a.draft - 1;
-  if (target ? place > len : place >= len) return;
-  const Scale q(a);
-  const int lo = j * a.slice, hi = min(lo + a.slice, a.vocab);
-  const Part r = target ? slice_part<TX, GREEDY>(row_of<TX>(a.x, b, place), lo, hi, q)
-                        : slice_part<TD, GREEDY>(row_of<TD>(a.d, b, place), lo, hi, q);
-  if (threadIdx.x == 0) a.parts[(static_cast<int64_t>(b) * a.rows + i) * a.slices + j] = {r.m, r.best, r.s};
-}
-
-// A row's part from its slices', in every lane of the wave.
-__device__ __forceinline__ Part row_part(const VerifyArgs& a, int b, int i, const Scale& q) {
-  const int lane = threadIdx.x & 63;
-  Part r = {kLowest, INT32_MAX, 0.0};
-  if (lane < a.slices) {
-    const VerifyPart p = a.parts[(static_cast<int64_t>(b) * a.rows + i) * a.slices + lane];
-    r = {p.m, p.best, p.s};
-  }
-  const float m = wave_max(r.m);
-  r.s = r.s == 0.0 ? 0.0 : r.s * q.exp(r.m - m);
-  r.s = wave_sum(r.s);
-  r.best = wave_min(r.m == m ? r.best : INT32_MAX);
-  r.m = m;
-  return r;
-}
 __device__ __forceinline__ bool has_distribution(const Part& p) { return p.s > 0.0 && p.s < static_cast<double>(INFINITY); }
 
-// How sequence b ends, found by a whole workgroup: the place r and the row's
-// parts there; with `out` the kept tokens and their log-probabilities are
-// written.
-struct End {
-  int r;        // place that takes its token
-  int y;        // the token drafted there, -1: none (or past the vocabulary: -2)
-  int mode;     // 0: no distribution, 1: from p, 2: from max(p - q, 0)
-  float mp, mq;
-  int best;
-  double sp;
-};
-template <typename TX, typename TD>
-__device__ __forceinline__ End find_end(const VerifyArgs& a, int b, bool out) {
-  __shared__ int first[kWaves];
-  __shared__ End end;
-  __shared__ float kept[MUON_MAX_DRAFT];
+// How sequence b ends, found by a whole workgroup once all its parts are there:
+// the place and the row's parts there; the kept tokens are written.
+// (mode 0: no distribution, 1: from p, 2: from max(p - q, 0); y: the token
+// drafted there, -1: none, -2: one past the vocabulary)
+// part(row, slice) of the sequence's rows (0 .. draft: the target's).
+template <typename TX, typename TD, typename F>
+__device__ __forceinline__ VerifyEnd find_end(const VerifyArgs& a, int b, int len, int slices, F&& part) {
+  // Places are looked at kAtOnce at a time, a thread each; their rows' parts are
+  // joined by as many lanes as a row has slices (rounded up to a power of two).
+  constexpr int kAtOnce = 16;
+  __shared__ Part rows[2 * kAtOnce];
+  __shared__ VerifyEnd end;
   const bool greedy = a.inv_t == 0.0;
   const Scale q(a);
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int len = drafted_places(a, b);
-  End mine = {INT32_MAX, -1, 0, 0.0f, 0.0f, 0, 0.0};
-  // each wave takes every kWaves-th place, up to the first that is not kept
-  for (int i = wave; i <= len; i += kWaves) {
-    const Part P = row_part(a, b, i, q);
-    const int64_t y = i < len ? a.drafted[static_cast<int64_t>(b) * a.draft + i] : -1;
-    const bool named = y >= 0 && y < a.vocab;
-    const bool ok = has_distribution(P);
-    Part Q = {0.0f, 0, 1.0};
-    bool near = true;
-    double lp = 0.0;
-    bool keep = false;
-    if (ok && named) {
-      const float xy = muon::Elem<TX>::load(row_of<TX>(a.x, b, i) + y);
-      lp = (static_cast<double>(xy) - static_cast<double>(P.m)) * (greedy ? 1.0 : a.inv_t) - log(P.s);
+  const int64_t places = static_cast<int64_t>(b) * (a.draft + 1);
+  const int lanes = slices > 1 ? 1 << (32 - __builtin_clz(slices - 1)) : 1, of = static_cast<int>(threadIdx.x) & (lanes - 1);
+  for (int i0 = 0;; i0 += kAtOnce) {
+    const int n = min(kAtOnce, len + 1 - i0);
+    // what a place's thread needs beside the rows' parts
+    const int i = i0 + static_cast<int>(threadIdx.x);
+    const bool mine = static_cast<int>(threadIdx.x) < n;
+    int64_t y = -1;
+    float xy = 0.0f, dy = 0.0f, u = 0.0f;
+    bool named = false;
+    if (mine && i < len) {
+      y = a.drafted[static_cast<int64_t>(b) * a.draft + i];
+      named = y >= 0 && y < a.vocab;
+      if (named) xy = muon::Elem<TX>::load(row_of<TX>(a.x, b, i) + y);
+      if (named && a.d.base) dy = muon::Elem<TD>::load(row_of<TD>(a.d, b, i) + y);
+      if (!greedy) u = a.uniforms[places + i];
     }
-    if (greedy) {
-      keep = ok && named && y == P.best;
-    } else if (ok && y >= 0) {
-      double qx = 1.0;
-      if (a.d.base) {
-        Q = row_part(a, b, a.draft + 1 + i, q);
-        near = has_distribution(Q);
-        if (near && named) qx = exp((static_cast<double>(muon::Elem<TD>::load(row_of<TD>(a.d, b, i) + y)) - static_cast<double>(Q.m)) * a.inv_t) / Q.s;
+    for (int g = static_cast<int>(threadIdx.x) / lanes; g < 2 * n; g += kThreads / lanes) {
+      const int place = i0 + (g < n ? g : g - n), row = g < n ? place : a.draft + 1 + place;
+      Part r = {kLowest, INT32_MAX, 0.0};
+      if (of < slices && (g < n || (a.d.base && place < len))) r = part(row, of);
+      float m = r.m;
+      for (int k = 1; k < lanes; k *= 2) m = fmaxf(m, __shfl_xor(m, k));
+      double s = r.s == 0.0 ? 0.0 : r.s * q.exp(r.m - m);
+      int best = r.m == m ? r.best : INT32_MAX;
+      for (int k = 1; k < lanes; k *= 2) {
+        s += __shfl_xor(s, k);
+        best = min(best, __shfl_xor(best, k));
       }
-      keep = named && near && static_cast<double>(a.uniforms[static_cast<int64_t>(b) * (a.draft + 1) + i]) * qx < exp(lp);
+      if (of == 0) rows[g] = {m, best, s};
     }
-    if (keep) {
-      if (lane == 0) kept[i] = static_cast<float>(lp);
-      continue;
+    __syncthreads();
+    bool keep = false;
+    VerifyEnd e = {i, -1, 0, 0.0f, 0.0f, 0, 0.0};
+    double lp = 0.0;
+    if (mine) {
+      const Part P = rows[threadIdx.x];
+      const bool ok = has_distribution(P);
+      float mq = 0.0f;
+      bool near = true;
+      if (ok && named) lp = (static_cast<double>(xy) - static_cast<double>(P.m)) * (greedy ? 1.0 : a.inv_t) - log(P.s);
+      if (greedy) {
+        keep = ok && named && y == P.best;
+      } else if (ok && y >= 0) {
+        double qx = 1.0;
+        if (a.d.base) {
+          const Part Q = rows[n + threadIdx.x];
+          near = has_distribution(Q);
+          mq = Q.m;
+          if (near && named) qx = exp((static_cast<double>(dy) - static_cast<double>(Q.m)) * a.inv_t) / Q.s;
+        }
+        keep = named && near && static_cast<double>(u) * qx < exp(lp);
+      }
+      e = {i, named ? static_cast<int>(y) : y >= 0 ? -2 : -1, !ok ? 0 : (y >= 0 && near && !greedy ? 2 : 1), P.m, mq, P.best, P.s};
     }
-    mine = {i, named ? static_cast<int>(y) : y >= 0 ? -2 : -1, !ok ? 0 : (y >= 0 && near && !greedy ? 2 : 1), P.m, Q.m, P.best, P.s};
-    break;
+    // the first place that is not kept (all of them lie in the first wave)
+    const uint64_t ends = __ballot(mine && !keep);
+    const int stop = ends ? __builtin_ctzll(ends) : n;
+    if (static_cast<int>(threadIdx.x) < min(stop, n)) {
+      a.tokens[places + i] = y;
+      if (a.logps) a.logps[places + i] = static_cast<float>(lp);
+    }
+    if (ends && static_cast<int>(threadIdx.x) == stop) end = e;
+    const bool done = __syncthreads_or(ends != 0);
+    if (done) break;
   }
-  __syncthreads();
-  if (lane == 0) first[wave] = mine.r;
-  __syncthreads();
-  int r = INT32_MAX;
-  for (int w = 0; w < kWaves; ++w) r = min(r, first[w]);
-  if (mine.r == r && lane == 0) end = mine;
-  if (out)
-    for (int i = threadIdx.x; i < r; i += kThreads) {
-      const int64_t at = static_cast<int64_t>(b) * (a.draft + 1) + i;
-      a.tokens[at] = a.drafted[static_cast<int64_t>(b) * a.draft + i];
-      if (a.logps) a.logps[at] = kept[i];
-    }
-  __syncthreads();
   return end;
-}
-
-// Scores [lo, hi) of a row through f(index, score), a thread's in ascending order.
-template <typename T, typename F>
-__device__ __forceinline__ void each_score(const T* row, int lo, int hi, F&& f) {
-  for (int i = lo + static_cast<int>(threadIdx.x) * kVec<T>; i < hi; i += kThreads * kVec<T>) {
-    float v[kVec<T>];
-    piece(row, i, hi, v);
-#pragma unroll
-    for (int j = 0; j < kVec<T>; ++j) f(i + j, v[j]);
-  }
 }
 
 __device__ __forceinline__ double block_sum(double v) {
@@ -307,208 +327,405 @@ __device__ __forceinline__ double block_sum(double v) {
   return v;
 }
 
-// Sums over a slice of the row that is drawn from, around its maximum: of
-// exp(x), and of exp of the draft's scores, or, without those, of exp(x) without
-// the drafted token.
-template <typename TX, typename TD>
-__global__ __launch_bounds__(kThreads) void verify_sums_kernel(VerifyArgs a) {
-  __shared__ double table[32];
-  fill_table(table);
-  const int b = blockIdx.y, j = blockIdx.x;
-  const End e = find_end<TX, TD>(a, b, j == 0);
-  if (j == 0 && threadIdx.x == 0) a.ends[b] = {e.r, e.y, e.mode, e.mp, e.mq, e.best, e.sp};
-  if (e.mode == 0) return;
-  const Exp2 ex = {table};
-  const int lo = j * a.cut, hi = min(lo + a.cut, a.vocab);
-  double sp = 0.0, sq = 0.0;
-  const double mp = e.mp, mq = e.mq;
-  each_score(row_of<TX>(a.x, b, e.r), lo, hi, [&](int v, float x) {
-    const double p = ex((static_cast<double>(x) - mp) * a.kd);
-    sp += p;
-    if (v != e.y) sq += p;
+// The token `next` (-1: none) at the end of a sequence, and what lies behind it;
+// score(write) calls write(x) in the one thread that holds its score.
+template <typename F>
+__device__ __forceinline__ void finish(const VerifyArgs& a, int b, const VerifyEnd& e, int next, double log_sum, F&& score) {
+  const int64_t at = static_cast<int64_t>(b) * (a.draft + 1);
+  score([&](float x) {
+    if (a.logps)
+      a.logps[at + e.r] = static_cast<float>((static_cast<double>(x) - static_cast<double>(e.mp)) * (a.inv_t == 0.0 ? 1.0 : a.inv_t) - log_sum);
   });
-  if (e.mode == 2 && a.d.base) {
-    sq = 0.0;
-    each_score(row_of<TD>(a.d, b, e.r), lo, hi, [&](int, float x) { sq += ex((static_cast<double>(x) - mq) * a.kd); });
+  if (threadIdx.x == 0) {
+    a.accepted[b] = e.r;
+    a.tokens[at + e.r] = next;
+    if (a.logps && next < 0) a.logps[at + e.r] = __uint_as_float(0x7fc00000u);
   }
-  sp = block_sum(sp);
-  sq = block_sum(sq);
-  if (threadIdx.x == 0) a.sums[static_cast<int64_t>(b) * a.cuts + j] = make_double2(sp, sq);
+  for (int i = e.r + 1 + static_cast<int>(threadIdx.x); i <= a.draft; i += kThreads) {
+    a.tokens[at + i] = -1;
+    if (a.logps) a.logps[at + i] = 0.0f;
+  }
 }
 
-// The sum of column c (0: p, 1: q) of a sequence's sums, in every lane of the wave.
-__device__ __forceinline__ double2 all_sums(const VerifyArgs& a, int b) {
-  double2 t = make_double2(0.0, 0.0);
-  for (int j = threadIdx.x & 63; j < a.cuts; j += 64) {
-    const double2 s = a.sums[static_cast<int64_t>(b) * a.cuts + j];
-    t.x += s.x;
-    t.y += s.y;
+template <typename TX, typename TD, bool GREEDY>
+__global__ __launch_bounds__(kThreads) void verify_pairs_kernel(VerifyArgs a) {
+  const int j = blockIdx.x, b = blockIdx.z, i = blockIdx.y;  // rows 0 .. draft: the target's, beyond: the draft's
+  const int len = drafted_places(a, b);
+  const bool target = i <= a.draft;
+  const int place = target ? i : i - a.draft - 1;
+  if (target ? place > len : place >= len) return;
+  const Scale q(a);
+  const int lo = j * a.slice, hi = min(lo + a.slice, a.vocab);
+  const Part r = target ? slice_part<TX, GREEDY>(row_of<TX>(a.x, b, place), lo, hi, q)
+                        : slice_part<TD, GREEDY>(row_of<TD>(a.d, b, place), lo, hi, q);
+  if (threadIdx.x == 0) {
+    uint64_t* at = a.parts + ((static_cast<int64_t>(b) * a.rows + i) * a.slices + j) * 2;
+    publish(at, static_cast<uint64_t>(__float_as_uint(r.m)) | static_cast<uint64_t>(static_cast<uint32_t>(r.best)) << 32);
+    publish_double(at + 1, r.s);
   }
-  return make_double2(wave_sum(t.x), wave_sum(t.y));
+  const int index = (target ? place : len + 1 + place) * a.slices + j, count = (len + 1 + (a.d.base ? len : 0)) * a.slices;
+  if (!last_of_sequence(a, b, index, count)) return;
+  const VerifyEnd e = find_end<TX, TD>(a, b, len, a.slices, [&](int row, int slice) -> Part {
+    const uint64_t* at = a.parts + ((static_cast<int64_t>(b) * a.rows + row) * a.slices + slice) * 2;
+    const uint64_t w = published(at);
+    return {__uint_as_float(static_cast<uint32_t>(w)), static_cast<int>(w >> 32), published_double(at + 1)};
+  });
+  if (GREEDY || e.mode == 0)
+    finish(a, b, e, e.mode ? e.best : -1, log(e.sp), [&](auto&& write) {
+      if (e.mode && threadIdx.x == 0) write(e.mp);  // (the largest score itself)
+    });
+  if (threadIdx.x == 0) a.ends[b] = e;
 }
 
-// max(p - q, 0) of one token.
-struct Weight {
-  double mp, mq, kd, ip, iq;
-  Exp2 ex;
-  __device__ __forceinline__ double operator()(float x, float d) const {
-    const double p = ex((static_cast<double>(x) - mp) * kd) * ip, q = ex((static_cast<double>(d) - mq) * kd) * iq;
-    return fmax(p - q, 0.0);
-  }
+// max(p - q, 0) of a token.
+struct Rest {
+  Exp p, q;
+  double ip, iq;
+  __device__ __forceinline__ double operator()(float x, float d) const { return fmax(p(x) * ip - q(d) * iq, 0.0); }
 };
 
-template <typename TX, typename TD>
-__global__ __launch_bounds__(kThreads) void verify_weights_kernel(VerifyArgs a) {
-  __shared__ double table[32];
-  fill_table(table);
-  __syncthreads();
-  const int b = blockIdx.y, j = blockIdx.x;
-  const VerifyEnd e = a.ends[b];
-  if (e.mode != 2) return;
-  const double2 t = all_sums(a, b);
-  const Weight w = {e.mp, e.mq, a.kd, 1.0 / t.x, 1.0 / t.y, {table}};
-  const int lo = j * a.cut, hi = min(lo + a.cut, a.vocab);
-  const TX* x = row_of<TX>(a.x, b, e.r);
-  const TD* d = row_of<TD>(a.d, b, e.r);
-  constexpr int N = kVec<TX> > kVec<TD> ? kVec<TX> : kVec<TD>;
-  double s = 0.0;
-  for (int i = lo + static_cast<int>(threadIdx.x) * N; i < hi; i += kThreads * N) {
-    float vx[N], vd[N];
+// N scores of a row from i on, -infinity from `end` on.
+template <typename T, int N>
+__device__ __forceinline__ void pieces(const T* row, int i, int end, float (&v)[N]) {
 #pragma unroll
-    for (int c = 0; c < N; c += kVec<TX>) piece(x, i + c, hi, *reinterpret_cast<float(*)[kVec<TX>]>(vx + c));
+  for (int c = 0; c < N; c += kVec<T>) {
+    float w[kVec<T>];
+    piece(row, i + c, end, w);
 #pragma unroll
-    for (int c = 0; c < N; c += kVec<TD>) piece(d, i + c, hi, *reinterpret_cast<float(*)[kVec<TD>]>(vd + c));
-#pragma unroll
-    for (int c = 0; c < N; ++c) s += w(vx[c], vd[c]);
+    for (int j = 0; j < kVec<T>; ++j) v[c + j] = w[j];
   }
-  s = block_sum(s);
-  if (threadIdx.x == 0) a.weights[static_cast<int64_t>(b) * a.cuts + j] = s;
 }
 
-// The token at the end of each sequence, and the outputs behind the kept ones.
-template <typename TX, typename TD>
-__global__ __launch_bounds__(kThreads) void verify_take_kernel(VerifyArgs a) {
-  __shared__ double table[32], before[kWaves];
-  __shared__ int chosen, last;
-  const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const bool greedy = a.inv_t == 0.0;
-  End e;
-  double sum = 0.0;
-  int64_t next = -1;
-  fill_table(table);
-  if (threadIdx.x == 0) chosen = INT32_MAX, last = -1;
-  if (greedy) {
-    e = find_end<TX, TD>(a, b, true);
-    if (e.mode) next = e.best;
-    sum = e.sp;
-  } else {
-    const VerifyEnd s = a.ends[b];
-    e = {s.r, s.y, s.mode, s.mp, s.mq, s.best, s.sp};
-    __syncthreads();
+// What the weights of a row's tokens are: exp(x) around the maximum, that
+// without the drafted token, or max(p - q, 0).
+enum Form { P, LESS, REST };
+
+// Scores lo + (h kThreads + thread) kN .. of a slice, both halves h asked for at once.
+template <typename T>
+__device__ __forceinline__ void both_halves(const T* row, int lo, int hi, float (&v)[2][kN]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int i = lo + (h * kThreads + static_cast<int>(threadIdx.x)) * kN;
+    if (i < hi) pieces(row, i, hi, v[h]);
   }
-  if (!greedy && e.mode) {
-    const double2 t = all_sums(a, b);
-    sum = t.x;
-    // the slices' weights: one of three forms; a lane holds kRun of them
-    enum { P, LESS, REST };
-    int form = e.mode == 1 ? P : a.d.base ? REST : LESS;
-    double held[kRun], upto;
-    auto take_form = [&] {
-      double s = 0.0;
+}
+__device__ __forceinline__ bool in_half(int lo, int hi, int h) { return lo + (h * kThreads + static_cast<int>(threadIdx.x)) * kN < hi; }
+
+// Sums of a slice of the row that is drawn from, in every thread: of exp(x)
+// around its maximum, and of exp of the draft's scores, or, without those, of
+// exp(x) without the drafted token.
+template <typename TX, typename TD>
+__device__ __forceinline__ double2 slice_sums(const VerifyArgs& a, int b, const VerifyEnd& e, bool rest, int lo, int hi, const double* table) {
+  float x[2][kN], d[2][kN];
+  both_halves(row_of<TX>(a.x, b, e.r), lo, hi, x);
+  if (rest) both_halves(row_of<TD>(a.d, b, e.r), lo, hi, d);
+  const Exp p(table, a.kd, e.mp), q(table, a.kd, e.mq);
+  double sp = 0.0, sq = 0.0;
 #pragma unroll
-      for (int i = 0; i < kRun; ++i) {
-        const int j = kRun * lane + i;
-        const int64_t at = static_cast<int64_t>(b) * a.cuts + j;
-        held[i] = j >= a.cuts ? 0.0 : form == REST ? a.weights[at] : form == LESS ? a.sums[at].y : a.sums[at].x;
-        s += held[i];
-      }
-      upto = s;  // inclusive over the lanes
-      for (int k = 1; k < 64; k *= 2) {
-        const double o = __shfl_up(upto, k);
-        if (lane >= k) upto += o;
-      }
-      return __shfl(upto, 63);
-    };
-    double total = take_form();
-    if (!(total > 0.0)) form = P, total = take_form();
-    const double want = static_cast<double>(a.uniforms[static_cast<int64_t>(b) * (a.draft + 1) + a.draft]) * total;
-    // the first slice whose running sum exceeds it, else the last with weight
-    double own = 0.0;
+  for (int h = 0; h < 2; ++h) {
+    if (!in_half(lo, hi, h)) continue;
+    const int i = lo + (h * kThreads + static_cast<int>(threadIdx.x)) * kN;
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) own += held[i];
-    double run = upto - own;
-    const uint64_t over = __ballot(own > 0.0 && upto > want), some = __ballot(own > 0.0);
-    const int src = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some);
-    int at = -1;
-    double its = 0.0;
-#pragma unroll
-    for (int i = 0; i < kRun; ++i) {
-      if (!(held[i] > 0.0) || (at >= 0 && run + its > want)) continue;
-      run += its;  // the sum in front of slice `at`
-      its = held[i];
-      at = kRun * lane + i;
+    for (int c = 0; c < kN; ++c) {
+      const double w = p(x[h][c]);
+      sp += w;
+      if (!rest && i + c != e.y) sq += w;
     }
-    at = __shfl(at, src);
-    run = __shfl(run, src);
-    // `at` holds the token, unless rounding puts u past its last weight; then its last
-    const TX* x = row_of<TX>(a.x, b, e.r);
-    const TD* d = form == REST ? row_of<TD>(a.d, b, e.r) : nullptr;
-    const Weight w = {e.mp, e.mq, a.kd, 1.0 / t.x, 1.0 / t.y, {table}};
-    const int lo = at * a.cut, hi = min(lo + a.cut, a.vocab);
-    // a contiguous run of tokens per thread
-    const int per = (hi - lo + kThreads - 1) / kThreads, first = min(lo + per * static_cast<int>(threadIdx.x), hi), past = min(first + per, hi);
-    auto weight = [&](int v) {
-      const float xv = muon::Elem<TX>::load(x + v);
-      if (form == REST) return w(xv, muon::Elem<TD>::load(d + v));
-      if (form == LESS && v == e.y) return 0.0;
-      return w.ex((static_cast<double>(xv) - w.mp) * a.kd);
-    };
-    double mine = 0.0;
+    if (rest) {
+#pragma unroll
+      for (int c = 0; c < kN; ++c) sq += q(d[h][c]);
+    }
+  }
+  return make_double2(block_sum(sp), block_sum(sq));
+}
+
+// Sum of max(p - q, 0) over a slice, in every thread.
+template <typename TX, typename TD>
+__device__ __forceinline__ double slice_rest(const VerifyArgs& a, int b, const VerifyEnd& e, const Rest& w, int lo, int hi) {
+  float x[2][kN], d[2][kN];
+  both_halves(row_of<TX>(a.x, b, e.r), lo, hi, x);
+  both_halves(row_of<TD>(a.d, b, e.r), lo, hi, d);
+  double s = 0.0;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (!in_half(lo, hi, h)) continue;
+#pragma unroll
+    for (int c = 0; c < kN; ++c) s += w(x[h][c], d[h][c]);
+  }
+  return block_sum(s);
+}
+
+// The lowest token of slice [lo, hi) up to which the weights, on top of `run`,
+// exceed `want`, or its last one with any weight; and the sequence's outputs.
+template <typename TX, typename TD>
+__device__ __forceinline__ void take_token(const VerifyArgs& a, int b, const VerifyEnd& e, Form form, const Rest& w, double sum_p,
+                                           int lo, int hi, double run, double want) {
+  struct Found {  // by a wave: the token, its score
+    int v;
+    float x;
+  };
+  __shared__ double before[kWaves];
+  __shared__ Found over[kWaves], last[kWaves];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  if (lane == 0) over[wave] = last[wave] = {-1, 0.0f};
+  const TX* x = row_of<TX>(a.x, b, e.r);
+  const double log_sum = log(sum_p);
+  Found next = {-1, 0.0f};
+#pragma unroll 1
+  for (int i0 = lo; i0 < hi && next.v < 0; i0 += kThreads * kN) {
+    const int i = i0 + static_cast<int>(threadIdx.x) * kN;
+    double mine[kN], sum = 0.0;
+    float v[kN];
     int my_last = -1;
-    for (int v = first; v < past; ++v) {
-      const double s = weight(v);
-      if (s > 0.0) my_last = v;
-      mine += s;
+    if (i < hi) {
+      float d[kN];
+      pieces(x, i, hi, v);
+      if (form == REST) pieces(row_of<TD>(a.d, b, e.r), i, hi, d);
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        mine[c] = form == REST ? w(v[c], d[c]) : w.p(v[c]);
+        if ((form == LESS && i + c == e.y) || i + c >= hi) mine[c] = 0.0;
+        sum += mine[c];
+        if (mine[c] > 0.0) my_last = c;
+      }
     }
-    double scan = mine;  // inclusive over the wave
+    double scan = sum;  // inclusive over the wave
     for (int k = 1; k < 64; k *= 2) {
       const double o = __shfl_up(scan, k);
       if (lane >= k) scan += o;
     }
     if (lane == 63) before[wave] = scan;
     __syncthreads();
-    double base = run;
-    for (int k = 0; k < wave; ++k) base += before[k];
-    double here = base + (scan - mine);
-    if (my_last >= 0) atomicMax(&last, my_last);
-    if (mine > 0.0 && here + mine > want) {
-      for (int v = first; v < past; ++v) {
-        const double s = weight(v);
-        here += s;
-        if (s > 0.0 && here > want) {
-          atomicMin(&chosen, v);
-          break;
-        }
+    double here = run + (scan - sum);
+    for (int k = 0; k < kWaves; ++k) {
+      if (k < wave) here += before[k];
+      run += before[k];
+    }
+    int pick = -1;
+    if (my_last >= 0) {
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        here += mine[c];
+        if (pick < 0 && mine[c] > 0.0 && here > want) pick = c;
       }
     }
+    const uint64_t picks = __ballot(pick >= 0), lasts = __ballot(my_last >= 0);
+    auto found = [&](int at) {
+      Found f = {i + at, 0.0f};
+#pragma unroll
+      for (int c = 0; c < kN; ++c)
+        if (c == at) f.x = v[c];
+      return f;
+    };
+    if (picks && lane == __builtin_ctzll(picks)) over[wave] = found(pick);
+    if (lasts && lane == 63 - __builtin_clzll(lasts)) last[wave] = found(my_last);
     __syncthreads();
-    next = chosen != INT32_MAX ? chosen : last;
+    for (int k = kWaves - 1; k >= 0; --k)
+      if (over[k].v >= 0) next = over[k];
   }
-  if (threadIdx.x == 0) {
-    double lp = __longlong_as_double(0x7ff8000000000000ll);
-    if (next >= 0) lp = (static_cast<double>(muon::Elem<TX>::load(row_of<TX>(a.x, b, e.r) + next)) - static_cast<double>(e.mp)) * (greedy ? 1.0 : a.inv_t) - log(sum);
-    a.accepted[b] = e.r;
-    a.tokens[static_cast<int64_t>(b) * (a.draft + 1) + e.r] = next;
-    if (a.logps) a.logps[static_cast<int64_t>(b) * (a.draft + 1) + e.r] = static_cast<float>(lp);
-  }
-  for (int i = e.r + 1 + static_cast<int>(threadIdx.x); i <= a.draft; i += kThreads) {
-    a.tokens[static_cast<int64_t>(b) * (a.draft + 1) + i] = -1;
-    if (a.logps) a.logps[static_cast<int64_t>(b) * (a.draft + 1) + i] = 0.0f;
-  }
+  if (next.v < 0)
+    for (int k = 0; k < kWaves; ++k)
+      if (last[k].v > next.v) next = last[k];
+  finish(a, b, e, next.v, log_sum, [&](auto&& write) {
+    if (threadIdx.x == 0) write(next.x);
+  });
 }
 
-// Sequences of one launch: the grid's third dimension, and the second of others.
-constexpr int kMostBatch = 65535;
+// The token that u picks, by a whole workgroup, once a sequence's sums (and,
+// with draft scores, its weights) are there.
+template <typename TX, typename TD>
+__device__ __forceinline__ void pick_slice(const VerifyArgs& a, int b, const VerifyEnd& e, const double* table) {
+  const int lane = threadIdx.x & 63;
+  Form form = e.mode == 1 ? P : a.d.base ? REST : LESS;
+  const float u = a.uniforms[static_cast<int64_t>(b) * (a.draft + 1) + a.draft];
+  // a lane holds kRun slices' weights
+  double of_p[kRun], of_q[kRun], held[kRun], upto, sum_p = 0.0, sum_q = 0.0;
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    const int j = kRun * lane + i;
+    const int64_t at = static_cast<int64_t>(b) * a.cuts + j;
+    of_p[i] = of_q[i] = held[i] = 0.0;
+    if (j < a.cuts) {
+      of_p[i] = published_double(a.sums + 2 * at);
+      of_q[i] = published_double(a.sums + 2 * at + 1);
+      if (form == REST) held[i] = published_double(a.weights + at);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    sum_p += of_p[i];
+    sum_q += of_q[i];
+    if (form != REST) held[i] = form == LESS ? of_q[i] : of_p[i];
+  }
+  sum_p = wave_sum(sum_p);
+  sum_q = wave_sum(sum_q);
+  double total = 0.0, own = 0.0;
+#pragma unroll 1
+  for (int tries = 0; tries < 2; ++tries) {
+    own = 0.0;
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) own += held[i];
+    upto = own;  // inclusive over the lanes
+    for (int k = 1; k < 64; k *= 2) {
+      const double o = __shfl_up(upto, k);
+      if (lane >= k) upto += o;
+    }
+    total = __shfl(upto, 63);
+    if (total > 0.0) break;
+    form = P;  // nothing is left over
+#pragma unroll
+    for (int i = 0; i < kRun; ++i) held[i] = of_p[i];
+  }
+  const double want = static_cast<double>(u) * total;
+  // the first slice whose running sum exceeds it, else the last with weight
+  double run = upto - own;
+  const uint64_t over = __ballot(own > 0.0 && upto > want), some = __ballot(own > 0.0);
+  const int src = over ? __builtin_ctzll(over) : 63 - __builtin_clzll(some);
+  int at = -1;
+  double its = 0.0;
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) {
+    if (!(held[i] > 0.0) || (at >= 0 && run + its > want)) continue;
+    run += its;  // the sum in front of slice `at`
+    its = held[i];
+    at = kRun * lane + i;
+  }
+  at = __shfl(at, src);
+  run = __shfl(run, src);
+  const Rest w = {{table, a.kd, e.mp}, {table, a.kd, e.mq}, 1.0 / sum_p, 1.0 / sum_q};
+  const int lo = at * a.cut;
+  take_token<TX, TD>(a, b, e, form, w, sum_p, lo, min(lo + a.cut, a.vocab), run, want);
+}
+
+template <typename TX, typename TD>
+__global__ __launch_bounds__(kThreads) void verify_sums_kernel(VerifyArgs a) {
+  __shared__ double table[32];
+  const int b = blockIdx.y, j = blockIdx.x;
+  const VerifyEnd e = a.ends[b];
+  fill_table(table);
+  __syncthreads();
+  if (e.mode == 0) return;
+  const bool rest = e.mode == 2 && a.d.base;
+  const int lo = j * a.cut;
+  const double2 s = slice_sums<TX, TD>(a, b, e, rest, lo, min(lo + a.cut, a.vocab), table);
+  if (threadIdx.x == 0) {
+    uint64_t* at = a.sums + (static_cast<int64_t>(b) * a.cuts + j) * 2;
+    publish_double(at, s.x);
+    publish_double(at + 1, s.y);
+  }
+  if (rest) return;
+  if (last_of_sequence(a, b, j, a.cuts)) pick_slice<TX, TD>(a, b, e, table);
+}
+
+template <typename TX, typename TD>
+__global__ __launch_bounds__(kThreads) void verify_weights_kernel(VerifyArgs a) {
+  __shared__ double table[32];
+  const int b = blockIdx.y, j = blockIdx.x;
+  const VerifyEnd e = a.ends[b];
+  double2 t = make_double2(0.0, 0.0);
+  for (int i = threadIdx.x & 63; i < a.cuts; i += 64) {
+    const double* at = reinterpret_cast<const double*>(a.sums) + (static_cast<int64_t>(b) * a.cuts + i) * 2;
+    t.x += at[0];
+    t.y += at[1];
+  }
+  fill_table(table);
+  __syncthreads();
+  if (e.mode != 2) return;
+  const Rest w = {{table, a.kd, e.mp}, {table, a.kd, e.mq}, 1.0 / wave_sum(t.x), 1.0 / wave_sum(t.y)};
+  const int lo = j * a.cut;
+  const double s = slice_rest<TX, TD>(a, b, e, w, lo, min(lo + a.cut, a.vocab));
+  if (threadIdx.x == 0) publish_double(a.weights + static_cast<int64_t>(b) * a.cuts + j, s);
+  if (last_of_sequence(a, b, j, a.cuts)) pick_slice<TX, TD>(a, b, e, table);
+}
+
+// Vocabularies of one slice and few rows: all of it in one workgroup a sequence.
+constexpr int kSmallRows = 32, kSmall = 1 << 15;
+
+template <typename TX, typename TD>
+__global__ __launch_bounds__(kThreads) void verify_small_kernel(VerifyArgs a) {
+  __shared__ double table[32];
+  __shared__ Part parts[kSmallRows];
+  const int b = blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const bool greedy = a.inv_t == 0.0;
+  const Scale q(a);
+  fill_table(table);
+  const int len = drafted_places(a, b);
+  // a wave per row, three rows of a wave at once
+  constexpr int R = 3;
+  for (int i0 = wave; i0 < a.rows; i0 += R * kWaves) {
+    float m[R];
+    double s[R];
+    int best[R];
+    auto place_of = [&](int i) { return i <= a.draft ? i : i - a.draft - 1; };
+    auto needed = [&](int i) { return i < a.rows && (i <= a.draft ? i <= len : place_of(i) < len); };
+#pragma unroll
+    for (int r = 0; r < R; ++r) m[r] = kLowest, s[r] = 0.0, best[r] = INT32_MAX;
+#pragma unroll 1
+    for (int v0 = lane * kN; v0 - lane * kN < a.vocab; v0 += 128 * kN) {
+      float v[R][2 * kN];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const int i = i0 + r * kWaves;
+        if (!needed(i)) continue;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float half[kN];
+          if (i <= a.draft) pieces(row_of<TX>(a.x, b, i), v0 + h * 64 * kN, a.vocab, half);
+          else pieces(row_of<TD>(a.d, b, place_of(i)), v0 + h * 64 * kN, a.vocab, half);
+#pragma unroll
+          for (int c = 0; c < kN; ++c) v[r][h * kN + c] = half[c];
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        if (!needed(i0 + r * kWaves)) continue;
+        float top = m[r];
+#pragma unroll
+        for (int c = 0; c < 2 * kN; ++c) top = fmaxf(top, v[r][c]);
+        top = wave_max(top);
+        if (top > m[r]) {
+          s[r] *= q.exp(m[r] - top);
+          m[r] = top;
+          best[r] = INT32_MAX;
+        }
+        float e[2 * kN];
+#pragma unroll
+        for (int c = 2 * kN - 1; c >= 0; --c) {
+          e[c] = __builtin_amdgcn_exp2f((v[r][c] - top) * q.each[c % 8]);
+          if (v[r][c] == top) best[r] = min(best[r], v0 + (c / kN) * 64 * kN + c % kN);
+        }
+#pragma unroll
+        for (int h = kN; h > 0; h /= 2)
+#pragma unroll
+          for (int c = 0; c < h; ++c) e[c] += e[c + h];
+        s[r] += static_cast<double>(e[0]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int i = i0 + r * kWaves;
+      if (!needed(i)) continue;
+      const double sum = wave_sum(s[r]);
+      const int at = wave_min(best[r]);
+      if (lane == 0) parts[i] = {m[r], at, m[r] == INFINITY ? static_cast<double>(NAN) : sum};
+    }
+  }
+  __syncthreads();
+  const VerifyEnd e = find_end<TX, TD>(a, b, len, 1, [&](int row, int) { return parts[row]; });
+  if (greedy || e.mode == 0) {
+    finish(a, b, e, e.mode ? e.best : -1, log(e.sp), [&](auto&& write) {
+      if (e.mode && threadIdx.x == 0) write(e.mp);
+    });
+    return;
+  }
+  const float u = a.uniforms[static_cast<int64_t>(b) * (a.draft + 1) + a.draft];
+  Form form = e.mode == 1 ? P : a.d.base ? REST : LESS;
+  const double2 s = slice_sums<TX, TD>(a, b, e, form == REST, 0, a.vocab, table);
+  const Rest w = {{table, a.kd, e.mp}, {table, a.kd, e.mq}, 1.0 / s.x, 1.0 / s.y};
+  double total = form == REST ? slice_rest<TX, TD>(a, b, e, w, 0, a.vocab) : form == LESS ? s.y : s.x;
+  if (!(total > 0.0)) form = P, total = s.x;
+  take_token<TX, TD>(a, b, e, form, w, s.x, 0, a.vocab, 0.0, static_cast<double>(u) * total);
+}
 
 template <typename TX, typename TD>
 hipError_t go(hipStream_t s, VerifyArgs a, int b0, int n) {
@@ -521,6 +738,12 @@ hipError_t go(hipStream_t s, VerifyArgs a, int b0, int n) {
   a.accepted += b0;
   if (a.logps) a.logps += places;
   const unsigned nb = static_cast<unsigned>(n);
+  // One workgroup for a sequence, against three launches over slices: measured
+  // where the rows hold up to kSmall scores in all.
+  if (a.vocab <= kMostCut && a.rows <= kSmallRows && a.rows * a.vocab <= kSmall) {
+    verify_small_kernel<TX, TD><<<nb, kThreads, 0, s>>>(a);
+    return hipGetLastError();
+  }
   const dim3 grid(static_cast<unsigned>(a.slices), static_cast<unsigned>(a.rows), nb), cuts(static_cast<unsigned>(a.cuts), nb);
   if (a.inv_t == 0.0) {
     verify_pairs_kernel<TX, TD, true><<<grid, kThreads, 0, s>>>(a);
@@ -529,7 +752,6 @@ hipError_t go(hipStream_t s, VerifyArgs a, int b0, int n) {
     verify_sums_kernel<TX, TD><<<cuts, kThreads, 0, s>>>(a);
     if (a.d.base) verify_weights_kernel<TX, TD><<<cuts, kThreads, 0, s>>>(a);
   }
-  verify_take_kernel<TX, TD><<<nb, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -541,41 +763,48 @@ VerifyPlan verify_plan(int64_t batch, int64_t draft, int64_t vocab, int bytes) {
   p.slices = static_cast<int>((vocab + most - 1) / most);
   // whole pieces of 16 bytes
   p.slice = static_cast<int>(((vocab + p.slices - 1) / p.slices + 7) / 8 * 8);
-  p.launch = static_cast<int>(batch < kMostBatch ? batch : kMostBatch);
-  // the second reading: as many workgroups as fill the card, of 2048 scores at least
-  int64_t cuts = (vocab + 2047) / 2048;
+  p.rows = static_cast<int>(2 * draft + 1);
+  // sequences of one launch: their counters have to fit the exchange words
+  p.groups = 2 + (p.rows * p.slices - 1) / kTogether;
+  const int64_t most_batch = kExchangeWords / kCounterStride / p.groups;
+  p.launch = static_cast<int>(batch < most_batch ? batch : most_batch);
+  // the second reading: slices of 2048 scores, of 4096 where there are many
   static_assert(MUON_MAX_VOCAB / 2048 <= kMostCuts, "a wave holds a row's sums");
-  const int64_t enough = (2048 + p.launch - 1) / (p.launch > 0 ? p.launch : 1);
-  if (cuts > enough) cuts = enough;
+  const int64_t fine = (vocab + 2047) / 2048, cuts = fine * p.launch > 2048 ? (vocab + kMostCut - 1) / kMostCut : fine;
   p.cut = static_cast<int>(((vocab + cuts - 1) / cuts + 7) / 8 * 8);
   p.cuts = static_cast<int>((vocab + p.cut - 1) / p.cut);
-  p.rows = static_cast<int>(2 * draft + 1);
   size_t at = 0;
   auto take = [&](size_t bytes_) {
     const size_t was = at;
     at += (bytes_ + 255) & ~static_cast<size_t>(255);
     return was;
   };
-  p.parts = take(sizeof(VerifyPart) * static_cast<size_t>(p.launch) * static_cast<size_t>(p.rows) * static_cast<size_t>(p.slices));
+  p.parts = take(2 * sizeof(uint64_t) * static_cast<size_t>(p.launch) * static_cast<size_t>(p.rows) * static_cast<size_t>(p.slices));
   p.ends = take(sizeof(VerifyEnd) * static_cast<size_t>(p.launch));
-  p.sums = take(sizeof(double2) * static_cast<size_t>(p.launch) * static_cast<size_t>(p.cuts));
-  p.weights = take(sizeof(double) * static_cast<size_t>(p.launch) * static_cast<size_t>(p.cuts));
+  p.sums = take(2 * sizeof(uint64_t) * static_cast<size_t>(p.launch) * static_cast<size_t>(p.cuts));
+  p.weights = take(sizeof(uint64_t) * static_cast<size_t>(p.launch) * static_cast<size_t>(p.cuts));
   p.total = at;
   return p;
 }
 
-hipError_t launch_verify(hipStream_t s, VerifyArgs a, int64_t batch, const VerifyPlan& p, char* ws) {
+hipError_t launch_verify(hipStream_t s, VerifyArgs a, int64_t batch, const VerifyPlan& p, char* ws, Exchange& x) {
+  if (x.dirty) {
+    const hipError_t e = clear_exchange(s, x);
+    if (e != hipSuccess) return e;
+  }
+  a.counters = x.words;
+  a.groups = p.groups;
   a.slices = p.slices;
   a.slice = p.slice;
   a.cut = p.cut;
   a.cuts = p.cuts;
   a.rows = a.d.base ? 2 * a.draft + 1 : a.draft + 1;
-  a.parts = reinterpret_cast<VerifyPart*>(ws + p.parts);
+  a.parts = reinterpret_cast<uint64_t*>(ws + p.parts);
   a.ends = reinterpret_cast<VerifyEnd*>(ws + p.ends);
-  a.sums = reinterpret_cast<double2*>(ws + p.sums);
-  a.weights = reinterpret_cast<double*>(ws + p.weights);
-  for (int64_t b0 = 0; b0 < batch; b0 += kMostBatch) {
-    const int n = static_cast<int>(batch - b0 < kMostBatch ? batch - b0 : kMostBatch), b = static_cast<int>(b0);
+  a.sums = reinterpret_cast<uint64_t*>(ws + p.sums);
+  a.weights = reinterpret_cast<uint64_t*>(ws + p.weights);
+  for (int64_t b0 = 0; b0 < batch; b0 += p.launch) {
+    const int n = static_cast<int>(batch - b0 < p.launch ? batch - b0 : p.launch), b = static_cast<int>(b0);
     hipError_t e;
     if (a.x_bf16) e = a.d_bf16 || !a.d.base ? go<bf16_t, bf16_t>(s, a, b, n) : go<bf16_t, float>(s, a, b, n);
     else e = a.d_bf16 ? go<float, bf16_t>(s, a, b, n) : go<float, float>(s, a, b, n);
