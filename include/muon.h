@@ -652,9 +652,12 @@ muon_status_t muon_quantize_rows(muon_ctx_t* ctx, void* stream, const muon_rows_
 muon_status_t muon_dequantize_rows(muon_ctx_t* ctx, void* stream, const muon_rows8_t* q,
                                    const muon_rows_t* out);
 
-/* Workspace in bytes of any of the calls below for a layer of n x k weights
- * and up to `tokens` tokens (pure host function; 0 for arguments out of
- * range). */
+/* Workspace in bytes with which the calls below are fastest for a layer of n x k
+ * weights and up to `tokens` tokens (pure host function; 0 for arguments out of
+ * range): tokens * (k + 20) bytes for muon_linear8 without x8, which it needs,
+ * and up to 128 MiB of partial sums of products that are cut along their
+ * contraction.  With less room for those they are cut less; the sums of
+ * gradients then round differently. */
 size_t muon_linear8_workspace_bytes(int64_t tokens, int64_t n, int64_t k);
 
 /* out[m][n] = (sum_k a[m][k] b[n][k]) * (a.scale[m] * b.scale[n]): the integers'

@@ -4,6 +4,7 @@
 //   inputs:  sum over channels of grad_y (rows) and the weights.
 #include "linear8.h"
 #include "ns_mfma_common.h"
+#include "tile_plan.h"
 
 namespace {
 
@@ -46,7 +47,8 @@ struct YStage {
     off = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.y.ld) * 2u + static_cast<uint32_t>(chunk) * 16u;
   }
   // fast: every chunk is inside
-  __device__ __forceinline__ void load(const Grad8Args& a, int64_t m0, int64_t c0, bool fast) {
+  // (contraction indices from `past` on count as zeros)
+  __device__ __forceinline__ void load(const Grad8Args& a, int64_t m0, int64_t c0, int64_t past, bool fast) {
     const int64_t r0 = COLS ? c0 : m0, k0 = COLS ? m0 : c0;
     const char* base = uniform_ptr(a.y.p + (r0 * a.y.ld + k0) * 2);
     const int64_t step = a.y.ld * (2 * STEP);
@@ -55,8 +57,8 @@ struct YStage {
       for (int q = 0; q < NC; ++q) v[q] = *reinterpret_cast<const u32x4_any*>(base + q * step + off);
       return;
     }
-    const int left = static_cast<int>(min((COLS ? a.m : a.c) - k0, int64_t{1} << 20)) - 8 * chunk;
-    const int rows = static_cast<int>(min((COLS ? a.c : a.m) - r0, int64_t{1} << 20)) - row;
+    const int left = static_cast<int>(min((COLS ? a.m : past) - k0, int64_t{1} << 20)) - 8 * chunk;
+    const int rows = static_cast<int>(min((COLS ? past : a.m) - r0, int64_t{1} << 20)) - row;
 #pragma unroll
     for (int q = 0; q < NC; ++q) {
       v[q] = u32x4_t{0, 0, 0, 0};
@@ -96,7 +98,7 @@ struct QStage {
     chunk = tid % CPR;
     off = static_cast<uint32_t>(row) * static_cast<uint32_t>(a.q.ld) + static_cast<uint32_t>(chunk) * 16u;
   }
-  __device__ __forceinline__ void load(const Grad8Args& a, int64_t n0, int64_t c0, bool fast) {
+  __device__ __forceinline__ void load(const Grad8Args& a, int64_t n0, int64_t c0, int64_t past, bool fast) {
     const char* base = uniform_ptr(reinterpret_cast<const char*>(a.q.p) + c0 * a.q.ld + n0);
     const float* scale = uniform_ptr(a.q.scale + c0);
     const int64_t step = a.q.ld * STEP;
@@ -109,7 +111,7 @@ struct QStage {
       return;
     }
     const int left = static_cast<int>(min(a.n - n0, int64_t{1} << 20)) - 16 * chunk;
-    const int rows = static_cast<int>(min(a.c - c0, int64_t{1} << 20)) - row;
+    const int rows = static_cast<int>(min(past - c0, int64_t{1} << 20)) - row;
 #pragma unroll
     for (int q = 0; q < NC; ++q) {
       v[q] = u32x4_t{0, 0, 0, 0};
@@ -155,7 +157,7 @@ __device__ __forceinline__ int of_off(int r, int c) {
 }
 
 template <typename O, int TM, int TN, int NWN, int PARTS, bool COLS>
-__global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, int tiles_m, int tiles_n) {
+__global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, TileWork work) {
   constexpr int NW = 2 * NWN, NT = 64 * NW;
   constexpr int WM = TM / 2, WN = TN / NWN, FM = WM / 32, FN = WN / 32;
   constexpr int YB = TM * kC * 2, STAGE = YB + PARTS * TN * kC * 2;
@@ -164,17 +166,11 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, i
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / NWN, wn = wave % NWN;
-  const int64_t total = static_cast<int64_t>(tiles_m) * tiles_n;
   const int G = static_cast<int>(gridDim.x), hw = static_cast<int>(blockIdx.x);
   const int64_t first = G % 8 == 0 ? static_cast<int64_t>(hw % 8) * (G / 8) + hw / 8 : hw;
-  const int KT = static_cast<int>((a.c + kC - 1) / kC);
-  for (int64_t l = first; l < total; l += G) {
-    // bands of four tile columns, row by row inside a band
-    constexpr int GN = 4;
-    const int64_t band = l / (static_cast<int64_t>(tiles_m) * GN);
-    const int w = static_cast<int>(min(static_cast<int64_t>(GN), tiles_n - band * GN));
-    const int64_t r = l - band * tiles_m * GN;
-    const int64_t m0 = r / w * TM, n0 = (band * GN + r % w) * TN;
+  for (int64_t l = first; l < work.units; l += G) {
+    const TileUnit unit = tile_unit(work, l);
+    const int64_t m0 = unit.ti * TM, n0 = unit.tj * TN, past = min(a.c, static_cast<int64_t>(unit.past) * kC);
     const bool inside_m = m0 + TM <= a.m, inside_n = n0 + TN <= a.n;
 
     f32x16_t acc[FM][FN];
@@ -190,9 +186,9 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, i
     const int ya = ys.address(), qa = qs.address();
     auto load = [&](int kt) __attribute__((always_inline)) {
       const int64_t c0 = static_cast<int64_t>(kt) * kC;
-      const bool full = c0 + kC <= a.c;
-      ys.load(a, m0, c0, full && inside_m);
-      qs.load(a, n0, c0, full && inside_n);
+      const bool full = c0 + kC <= past;
+      ys.load(a, m0, c0, past, full && inside_m);
+      qs.load(a, n0, c0, past, full && inside_n);
     };
     constexpr int NY = YStage<TM, NT, COLS>::NC, NQ = QStage<TN, NT, PARTS>::NC;
     bf16x8_t fa[2][PARTS][FN], fb[2][FM];
@@ -261,13 +257,13 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, i
         }
       });
     };
-    load(0);
+    load(unit.first);
     static_for<3>([&](auto P) { store_part(st, decltype(P)::value); });
-    load(1);
+    load(unit.first + 1);
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
     frags(st, 0, ic<0>{});
     // whole rounds of two stages: past the end they hold zeros
-    for (int kt = 0; kt < KT; kt += 2) static_for<2>([&](auto S) { stage(S, kt + decltype(S)::value); });
+    for (int kt = unit.first; kt < unit.past; kt += 2) static_for<2>([&](auto S) { stage(S, kt + decltype(S)::value); });
 
     // ---- epilogue: fp32 sums through LDS, row-contiguous stores
     int el = lane;
@@ -277,6 +273,7 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, i
     constexpr int ROUNDS = TM * TN * 4 > 2 * STAGE ? 2 : 1, RR = TM / ROUNDS;
     static_assert(RR * TN * 4 <= 2 * STAGE, "output rows fit the stage buffers");
     O* out = reinterpret_cast<O*>(a.out.p);
+    float* part = reinterpret_cast<float*>(work.parts) + unit.slot * (TM * TN);
     const bool wide = ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(a.out.ld * E)) & 15u) == 0;
     static_for<ROUNDS>([&](auto R) {
       constexpr int rd = decltype(R)::value;
@@ -295,8 +292,17 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, i
         });
       }
       __syncthreads();
-      constexpr int C = 16 / E, CH = TN / C;
       const int et = wave * 64 + el;
+      if (unit.slot >= 0) {
+#pragma unroll 4
+        for (int it = 0; it < RR * TN / 4 / NT; ++it) {
+          const int e = et + it * NT, row = e / (TN / 4), c = 4 * (e % (TN / 4));
+          *reinterpret_cast<float4*>(part + (rd * RR + row) * TN + c) = *reinterpret_cast<const float4*>(st + of_off<TN>(row, c));
+        }
+        __syncthreads();
+        return;
+      }
+      constexpr int C = 16 / E, CH = TN / C;
 #pragma unroll 2
       for (int it = 0; it < RR * CH / NT; ++it) {
         const int e = et + it * NT, row = e / CH, c = C * (e % CH);
@@ -333,13 +339,38 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, i
   }
 }
 
+// The parts of the tiles that were cut, added in order: four outputs a thread.
+template <typename O, int TM, int TN>
+__global__ __launch_bounds__(256) void grad8_join_kernel(Grad8Args a, TileWork work) {
+  constexpr int PER = TM * TN / 1024;  // workgroups of a tile
+  const int64_t t = blockIdx.x / PER;
+  const int e = static_cast<int>(blockIdx.x % PER) * 256 + static_cast<int>(threadIdx.x), row = e / (TN / 4), c = 4 * (e % (TN / 4));
+  const TileUnit unit = tile_unit(work, work.whole + t);
+  const float* part = reinterpret_cast<const float*>(work.parts) + t * work.splits * (TM * TN) + row * TN + c;
+  const int64_t m = unit.ti * TM + row, n = unit.tj * TN + c;
+  if (m >= a.m || n >= a.n) return;
+  float4 v = *reinterpret_cast<const float4*>(part);
+  for (int p = 1; p < work.splits; ++p) {
+    const float4 w = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(p) * (TM * TN));
+    v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+  }
+  O* to = reinterpret_cast<O*>(a.out.p) + m * a.out.ld + n;
+  const float f[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (n + q < a.n) muon::Elem<O>::store(to + q, a.accumulate ? muon::Elem<O>::load(to + q) + f[q] : f[q]);
+}
+
 template <typename O, int TM, int TN, int NWN, int PARTS>
-hipError_t go_tiles(hipStream_t s, const Grad8Args& a) {
-  const int tm = static_cast<int>((a.m + TM - 1) / TM), tn = static_cast<int>((a.n + TN - 1) / TN);
-  const int64_t tiles = static_cast<int64_t>(tm) * tn, cap = a.cus * (NWN == 4 ? 1 : 2);
-  const unsigned grid = static_cast<unsigned>(tiles < cap ? tiles : cap);
-  if (a.of_columns) grad8_tile_kernel<O, TM, TN, NWN, PARTS, true><<<grid, 128 * NWN, 0, s>>>(a, tm, tn);
-  else grad8_tile_kernel<O, TM, TN, NWN, PARTS, false><<<grid, 128 * NWN, 0, s>>>(a, tm, tn);
+hipError_t go_tiles(hipStream_t s, const Grad8Args& a, const TilePlan& p) {
+  const TileWork w = tile_work(p, a.ws);
+  const unsigned grid = static_cast<unsigned>(p.grid);
+  if (a.of_columns) grad8_tile_kernel<O, TM, TN, NWN, PARTS, true><<<grid, 128 * NWN, 0, s>>>(a, w);
+  else grad8_tile_kernel<O, TM, TN, NWN, PARTS, false><<<grid, 128 * NWN, 0, s>>>(a, w);
+  if (p.splits > 1) {
+    const int64_t cut = static_cast<int64_t>(p.tm) * p.tn - p.whole;
+    grad8_join_kernel<O, TM, TN><<<static_cast<unsigned>(cut * (TM * TN / 1024)), 256, 0, s>>>(a, w);
+  }
   return hipGetLastError();
 }
 
@@ -347,8 +378,12 @@ hipError_t go_tiles(hipStream_t s, const Grad8Args& a) {
 
 hipError_t launch_grad8(hipStream_t s, const Grad8Args& a) {
   if (a.m == 0 || a.n == 0) return hipSuccess;
-  const int64_t t256 = ((a.m + 255) / 256) * ((a.n + 255) / 256);
-  const bool large = t256 * 2 >= a.cus;
-  if (a.out.bf16) return large ? go_tiles<bf16_t, 256, 256, 4, 1>(s, a) : go_tiles<bf16_t, 128, 128, 2, 1>(s, a);
-  return large ? go_tiles<float, 256, 128, 4, 2>(s, a) : go_tiles<float, 128, 64, 2, 2>(s, a);
+  const int stages = static_cast<int>((a.c + kC - 1) / kC), parts = a.out.bf16 ? 1 : 2;
+  // (two small tiles on a CU take 0.6 of a large one's time for half its products)
+  double large, small;
+  const TilePlan l = plan_tiles(a.m, a.n, 256, 256 / parts, stages, a.cus, a.ws_bytes, &large);
+  const TilePlan q = plan_tiles(a.m, a.n, 128, 128 / parts, stages, 2 * a.cus, a.ws_bytes, &small);
+  const bool big = large <= 0.6 * small;
+  if (a.out.bf16) return big ? go_tiles<bf16_t, 256, 256, 4, 1>(s, a, l) : go_tiles<bf16_t, 128, 128, 2, 1>(s, a, q);
+  return big ? go_tiles<float, 256, 128, 4, 2>(s, a, l) : go_tiles<float, 128, 64, 2, 2>(s, a, q);
 }

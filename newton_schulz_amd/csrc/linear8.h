@@ -30,6 +30,8 @@ struct Matmul8Args {
   int64_t m, n;
   int k;
   int cus;
+  char* ws;  // for partial sums
+  size_t ws_bytes;
 };
 hipError_t launch_matmul8(hipStream_t s, const Matmul8Args& a);
 
@@ -42,6 +44,8 @@ struct Grad8Args {
   int64_t m, n, c;
   int accumulate;
   int cus;
+  char* ws;  // for partial sums
+  size_t ws_bytes;
 };
 hipError_t launch_grad8(hipStream_t s, const Grad8Args& a);
 

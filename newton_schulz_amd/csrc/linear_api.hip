@@ -61,20 +61,33 @@ void spans8(Span* s, const muon_rows8_t& x, size_t bytes, bool written) {
   s[1] = {bytes ? x.scale : nullptr, bytes ? static_cast<size_t>(x.rows) * 4 : 0, 4, written, false, "scale"};
 }
 
-// What linear8 keeps in the workspace where nobody keeps the activations.
+// The workspace of a call: first what linear8 keeps there where nobody keeps
+// the activations, then room for the partial sums of products cut along their
+// contraction.  A call takes as much of the latter as the context has, up to
+// kMostParts; more than 32 parts of the output are never there.
 struct LinearLayout {
-  size_t q, scale, total;
+  size_t q, scale, parts;
 };
 LinearLayout linear_layout(int64_t tokens, int64_t k) {
   LinearLayout l;
   l.q = 0;
   l.scale = up256(static_cast<size_t>(tokens * up16(k)));
-  l.total = l.scale + up256(static_cast<size_t>(tokens) * 4);
+  l.parts = l.scale + up256(static_cast<size_t>(tokens) * 4);
   return l;
 }
+constexpr size_t kMostParts = size_t{128} << 20;
+size_t parts_bytes(int64_t rows, int64_t cols) {
+  // whole tiles of 128 x 128
+  const size_t tiles = static_cast<size_t>((rows + 127) / 128) * static_cast<size_t>((cols + 127) / 128);
+  return tiles > kMostParts / (32 * 65536) ? kMostParts : tiles * 32 * 65536;
+}
+size_t parts_room(const muon_ctx* c, size_t from) {
+  return c->ws_bytes > from ? (c->ws_bytes - from < kMostParts ? c->ws_bytes - from : kMostParts) : 0;
+}
 
-muon_status_t matmul8(muon_ctx* c, hipStream_t s, const Bytes& a, int64_t m, const muon_rows8_t& b, const muon_rows_t& out) {
-  const Matmul8Args t = {a, bytes8(b), values(out), m, b.rows, static_cast<int>(b.cols), c->cus};
+muon_status_t matmul8(muon_ctx* c, hipStream_t s, const Bytes& a, int64_t m, const muon_rows8_t& b, const muon_rows_t& out,
+                      size_t from) {
+  const Matmul8Args t = {a, bytes8(b), values(out), m, b.rows, static_cast<int>(b.cols), c->cus, c->ws + from, parts_room(c, from)};
   return timed(c, s, MUON_K_LINEAR8, "8-bit product launch", [&] { return launch_matmul8(s, t); });
 }
 
@@ -98,7 +111,7 @@ muon_status_t grad8(muon_ctx* c, void* stream, const muon_rows_t* y, const muon_
   if (st == MUON_OK) st = check_ctx(c, 0);
   if (st != MUON_OK || m == 0) return st;
   DeviceGuard g(c->device);
-  const Grad8Args t = {values(*y), of_columns, bytes8(*q), values(*out), m, q->cols, contraction, accumulate != 0, c->cus};
+  const Grad8Args t = {values(*y), of_columns, bytes8(*q), values(*out), m, q->cols, contraction, accumulate != 0, c->cus, c->ws, parts_room(c, 0)};
   hipStream_t s = static_cast<hipStream_t>(stream);
   return timed(c, s, MUON_K_LINEAR8, "8-bit gradient launch", [&] { return launch_grad8(s, t); });
 }
@@ -146,7 +159,12 @@ muon_status_t muon_dequantize_rows(muon_ctx_t* c, void* stream, const muon_rows8
 
 size_t muon_linear8_workspace_bytes(int64_t tokens, int64_t n, int64_t k) {
   if (tokens < 0 || tokens > MUON_MAX_ROWS8 || n < 0 || n > MUON_MAX_ROWS8 || k < 1 || k > MUON_MAX_COLS8) return 0;
-  return linear_layout(tokens, k).total;
+  size_t parts = 0;
+  if (tokens && n) {
+    const size_t of[] = {parts_bytes(tokens, n), parts_bytes(tokens, k), parts_bytes(n, k)};
+    for (size_t p : of) parts = p > parts ? p : parts;
+  }
+  return linear_layout(tokens, k).parts + parts;
 }
 
 muon_status_t muon_matmul8(muon_ctx_t* c, void* stream, const muon_rows8_t* a, const muon_rows8_t* b,
@@ -168,7 +186,7 @@ muon_status_t muon_matmul8(muon_ctx_t* c, void* stream, const muon_rows8_t* a, c
   if (st == MUON_OK) st = check_ctx(c, 0);
   if (st != MUON_OK || a->rows == 0) return st;
   DeviceGuard g(c->device);
-  return matmul8(c, static_cast<hipStream_t>(stream), bytes8(*a), a->rows, *b, *out);
+  return matmul8(c, static_cast<hipStream_t>(stream), bytes8(*a), a->rows, *b, *out, 0);
 }
 
 muon_status_t muon_linear8(muon_ctx_t* c, void* stream, const muon_rows_t* x, const muon_rows8_t* w,
@@ -191,7 +209,7 @@ muon_status_t muon_linear8(muon_ctx_t* c, void* stream, const muon_rows_t* x, co
   if (x8) spans8(spans + 4, *x8, qb, true);
   st = check_spans(c, spans, x8 ? 6 : 4, false);
   const LinearLayout l = linear_layout(x->rows, x->cols);
-  if (st == MUON_OK) st = check_ctx(c, l.total);
+  if (st == MUON_OK) st = check_ctx(c, x8 ? 0 : l.parts);
   if (st != MUON_OK || x->rows == 0) return st;
   DeviceGuard g(c->device);
   hipStream_t s = static_cast<hipStream_t>(stream);
@@ -199,7 +217,7 @@ muon_status_t muon_linear8(muon_ctx_t* c, void* stream, const muon_rows_t* x, co
                      : Bytes{reinterpret_cast<int8_t*>(c->ws + l.q), reinterpret_cast<float*>(c->ws + l.scale), up16(x->cols)};
   st = timed(c, s, MUON_K_LINEAR8, "quantisation launch",
              [&] { return launch_quantize_rows(s, values(*x), q, x->rows, static_cast<int>(x->cols)); });
-  return st == MUON_OK ? matmul8(c, s, q, x->rows, *w, *out) : st;
+  return st == MUON_OK ? matmul8(c, s, q, x->rows, *w, *out, x8 ? 0 : l.parts) : st;
 }
 
 muon_status_t muon_input_grad8(muon_ctx_t* c, void* stream, const muon_rows_t* grad_y, const muon_rows8_t* w,

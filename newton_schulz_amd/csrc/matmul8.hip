@@ -5,6 +5,7 @@
 // the two scales.
 #include "linear8.h"
 #include "ns_mfma_common.h"
+#include "tile_plan.h"
 
 namespace {
 
@@ -65,8 +66,9 @@ struct Stage8 {
   u32x4_t rsrc;
 
   // Rows [row0, row0 + T) of `rows`.  A chunk that is not whole in the last
-  // row would reach past the memory: finish() brings it.
-  __device__ __forceinline__ void init(const Bytes& x, int64_t rows, int k, int64_t row0, int wave, int lane) {
+  // row would reach past the memory: finish() brings it.  From `past` on they
+  // hold zeros.
+  __device__ __forceinline__ void init(const Bytes& x, int64_t rows, int k, int past, int64_t row0, int wave, int lane) {
     const int here = static_cast<int>(min(rows - row0, static_cast<int64_t>(T)));
     const int ld = static_cast<int>(x.ld);
     rsrc = rsrc_words(uniform_ptr(x.p + row0 * x.ld), static_cast<uint32_t>(here - 1) * ld + (k & ~15) + (k & 15 ? 16 : 0));
@@ -75,7 +77,7 @@ struct Stage8 {
       const int row = 8 * (wave + NW * q) + lane / 8;
       const int chunk = (lane % 8) ^ rt_swz<64>(row);
       kc[q] = 16 * chunk;
-      lim[q] = (row0 + row == rows - 1 || ld == 0) ? k & ~15 : k;
+      lim[q] = min((row0 + row == rows - 1 || ld == 0) ? k & ~15 : k, past);
       base[q] = row < here ? static_cast<uint32_t>(row) * ld + 16 * chunk : kOOB;
     }
   }
@@ -122,7 +124,7 @@ __device__ __forceinline__ int out_off(int r, int c) {
 }
 
 template <typename O, int T>
-__global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(Matmul8Args a, int tiles_m, int tiles_n) {
+__global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(Matmul8Args a, TileWork work) {
   constexpr int NWN = T == 256 ? 4 : 2, NW = 2 * NWN, NT = 64 * NW;
   constexpr int WM = T / 2, WN = T / NWN, FM = WM / 32, FN = WN / 32;
   constexpr int HALF = T * kBytes, STAGE = 2 * HALF;
@@ -134,16 +136,11 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / NWN, wn = wave % NWN;
 
-  const int64_t total = static_cast<int64_t>(tiles_m) * tiles_n;
   const int G = static_cast<int>(gridDim.x), hw = static_cast<int>(blockIdx.x);
   const int64_t first = G % 8 == 0 ? static_cast<int64_t>(hw % 8) * (G / 8) + hw / 8 : hw;
-  for (int64_t l = first; l < total; l += G) {
-    // bands of four tile columns, row by row inside a band
-    constexpr int GN = 4;
-    const int64_t band = l / (static_cast<int64_t>(tiles_m) * GN);
-    const int w = static_cast<int>(min(static_cast<int64_t>(GN), tiles_n - band * GN));
-    const int64_t r = l - band * tiles_m * GN;
-    const int64_t m0 = r / w * T, n0 = (band * GN + r % w) * T;
+  for (int64_t l = first; l < work.units; l += G) {
+    const TileUnit unit = tile_unit(work, l);
+    const int64_t m0 = unit.ti * T, n0 = unit.tj * T;
 
     i32x16_t acc[FM][FN];
 #pragma unroll
@@ -152,9 +149,9 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
       for (int ni = 0; ni < FN; ++ni) acc[mi][ni] = (i32x16_t)(0);
 
     Stage8<T, NW> om, on;
-    om.init(a.a, a.m, a.k, m0, wave, lane);
-    on.init(a.b, a.n, a.k, n0, wave, lane);
-    const int KT = (a.k + kBytes - 1) / kBytes, KF = a.k / kBytes;
+    om.init(a.a, a.m, a.k, unit.past * kBytes, m0, wave, lane);
+    on.init(a.b, a.n, a.k, unit.past * kBytes, n0, wave, lane);
+    const int KT = work.stages, KF = min(a.k / kBytes, unit.past);
     auto issue = [&](char* st, int kt) {
       const bool full = kt < KF;
       om.issue(st, kt * kBytes, wave, full);
@@ -189,7 +186,7 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
     };
     // stage kt has landed in st: complete its last chunk
     auto complete = [&](char* st, int kt) {
-      if ((a.k & 15) && kt == KT - 1) {
+      if ((a.k & 15) && kt == KT - 1 && kt < unit.past) {
         Stage8<T, NW>::finish(st, a.a, a.m, a.k, m0, kt * kBytes, tid);
         Stage8<T, NW>::finish(st + HALF, a.b, a.n, a.k, n0, kt * kBytes, tid);
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -221,22 +218,66 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
       });
     };
     // whole rounds of two stages: stages at or past K load zeros
-    issue(st0, 0);
-    issue(st1, 1);
+    issue(st0, unit.first);
+    issue(st1, unit.first + 1);
     asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(NL) : "memory");
-    complete(st0, 0);
+    complete(st0, unit.first);
     frags(st0, 0, ic<0>{});
-    for (int kt = 0; kt < KT; kt += 2) static_for<2>([&](auto S) { stage(S, kt + decltype(S)::value); });
+    for (int kt = unit.first; kt < unit.past; kt += 2) static_for<2>([&](auto S) { stage(S, kt + decltype(S)::value); });
 
     // ---- epilogue: scaled values through LDS, row-contiguous stores
     int el = lane;
     asm volatile("" : "+v"(el));
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
     __syncthreads();
-    constexpr int E = static_cast<int>(sizeof(O));
-    constexpr int HROWS = E == 2 ? T / 2 : T / 4;   // rows that one stage buffer holds
-    constexpr int ROUNDS = E == 2 ? 1 : 2;          // of 2 HROWS rows
-    static_assert(HROWS * T * E <= STAGE, "output rows fit the stage buffers");
+    // in rounds of the rows that the stage buffers hold: all of a tile of bf16, or
+    // the rows of the waves wm == round (fp32, and integers that are not all of the sum)
+    auto rounds = [&](auto Z, auto&& put, auto&& get) __attribute__((always_inline)) {
+      using S = decltype(Z);
+      constexpr int E = static_cast<int>(sizeof(S));
+      constexpr int HROWS = E == 2 ? T / 2 : T / 4, ROUNDS = E == 2 ? 1 : 2;
+      static_assert(HROWS * T * E <= STAGE, "output rows fit the stage buffers");
+      static_for<ROUNDS>([&](auto R) {
+        constexpr int rd = decltype(R)::value;
+        if (ROUNDS == 1 || wm == rd) {
+          static_for<FM>([&](auto MI) {
+            constexpr int mi = decltype(MI)::value;
+            const int il = wm * WM + mi * 32 + (el & 31), row = ROUNDS == 1 ? il : il - rd * WM;
+            char* half = row >= HROWS ? st1 : st0;
+            put(MI, il, [&](int jl) { return half + out_off<S, T>(row >= HROWS ? row - HROWS : row, jl); });
+          });
+        }
+        __syncthreads();
+        constexpr int C = 16 / E, CH = T / C;  // elements of a chunk, chunks of a row
+        const int et = wave * 64 + el;
+#pragma unroll 4
+        for (int it = 0; it < 2 * HROWS * CH / NT; ++it) {
+          const int e = et + it * NT, row = e / CH, c = e % CH;
+          const char* half = row >= HROWS ? st1 : st0;
+          get(rd * 2 * HROWS + row, C * c, *reinterpret_cast<const u32x4_t*>(half + out_off<S, T>(row >= HROWS ? row - HROWS : row, C * c)));
+        }
+        __syncthreads();
+      });
+    };
+    if (unit.slot >= 0) {
+      int* part = reinterpret_cast<int*>(work.parts) + unit.slot * (T * T);
+      rounds(
+          0,
+          [&](auto MI, int, auto&& at) __attribute__((always_inline)) {
+            constexpr int mi = decltype(MI)::value;
+            static_for<FN>([&](auto NI) {
+              constexpr int ni = decltype(NI)::value;
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<i32x4_t*>(at(wn * WN + ni * 32 + 8 * g + 4 * (el >> 5))) =
+                    i32x4_t{acc[mi][ni][4 * g], acc[mi][ni][4 * g + 1], acc[mi][ni][4 * g + 2], acc[mi][ni][4 * g + 3]};
+              __builtin_amdgcn_sched_barrier(0);
+            });
+          },
+          [&](int row, int c, u32x4_t v) __attribute__((always_inline)) { *reinterpret_cast<u32x4_t*>(part + row * T + c) = v; });
+      continue;
+    }
+    constexpr int E = static_cast<int>(sizeof(O)), C = 16 / E;
     float sb[FN][4][4];
 #pragma unroll
     for (int ni = 0; ni < FN; ++ni)
@@ -249,76 +290,85 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
         }
     O* out = reinterpret_cast<O*>(a.out.p);
     const bool wide = ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(a.out.ld * E)) & 15u) == 0;
-    static_for<ROUNDS>([&](auto R) {
-      constexpr int rd = decltype(R)::value;
-      // round rd: all of the tile (bf16), or the rows of the waves wm == rd (fp32)
-      if (ROUNDS == 1 || wm == rd) {
-        static_for<FM>([&](auto MI) {
+    rounds(
+        O{},
+        [&](auto MI, int il, auto&& at) __attribute__((always_inline)) {
           constexpr int mi = decltype(MI)::value;
-          const int il = wm * WM + mi * 32 + (el & 31);
           const float sa = m0 + il < a.m ? a.a.scale[m0 + il] : 0.0f;
-          const int row = ROUNDS == 1 ? il : il - rd * WM;
-          char* half = row >= HROWS ? st1 : st0;
-          const int hr = row >= HROWS ? row - HROWS : row;
           static_for<FN>([&](auto NI) {
             constexpr int ni = decltype(NI)::value;
             static_for<4>([&](auto GI) {
               constexpr int g = decltype(GI)::value;
-              const int jl = wn * WN + ni * 32 + 8 * g + 4 * (el >> 5);
               float v[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) v[q] = static_cast<float>(acc[mi][ni][4 * g + q]) * (sa * sb[ni][g][q]);
-              char* at = half + out_off<O, T>(hr, jl);
-              if constexpr (E == 2) *reinterpret_cast<uint2*>(at) = make_uint2(muon::pack_bf16x2(v[0], v[1]), muon::pack_bf16x2(v[2], v[3]));
-              else *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2], v[3]);
+              char* to = at(wn * WN + ni * 32 + 8 * g + 4 * (el >> 5));
+              if constexpr (E == 2) *reinterpret_cast<uint2*>(to) = make_uint2(muon::pack_bf16x2(v[0], v[1]), muon::pack_bf16x2(v[2], v[3]));
+              else *reinterpret_cast<float4*>(to) = make_float4(v[0], v[1], v[2], v[3]);
             });
             __builtin_amdgcn_sched_barrier(0);
           });
+        },
+        [&](int row, int c, u32x4_t v) __attribute__((always_inline)) {
+          const int64_t m = m0 + row, n = n0 + c;
+          if (m >= a.m || n >= a.n) return;
+          O* to = out + m * a.out.ld + n;
+          if (wide && n + C <= a.n) {
+            __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(to));
+          } else {
+            const O* from = reinterpret_cast<const O*>(&v);
+            for (int q = 0; q < C; ++q)
+              if (n + q < a.n) to[q] = from[q];
+          }
         });
-      }
-      __syncthreads();
-      constexpr int C = 16 / E, CH = T / C;  // elements of a chunk, chunks of a row
-      const int et = wave * 64 + el;
-#pragma unroll 4
-      for (int it = 0; it < 2 * HROWS * CH / NT; ++it) {
-        const int e = et + it * NT, row = e / CH, c = e % CH;
-        const char* half = row >= HROWS ? st1 : st0;
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(half + out_off<O, T>(row >= HROWS ? row - HROWS : row, C * c));
-        const int64_t m = m0 + rd * 2 * HROWS + row, n = n0 + C * c;
-        if (m >= a.m || n >= a.n) continue;
-        O* to = out + m * a.out.ld + n;
-        if (wide && n + C <= a.n) {
-          __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(to));
-        } else {
-          const O* from = reinterpret_cast<const O*>(&v);
-          for (int q = 0; q < C; ++q)
-            if (n + q < a.n) to[q] = from[q];
-        }
-      }
-      __syncthreads();
-    });
   }
 }
 
-template <typename O>
-hipError_t go_tiles(hipStream_t s, const Matmul8Args& a, int T) {
-  const int tm = static_cast<int>((a.m + T - 1) / T), tn = static_cast<int>((a.n + T - 1) / T);
-  const int64_t tiles = static_cast<int64_t>(tm) * tn, cap = a.cus * (T == 256 ? 1 : 2);
-  const unsigned grid = static_cast<unsigned>(tiles < cap ? tiles : cap);
-  if (T == 256) matmul8_tile_kernel<O, 256><<<grid, 512, 0, s>>>(a, tm, tn);
-  else matmul8_tile_kernel<O, 128><<<grid, 256, 0, s>>>(a, tm, tn);
+// The parts of the tiles that were cut, added in order: four outputs a thread.
+template <typename O, int T>
+__global__ __launch_bounds__(256) void matmul8_join_kernel(Matmul8Args a, TileWork work) {
+  constexpr int PER = T * T / 1024;  // workgroups of a tile
+  const int64_t t = blockIdx.x / PER;
+  const int e = static_cast<int>(blockIdx.x % PER) * 256 + static_cast<int>(threadIdx.x), row = e / (T / 4), c = 4 * (e % (T / 4));
+  const TileUnit unit = tile_unit(work, work.whole + t);
+  const int* part = reinterpret_cast<const int*>(work.parts) + t * work.splits * (T * T) + row * T + c;
+  const int64_t m = unit.ti * T + row, n = unit.tj * T + c;
+  if (m >= a.m || n >= a.n) return;
+  i32x4_t v = *reinterpret_cast<const i32x4_t*>(part);
+  for (int p = 1; p < work.splits; ++p) v += *reinterpret_cast<const i32x4_t*>(part + static_cast<int64_t>(p) * (T * T));
+  O* to = reinterpret_cast<O*>(a.out.p) + m * a.out.ld + n;
+  const float sa = a.a.scale[m];
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    if (n + q < a.n) muon::Elem<O>::store(to + q, static_cast<float>(v[q]) * (sa * a.b.scale[n + q]));
+}
+
+template <typename O, int T>
+hipError_t go_tiles(hipStream_t s, const Matmul8Args& a, const TilePlan& p) {
+  const TileWork w = tile_work(p, a.ws);
+  matmul8_tile_kernel<O, T><<<static_cast<unsigned>(p.grid), T == 256 ? 512 : 256, 0, s>>>(a, w);
+  if (p.splits > 1) {
+    const int64_t cut = static_cast<int64_t>(p.tm) * p.tn - p.whole;
+    matmul8_join_kernel<O, T><<<static_cast<unsigned>(cut * (T * T / 1024)), 256, 0, s>>>(a, w);
+  }
   return hipGetLastError();
+}
+
+template <typename O>
+hipError_t go(hipStream_t s, const Matmul8Args& a) {
+  const int stages = (a.k + kBytes - 1) / kBytes;
+  // (two small tiles on a CU take 0.6 of a large one's time for half its products)
+  double large, small;
+  const TilePlan l = plan_tiles(a.m, a.n, 256, 256, stages, a.cus, a.ws_bytes, &large);
+  const TilePlan q = plan_tiles(a.m, a.n, 128, 128, stages, 2 * a.cus, a.ws_bytes, &small);
+  return large <= 0.6 * small ? go_tiles<O, 256>(s, a, l) : go_tiles<O, 128>(s, a, q);
 }
 
 }  // namespace
 
 hipError_t launch_matmul8(hipStream_t s, const Matmul8Args& a) {
   if (a.m == 0 || a.n == 0) return hipSuccess;
-  if (a.m > 32) {
-    const int64_t t256 = ((a.m + 255) / 256) * ((a.n + 255) / 256);
-    const int tile = t256 * 2 >= a.cus ? 256 : 128;
-    return a.out.bf16 ? go_tiles<bf16_t>(s, a, tile) : go_tiles<float>(s, a, tile);
-  }
+  if (a.m > 32) return a.out.bf16 ? go<bf16_t>(s, a) : go<float>(s, a);
   const unsigned grid = static_cast<unsigned>(((a.m + kTile - 1) / kTile) * ((a.n + kTile - 1) / kTile));
   if (a.out.bf16) matmul8_simple_kernel<bf16_t><<<grid, 256, 0, s>>>(a);
   else matmul8_simple_kernel<float><<<grid, 256, 0, s>>>(a);
