@@ -25,7 +25,8 @@ hipError_t launch_dequantize_rows(hipStream_t s, Bytes q, Values out, int64_t ro
 
 // out[m][n] = sum_k a[m][k] b[n][k] * (sa[m] sb[n])
 struct Matmul8Args {
-  Bytes a, b;
+  Bytes a, b;  // launch_linear8: a receives the rounded rows, or its p is nullptr
+  Values x;    // launch_linear8: the rows
   Values out;
   int64_t m, n;
   int k;
@@ -34,6 +35,9 @@ struct Matmul8Args {
   size_t ws_bytes;
 };
 hipError_t launch_matmul8(hipStream_t s, const Matmul8Args& a);
+// The product of rows of values, rounded within the launch: for calls of few tokens.
+bool linear8_rounds(const Matmul8Args& a);
+hipError_t launch_linear8(hipStream_t s, const Matmul8Args& a);
 
 // out[i][j] (+)= sum_c y(i, c) scale[c] q[c][j]; y(i, c) at y[i][c], or, of_columns, at y[c][i]
 struct Grad8Args {

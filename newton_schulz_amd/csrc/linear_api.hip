@@ -85,10 +85,8 @@ size_t parts_room(const muon_ctx* c, size_t from) {
   return c->ws_bytes > from ? (c->ws_bytes - from < kMostParts ? c->ws_bytes - from : kMostParts) : 0;
 }
 
-muon_status_t matmul8(muon_ctx* c, hipStream_t s, const Bytes& a, int64_t m, const muon_rows8_t& b, const muon_rows_t& out,
-                      size_t from) {
-  const Matmul8Args t = {a, bytes8(b), values(out), m, b.rows, static_cast<int>(b.cols), c->cus, c->ws + from, parts_room(c, from)};
-  return timed(c, s, MUON_K_LINEAR8, "8-bit product launch", [&] { return launch_matmul8(s, t); });
+Matmul8Args matmul8_args(muon_ctx* c, const Bytes& a, int64_t m, const muon_rows8_t& b, const muon_rows_t& out, size_t from) {
+  return {a, bytes8(b), Values{}, values(out), m, b.rows, static_cast<int>(b.cols), c->cus, c->ws + from, parts_room(c, from)};
 }
 
 muon_status_t grad8(muon_ctx* c, void* stream, const muon_rows_t* y, const muon_rows8_t* q, const muon_rows_t* out,
@@ -186,7 +184,9 @@ muon_status_t muon_matmul8(muon_ctx_t* c, void* stream, const muon_rows8_t* a, c
   if (st == MUON_OK) st = check_ctx(c, 0);
   if (st != MUON_OK || a->rows == 0) return st;
   DeviceGuard g(c->device);
-  return matmul8(c, static_cast<hipStream_t>(stream), bytes8(*a), a->rows, *b, *out, 0);
+  const Matmul8Args t = matmul8_args(c, bytes8(*a), a->rows, *b, *out, 0);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return timed(c, s, MUON_K_LINEAR8, "8-bit product launch", [&] { return launch_matmul8(s, t); });
 }
 
 muon_status_t muon_linear8(muon_ctx_t* c, void* stream, const muon_rows_t* x, const muon_rows8_t* w,
@@ -213,11 +213,14 @@ muon_status_t muon_linear8(muon_ctx_t* c, void* stream, const muon_rows_t* x, co
   if (st != MUON_OK || x->rows == 0) return st;
   DeviceGuard g(c->device);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const Bytes q = x8 ? bytes8(*x8)
-                     : Bytes{reinterpret_cast<int8_t*>(c->ws + l.q), reinterpret_cast<float*>(c->ws + l.scale), up16(x->cols)};
-  st = timed(c, s, MUON_K_LINEAR8, "quantisation launch",
-             [&] { return launch_quantize_rows(s, values(*x), q, x->rows, static_cast<int>(x->cols)); });
-  return st == MUON_OK ? matmul8(c, s, q, x->rows, *w, *out, x8 ? 0 : l.parts) : st;
+  Matmul8Args t = matmul8_args(c, x8 ? bytes8(*x8) : Bytes{}, x->rows, *w, *out, x8 ? 0 : l.parts);
+  t.x = values(*x);
+  if (linear8_rounds(t)) return timed(c, s, MUON_K_LINEAR8, "8-bit layer launch", [&] { return launch_linear8(s, t); });
+  if (x8 == nullptr) t.a = {reinterpret_cast<int8_t*>(c->ws + l.q), reinterpret_cast<float*>(c->ws + l.scale), up16(x->cols)};
+  return timed(c, s, MUON_K_LINEAR8, "8-bit layer launch", [&] {
+    const hipError_t e = launch_quantize_rows(s, t.x, t.a, x->rows, t.k);
+    return e == hipSuccess ? launch_matmul8(s, t) : e;
+  });
 }
 
 muon_status_t muon_input_grad8(muon_ctx_t* c, void* stream, const muon_rows_t* grad_y, const muon_rows8_t* w,

@@ -3,58 +3,237 @@
 // Mathematics.  The integers' sum is exact in 32 bits (at most 131071 products
 // of at most 2^14); it is rounded to fp32 once and multiplied by the product of
 // the two scales.
+#include <type_traits>
+
 #include "linear8.h"
 #include "ns_mfma_common.h"
+#include "rows8_device.h"
 #include "tile_plan.h"
 
 namespace {
 
-constexpr int kTile = 64, kStep = 64, kPitch = kStep + 4;
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
-template <typename T>
-__global__ __launch_bounds__(256) void matmul8_simple_kernel(Matmul8Args a) {
-  __shared__ int8_t ta[kTile * kPitch], tb[kTile * kPitch];
-  const int64_t tiles_n = (a.n + kTile - 1) / kTile;
-  const int64_t m0 = static_cast<int64_t>(blockIdx.x) / tiles_n * kTile, n0 = static_cast<int64_t>(blockIdx.x) % tiles_n * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  int acc[4][4] = {};
-  for (int k0 = 0; k0 < a.k; k0 += kStep) {
-    __syncthreads();
-    for (int e = threadIdx.x; e < kTile * kStep; e += 256) {
-      const int r = e / kStep, c = e % kStep;
-      const bool in = k0 + c < a.k;
-      ta[r * kPitch + c] = in && m0 + r < a.m ? a.a.p[(m0 + r) * a.a.ld + k0 + c] : 0;
-      tb[r * kPitch + c] = in && n0 + r < a.n ? a.b.p[(n0 + r) * a.b.ld + k0 + c] : 0;
-    }
-    __syncthreads();
-    for (int c = 0; c < kStep; c += 4) {
-      int va[4], vb[4];
+// ---------------------------------------------------------------------------
+// few tokens: the weights stream through registers
+// ---------------------------------------------------------------------------
+
+// 16 bytes of a row from k on, zeros at and behind its end.
+__device__ __forceinline__ i32x4_t row_tail(const int8_t* row, int k, int end) {
+  if (k + 16 <= end) return *reinterpret_cast<const i32x4_t*>(row + k);
+  i32x4_t v = {0, 0, 0, 0};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) va[i] = *reinterpret_cast<const int*>(ta + (ty + 16 * i) * kPitch + c);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) vb[j] = *reinterpret_cast<const int*>(tb + (tx + 16 * j) * kPitch + c);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = __builtin_amdgcn_sdot4(va[i], vb[j], acc[i][j], false);
-    }
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int64_t m = m0 + ty + 16 * i, n = n0 + tx + 16 * j;
-      if (m < a.m && n < a.n)
-        muon::Elem<T>::store(reinterpret_cast<T*>(a.out.p) + m * a.out.ld + n,
-                             static_cast<float>(acc[i][j]) * (a.a.scale[m] * a.b.scale[n]));
-    }
+  for (int i = 0; i < 15; ++i)
+    if (k + i < end) v[i / 4] |= static_cast<int>(static_cast<uint32_t>(static_cast<uint8_t>(row[k + i])) << (8 * (i & 3)));
+  return v;
 }
 
+// Up to 16 MG rows of a by 16 NB columns (rows of b) at a time; a workgroup's KS
+// waves share the contraction.  b's 16 rows by 64 bytes are one matrix-core
+// operand as they lie in memory: lane l holds row l % 16, bytes 16 (l / 16) ..
+// + 15.  Rows past the end repeat the last one and are not stored.
+//
+// Where a comes from: FROM = Bytes8: as many loads again as for b (through L1
+// they take their time: 151936 columns of 2560 took 74 us for one row and 121
+// for sixteen); Staged: brought into LDS once, XB bytes at most, by workgroups
+// that walk the columns; bf16_t, float: rounded to 8 bits on the way there.
+struct Bytes8 {};
+struct Staged {};
+
+template <typename O, typename FROM, int NB, int MG, int KS, int XB>
+__global__ __launch_bounds__(64 * KS) void matmul8_stream_kernel(Matmul8Args a) {
+  constexpr bool LDS = !std::is_same_v<FROM, Bytes8>;
+  constexpr int U = LDS ? 8 / NB : NB + MG <= 2 ? 8 : NB + MG <= 5 ? 4 : 2;  // steps of 64 asked for at once
+  __shared__ i32x4_t sums[KS][NB * MG][64];
+  __shared__ __attribute__((aligned(16))) char xs[LDS ? XB : 16];
+  __shared__ float xscale[16 * MG];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, h = lane >> 4, m = static_cast<int>(a.m);
+  const int steps = (a.k + 63) / 64, per = (steps + KS - 1) / KS, s0 = min(wave * per, steps), s1 = min(s0 + per, steps), full = min(s1, a.k / 64);
+  const int8_t* pa[MG];
+  const char* xa[MG];
+  if constexpr (LDS) {
+    // 16-byte chunk c of row i at (c m + i) 16: a step's operand lies together;
+    // zeros behind k, so that whatever b's rows hold there meets nothing
+    const int chunks = 4 * steps;
+    if constexpr (std::is_same_v<FROM, Staged>) {
+      for (int e = threadIdx.x; e < chunks * m; e += 64 * KS) {
+        const int i = e / chunks, c = e % chunks;
+        *reinterpret_cast<i32x4_t*>(xs + (c * m + i) * 16) = row_tail(a.a.p + i * a.a.ld, 16 * c, a.k);
+      }
+      if (static_cast<int>(threadIdx.x) < m) xscale[threadIdx.x] = a.a.scale[threadIdx.x];
+    } else {
+      constexpr int N = muon::Piece<FROM>::N, P = 16 / N;
+      for (int i = wave; i < m; i += KS) {
+        const FROM* row = reinterpret_cast<const FROM*>(a.x.p) + i * a.x.ld;
+        uint32_t top = 0;
+        for (int p = lane; p * N < a.k; p += 64) top = muon::piece_top<FROM>(muon::load_piece(row, p, a.k), top);
+        const float s = muon::row_scale(muon::wave_top(top));
+        const muon::RowRounding rounding(s);
+        if (lane == 0) xscale[i] = s;
+        for (int c = lane; c < chunks; c += 64) {
+          u32x4_t w = {0, 0, 0, 0};
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            if ((P * c + q) * N >= a.k) continue;
+            float v[N];
+            uint32_t b[N / 4];
+            muon::Piece<FROM>::values(muon::load_piece(row, P * c + q, a.k), v);
+            muon::to_bytes(v, rounding, b);
+#pragma unroll
+            for (int j = 0; j < N / 4; ++j) w[q * (N / 4) + j] = b[j];
+          }
+          *reinterpret_cast<u32x4_t*>(xs + (c * m + i) * 16) = w;
+          if (blockIdx.x == 0 && a.a.p) {  // kept for the backward pass
+            int8_t* to = a.a.p + i * a.a.ld + 16 * c;
+            if (16 * c + 16 <= a.k) {
+              *reinterpret_cast<u32x4_t*>(to) = w;
+            } else {
+              for (int j = 0; 16 * c + j < a.k; ++j) to[j] = static_cast<int8_t>(w[j / 4] >> (8 * (j & 3)));
+            }
+          }
+        }
+        if (blockIdx.x == 0 && a.a.p && lane == 0) a.a.scale[i] = s;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < MG; ++j) xa[j] = xs + (h * m + min(16 * j + r, m - 1)) * 16;
+  } else {
+#pragma unroll
+    for (int j = 0; j < MG; ++j) pa[j] = a.a.p + static_cast<int64_t>(min(16 * j + r, m - 1)) * a.a.ld;
+    if (static_cast<int>(threadIdx.x) < m) xscale[threadIdx.x] = a.a.scale[threadIdx.x];
+  }
+  const int64_t groups = (a.n + 16 * NB - 1) / (16 * NB);
+  for (int64_t g = blockIdx.x; g < groups; g += gridDim.x) {
+    const int64_t n0 = g * (16 * NB);
+    const int8_t* pb[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) pb[i] = a.b.p + min(n0 + 16 * i + r, a.n - 1) * a.b.ld;
+    i32x4_t acc[NB][MG];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < MG; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+    auto of_a = [&](int s, int j) __attribute__((always_inline)) {
+      if constexpr (LDS) return *reinterpret_cast<const i32x4_t*>(xa[j] + s * 64 * m);
+      else return *reinterpret_cast<const i32x4_t*>(pa[j] + 64 * s + 16 * h);
+    };
+    auto some = [&](int s, auto N) __attribute__((always_inline)) {
+      constexpr int n = decltype(N)::value;
+      i32x4_t vb[n][NB], va[n][MG];
+#pragma unroll
+      for (int u = 0; u < n; ++u) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) vb[u][i] = *reinterpret_cast<const i32x4_t*>(pb[i] + 64 * (s + u) + 16 * h);
+#pragma unroll
+        for (int j = 0; j < MG; ++j) va[u][j] = of_a(s + u, j);
+      }
+#pragma unroll
+      for (int u = 0; u < n; ++u)
+#pragma unroll
+        for (int i = 0; i < NB; ++i)
+#pragma unroll
+          for (int j = 0; j < MG; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vb[u][i], va[u][j], acc[i][j], 0, 0, 0);
+    };
+    int s = s0;
+    for (; s + U <= full; s += U) some(s, ic<U>{});
+    if constexpr (U > 2)
+      for (; s + 2 <= full; s += 2) some(s, ic<2>{});
+    for (; s < full; ++s) some(s, ic<1>{});
+    if (s < s1) {
+      const int k = 64 * s + 16 * h;
+      i32x4_t vb[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) vb[i] = row_tail(pb[i], k, a.k);
+#pragma unroll
+      for (int j = 0; j < MG; ++j) {
+        i32x4_t va;
+        if constexpr (LDS) va = of_a(s, j);
+        else va = row_tail(pa[j], k, a.k);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vb[i], va, acc[i][j], 0, 0, 0);
+      }
+    }
+    __syncthreads();  // the last group's sums have been read
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < MG; ++j) sums[wave][i * MG + j][lane] = acc[i][j];
+    __syncthreads();
+    // lane l of an accumulator: row l % 16 of a, four columns from 4 (l / 16) on
+    for (int f = wave; f < NB * MG; f += KS) {
+      i32x4_t v = sums[0][f][lane];
+#pragma unroll
+      for (int w = 1; w < KS; ++w) v += sums[w][f][lane];
+      const int mi = 16 * (f % MG) + r;
+      const int64_t n = n0 + 16 * (f / MG) + 4 * h;
+      if (mi >= m) continue;
+      O* to = reinterpret_cast<O*>(a.out.p) + mi * a.out.ld + n;
+      const float sa = xscale[mi];
+      float x[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[q] = n + q < a.n ? static_cast<float>(v[q]) * (sa * a.b.scale[n + q]) : 0.0f;
+      if (n + 4 <= a.n && (reinterpret_cast<uintptr_t>(to) & (4 * sizeof(O) - 1)) == 0) {
+        if constexpr (sizeof(O) == 2) *reinterpret_cast<uint2*>(to) = make_uint2(muon::pack_bf16x2(x[0], x[1]), muon::pack_bf16x2(x[2], x[3]));
+        else *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+      } else {
+        for (int q = 0; q < 4; ++q)
+          if (n + q < a.n) muon::Elem<O>::store(to + q, x[q]);
+      }
+    }
+  }
+}
+
+// a in LDS: as many workgroups as find room on the CUs.
+template <typename O, typename FROM, int MG, int KS, int XB>
+hipError_t go_staged(hipStream_t s, const Matmul8Args& a) {
+  constexpr int bytes = XB + KS * MG * 1024 + 64 * MG, room = 160 * 1024 / bytes, waves = 32 / KS;
+  const int64_t groups = (a.n + 15) / 16, cap = static_cast<int64_t>(a.cus) * (room < waves ? room : waves);
+  matmul8_stream_kernel<O, FROM, 1, MG, KS, XB><<<static_cast<unsigned>(groups < cap ? groups : cap), 64 * KS, 0, s>>>(a);
+  return hipGetLastError();
+}
+constexpr int kStagedSmall = 16 << 10, kStagedMost = 44 << 10, kStagedWide = 124 << 10;
+inline int64_t staged_bytes(const Matmul8Args& a) { return a.m * ((a.k + 63) / 64) * 64; }
+
+template <typename O, typename FROM, int MG>
+hipError_t go_staged(hipStream_t s, const Matmul8Args& a) {
+  if (staged_bytes(a) <= kStagedSmall) return go_staged<O, FROM, MG, 4, kStagedSmall>(s, a);
+  if (staged_bytes(a) <= kStagedMost) return go_staged<O, FROM, MG, 4, kStagedMost>(s, a);
+  return go_staged<O, FROM, MG, 16, kStagedWide>(s, a);
+}
+template <typename O, int NB, int MG>
+hipError_t go_stream(hipStream_t s, const Matmul8Args& a) {
+  const int64_t groups = (a.n + 16 * NB - 1) / (16 * NB);
+  const unsigned grid = static_cast<unsigned>(groups);
+  // four waves a workgroup, sixteen where there are fewer workgroups than CUs
+  if constexpr (NB == 1) {
+    if (groups < a.cus) {
+      matmul8_stream_kernel<O, Bytes8, NB, MG, 16, 0><<<grid, 1024, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  }
+  matmul8_stream_kernel<O, Bytes8, NB, MG, 4, 0><<<grid, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+template <typename O, int MG>
+hipError_t go_stream(hipStream_t s, const Matmul8Args& a) {
+  if constexpr (MG <= 2) {
+    if (staged_bytes(a) <= kStagedWide) return go_staged<O, Staged, MG>(s, a);
+  }
+  // as many columns a workgroup as leave eight workgroups to a CU
+  return a.n >= int64_t{64} * 8 * a.cus ? go_stream<O, 4, MG>(s, a) : go_stream<O, 1, MG>(s, a);
+}
+constexpr int kMostStreamed = 64;
+template <typename O>
+hipError_t go_stream(hipStream_t s, const Matmul8Args& a) {
+  return a.m <= 16 ? go_stream<O, 1>(s, a) : a.m <= 32 ? go_stream<O, 2>(s, a) : go_stream<O, 4>(s, a);
+}
 
 // ---------------------------------------------------------------------------
 // tiles of T x T outputs on the matrix cores
 // ---------------------------------------------------------------------------
-typedef int i32x4_t __attribute__((ext_vector_type(4)));
-typedef int i32x16_t __attribute__((ext_vector_type(16)));
-
 constexpr int kBytes = 128;  // of k in a stage
 
 // One operand's stage: T rows of 128 bytes, in LDS as rt_off lays them out.
@@ -364,13 +543,24 @@ hipError_t go(hipStream_t s, const Matmul8Args& a) {
   return large <= 0.6 * small ? go_tiles<O, 256>(s, a, l) : go_tiles<O, 128>(s, a, q);
 }
 
+// Rows of values, rounded by every workgroup for itself.
+template <typename O>
+hipError_t go_rounding(hipStream_t s, const Matmul8Args& a) {
+  if (a.x.bf16) return a.m <= 16 ? go_staged<O, bf16_t, 1>(s, a) : go_staged<O, bf16_t, 2>(s, a);
+  return a.m <= 16 ? go_staged<O, float, 1>(s, a) : go_staged<O, float, 2>(s, a);
+}
+
 }  // namespace
+
+bool linear8_rounds(const Matmul8Args& a) { return a.m <= 32 && staged_bytes(a) <= kStagedMost; }
+
+hipError_t launch_linear8(hipStream_t s, const Matmul8Args& a) {
+  if (a.m == 0 || a.n == 0) return hipSuccess;
+  return a.out.bf16 ? go_rounding<bf16_t>(s, a) : go_rounding<float>(s, a);
+}
 
 hipError_t launch_matmul8(hipStream_t s, const Matmul8Args& a) {
   if (a.m == 0 || a.n == 0) return hipSuccess;
-  if (a.m > 32) return a.out.bf16 ? go<bf16_t>(s, a) : go<float>(s, a);
-  const unsigned grid = static_cast<unsigned>(((a.m + kTile - 1) / kTile) * ((a.n + kTile - 1) / kTile));
-  if (a.out.bf16) matmul8_simple_kernel<bf16_t><<<grid, 256, 0, s>>>(a);
-  else matmul8_simple_kernel<float><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError();
+  if (a.m <= kMostStreamed) return a.out.bf16 ? go_stream<bf16_t>(s, a) : go_stream<float>(s, a);
+  return a.out.bf16 ? go<bf16_t>(s, a) : go<float>(s, a);
 }

@@ -1,89 +1,154 @@
 // Rows of values in 8 bits, a scale per row, and back.
 //
-// Mathematics.  s = max |x| / 127 in binary32; q is the integer nearest to the
-// exact x / s, ties to even.  x / s is formed as x (1 / s): its error, below
-// 2^-22 of the quotient (|q| <= 127: 2^-15), matters only next to a half, where
-// the remainder x - q s (exact as one fused multiply-add: |x - q s| <= s, and
-// both are multiples of the smaller's last place) is compared with s / 2.
+// Both are bound by HBM: every value is read once and every byte written once.
+// A row is held in registers between its maximum and its rounding, by a wave
+// where it fits (five 16-byte pieces a lane at 2560 bf16 values), else by a
+// workgroup; rows beyond 1024 threads of eight pieces are read twice.  Rows lie
+// in the order of workgroups, so that what is in flight is one moving window
+// of addresses.
 #include "linear8.h"
-#include "muon_device.h"
+#include "rows8_device.h"
 
 using muon::bf16_t;
+using muon::load_piece;
+using muon::Piece;
+using muon::u32x4;
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr float kMostScale = 0x1.020406p+121f;  // 127 times the next larger number overflows
+constexpr int kHeld = 8;  // pieces a thread holds
 
-// x / s to the nearest integer, ties to even, given an estimate of it.
-__device__ __forceinline__ float nearest(float x, float s, float estimate) {
-  float q = rintf(estimate);
-  const float r = __builtin_fmaf(-q, s, x);  // exact
-  const float over = 2.0f * fabsf(r);
-  if (over >= s) {
-    // at or past the half: the neighbour on r's side, or of two the even one
-    const float next = q + copysignf(1.0f, r);
-    const bool odd = (static_cast<int>(q) & 1) != 0;
-    if (over > s || odd) q = next;
+// The bytes of piece p.
+template <typename T>
+__device__ __forceinline__ void store_bytes(int8_t* row, int p, int cols, u32x4 w, const muon::RowRounding& row8) {
+  constexpr int N = Piece<T>::N;
+  float v[N];
+  uint32_t b[N / 4];
+  Piece<T>::values(w, v);
+  muon::to_bytes(v, row8, b);
+  int8_t* at = row + p * N;
+  if ((p + 1) * N <= cols) {
+    if constexpr (N == 8) *reinterpret_cast<uint2*>(at) = make_uint2(b[0], b[1]);
+    else *reinterpret_cast<uint32_t*>(at) = b[0];
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (p * N + i < cols) at[i] = static_cast<int8_t>(b[i / 4] >> (8 * (i & 3)));
   }
-  return fminf(fmaxf(q, -127.0f), 127.0f);
 }
 
+// NT threads a row, 256 / NT rows a workgroup (NT = 64), or one.
+template <typename T, int NT>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void quantize_kernel(const T* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
+                                                                       int64_t rows, int cols) {
+  constexpr int ROWS = NT < 256 ? 256 / NT : 1;
+  __shared__ uint32_t tops[NT / 64];
+  const int t = static_cast<int>(threadIdx.x) % NT;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * ROWS + threadIdx.x / NT;
+  if (r >= rows) return;  // (whole waves; the only row of a workgroup is always there)
+  const T* row = x + r * ldx;
+  const int pieces = (cols + Piece<T>::N - 1) / Piece<T>::N;
+  const bool holds = pieces <= NT * kHeld;
+  u32x4 held[kHeld];
+  uint32_t top = 0;
+  if (holds) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i * NT + t < pieces) held[i] = load_piece(row, i * NT + t, cols);
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i * NT + t < pieces) top = muon::piece_top<T>(held[i], top);
+  } else {
+    for (int p = t; p < pieces; p += NT) top = muon::piece_top<T>(load_piece(row, p, cols), top);
+  }
+  top = muon::wave_top(top);
+  if constexpr (NT > 64) {
+    if ((t & 63) == 0) tops[t >> 6] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NT / 64; ++w) top = max(top, tops[w]);
+  }
+  const float s = muon::row_scale(top);
+  const muon::RowRounding rounding(s);
+  if (t == 0) scale[r] = s;
+  int8_t* to = q + r * ldq;
+  if (holds) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i)
+      if (i * NT + t < pieces) store_bytes<T>(to, i * NT + t, cols, held[i], rounding);
+  } else {
+    for (int p = t; p < pieces; p += NT) store_bytes<T>(to, p, cols, load_piece(row, p, cols), rounding);
+  }
+}
+
+// 16 bytes a thread at a time; a workgroup's threads share `per` pieces of a row.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void quantize_kernel(const T* x, int64_t ldx, int8_t* q, int64_t ldq, float* scale,
-                                                            int64_t rows, int cols) {
-  __shared__ float wave_top[kThreads / 64];
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const T* row = x + r * ldx;
-    // the largest magnitude by its bits: NaN and infinity come out on top
-    uint32_t top = 0;
-    for (int c = threadIdx.x; c < cols; c += kThreads)
-      top = max(top, __float_as_uint(muon::Elem<T>::load(row + c)) & 0x7fffffffu);
-    for (int d = 32; d > 0; d /= 2) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) wave_top[threadIdx.x >> 6] = __uint_as_float(top);
-    __syncthreads();
-    for (int w = 0; w < kThreads / 64; ++w) top = max(top, __float_as_uint(wave_top[w]));
-    const bool bad = top >= 0x7f800000u;
-    const float s = bad ? __uint_as_float(0x7fc00000u) : fminf(__uint_as_float(top) / 127.0f, kMostScale);
-    if (threadIdx.x == 0) scale[r] = s;
-    const bool zero = bad || s == 0.0f;
-    for (int c = threadIdx.x; c < cols; c += kThreads) {
-      const float v = muon::Elem<T>::load(row + c);
-      // (1 / s overflows where s is denormal: the quotient itself then)
-      q[r * ldq + c] = zero ? 0 : static_cast<int8_t>(nearest(v, s, s < 1.2e-38f ? v / s : v * (1.0f / s)));
+__global__ __launch_bounds__(256) void dequantize_kernel(const int8_t* q, int64_t ldq, const float* scale, T* out, int64_t ldo,
+                                                         int64_t rows, int cols, int per) {
+  const int t = static_cast<int>(threadIdx.x) % per;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / per) + threadIdx.x / per;
+  if (r >= rows || static_cast<int>(threadIdx.x) / per >= 256 / per) return;
+  const float s = scale[r];
+  const int8_t* row = q + r * ldq;
+  T* to = out + r * ldo;
+  for (int c = 16 * t; c < cols; c += 16 * per) {
+    if (c + 16 <= cols) {
+      const u32x4 w = *reinterpret_cast<const u32x4*>(row + c);
+      float v[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = s * static_cast<float>(static_cast<int>(w[i / 4] << (24 - 8 * (i & 3))) >> 24);
+      muon::u32x4_any* at = reinterpret_cast<muon::u32x4_any*>(to + c);
+      if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          at[h] = u32x4{muon::pack_bf16x2(v[8 * h], v[8 * h + 1]), muon::pack_bf16x2(v[8 * h + 2], v[8 * h + 3]),
+                        muon::pack_bf16x2(v[8 * h + 4], v[8 * h + 5]), muon::pack_bf16x2(v[8 * h + 6], v[8 * h + 7])};
+      } else {
+#pragma unroll
+        for (int h = 0; h < 4; ++h)
+          at[h] = u32x4{__float_as_uint(v[4 * h]), __float_as_uint(v[4 * h + 1]), __float_as_uint(v[4 * h + 2]), __float_as_uint(v[4 * h + 3])};
+      }
+    } else {
+      for (int i = c; i < cols; ++i) muon::Elem<T>::store(to + i, s * static_cast<float>(row[i]));
     }
   }
 }
 
+template <typename T, int NT>
+void quantize(hipStream_t s, const Values& x, const Bytes& q, int64_t rows, int cols) {
+  constexpr int ROWS = NT < 256 ? 256 / NT : 1;
+  quantize_kernel<T, NT><<<static_cast<unsigned>((rows + ROWS - 1) / ROWS), NT < 256 ? 256 : NT, 0, s>>>(
+      reinterpret_cast<const T*>(x.p), x.ld, q.p, q.ld, q.scale, rows, cols);
+}
 template <typename T>
-__global__ __launch_bounds__(kThreads) void dequantize_kernel(const int8_t* q, int64_t ldq, const float* scale, T* out,
-                                                              int64_t ldo, int64_t rows, int cols) {
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
-    const float s = scale[r];
-    for (int c = threadIdx.x; c < cols; c += kThreads)
-      muon::Elem<T>::store(out + r * ldo + c, s * static_cast<float>(q[r * ldq + c]));
-  }
+hipError_t quantize(hipStream_t s, const Values& x, const Bytes& q, int64_t rows, int cols) {
+  const int pieces = (cols + Piece<T>::N - 1) / Piece<T>::N;
+  // A wave's lanes hold up to 512 pieces; where there are few rows more threads read one sooner.
+  if (pieces <= 64 * kHeld && (rows >= 1024 || pieces <= 64)) quantize<T, 64>(s, x, q, rows, cols);
+  else if (pieces <= 256 * kHeld) quantize<T, 256>(s, x, q, rows, cols);
+  else quantize<T, 1024>(s, x, q, rows, cols);
+  return hipGetLastError();
 }
 
-unsigned row_grid(int64_t rows) { return static_cast<unsigned>(rows < (1 << 20) ? rows : (1 << 20)); }
+template <typename T>
+hipError_t dequantize(hipStream_t s, const Bytes& q, const Values& out, int64_t rows, int cols) {
+  const int pieces = (cols + 15) / 16;
+  int per = 1;  // threads of a row: a power of two
+  while (per < 256 && per < pieces) per *= 2;
+  const int64_t each = 256 / per;
+  dequantize_kernel<T><<<static_cast<unsigned>((rows + each - 1) / each), 256, 0, s>>>(
+      q.p, q.ld, q.scale, reinterpret_cast<T*>(out.p), out.ld, rows, cols, per);
+  return hipGetLastError();
+}
 
 }  // namespace
 
 hipError_t launch_quantize_rows(hipStream_t s, Values x, Bytes q, int64_t rows, int cols) {
   if (rows == 0) return hipSuccess;
-  if (x.bf16)
-    quantize_kernel<bf16_t><<<row_grid(rows), kThreads, 0, s>>>(reinterpret_cast<const bf16_t*>(x.p), x.ld, q.p, q.ld, q.scale, rows, cols);
-  else
-    quantize_kernel<float><<<row_grid(rows), kThreads, 0, s>>>(reinterpret_cast<const float*>(x.p), x.ld, q.p, q.ld, q.scale, rows, cols);
-  return hipGetLastError();
+  return x.bf16 ? quantize<bf16_t>(s, x, q, rows, cols) : quantize<float>(s, x, q, rows, cols);
 }
 
 hipError_t launch_dequantize_rows(hipStream_t s, Bytes q, Values out, int64_t rows, int cols) {
   if (rows == 0) return hipSuccess;
-  if (out.bf16)
-    dequantize_kernel<bf16_t><<<row_grid(rows), kThreads, 0, s>>>(q.p, q.ld, q.scale, reinterpret_cast<bf16_t*>(out.p), out.ld, rows, cols);
-  else
-    dequantize_kernel<float><<<row_grid(rows), kThreads, 0, s>>>(q.p, q.ld, q.scale, reinterpret_cast<float*>(out.p), out.ld, rows, cols);
-  return hipGetLastError();
+  return out.bf16 ? dequantize<bf16_t>(s, q, out, rows, cols) : dequantize<float>(s, q, out, rows, cols);
 }

@@ -1,0 +1,130 @@
+// Rounding of values to 8 bits (device functions).
+//
+// Mathematics.  s = max |x| / 127 in binary32; q is the integer nearest to the
+// exact x / s, ties to even.  x / s is estimated as x (1 / s): with two
+// roundings of 2^-24 and |q| <= 127 the estimate is off by less than 2^-15.9, so
+// only where it lies that close to a half does the remainder x - q s decide,
+// which one fused multiply-add forms exactly (|x - q s| <= s, and both are
+// multiples of the smaller's last place).
+#pragma once
+
+#include "muon_device.h"
+
+namespace muon {
+
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef u32x4 u32x4_any __attribute__((aligned(2)));  // 16 bytes at any element's address
+
+constexpr float kMostScale = 0x1.020406p+121f;  // 127 times the next larger number overflows
+
+// The scale of a row whose largest magnitude has the bits `top` (NaN and
+// infinity have the largest bits): NaN where something is not finite.
+__device__ __forceinline__ float row_scale(uint32_t top) {
+  if (top >= 0x7f800000u) return __uint_as_float(0x7fc00000u);
+  return fminf(__uint_as_float(top) / 127.0f, kMostScale);
+}
+
+// x / s to the nearest integer, ties to even, of an estimate.
+__device__ __forceinline__ float nearest_exact(float x, float s, float estimate) {
+  float q = rintf(estimate);
+  const float r = __builtin_fmaf(-q, s, x);  // exact
+  const float over = 2.0f * fabsf(r);
+  if (over >= s) {
+    // at or past the half: the neighbour on r's side, or of two the even one
+    const float next = q + copysignf(1.0f, r);
+    const bool odd = (static_cast<int>(q) & 1) != 0;
+    if (over > s || odd) q = next;
+  }
+  return fminf(fmaxf(q, -127.0f), 127.0f);
+}
+
+// How a row of scale s is rounded.
+struct RowRounding {
+  float lift;    // 1, or 2^64 for scales whose inverse overflows (an exact product)
+  float s, inv;  // lift s, and its inverse; 0 where every byte is 0 (s is 0 or NaN)
+  __device__ __forceinline__ explicit RowRounding(float scale) {
+    lift = scale < 1.2e-38f ? 0x1p64f : 1.0f;
+    s = scale * lift;
+    inv = s > 0.0f ? 1.0f / s : 0.0f;
+  }
+};
+
+// N values (a multiple of 4) of a row as bytes.
+template <int N>
+__device__ __forceinline__ void to_bytes(float (&x)[N], const RowRounding& row, uint32_t (&w)[N / 4]) {
+  int q[N];
+  float far = 0.0f;
+  if (row.lift != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] *= row.lift;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float e = x[i] * row.inv, n = rintf(e);
+    far = fmaxf(far, fabsf(e - n));
+    q[i] = static_cast<int>(n);
+  }
+  if (far > 0.5f - 0x1p-15f) {
+    asm volatile("" : "+v"(q[0]));  // stays a branch
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = static_cast<int>(nearest_exact(x[i], row.s, x[i] * row.inv));
+  }
+  if (row.inv == 0.0f) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) q[i] = 0;
+  }
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i)
+    w[i] = static_cast<uint32_t>(q[4 * i] & 255) | static_cast<uint32_t>(q[4 * i + 1] & 255) << 8 |
+           static_cast<uint32_t>(q[4 * i + 2] & 255) << 16 | static_cast<uint32_t>(q[4 * i + 3]) << 24;
+}
+
+// 16 bytes as values, and the largest magnitude's bits among them.
+template <typename T> struct Piece;
+template <> struct Piece<bf16_t> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void values(u32x4 w, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Piece<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void values(u32x4 w, float (&v)[N]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
+  }
+};
+template <typename T> __device__ __forceinline__ uint32_t piece_top(u32x4 w, uint32_t top) {
+  float v[Piece<T>::N];
+  Piece<T>::values(w, v);
+#pragma unroll
+  for (int i = 0; i < Piece<T>::N; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  return top;
+}
+// Piece p of a row of `cols` values, zeros behind its end.
+template <typename T> __device__ __forceinline__ u32x4 load_piece(const T* row, int p, int cols) {
+  constexpr int N = Piece<T>::N;
+  const T* at = row + p * N;
+  if ((p + 1) * N <= cols) return *reinterpret_cast<const u32x4_any*>(at);
+  u32x4 w = {0, 0, 0, 0};
+  if constexpr (N == 8) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (p * N + i < cols) w[i / 2] |= static_cast<uint32_t>(at[i]) << (16 * (i & 1));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (p * N + i < cols) w[i] = __float_as_uint(at[i]);
+  }
+  return w;
+}
+__device__ __forceinline__ uint32_t wave_top(uint32_t top) {
+  for (int d = 32; d > 0; d /= 2) top = max(top, static_cast<uint32_t>(__shfl_xor(static_cast<int>(top), d)));
+  return top;
+}
+
+}  // namespace muon
