@@ -12,6 +12,7 @@ namespace {
 // tiles on the matrix cores
 // ---------------------------------------------------------------------------
 typedef u32x4_t u32x4_any __attribute__((aligned(2)));
+typedef u32x4_t u32x4_bytes __attribute__((aligned(1)));
 
 constexpr int kC = 64;  // of the contraction in a stage
 
@@ -31,6 +32,30 @@ __device__ __forceinline__ bf16x8_t km_frag(const char* t, int cb, int kk, int l
   const u32x2_t lo = __builtin_bit_cast(u32x2_t, ld_tr16(t + km_off<R>(k, col)));
   const u32x2_t hi = __builtin_bit_cast(u32x2_t, ld_tr16(t + km_off<R>(k + 4, col)));
   return __builtin_bit_cast(bf16x8_t, u32x4_t{lo.x, lo.y, hi.x, hi.y});
+}
+
+// w shifted right by `bits` (a multiple of 8 below 128): the bytes behind become zeros.
+__device__ __forceinline__ u32x4_t shift_right(u32x4_t w, int bits) {
+  uint64_t lo = static_cast<uint64_t>(w[1]) << 32 | w[0], hi = static_cast<uint64_t>(w[3]) << 32 | w[2];
+  if (bits & 64) lo = hi, hi = 0;
+  const int s = bits & 63;
+  lo = lo >> s | (hi << 1) << (63 - s);
+  hi >>= s;
+  return u32x4_t{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
+}
+// The first `left` bytes from `at` on, fewer than 16, zeros behind them: read
+// with what lies in front of them where a row has `before` bytes there, else one
+// by one.
+template <typename V>
+__device__ __forceinline__ u32x4_t row_end(const char* at, int left, int64_t before) {
+  if (before >= 16 - left) return shift_right(*reinterpret_cast<const V*>(at - (16 - left)), 8 * (16 - left));
+  uint64_t lo = 0, hi = 0;
+#pragma unroll 1
+  for (int i = left - 1; i >= 0; --i) {
+    hi = hi << 8 | lo >> 56;
+    lo = lo << 8 | static_cast<uint8_t>(at[i]);
+  }
+  return u32x4_t{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
 }
 
 // 16 bytes of y through registers: TM rows of the output by 64 of the
@@ -64,14 +89,7 @@ struct YStage {
       v[q] = u32x4_t{0, 0, 0, 0};
       if (q * STEP >= rows || left <= 0) continue;
       const char* at = base + q * step + off;
-      if (left >= 8) {
-        v[q] = *reinterpret_cast<const u32x4_any*>(at);
-      } else {
-        const bf16_t* h = reinterpret_cast<const bf16_t*>(at);
-#pragma unroll
-        for (int i = 0; i < 7; ++i)
-          if (i < left) v[q][i / 2] |= static_cast<uint32_t>(h[i]) << (16 * (i & 1));
-      }
+      v[q] = left >= 8 ? *reinterpret_cast<const u32x4_any*>(at) : row_end<u32x4_any>(at, 2 * left, 2 * k0 + 16 * chunk);
     }
   }
   // lds: from address()
@@ -120,15 +138,10 @@ struct QStage {
       s[q] = scale[row + q * STEP];
       if (left <= 0) continue;
       const char* at = base + q * step + off;
-      // (rows lie 16 bytes apart at least, so only the last one's end may be the memory's)
-      if (left >= 16 || (q * STEP + 1 < rows && a.q.ld != 0)) {
-        v[q] = *reinterpret_cast<const u32x4_t*>(at);
-      } else {
-        const uint8_t* b = reinterpret_cast<const uint8_t*>(at);
-#pragma unroll
-        for (int i = 0; i < 15; ++i)
-          if (i < left) v[q][i / 4] |= static_cast<uint32_t>(b[i]) << (8 * (i & 3));
-      }
+      // (rows lie 16 bytes apart at least, so only the last one's end may be the
+      // memory's; what lies behind a row's end meets no output)
+      const bool whole = left >= 16 || (q * STEP + 1 < rows && a.q.ld != 0);
+      v[q] = whole ? *reinterpret_cast<const u32x4_t*>(at) : row_end<u32x4_bytes>(at, left, n0 + 16 * chunk);
     }
   }
   __device__ __forceinline__ int address() const { return km_off<TN>(row, 16 * chunk); }
@@ -167,10 +180,10 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, T
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / NWN, wn = wave % NWN;
   const int G = static_cast<int>(gridDim.x), hw = static_cast<int>(blockIdx.x);
-  const int64_t first = G % 8 == 0 ? static_cast<int64_t>(hw % 8) * (G / 8) + hw / 8 : hw;
-  for (int64_t l = first; l < work.units; l += G) {
+  const int first = G % 8 == 0 ? (hw % 8) * (G / 8) + hw / 8 : hw;
+  for (int l = first; l < work.units; l += G) {
     const TileUnit unit = tile_unit(work, l);
-    const int64_t m0 = unit.ti * TM, n0 = unit.tj * TN, past = min(a.c, static_cast<int64_t>(unit.past) * kC);
+    const int64_t m0 = static_cast<int64_t>(unit.ti) * TM, n0 = static_cast<int64_t>(unit.tj) * TN, past = min(a.c, static_cast<int64_t>(unit.past) * kC);
     const bool inside_m = m0 + TM <= a.m, inside_n = n0 + TN <= a.n;
 
     f32x16_t acc[FM][FN];
@@ -231,9 +244,17 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, T
         __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
       });
     };
-    auto stage = [&](auto S, int kt) __attribute__((always_inline)) {
-      char* cur = st + decltype(S)::value * STAGE;
-      char* nxt = st + (1 - decltype(S)::value) * STAGE;
+    static_assert((STAGE & (STAGE - 1)) == 0, "stages alternate by one bit of the address");
+    load(unit.first);
+    static_for<3>([&](auto P) { store_part(st, decltype(P)::value); });
+    load(unit.first + 1);
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    frags(st, 0, ic<0>{});
+    uint32_t at = 0;  // the stage's buffer
+#pragma unroll 1
+    for (int kt = unit.first; kt < unit.past; ++kt, at ^= STAGE) {
+      char* cur = st + at;
+      char* nxt = st + (at ^ STAGE);
       static_for<KK>([&](auto KI) {
         constexpr int kk = decltype(KI)::value;
         constexpr int b = kk & 1;
@@ -256,14 +277,7 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, T
           __builtin_amdgcn_sched_barrier(0);
         }
       });
-    };
-    load(unit.first);
-    static_for<3>([&](auto P) { store_part(st, decltype(P)::value); });
-    load(unit.first + 1);
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    frags(st, 0, ic<0>{});
-    // whole rounds of two stages: past the end they hold zeros
-    for (int kt = unit.first; kt < unit.past; kt += 2) static_for<2>([&](auto S) { stage(S, kt + decltype(S)::value); });
+    }
 
     // ---- epilogue: fp32 sums through LDS, row-contiguous stores
     int el = lane;
@@ -273,10 +287,10 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, T
     constexpr int ROUNDS = TM * TN * 4 > 2 * STAGE ? 2 : 1, RR = TM / ROUNDS;
     static_assert(RR * TN * 4 <= 2 * STAGE, "output rows fit the stage buffers");
     O* out = reinterpret_cast<O*>(a.out.p);
-    float* part = reinterpret_cast<float*>(work.parts) + unit.slot * (TM * TN);
-    const bool wide = ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(a.out.ld * E)) & 15u) == 0;
-    static_for<ROUNDS>([&](auto R) {
-      constexpr int rd = decltype(R)::value;
+    float* part = reinterpret_cast<float*>(work.parts) + static_cast<int64_t>(unit.slot) * (TM * TN);
+    const int et = wave * 64 + el;
+#pragma unroll 1
+    for (int rd = 0; rd < ROUNDS; ++rd) {
       if (ROUNDS == 1 || wm == rd) {
         static_for<FM>([&](auto MI) {
           constexpr int mi = decltype(MI)::value;
@@ -292,50 +306,55 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, T
         });
       }
       __syncthreads();
-      const int et = wave * 64 + el;
       if (unit.slot >= 0) {
-#pragma unroll 4
-        for (int it = 0; it < RR * TN / 4 / NT; ++it) {
-          const int e = et + it * NT, row = e / (TN / 4), c = 4 * (e % (TN / 4));
+#pragma unroll 2
+        for (int e = et; e < RR * TN / 4; e += NT) {
+          const int row = e / (TN / 4), c = 4 * (e % (TN / 4));
           *reinterpret_cast<float4*>(part + (rd * RR + row) * TN + c) = *reinterpret_cast<const float4*>(st + of_off<TN>(row, c));
         }
-        __syncthreads();
-        return;
-      }
-      constexpr int C = 16 / E, CH = TN / C;
+      } else {
+        constexpr int C = 16 / E, CH = TN / C;
 #pragma unroll 2
-      for (int it = 0; it < RR * CH / NT; ++it) {
-        const int e = et + it * NT, row = e / CH, c = C * (e % CH);
-        const int64_t m = m0 + rd * RR + row, n = n0 + c;
-        if (m >= a.m || n >= a.n) continue;
-        float v[C];
+        for (int e = et; e < RR * CH; e += NT) {
+          const int row = e / CH, c = C * (e % CH);
+          const int64_t m = m0 + rd * RR + row, n = n0 + c;
+          if (m >= a.m || n >= a.n) continue;
+          float v[C];
 #pragma unroll
-        for (int q = 0; q < C; q += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(st + of_off<TN>(row, c + q));
-          v[q] = f.x, v[q + 1] = f.y, v[q + 2] = f.z, v[q + 3] = f.w;
-        }
-        O* to = out + m * a.out.ld + n;
-        if (wide && n + C <= a.n) {
-          u32x4_t w4;
-          if (a.accumulate) {
-            w4 = *reinterpret_cast<const u32x4_t*>(to);
-#pragma unroll
-            for (int q = 0; q < C; ++q) v[q] += muon::Elem<O>::load(reinterpret_cast<const O*>(&w4) + q);
+          for (int q = 0; q < C; q += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(st + of_off<TN>(row, c + q));
+            v[q] = f.x, v[q + 1] = f.y, v[q + 2] = f.z, v[q + 3] = f.w;
           }
+          O* to = out + m * a.out.ld + n;
+          if (n + C <= a.n) {
+            u32x4_t w4;
+            if (a.accumulate) {
+              w4 = *reinterpret_cast<const u32x4_any*>(to);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            if constexpr (E == 2) w4[q] = muon::pack_bf16x2(v[2 * q], v[2 * q + 1]);
-            else w4[q] = __float_as_uint(v[q]);
+              for (int q = 0; q < 4; ++q) {
+                if constexpr (E == 2) {
+                  v[2 * q] += __uint_as_float(w4[q] << 16);
+                  v[2 * q + 1] += __uint_as_float(w4[q] & 0xffff0000u);
+                } else {
+                  v[q] += __uint_as_float(w4[q]);
+                }
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if constexpr (E == 2) w4[q] = muon::pack_bf16x2(v[2 * q], v[2 * q + 1]);
+              else w4[q] = __float_as_uint(v[q]);
+            }
+            *reinterpret_cast<u32x4_any*>(to) = w4;
+          } else {
+#pragma unroll
+            for (int q = 0; q < C - 1; ++q)
+              if (n + q < a.n) muon::Elem<O>::store(to + q, a.accumulate ? muon::Elem<O>::load(to + q) + v[q] : v[q]);
           }
-          __builtin_nontemporal_store(w4, reinterpret_cast<u32x4_t*>(to));
-        } else {
-#pragma unroll
-          for (int q = 0; q < C; ++q)
-            if (n + q < a.n) muon::Elem<O>::store(to + q, a.accumulate ? muon::Elem<O>::load(to + q) + v[q] : v[q]);
         }
       }
       __syncthreads();
-    });
+    }
   }
 }
 
@@ -343,11 +362,11 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, T
 template <typename O, int TM, int TN>
 __global__ __launch_bounds__(256) void grad8_join_kernel(Grad8Args a, TileWork work) {
   constexpr int PER = TM * TN / 1024;  // workgroups of a tile
-  const int64_t t = blockIdx.x / PER;
+  const int t = static_cast<int>(blockIdx.x / PER);
   const int e = static_cast<int>(blockIdx.x % PER) * 256 + static_cast<int>(threadIdx.x), row = e / (TN / 4), c = 4 * (e % (TN / 4));
   const TileUnit unit = tile_unit(work, work.whole + t);
-  const float* part = reinterpret_cast<const float*>(work.parts) + t * work.splits * (TM * TN) + row * TN + c;
-  const int64_t m = unit.ti * TM + row, n = unit.tj * TN + c;
+  const float* part = reinterpret_cast<const float*>(work.parts) + static_cast<int64_t>(t) * work.splits * (TM * TN) + row * TN + c;
+  const int64_t m = static_cast<int64_t>(unit.ti) * TM + row, n = static_cast<int64_t>(unit.tj) * TN + c;
   if (m >= a.m || n >= a.n) return;
   float4 v = *reinterpret_cast<const float4*>(part);
   for (int p = 1; p < work.splits; ++p) {
@@ -368,7 +387,7 @@ hipError_t go_tiles(hipStream_t s, const Grad8Args& a, const TilePlan& p) {
   if (a.of_columns) grad8_tile_kernel<O, TM, TN, NWN, PARTS, true><<<grid, 128 * NWN, 0, s>>>(a, w);
   else grad8_tile_kernel<O, TM, TN, NWN, PARTS, false><<<grid, 128 * NWN, 0, s>>>(a, w);
   if (p.splits > 1) {
-    const int64_t cut = static_cast<int64_t>(p.tm) * p.tn - p.whole;
+    const int64_t cut = p.tm * p.tn - p.whole;
     grad8_join_kernel<O, TM, TN><<<static_cast<unsigned>(cut * (TM * TN / 1024)), 256, 0, s>>>(a, w);
   }
   return hipGetLastError();
@@ -379,11 +398,7 @@ hipError_t go_tiles(hipStream_t s, const Grad8Args& a, const TilePlan& p) {
 hipError_t launch_grad8(hipStream_t s, const Grad8Args& a) {
   if (a.m == 0 || a.n == 0) return hipSuccess;
   const int stages = static_cast<int>((a.c + kC - 1) / kC), parts = a.out.bf16 ? 1 : 2;
-  // (two small tiles on a CU take 0.6 of a large one's time for half its products)
-  double large, small;
-  const TilePlan l = plan_tiles(a.m, a.n, 256, 256 / parts, stages, a.cus, a.ws_bytes, &large);
-  const TilePlan q = plan_tiles(a.m, a.n, 128, 128 / parts, stages, 2 * a.cus, a.ws_bytes, &small);
-  const bool big = large <= 0.6 * small;
-  if (a.out.bf16) return big ? go_tiles<bf16_t, 256, 256, 4, 1>(s, a, l) : go_tiles<bf16_t, 128, 128, 2, 1>(s, a, q);
-  return big ? go_tiles<float, 256, 128, 4, 2>(s, a, l) : go_tiles<float, 128, 64, 2, 2>(s, a, q);
+  const TilePlan p = plan_product(a.m, a.n, parts, stages, a.cus, a.ws_bytes);
+  if (a.out.bf16) return p.large ? go_tiles<bf16_t, 256, 256, 4, 1>(s, a, p) : go_tiles<bf16_t, 128, 128, 2, 1>(s, a, p);
+  return p.large ? go_tiles<float, 256, 128, 4, 2>(s, a, p) : go_tiles<float, 128, 64, 2, 2>(s, a, p);
 }

@@ -10,8 +10,9 @@ namespace {
 
 // A tile's 256 rows lie within 2 GiB (offsets of its loads): strides up to 2^22.
 constexpr int64_t kMostStride = int64_t{1} << 22;
-constexpr int64_t kMostOut = int64_t{1} << 39;  // elements of a product
+constexpr int64_t kMostTiles = int64_t{1} << 26;  // of 128 x 64 outputs: units of work and their workgroups are counted in 32 bits
 
+inline int64_t tiles(int64_t rows, int64_t cols) { return ((rows + 127) / 128) * ((cols + 63) / 64); }
 inline int64_t up16(int64_t n) { return (n + 15) & ~int64_t{15}; }
 
 // Rows of values; bytes receives their extent.
@@ -100,7 +101,7 @@ muon_status_t grad8(muon_ctx* c, void* stream, const muon_rows_t* y, const muon_
   const int64_t m = of_columns ? y->cols : y->rows, contraction = of_columns ? y->rows : y->cols;
   if (contraction != q->rows || out->rows != m || out->cols != q->cols)
     return fail(c, MUON_ESHAPE, "the gradient's shapes do not match");
-  if (m * q->cols > kMostOut) return fail(c, MUON_ESHAPE, "too many elements");
+  if (tiles(m, q->cols) > kMostTiles) return fail(c, MUON_ESHAPE, "too many elements");
   Span spans[4];
   spans[0] = span(*y, yb, false);
   spans[1] = span(*out, ob, true);
@@ -175,7 +176,7 @@ muon_status_t muon_matmul8(muon_ctx_t* c, void* stream, const muon_rows8_t* a, c
   if (st != MUON_OK) return st;
   if (a->cols != b->cols || out->rows != a->rows || out->cols != b->rows)
     return fail(c, MUON_ESHAPE, "the product's shapes do not match");
-  if (out->rows * out->cols > kMostOut) return fail(c, MUON_ESHAPE, "too many elements");
+  if (tiles(out->rows, out->cols) > kMostTiles) return fail(c, MUON_ESHAPE, "too many elements");
   Span spans[5];
   spans[0] = span(*out, ob, true);
   spans8(spans + 1, *a, ab, false);
@@ -201,7 +202,7 @@ muon_status_t muon_linear8(muon_ctx_t* c, void* stream, const muon_rows_t* x, co
   if (x->cols != w->cols || out->rows != x->rows || out->cols != w->rows)
     return fail(c, MUON_ESHAPE, "the product's shapes do not match");
   if (x8 && (x8->rows != x->rows || x8->cols != x->cols)) return fail(c, MUON_ESHAPE, "values and 8-bit rows differ in shape");
-  if (out->rows * out->cols > kMostOut) return fail(c, MUON_ESHAPE, "too many elements");
+  if (tiles(out->rows, out->cols) > kMostTiles) return fail(c, MUON_ESHAPE, "too many elements");
   Span spans[6] = {};
   spans[0] = span(*out, ob, true);
   spans[1] = span(*x, xb, false);

@@ -12,6 +12,7 @@
 
 namespace {
 
+using muon::u32x4_any;
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x16_t __attribute__((ext_vector_type(16)));
 
@@ -19,14 +20,28 @@ typedef int i32x16_t __attribute__((ext_vector_type(16)));
 // few tokens: the weights stream through registers
 // ---------------------------------------------------------------------------
 
-// 16 bytes of a row from k on, zeros at and behind its end.
+// 16 bytes of a row from k on, zeros at and behind its end: read with what lies
+// in front of them where the row has that, else one by one.
+typedef i32x4_t i32x4_bytes __attribute__((aligned(1)));
 __device__ __forceinline__ i32x4_t row_tail(const int8_t* row, int k, int end) {
   if (k + 16 <= end) return *reinterpret_cast<const i32x4_t*>(row + k);
-  i32x4_t v = {0, 0, 0, 0};
-#pragma unroll
-  for (int i = 0; i < 15; ++i)
-    if (k + i < end) v[i / 4] |= static_cast<int>(static_cast<uint32_t>(static_cast<uint8_t>(row[k + i])) << (8 * (i & 3)));
-  return v;
+  uint64_t lo = 0, hi = 0;
+  if (k < end && end >= 16) {
+    const i32x4_t w = *reinterpret_cast<const i32x4_bytes*>(row + end - 16);
+    lo = static_cast<uint64_t>(static_cast<uint32_t>(w[1])) << 32 | static_cast<uint32_t>(w[0]);
+    hi = static_cast<uint64_t>(static_cast<uint32_t>(w[3])) << 32 | static_cast<uint32_t>(w[2]);
+    const int bits = 8 * (k + 16 - end), s = bits & 63;
+    if (bits & 64) lo = hi, hi = 0;
+    lo = lo >> s | (hi << 1) << (63 - s);
+    hi >>= s;
+  } else {
+#pragma unroll 1
+    for (int i = end - 1; i >= k; --i) {
+      hi = hi << 8 | lo >> 56;
+      lo = lo << 8 | static_cast<uint8_t>(row[i]);
+    }
+  }
+  return i32x4_t{static_cast<int>(lo), static_cast<int>(lo >> 32), static_cast<int>(hi), static_cast<int>(hi >> 32)};
 }
 
 // Up to 16 MG rows of a by 16 NB columns (rows of b) at a time; a workgroup's KS
@@ -64,37 +79,61 @@ __global__ __launch_bounds__(64 * KS) void matmul8_stream_kernel(Matmul8Args a) 
       }
       if (static_cast<int>(threadIdx.x) < m) xscale[threadIdx.x] = a.a.scale[threadIdx.x];
     } else {
-      constexpr int N = muon::Piece<FROM>::N, P = 16 / N;
-      for (int i = wave; i < m; i += KS) {
+      // a thread holds its chunks between the rows' maxima and their rounding
+      constexpr int N = muon::Piece<FROM>::N, P = 16 / N, Q = XB / 16 / (64 * KS);
+      __shared__ uint32_t tops[16 * MG];
+      u32x4_t held[Q][P];
+      if (static_cast<int>(threadIdx.x) < m) tops[threadIdx.x] = 0;
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int e = static_cast<int>(threadIdx.x) + q * 64 * KS, i = e / chunks, c = e % chunks;
+        if (i >= m) continue;
         const FROM* row = reinterpret_cast<const FROM*>(a.x.p) + i * a.x.ld;
-        uint32_t top = 0;
-        for (int p = lane; p * N < a.k; p += 64) top = muon::piece_top<FROM>(muon::load_piece(row, p, a.k), top);
-        const float s = muon::row_scale(muon::wave_top(top));
-        const muon::RowRounding rounding(s);
-        if (lane == 0) xscale[i] = s;
-        for (int c = lane; c < chunks; c += 64) {
-          u32x4_t w = {0, 0, 0, 0};
 #pragma unroll
-          for (int q = 0; q < P; ++q) {
-            if ((P * c + q) * N >= a.k) continue;
-            float v[N];
-            uint32_t b[N / 4];
-            muon::Piece<FROM>::values(muon::load_piece(row, P * c + q, a.k), v);
-            muon::to_bytes(v, rounding, b);
-#pragma unroll
-            for (int j = 0; j < N / 4; ++j) w[q * (N / 4) + j] = b[j];
-          }
-          *reinterpret_cast<u32x4_t*>(xs + (c * m + i) * 16) = w;
-          if (blockIdx.x == 0 && a.a.p) {  // kept for the backward pass
-            int8_t* to = a.a.p + i * a.a.ld + 16 * c;
-            if (16 * c + 16 <= a.k) {
-              *reinterpret_cast<u32x4_t*>(to) = w;
-            } else {
-              for (int j = 0; 16 * c + j < a.k; ++j) to[j] = static_cast<int8_t>(w[j / 4] >> (8 * (j & 3)));
-            }
-          }
+        for (int p = 0; p < P; ++p) {
+          held[q][p] = u32x4_t{0, 0, 0, 0};
+          if ((P * c + p) * N < a.k) held[q][p] = muon::load_piece(row, P * c + p, a.k);
         }
-        if (blockIdx.x == 0 && a.a.p && lane == 0) a.a.scale[i] = s;
+      }
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int i = (static_cast<int>(threadIdx.x) + q * 64 * KS) / chunks;
+        if (i >= m) continue;
+        uint32_t top = 0;
+#pragma unroll
+        for (int p = 0; p < P; ++p) top = muon::piece_top<FROM>(held[q][p], top);
+        atomicMax(&tops[i], top);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        const int e = static_cast<int>(threadIdx.x) + q * 64 * KS, i = e / chunks, c = e % chunks;
+        if (i >= m) continue;
+        const float s = muon::row_scale(tops[i]);
+        const muon::RowRounding rounding(s);
+        u32x4_t w;
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          float v[N];
+          uint32_t b[N / 4];
+          muon::Piece<FROM>::values(held[q][p], v);
+          muon::to_bytes(v, rounding, b);
+#pragma unroll
+          for (int j = 0; j < N / 4; ++j) w[p * (N / 4) + j] = b[j];
+        }
+        *reinterpret_cast<u32x4_t*>(xs + (c * m + i) * 16) = w;
+        if (c == 0) xscale[i] = s;
+        if (blockIdx.x == 0 && a.a.p) {  // kept for the backward pass
+          int8_t* to = a.a.p + i * a.a.ld + 16 * c;
+          if (16 * c + 16 <= a.k) {
+            *reinterpret_cast<u32x4_t*>(to) = w;
+          } else {
+#pragma unroll 1
+            for (int j = 0; 16 * c + j < a.k; ++j) to[j] = static_cast<int8_t>(w[j / 4] >> (8 * (j & 3)));
+          }
+          if (c == 0) a.a.scale[i] = s;
+        }
       }
     }
     __syncthreads();
@@ -200,8 +239,11 @@ inline int64_t staged_bytes(const Matmul8Args& a) { return a.m * ((a.k + 63) / 6
 template <typename O, typename FROM, int MG>
 hipError_t go_staged(hipStream_t s, const Matmul8Args& a) {
   if (staged_bytes(a) <= kStagedSmall) return go_staged<O, FROM, MG, 4, kStagedSmall>(s, a);
-  if (staged_bytes(a) <= kStagedMost) return go_staged<O, FROM, MG, 4, kStagedMost>(s, a);
-  return go_staged<O, FROM, MG, 16, kStagedWide>(s, a);
+  if constexpr (std::is_same_v<FROM, Staged>) {
+    if (staged_bytes(a) <= kStagedMost) return go_staged<O, FROM, MG, 4, kStagedMost>(s, a);
+    return go_staged<O, FROM, MG, 16, kStagedWide>(s, a);
+  }
+  return hipErrorInvalidValue;
 }
 template <typename O, int NB, int MG>
 hipError_t go_stream(hipStream_t s, const Matmul8Args& a) {
@@ -220,12 +262,15 @@ hipError_t go_stream(hipStream_t s, const Matmul8Args& a) {
 template <typename O, int MG>
 hipError_t go_stream(hipStream_t s, const Matmul8Args& a) {
   if constexpr (MG <= 2) {
-    if (staged_bytes(a) <= kStagedWide) return go_staged<O, Staged, MG>(s, a);
+    // (staged rows serve a workgroup's columns one after another: not where there are few)
+    if (staged_bytes(a) <= kStagedWide && a.n >= 16 * a.cus) return go_staged<O, Staged, MG>(s, a);
   }
-  // as many columns a workgroup as leave eight workgroups to a CU
-  return a.n >= int64_t{64} * 8 * a.cus ? go_stream<O, 4, MG>(s, a) : go_stream<O, 1, MG>(s, a);
+  return go_stream<O, 1, MG>(s, a);
 }
-constexpr int kMostStreamed = 64;
+// Up to here rows stream the weights, beyond tiles do: 9728 columns of 2560 for
+// 32 and 64 rows 13 and 21 us against 18, 4096 columns 7 and 10 against 16; 151936
+// columns 88 for 16 rows and 126 for 32 against 105.
+inline bool streams(const Matmul8Args& a) { return a.m <= 16 || (a.m <= 64 && a.n * a.m <= int64_t{1} << 19); }
 template <typename O>
 hipError_t go_stream(hipStream_t s, const Matmul8Args& a) {
   return a.m <= 16 ? go_stream<O, 1>(s, a) : a.m <= 32 ? go_stream<O, 2>(s, a) : go_stream<O, 4>(s, a);
@@ -265,32 +310,29 @@ struct Stage8 {
         rsrc, static_cast<uint32_t>(k0), [&](int q) { return lds + (wave + NW * q) * 1024; },
         [&](int q) { return (full || k0 + kc[q] < lim[q]) ? base[q] : kOOB; });
   }
-  // The chunk of 16 bytes that holds k, not whole: zeros behind k (what a row's
-  // memory holds there meets nothing), and in the last row all of it.
-  static __device__ __forceinline__ void finish(char* lds, const Bytes& x, int64_t rows, int k, int64_t row0, int k0, int tid) {
-    if (tid >= T) return;
-    const int64_t r = row0 + tid;
-    if (r >= rows) return;
-    char* at = lds + rt_off<64>(tid, ((k - 1) - k0) >> 4);
-    const int n = k & 15;
-    uint32_t w[4];
-    if (r == rows - 1 || x.ld == 0) {
-      const uint8_t* from = reinterpret_cast<const uint8_t*>(x.p) + r * x.ld + (k & ~15);
-      for (int i = 0; i < 4; ++i) {
-        w[i] = 0;
-        for (int j = 0; j < 4; ++j)
-          if (4 * i + j < n) w[i] |= static_cast<uint32_t>(from[4 * i + j]) << (8 * j);
-      }
-    } else {
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at);
-      for (int i = 0; i < 4; ++i) {
-        const int keep = n - 4 * i;
-        w[i] = keep >= 4 ? v[i] : keep <= 0 ? 0u : v[i] & ((1u << (8 * keep)) - 1u);
-      }
-    }
-    *reinterpret_cast<u32x4_t*>(at) = u32x4_t{w[0], w[1], w[2], w[3]};
-  }
 };
+
+// The chunk of 16 bytes that holds k, not whole, of T rows in LDS: zeros behind k
+// (what a row's memory holds there meets nothing), and in the last row, which
+// was not brought, all of it.
+template <int T>
+__device__ __forceinline__ void finish_rows(char* lds, const Bytes& x, int64_t rows, int k, int64_t row0, int k0, int tid) {
+  const int64_t r = row0 + tid;
+  if (tid >= T || r >= rows) return;
+  char* at = lds + rt_off<64>(tid, ((k - 1) - k0) >> 4);
+  const int n = k & 15;
+  if (r == rows - 1 || x.ld == 0) {
+    *reinterpret_cast<i32x4_t*>(at) = row_tail(x.p + r * x.ld, k & ~15, k);
+    return;
+  }
+  u32x4_t v = *reinterpret_cast<const u32x4_t*>(at);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int keep = n - 4 * i;
+    v[i] = keep >= 4 ? v[i] : keep <= 0 ? 0u : v[i] & ((1u << (8 * keep)) - 1u);
+  }
+  *reinterpret_cast<u32x4_t*>(at) = v;
+}
 
 // ---- staged output tile, fp32 or bf16, in two halves of T / 2 rows: element (r, c) of a
 // half; 16-byte chunks swizzled by the row.
@@ -307,19 +349,18 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
   constexpr int NWN = T == 256 ? 4 : 2, NW = 2 * NWN, NT = 64 * NW;
   constexpr int WM = T / 2, WN = T / NWN, FM = WM / 32, FN = WN / 32;
   constexpr int HALF = T * kBytes, STAGE = 2 * HALF;
-  __shared__ __attribute__((aligned(1024))) char st0[STAGE];
-  __shared__ __attribute__((aligned(1024))) char st1[STAGE];
-  auto buf = [&](auto I) -> char* { return decltype(I)::value % 2 ? st1 : st0; };
+  static_assert((STAGE & (STAGE - 1)) == 0, "stages alternate by one bit of the address");
+  __shared__ __attribute__((aligned(1024))) char st[2 * STAGE];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / NWN, wn = wave % NWN;
 
   const int G = static_cast<int>(gridDim.x), hw = static_cast<int>(blockIdx.x);
-  const int64_t first = G % 8 == 0 ? static_cast<int64_t>(hw % 8) * (G / 8) + hw / 8 : hw;
-  for (int64_t l = first; l < work.units; l += G) {
+  const int first = G % 8 == 0 ? (hw % 8) * (G / 8) + hw / 8 : hw;
+  for (int l = first; l < work.units; l += G) {
     const TileUnit unit = tile_unit(work, l);
-    const int64_t m0 = unit.ti * T, n0 = unit.tj * T;
+    const int64_t m0 = static_cast<int64_t>(unit.ti) * T, n0 = static_cast<int64_t>(unit.tj) * T;
 
     i32x16_t acc[FM][FN];
 #pragma unroll
@@ -363,17 +404,26 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
         if constexpr (decltype(I)::value < NRD) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       });
     };
-    // stage kt has landed in st: complete its last chunk
-    auto complete = [&](char* st, int kt) {
+    // stage kt has landed: complete its last chunk
+    auto complete = [&](char* sm, int kt) {
       if ((a.k & 15) && kt == KT - 1 && kt < unit.past) {
-        Stage8<T, NW>::finish(st, a.a, a.m, a.k, m0, kt * kBytes, tid);
-        Stage8<T, NW>::finish(st + HALF, a.b, a.n, a.k, n0, kt * kBytes, tid);
+#pragma unroll 1
+        for (int o = 0; o < 2; ++o)
+          finish_rows<T>(o ? sm + HALF : sm, o ? a.b : a.a, o ? a.n : a.m, a.k, o ? n0 : m0, kt * kBytes, tid);
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
       }
     };
-    auto stage = [&](auto S, int kt) {
-      char* cur = buf(S);
-      char* nxt = buf(ic<decltype(S)::value + 1>{});
+    // stages at or past the end load zeros
+    issue(st, unit.first);
+    issue(st + STAGE, unit.first + 1);
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(NL) : "memory");
+    complete(st, unit.first);
+    frags(st, 0, ic<0>{});
+    uint32_t at = 0;  // the stage's buffer
+#pragma unroll 1
+    for (int kt = unit.first; kt < unit.past; ++kt, at ^= STAGE) {
+      char* cur = st + at;
+      char* nxt = st + (at ^ STAGE);
       static_for<KK>([&](auto KI) {
         constexpr int kk = decltype(KI)::value;
         constexpr int b = kk & 1;
@@ -395,14 +445,7 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
           __builtin_amdgcn_sched_barrier(0);
         }
       });
-    };
-    // whole rounds of two stages: stages at or past K load zeros
-    issue(st0, unit.first);
-    issue(st1, unit.first + 1);
-    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(NL) : "memory");
-    complete(st0, unit.first);
-    frags(st0, 0, ic<0>{});
-    for (int kt = unit.first; kt < unit.past; kt += 2) static_for<2>([&](auto S) { stage(S, kt + decltype(S)::value); });
+    }
 
     // ---- epilogue: scaled values through LDS, row-contiguous stores
     int el = lane;
@@ -414,32 +457,26 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
     auto rounds = [&](auto Z, auto&& put, auto&& get) __attribute__((always_inline)) {
       using S = decltype(Z);
       constexpr int E = static_cast<int>(sizeof(S));
-      constexpr int HROWS = E == 2 ? T / 2 : T / 4, ROUNDS = E == 2 ? 1 : 2;
-      static_assert(HROWS * T * E <= STAGE, "output rows fit the stage buffers");
-      static_for<ROUNDS>([&](auto R) {
-        constexpr int rd = decltype(R)::value;
+      constexpr int ROUNDS = E == 2 ? 1 : 2, RR = T / ROUNDS;
+      static_assert(RR * T * E <= 2 * STAGE, "output rows fit the stage buffers");
+      constexpr int C = 16 / E, CH = T / C;  // elements of a chunk, chunks of a row
+#pragma unroll 1
+      for (int rd = 0; rd < ROUNDS; ++rd) {
         if (ROUNDS == 1 || wm == rd) {
           static_for<FM>([&](auto MI) {
-            constexpr int mi = decltype(MI)::value;
-            const int il = wm * WM + mi * 32 + (el & 31), row = ROUNDS == 1 ? il : il - rd * WM;
-            char* half = row >= HROWS ? st1 : st0;
-            put(MI, il, [&](int jl) { return half + out_off<S, T>(row >= HROWS ? row - HROWS : row, jl); });
+            const int il = wm * WM + decltype(MI)::value * 32 + (el & 31);
+            put(MI, il, [&](int jl) { return st + out_off<S, T>(ROUNDS == 1 ? il : il - rd * WM, jl); });
           });
         }
         __syncthreads();
-        constexpr int C = 16 / E, CH = T / C;  // elements of a chunk, chunks of a row
-        const int et = wave * 64 + el;
-#pragma unroll 4
-        for (int it = 0; it < 2 * HROWS * CH / NT; ++it) {
-          const int e = et + it * NT, row = e / CH, c = e % CH;
-          const char* half = row >= HROWS ? st1 : st0;
-          get(rd * 2 * HROWS + row, C * c, *reinterpret_cast<const u32x4_t*>(half + out_off<S, T>(row >= HROWS ? row - HROWS : row, C * c)));
-        }
+#pragma unroll 2
+        for (int e = wave * 64 + el; e < RR * CH; e += NT)
+          get(rd * RR + e / CH, C * (e % CH), *reinterpret_cast<const u32x4_t*>(st + out_off<S, T>(e / CH, C * (e % CH))));
         __syncthreads();
-      });
+      }
     };
     if (unit.slot >= 0) {
-      int* part = reinterpret_cast<int*>(work.parts) + unit.slot * (T * T);
+      int* part = reinterpret_cast<int*>(work.parts) + static_cast<int64_t>(unit.slot) * (T * T);
       rounds(
           0,
           [&](auto MI, int, auto&& at) __attribute__((always_inline)) {
@@ -468,7 +505,6 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
           sb[ni][g][q] = n < a.n ? a.b.scale[n] : 0.0f;
         }
     O* out = reinterpret_cast<O*>(a.out.p);
-    const bool wide = ((reinterpret_cast<uintptr_t>(out) | static_cast<uintptr_t>(a.out.ld * E)) & 15u) == 0;
     rounds(
         O{},
         [&](auto MI, int il, auto&& at) __attribute__((always_inline)) {
@@ -492,11 +528,12 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
           const int64_t m = m0 + row, n = n0 + c;
           if (m >= a.m || n >= a.n) return;
           O* to = out + m * a.out.ld + n;
-          if (wide && n + C <= a.n) {
-            __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(to));
+          if (n + C <= a.n) {
+            *reinterpret_cast<u32x4_any*>(to) = v;
           } else {
             const O* from = reinterpret_cast<const O*>(&v);
-            for (int q = 0; q < C; ++q)
+#pragma unroll
+            for (int q = 0; q < C - 1; ++q)
               if (n + q < a.n) to[q] = from[q];
           }
         });
@@ -507,11 +544,11 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
 template <typename O, int T>
 __global__ __launch_bounds__(256) void matmul8_join_kernel(Matmul8Args a, TileWork work) {
   constexpr int PER = T * T / 1024;  // workgroups of a tile
-  const int64_t t = blockIdx.x / PER;
+  const int t = static_cast<int>(blockIdx.x / PER);
   const int e = static_cast<int>(blockIdx.x % PER) * 256 + static_cast<int>(threadIdx.x), row = e / (T / 4), c = 4 * (e % (T / 4));
   const TileUnit unit = tile_unit(work, work.whole + t);
-  const int* part = reinterpret_cast<const int*>(work.parts) + t * work.splits * (T * T) + row * T + c;
-  const int64_t m = unit.ti * T + row, n = unit.tj * T + c;
+  const int* part = reinterpret_cast<const int*>(work.parts) + static_cast<int64_t>(t) * work.splits * (T * T) + row * T + c;
+  const int64_t m = static_cast<int64_t>(unit.ti) * T + row, n = static_cast<int64_t>(unit.tj) * T + c;
   if (m >= a.m || n >= a.n) return;
   i32x4_t v = *reinterpret_cast<const i32x4_t*>(part);
   for (int p = 1; p < work.splits; ++p) v += *reinterpret_cast<const i32x4_t*>(part + static_cast<int64_t>(p) * (T * T));
@@ -527,7 +564,7 @@ hipError_t go_tiles(hipStream_t s, const Matmul8Args& a, const TilePlan& p) {
   const TileWork w = tile_work(p, a.ws);
   matmul8_tile_kernel<O, T><<<static_cast<unsigned>(p.grid), T == 256 ? 512 : 256, 0, s>>>(a, w);
   if (p.splits > 1) {
-    const int64_t cut = static_cast<int64_t>(p.tm) * p.tn - p.whole;
+    const int64_t cut = p.tm * p.tn - p.whole;
     matmul8_join_kernel<O, T><<<static_cast<unsigned>(cut * (T * T / 1024)), 256, 0, s>>>(a, w);
   }
   return hipGetLastError();
@@ -535,12 +572,8 @@ hipError_t go_tiles(hipStream_t s, const Matmul8Args& a, const TilePlan& p) {
 
 template <typename O>
 hipError_t go(hipStream_t s, const Matmul8Args& a) {
-  const int stages = (a.k + kBytes - 1) / kBytes;
-  // (two small tiles on a CU take 0.6 of a large one's time for half its products)
-  double large, small;
-  const TilePlan l = plan_tiles(a.m, a.n, 256, 256, stages, a.cus, a.ws_bytes, &large);
-  const TilePlan q = plan_tiles(a.m, a.n, 128, 128, stages, 2 * a.cus, a.ws_bytes, &small);
-  return large <= 0.6 * small ? go_tiles<O, 256>(s, a, l) : go_tiles<O, 128>(s, a, q);
+  const TilePlan p = plan_product(a.m, a.n, 1, (a.k + kBytes - 1) / kBytes, a.cus, a.ws_bytes);
+  return p.large ? go_tiles<O, 256>(s, a, p) : go_tiles<O, 128>(s, a, p);
 }
 
 // Rows of values, rounded by every workgroup for itself.
@@ -552,7 +585,9 @@ hipError_t go_rounding(hipStream_t s, const Matmul8Args& a) {
 
 }  // namespace
 
-bool linear8_rounds(const Matmul8Args& a) { return a.m <= 32 && staged_bytes(a) <= kStagedMost; }
+// (beyond, the rounding that every workgroup repeats takes longer than a launch of its
+// own: thirteen rows of 2560 for 151936 columns 103 us against 91)
+bool linear8_rounds(const Matmul8Args& a) { return a.m <= 32 && staged_bytes(a) <= kStagedSmall; }
 
 hipError_t launch_linear8(hipStream_t s, const Matmul8Args& a) {
   if (a.m == 0 || a.n == 0) return hipSuccess;
@@ -561,6 +596,6 @@ hipError_t launch_linear8(hipStream_t s, const Matmul8Args& a) {
 
 hipError_t launch_matmul8(hipStream_t s, const Matmul8Args& a) {
   if (a.m == 0 || a.n == 0) return hipSuccess;
-  if (a.m <= kMostStreamed) return a.out.bf16 ? go_stream<bf16_t>(s, a) : go_stream<float>(s, a);
+  if (streams(a)) return a.out.bf16 ? go_stream<bf16_t>(s, a) : go_stream<float>(s, a);
   return a.out.bf16 ? go<bf16_t>(s, a) : go<float>(s, a);
 }

@@ -5,8 +5,8 @@
 // whole rounds would keep few of them busy, so each of those tiles is cut along
 // the contraction into `splits` parts, whose sums go to the workspace and are
 // joined, in order, by a launch more.  8192 x 2560 out of 9728 (gradient of the
-// inputs, 320 tiles of 256 x 256 on 256 CUs): 645 us in two rounds, see
-// grad8.hip for what the split makes of it.
+// inputs, 320 tiles of 256 x 256 on 256 CUs): 645 us in two rounds, 457 with
+// the last 64 tiles in four parts each.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -18,70 +18,81 @@ struct TilePlan {
   int stages;       // of the contraction
   int splits;       // parts of a tile that is cut
   int part;         // stages of a part
-  int64_t whole;    // tiles that are not cut
-  int64_t units;    // tiles and parts of tiles
+  int whole;        // tiles that are not cut
+  int units;        // tiles and parts of tiles
   int grid;
 };
 
 // What the kernel sees.
 struct TileWork {
-  int tm, tn, stages, splits, part;
-  int64_t whole, units;
+  int tm, tn, stages, splits, part, whole, units;
   char* parts;      // [cut tiles][splits] sums of a whole tile, rows contiguous
 };
 
 #ifdef __HIPCC__
 struct TileUnit {
-  int64_t ti, tj;   // tile row and column
+  int ti, tj;       // tile row and column
   int first, past;  // stages
-  int64_t slot;     // of the partial sums, or -1
+  int slot;         // of the partial sums, or -1
 };
-__device__ __forceinline__ TileUnit tile_unit(const TileWork& w, int64_t l) {
+__device__ __forceinline__ TileUnit tile_unit(const TileWork& w, int l) {
   TileUnit u;
   u.first = 0;
   u.past = w.stages;
   u.slot = -1;
-  int64_t t = l;
+  uint32_t t = static_cast<uint32_t>(l);
   if (l >= w.whole) {
     // neighbours work on the same stretch of the contraction
-    const int64_t cut = static_cast<int64_t>(w.tm) * w.tn - w.whole, p = (l - w.whole) / cut;
-    t = w.whole + (l - w.whole) % cut;
+    const uint32_t cut = static_cast<uint32_t>(w.tm * w.tn - w.whole), i = t - static_cast<uint32_t>(w.whole), p = i / cut;
+    t = static_cast<uint32_t>(w.whole) + i % cut;
     u.first = static_cast<int>(p) * w.part;
     u.past = min(u.first + w.part, w.stages);
-    u.slot = (t - w.whole) * w.splits + p;
+    u.slot = static_cast<int>(i % cut) * w.splits + static_cast<int>(p);
   }
   // bands of four tile columns, row by row inside a band: the tiles that an XCD
   // works on at once share their operands in its L2
-  constexpr int GN = 4;
-  const int64_t band = t / (static_cast<int64_t>(w.tm) * GN);
-  const int64_t wide = min(static_cast<int64_t>(GN), w.tn - band * GN);
-  const int64_t r = t - band * w.tm * GN;
-  u.ti = r / wide;
-  u.tj = band * GN + r % wide;
+  constexpr uint32_t GN = 4;
+  const uint32_t of_band = static_cast<uint32_t>(w.tm) * GN, band = t / of_band, r = t % of_band;
+  const uint32_t wide = min(GN, static_cast<uint32_t>(w.tn) - band * GN);
+  u.ti = static_cast<int>(wide == GN ? r / GN : r / wide);
+  u.tj = static_cast<int>(band * GN + (wide == GN ? r % GN : r % wide));
   return u;
 }
 #endif
 
-// Tiles of tile_m x tile_n, `slots` workgroups at a time, at most `room` bytes of partial
-// sums.  The costs are in stages of a workgroup: measured for 256-tiles, a tile's
-// start and end take three stages' time, the second launch and its partial sums two
-// and a sixteenth a part.
-inline TilePlan plan_tiles(int64_t m, int64_t n, int tile_m, int tile_n, int stages, int slots, size_t room, double* cost) {
-  constexpr double kEnds = 3.0, kJoin = 2.0, kJoinPart = 1.0 / 16;
+// What the pieces of a product take, in microseconds on an MI355X: a stage of a
+// workgroup, its start and end, the join.
+struct TileCost {
+  double stage, ends;
+};
+// 256 x 256 products, one workgroup of eight waves a CU (2048 x 4096 x 2560: a
+// stage in 1.9 us, the setup, the first loads and the stores 9); and 128 x 128,
+// two of four waves (two stages at once in 1.5 us, 0.9 if alone; 5).
+constexpr TileCost kLarge = {1.9, 9.0}, kSmallTwo = {1.5, 5.0}, kSmallOne = {0.9, 5.0};
+constexpr double kJoin = 3.0, kJoinBytes = 5.3e6;  // bytes a microsecond
+
+// Tiles of tile_m x tile_n, `slots` workgroups at a time, at most `room` bytes of
+// partial sums.
+inline TilePlan plan_tiles(int64_t m, int64_t n, int tile_m, int tile_n, int stages, int slots, size_t room, TileCost full,
+                           TileCost few, double* cost) {
   TilePlan p = {};
   p.tm = static_cast<int>((m + tile_m - 1) / tile_m);
   p.tn = static_cast<int>((n + tile_n - 1) / tile_n);
   p.stages = stages;
-  const int64_t tiles = static_cast<int64_t>(p.tm) * p.tn, rounds = tiles / slots, rest = tiles % slots;
+  const int tiles = p.tm * p.tn, rounds = tiles / slots, rest = tiles % slots;
   const size_t bytes = static_cast<size_t>(tile_m) * tile_n * 4;
-  double best = rest ? stages + kEnds : 0.0;
+  auto time = [&](int units, int per) {
+    const TileCost& c = 2 * units <= slots ? few : full;
+    return ((units + slots - 1) / slots) * (per * c.stage + c.ends);
+  };
+  double best = rest ? time(rest, stages) : 0.0;
   p.splits = 1;
   p.part = stages;
   for (int s = 2; rest && s <= 32 && s <= stages; ++s) {
     const int part = (stages + s - 1) / s, parts = (stages + part - 1) / part;
     if (parts < s) continue;
     if (static_cast<size_t>(rest) * s * bytes > room) break;
-    const double t = static_cast<double>((rest * s + slots - 1) / slots) * (part + kEnds) + kJoin + kJoinPart * static_cast<double>(rest) * s / 64;
+    const double t = time(rest * s, part) + kJoin + static_cast<double>(static_cast<size_t>(rest) * s * bytes) / kJoinBytes;
     if (t < best) {
       best = t;
       p.splits = s;
@@ -90,8 +101,17 @@ inline TilePlan plan_tiles(int64_t m, int64_t n, int tile_m, int tile_n, int sta
   }
   p.whole = p.splits > 1 ? tiles - rest : tiles;
   p.units = p.whole + (tiles - p.whole) * p.splits;
-  p.grid = static_cast<int>(p.units < slots ? p.units : slots);
-  *cost = static_cast<double>(rounds) * (stages + kEnds) + best;
+  p.grid = p.units < slots ? p.units : slots;
+  *cost = rounds * (stages * full.stage + full.ends) + best;
   return p;
 }
 inline TileWork tile_work(const TilePlan& p, char* parts) { return {p.tm, p.tn, p.stages, p.splits, p.part, p.whole, p.units, parts}; }
+
+// The plan of a product in tiles of 256 or 128 rows, 256 / parts or 128 / parts columns.
+inline TilePlan plan_product(int64_t m, int64_t n, int parts, int stages, int cus, size_t room) {
+  double large, small;
+  TilePlan l = plan_tiles(m, n, 256, 256 / parts, stages, cus, room, kLarge, kLarge, &large);
+  const TilePlan s = plan_tiles(m, n, 128, 128 / parts, stages, 2 * cus, room, kSmallTwo, kSmallOne, &small);
+  l.large = 1;
+  return large <= small ? l : s;
+}
