@@ -102,7 +102,8 @@ struct YStage {
 };
 
 // 16 integers a chunk through registers, stored as the bf16 values they stand
-// for: PARTS planes of 64 x TN, the second what the first one's rounding left.
+// for: PARTS planes of 64 x TN, the second and third what the rounding of those
+// before left.  Three hold all 24 bits of an fp32 value.
 template <int TN, int NT, int PARTS>
 struct QStage {
   static constexpr int CPR = TN / 16, STEP = NT / CPR, NC = TN * kC / 16 / NT;
@@ -147,19 +148,23 @@ struct QStage {
   __device__ __forceinline__ int address() const { return km_off<TN>(row, 16 * chunk); }
   // half h (8 integers) of chunk q
   __device__ __forceinline__ void store(char* lds, int at, int q, int h) const {
-    u32x4_t hi, lo;
+    u32x4_t w[PARTS];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int w = static_cast<int>(v[q][2 * h + i / 2]);
-      const int sh = 16 * (i & 1);
-      const float x0 = s[q] * static_cast<float>((w << (24 - sh)) >> 24), x1 = s[q] * static_cast<float>((w << (16 - sh)) >> 24);
-      hi[i] = muon::pack_bf16x2(x0, x1);
-      if constexpr (PARTS == 2)
-        lo[i] = muon::pack_bf16x2(x0 - __uint_as_float(hi[i] << 16), x1 - __uint_as_float(hi[i] & 0xffff0000u));
+      const int q4 = static_cast<int>(v[q][2 * h + i / 2]), sh = 16 * (i & 1);
+      float x0 = s[q] * static_cast<float>((q4 << (24 - sh)) >> 24), x1 = s[q] * static_cast<float>((q4 << (16 - sh)) >> 24);
+#pragma unroll
+      for (int p = 0; p < PARTS; ++p) {
+        w[p][i] = muon::pack_bf16x2(x0, x1);
+        if (p + 1 < PARTS) {
+          x0 -= __uint_as_float(w[p][i] << 16);
+          x1 -= __uint_as_float(w[p][i] & 0xffff0000u);
+        }
+      }
     }
     char* to = lds + at + q * STEP * 2 * TN + 16 * h;  // (the swizzle leaves a chunk's lowest bit)
-    *reinterpret_cast<u32x4_t*>(to) = hi;
-    if constexpr (PARTS == 2) *reinterpret_cast<u32x4_t*>(to + kC * TN * 2) = lo;
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) *reinterpret_cast<u32x4_t*>(to + p * (kC * TN * 2)) = w[p];
   }
 };
 
@@ -244,7 +249,6 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, T
         __builtin_amdgcn_sched_group_barrier(0x200, 1, 0);
       });
     };
-    static_assert((STAGE & (STAGE - 1)) == 0, "stages alternate by one bit of the address");
     load(unit.first);
     static_for<3>([&](auto P) { store_part(st, decltype(P)::value); });
     load(unit.first + 1);
@@ -252,9 +256,9 @@ __global__ __launch_bounds__(128 * NWN, 1) void grad8_tile_kernel(Grad8Args a, T
     frags(st, 0, ic<0>{});
     uint32_t at = 0;  // the stage's buffer
 #pragma unroll 1
-    for (int kt = unit.first; kt < unit.past; ++kt, at ^= STAGE) {
+    for (int kt = unit.first; kt < unit.past; ++kt, at = STAGE - at) {
       char* cur = st + at;
-      char* nxt = st + (at ^ STAGE);
+      char* nxt = st + (STAGE - at);
       static_for<KK>([&](auto KI) {
         constexpr int kk = decltype(KI)::value;
         constexpr int b = kk & 1;
@@ -397,8 +401,8 @@ hipError_t go_tiles(hipStream_t s, const Grad8Args& a, const TilePlan& p) {
 
 hipError_t launch_grad8(hipStream_t s, const Grad8Args& a) {
   if (a.m == 0 || a.n == 0) return hipSuccess;
-  const int stages = static_cast<int>((a.c + kC - 1) / kC), parts = a.out.bf16 ? 1 : 2;
+  const int stages = static_cast<int>((a.c + kC - 1) / kC), parts = a.out.bf16 ? 1 : 3;
   const TilePlan p = plan_product(a.m, a.n, parts, stages, a.cus, a.ws_bytes);
   if (a.out.bf16) return p.large ? go_tiles<bf16_t, 256, 256, 4, 1>(s, a, p) : go_tiles<bf16_t, 128, 128, 2, 1>(s, a, p);
-  return p.large ? go_tiles<float, 256, 128, 4, 2>(s, a, p) : go_tiles<float, 128, 64, 2, 2>(s, a, p);
+  return p.large ? go_tiles<float, 256, 128, 4, 3>(s, a, p) : go_tiles<float, 128, 64, 2, 3>(s, a, p);
 }

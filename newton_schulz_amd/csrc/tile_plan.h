@@ -107,11 +107,15 @@ inline TilePlan plan_tiles(int64_t m, int64_t n, int tile_m, int tile_n, int sta
 }
 inline TileWork tile_work(const TilePlan& p, char* parts) { return {p.tm, p.tn, p.stages, p.splits, p.part, p.whole, p.units, parts}; }
 
-// The plan of a product in tiles of 256 or 128 rows, 256 / parts or 128 / parts columns.
+// The plan of a product in tiles of 256 x 256 or 128 x 128; with an operand in
+// three parts of half as many columns, whose stages take one and a half times as long.
 inline TilePlan plan_product(int64_t m, int64_t n, int parts, int stages, int cus, size_t room) {
+  const int of = parts > 1 ? 2 : 1;
+  const double longer = parts > 1 ? 0.5 * parts : 1.0;
+  auto times = [&](TileCost c) { return TileCost{c.stage * longer, c.ends}; };
   double large, small;
-  TilePlan l = plan_tiles(m, n, 256, 256 / parts, stages, cus, room, kLarge, kLarge, &large);
-  const TilePlan s = plan_tiles(m, n, 128, 128 / parts, stages, 2 * cus, room, kSmallTwo, kSmallOne, &small);
+  TilePlan l = plan_tiles(m, n, 256, 256 / of, stages, cus, room, times(kLarge), times(kLarge), &large);
+  const TilePlan s = plan_tiles(m, n, 128, 128 / of, stages, 2 * cus, room, times(kSmallTwo), times(kSmallOne), &small);
   l.large = 1;
   return large <= small ? l : s;
 }

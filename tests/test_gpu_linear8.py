@@ -4,8 +4,8 @@ gfx950 GPU).
 Tolerances.  Integers, scales, values read back and products are compared bit
 for bit: every rounding of theirs is stated.  A gradient sums C products of a
 bf16 value and a value v = scale * q; with A = sum |grad_y| |v|,
-  * v enters rounded to bf16 (half a step: 2^-8) or as two bf16 parts (2^-16),
-    after one fp32 rounding of scale * q (2^-24);
+  * v enters rounded to bf16 (half a step: 2^-8), or, for fp32 outputs, as it
+    is, after one fp32 rounding of scale * q (2^-24);
   * the fp32 sum: every addition rounds at most 2^-23 (half a step, or the
     matrix cores' truncation) of a partial sum that A bounds, C + 8 of them;
   * storing: half a step of the output's type, and 2^-24 more of the sum with
@@ -210,7 +210,7 @@ def check_grads(ctx, t, n, k, dtype, accumulate, pad=0, seed=0):
         before = old[:, :k].double().cpu().numpy() if accumulate else 0.0
         want = want + before
         half = torch.finfo(dtype).eps / 2
-        tol = size * ((2.0 ** -8 if dtype == BF else 2.0 ** -16) + 2.0 ** -24 + (a.shape[1] + 8) * 2.0 ** -23)
+        tol = size * ((2.0 ** -8 if dtype == BF else 0.0) + 2.0 ** -24 + (a.shape[1] + 8) * 2.0 ** -23)
         tol = tol * (1 + half) + (half + 2.0 ** -24) * np.abs(want) + 2.0 ** -130
         off = np.abs(got[:, :k].double().cpu().numpy() - want)
         assert (off <= tol).all(), f"off by {off.max():.3e}, {(off / tol).max():.2f} of the tolerance"
@@ -378,7 +378,7 @@ def test_layer_trains_through_the_step(ctx):
         yd = gy.double().cpu().numpy()
         for got, ref, size in ((gx, yd @ w, np.abs(yd) @ np.abs(w)),
                                (step.view(step.grad, 0), yd.T @ xs, np.abs(yd.T) @ np.abs(xs))):
-            tol = size * (2.0 ** -16 + 210 * 2.0 ** -23) + 2.0 ** -24 * np.abs(ref)
+            tol = size * (2.0 ** -24 + 210 * 2.0 ** -23) + 2.0 ** -24 * np.abs(ref)
             assert (np.abs(got.cpu().numpy() - ref) <= tol).all()
         before = step.view(step.master, 0).clone()
         step.step()
