@@ -220,7 +220,10 @@ def _rows(t: torch.Tensor, name: str, device: torch.device) -> Rows:
     if t.dim() < 2:
         raise ValueError(f"{name} must be [rows, cols]")
     if t.dim() > 2:
-        t = t.flatten(0, -2) if t.numel() == 0 else t.view(-1, t.shape[-1])  # (raises where the rows have no one stride)
+        try:
+            t = t.flatten(0, -2) if t.numel() == 0 else t.view(-1, t.shape[-1])
+        except RuntimeError:
+            raise ValueError(f"the rows of {name} lie at no one stride") from None
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"the columns of {name} must be contiguous")
     return Rows(t.data_ptr(), _dtype(t), t.shape[0], t.shape[1], t.stride(0))

@@ -17,7 +17,7 @@ import numpy as np
 import pytest
 import torch
 
-from newton_schulz_amd import Context, MuonStep, linear8_workspace_bytes
+from newton_schulz_amd import Context, MuonError, MuonStep, Rows8, linear8_workspace_bytes
 from oracle import linear8_oracle as lo
 
 pytestmark = pytest.mark.gpu
@@ -385,6 +385,130 @@ def test_layer_trains_through_the_step(ctx):
         torch.cuda.synchronize()
         assert not torch.equal(before, step.view(step.master, 0))
         print(f"  pass {i} done", file=sys.stderr, flush=True)
+
+
+def test_offsets_past_32_bits(ctx):
+    """More than 2^31 elements of activations, of their 8-bit rows and of the
+    gradient of y: the first and last rows against the oracle, and the weights'
+    gradient against sums of 64 bits."""
+    t, n, k = (1 << 20) + 300, 2064, 2064
+    g = torch.Generator(device=DEV).manual_seed(7)
+    x = torch.empty(t, k, dtype=BF, device=DEV).normal_(generator=g)
+    x8, w = ctx.rows8(t, k), eight(ctx, n, k, 3)
+    ctx.quantize_rows(x, x8)
+    ends = [slice(0, 70), slice(t - 70, t)]
+    for e in ends:
+        q, s = lo.quantize_ref(x[e].float().cpu().numpy())
+        assert np.array_equal(x8.q[e].cpu().numpy(), q) and np.array_equal(x8.scale[e].cpu().numpy(), s)
+    back = torch.empty_like(x)
+    ctx.dequantize_rows(x8, back)
+    for e in ends:
+        assert torch.equal(back[e], (x8.scale[e, None] * x8.q[e].float()).to(BF))
+    print("  rows done", file=sys.stderr, flush=True)
+    y = back  # [t, n]
+    ctx.matmul8(x8, w, y)
+    for e in ends:
+        want = torch.from_numpy(lo.matmul8_ref(*(v.cpu().numpy() for v in (x8.q[e], x8.scale[e], w.q, w.scale)))).to(BF)
+        assert torch.equal(bits(y[e]), bits(want))
+    print("  product done", file=sys.stderr, flush=True)
+    gx = x
+    ctx.input_grad8(y, w, gx)
+    v = lo.values_ref(w.q.cpu().numpy(), w.scale.cpu().numpy())
+    for e in ends:
+        yd = y[e].double().cpu().numpy()
+        tol = np.abs(yd) @ np.abs(v) * (2.0 ** -8 + 2.0 ** -24 + (n + 8) * 2.0 ** -23) * (1 + 2.0 ** -8)
+        want = yd @ v
+        assert (np.abs(gx[e].double().cpu().numpy() - want) <= tol + 2.0 ** -8 * np.abs(want)).all()
+    # a few columns of the weights' gradient
+    gw = torch.empty(n, k, device=DEV)
+    ctx.weight_grad8(y, x8, gw)
+    some = torch.tensor([0, 1, 77, 1031, k - 1], device=DEV)
+    want, size = torch.zeros(n, 5, dtype=torch.float64, device=DEV), torch.zeros(n, 5, dtype=torch.float64, device=DEV)
+    for i in range(0, t, 1 << 17):
+        a = y[i:i + (1 << 17)].double()
+        b = x8.q[i:i + (1 << 17)][:, some].double() * x8.scale[i:i + (1 << 17), None].double()
+        want += a.t() @ b
+        size += a.abs().t() @ b.abs()
+    # every addition rounds at most 2^-23 of a partial sum, of random signs: a
+    # partial sum is bounded by `size`, and t roundings of that size and random
+    # sign exceed 8 sqrt(t) of them nowhere
+    tol = size * (2.0 ** -24 + 8 * t ** 0.5 * 2.0 ** -23) + 2.0 ** -24 * want.abs()
+    assert ((gw[:, some].double() - want).abs() <= tol).all()
+
+
+def test_two_contexts_at_once():
+    """Calls on two streams, each with a context of its own, keep their results."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    both = []
+    for i in range(2):
+        c = Context(DEV, 64 << 20)
+        t, n, k = 130 + i, 520, 1032
+        both.append((c, torch.cuda.Stream(), values(t, k, BF, i), eight(c, n, k, i), values(t, n, BF, 5 + i, scale=1e-3).contiguous(),
+                     torch.empty(t, n, device=DEV), c.rows8(t, k), torch.empty(n, k, device=DEV)))
+
+    def calls(c, s, x, w, gy, y, x8, gw):
+        c.linear8(x, w, y, x8=x8, stream=s)
+        c.weight_grad8(gy, x8, gw, stream=s)
+
+    for args in both:
+        calls(args[0], None, *args[2:])
+    want = [(a[5].clone(), a[7].clone()) for a in both]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for args in both:
+            calls(*args)
+    torch.cuda.synchronize()
+    for args, (y, gw) in zip(both, want):
+        assert torch.equal(args[5], y) and torch.equal(args[7], gw)
+        args[0].close()
+
+
+def test_recorded_step_and_offloaded_step_keep_8_bit_weights():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from newton_schulz_amd.offload import MuonOffloadStep
+    shapes = [(256, 512, 0), (130, 202, 0), (64, 37, 0)]
+    steps = [MuonStep(shapes, DEV, cap_bytes=1 << 19, keep_int8_weights=True) for _ in range(2)]
+    steps.append(MuonOffloadStep(shapes, DEV, cap_bytes=1 << 19, keep_int8_weights=True, grads_on_host=False))
+    for m in steps:
+        g = torch.Generator(device=DEV).manual_seed(1)
+        m.master.normal_(0, 0.02, generator=g)
+        m.grad.copy_(torch.randn(m.numel, generator=g, device=DEV) * 1e-3)
+    steps[0].capture()
+    for _ in range(3):
+        steps[0].replay()
+        steps[1].step()
+        steps[2].step()
+        torch.cuda.synchronize()
+        for m in steps[:1] + steps[2:]:
+            for i in range(len(shapes)):
+                assert torch.equal(m.weight8(i).q, steps[1].weight8(i).q)
+                assert torch.equal(m.weight8(i).scale, steps[1].weight8(i).scale)
+    q, s = lo.quantize_ref(steps[0].view(steps[0].master, 1).cpu().numpy())
+    assert np.array_equal(steps[0].weight8(1).q.cpu().numpy(), q)
+
+
+def test_refusals_of_the_binding(ctx):
+    w, x = eight(ctx, 9, 20, 1), torch.zeros(4, 20, device=DEV)
+    with pytest.raises(ValueError, match="no one stride"):
+        ctx.linear8(torch.zeros(2, 3, 20, device=DEV).transpose(0, 1), w, torch.empty(6, 9, device=DEV))
+    with pytest.raises(ValueError, match="contiguous"):
+        ctx.linear8(torch.zeros(20, 4, device=DEV).t(), w, torch.empty(4, 9, device=DEV))
+    with pytest.raises(ValueError, match="tensor on"):
+        ctx.linear8(x.cpu(), w, torch.empty(4, 9, device=DEV))
+    with pytest.raises(TypeError, match="dtype"):
+        ctx.linear8(x.half(), w, torch.empty(4, 9, device=DEV))
+    with pytest.raises(MuonError, match="do not match"):
+        ctx.linear8(x, w, torch.empty(4, 8, device=DEV))
+    with pytest.raises(MuonError, match="bf16"):
+        ctx.input_grad8(torch.zeros(4, 9, device=DEV), w, torch.empty(4, 20, device=DEV))
+    with pytest.raises(MuonError, match="16 bytes"):
+        ctx.quantize_rows(x, Rows8(torch.zeros(4, 20, dtype=torch.int8, device=DEV), torch.zeros(4, device=DEV)))
+    small = Context(DEV, 16)
+    with pytest.raises(MuonError, match="workspace"):
+        small.linear8(torch.zeros(64, 2000, device=DEV), eight(ctx, 9, 2000, 1), torch.empty(64, 9, device=DEV))
+    small.close()
 
 
 def test_workspace_is_what_a_call_needs():

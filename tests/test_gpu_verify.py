@@ -207,6 +207,37 @@ def test_streams_graphs_and_no_log_probabilities(ctx):
         assert torch.equal(tokens, want[0]) and torch.equal(accepted, want[1]) and torch.equal(lp, want[2])
 
 
+def test_more_sequences_than_a_launch_counts(ctx):
+    """Launches are cut where the counters of their sequences would not fit."""
+    c = Context(DEV, 256 << 20)
+    x, y, d, u = make(5000, 1, 50, F32, 13)
+    check(c, x, y, d, u, 1.0)
+    x, y, d, u = make(1, 2, 33000, BF, 14)  # three slices a row
+    many = 3000
+    args = [v.expand(many, *v.shape[1:]) for v in (x, d)]
+    u = torch.rand(many, 3, generator=torch.Generator().manual_seed(1)).to(DEV)
+    y = y.expand(many, 2).contiguous()
+    tokens, accepted, lp = call(c, args[0], y, args[1], u, 1.0)
+    for i in (0, 1, 511, 1024, 2047, 2048, many - 1):
+        one = call(c, x, y[:1], d, u[i:i + 1].contiguous(), 1.0)
+        assert torch.equal(tokens[i], one[0][0]) and accepted[i] == one[1][0] and torch.equal(lp[i], one[2][0]), i
+    c.close()
+
+
+def test_long_drafts(ctx):
+    """A thousand places, refused at once, at the end and not at all."""
+    c = Context(DEV, 256 << 20)
+    for dtype, vocab in ((F32, 60), (BF, 9000)):
+        x, y, d, u = make(4, 1024, vocab, dtype, 15, noise=0.01)
+        u[0, :] = 0.5
+        u[1, :1024] = 0.0
+        u[2, :1024] = 0.0
+        u[2, 1023] = 1.5
+        want = check(c, x, y, d, u, 1.0)
+        assert want[1][1] == 1024 and want[1][2] == 1023
+    c.close()
+
+
 def test_empty_batch_and_exact_workspace(ctx):
     call(ctx, torch.empty(0, 3, 50, device=DEV), torch.empty(0, 2, dtype=torch.int64, device=DEV), None,
          torch.empty(0, 3, device=DEV), 1.0)
