@@ -103,7 +103,7 @@ __global__ __launch_bounds__(64 * KS) void matmul8_stream_kernel(Matmul8Args a) 
         uint32_t top = 0;
 #pragma unroll
         for (int p = 0; p < P; ++p) top = muon::piece_top<FROM>(held[q][p], top);
-        atomicMax(&tops[i], top);
+        atomicMax(&tops[i], muon::top_bits<FROM>(top));
       }
       __syncthreads();
 #pragma unroll

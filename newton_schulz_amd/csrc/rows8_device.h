@@ -1,11 +1,13 @@
 // Rounding of values to 8 bits (device functions).
 //
 // Mathematics.  s = max |x| / 127 in binary32; q is the integer nearest to the
-// exact x / s, ties to even.  x / s is estimated as x (1 / s): with two
-// roundings of 2^-24 and |q| <= 127 the estimate is off by less than 2^-15.9, so
-// only where it lies that close to a half does the remainder x - q s decide,
-// which one fused multiply-add forms exactly (|x - q s| <= s, and both are
-// multiples of the smaller's last place).
+// exact x / s, ties to even.  x (1 / s) is off by less than 2^-16.9 (one rounding
+// of 2^-24, |q| <= 127.5), and a fused multiply-add with 3 2^22 rounds it to an
+// integer, which then stands in the sum's last bits.  Only where it lies within
+// 2^-15 of a half does the remainder x - q s decide, which one fused multiply-add
+// forms exactly (|x - q s| <= s, and both are multiples of the smaller's last
+// place).  (Multiplying, rounding, converting and packing took 24 VALU
+// instructions a value with the maximum, and 8192 x 9728 of them 57 us.)
 #pragma once
 
 #include "muon_device.h"
@@ -52,31 +54,30 @@ struct RowRounding {
 // N values (a multiple of 4) of a row as bytes.
 template <int N>
 __device__ __forceinline__ void to_bytes(float (&x)[N], const RowRounding& row, uint32_t (&w)[N / 4]) {
-  int q[N];
+  uint32_t q[N];
   float far = 0.0f;
   if (row.lift != 1.0f) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] *= row.lift;
   }
+  constexpr float kInteger = 12582912.0f;  // 3 2^22
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    const float e = x[i] * row.inv, n = rintf(e);
-    far = fmaxf(far, fabsf(e - n));
-    q[i] = static_cast<int>(n);
+    const float t = __builtin_fmaf(x[i], row.inv, kInteger);
+    far = fmaxf(far, fabsf(__builtin_fmaf(x[i], row.inv, -(t - kInteger))));
+    q[i] = __float_as_uint(t);
   }
   if (far > 0.5f - 0x1p-15f) {
     asm volatile("" : "+v"(q[0]));  // stays a branch
 #pragma unroll
-    for (int i = 0; i < N; ++i) q[i] = static_cast<int>(nearest_exact(x[i], row.s, x[i] * row.inv));
-  }
-  if (row.inv == 0.0f) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) q[i] = 0;
+    for (int i = 0; i < N; ++i) q[i] = static_cast<uint32_t>(static_cast<int>(nearest_exact(x[i], row.s, x[i] * row.inv)));
   }
 #pragma unroll
-  for (int i = 0; i < N / 4; ++i)
-    w[i] = static_cast<uint32_t>(q[4 * i] & 255) | static_cast<uint32_t>(q[4 * i + 1] & 255) << 8 |
-           static_cast<uint32_t>(q[4 * i + 2] & 255) << 16 | static_cast<uint32_t>(q[4 * i + 3]) << 24;
+  for (int i = 0; i < N / 4; ++i) {
+    // the lowest bytes of four words
+    const uint32_t lo = __builtin_amdgcn_perm(q[4 * i + 1], q[4 * i], 0x0c0c0400u), hi = __builtin_amdgcn_perm(q[4 * i + 3], q[4 * i + 2], 0x04000c0cu);
+    w[i] = row.inv == 0.0f ? 0u : lo | hi;
+  }
 }
 
 // 16 bytes as values, and the largest magnitude's bits among them.
@@ -98,18 +99,31 @@ template <> struct Piece<float> {
     for (int i = 0; i < 4; ++i) v[i] = __uint_as_float(w[i]);
   }
 };
+// The largest magnitude's bits so far, of bf16 in both halves of a word.
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
 template <typename T> __device__ __forceinline__ uint32_t piece_top(u32x4 w, uint32_t top) {
-  float v[Piece<T>::N];
-  Piece<T>::values(w, v);
 #pragma unroll
-  for (int i = 0; i < Piece<T>::N; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2)
+      top = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, w[i] & 0x7fff7fffu), __builtin_bit_cast(u16x2, top)));
+    else
+      top = max(top, w[i] & 0x7fffffffu);
+  }
   return top;
 }
-// Piece p of a row of `cols` values, zeros behind its end.
-template <typename T> __device__ __forceinline__ u32x4 load_piece(const T* row, int p, int cols) {
+// As bits of an fp32 magnitude.
+template <typename T> __device__ __forceinline__ uint32_t top_bits(uint32_t top) {
+  if constexpr (sizeof(T) == 2) return max(top << 16, top & 0xffff0000u);
+  else return top;
+}
+// Piece p of a row of `cols` values, zeros behind its end; PAST: past the caches.
+template <typename T, bool PAST = false> __device__ __forceinline__ u32x4 load_piece(const T* row, int p, int cols) {
   constexpr int N = Piece<T>::N;
   const T* at = row + p * N;
-  if ((p + 1) * N <= cols) return *reinterpret_cast<const u32x4_any*>(at);
+  if ((p + 1) * N <= cols) {
+    if constexpr (PAST) return __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(at));
+    else return *reinterpret_cast<const u32x4_any*>(at);
+  }
   u32x4 w = {0, 0, 0, 0};
   if constexpr (N == 8) {
 #pragma unroll
