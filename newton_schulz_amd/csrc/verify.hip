@@ -38,7 +38,8 @@ namespace {
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kRun = 4, kMostCuts = 64 * kRun;  // slices of the second reading that a lane holds, and of a row
-constexpr int kN = 8, kMostCut = 2 * kThreads * kN;  // scores that a thread takes at a time, and of a slice of the second reading
+constexpr int kN = 8, kMostCut = kThreads * kN;  // scores that a thread takes at a time, and of a slice of the second reading
+constexpr int kMostSmall = 2 * kMostCut;         // of a row that one workgroup takes
 // Counters of a sequence: of 32 workgroups each, then one of those; in lines of their own.
 constexpr int kTogether = 32, kCounterStride = 8;
 constexpr float kLowest = -FLT_MAX;
@@ -50,21 +51,30 @@ template <typename T> constexpr int kVec = 16 / static_cast<int>(sizeof(T));
 // Scores [i, i + kVec) of a row, those at or past `end` -infinity.
 template <typename T>
 __device__ __forceinline__ void piece(const T* row, int i, int end, float (&v)[kVec<T>]) {
+  u32x4 w;
   if (i + kVec<T> <= end) {
-    const u32x4 w = *reinterpret_cast<const u32x4_any*>(row + i);
-    if constexpr (sizeof(T) == 2) {
+    w = *reinterpret_cast<const u32x4_any*>(row + i);
+  } else {
+    // one by one, the last first: each pushes those behind it up
+    uint64_t lo = sizeof(T) == 2 ? 0xff80ff80ff80ff80ull : 0xff800000ff800000ull, hi = lo;
+    constexpr int bits = 8 * sizeof(T);
+#pragma unroll 1
+    for (int j = end - 1; j >= i; --j) {
+      hi = hi << bits | lo >> (64 - bits);
+      if constexpr (sizeof(T) == 2) lo = lo << bits | row[j];
+      else lo = lo << bits | __float_as_uint(row[j]);
+    }
+    w = u32x4{static_cast<uint32_t>(lo), static_cast<uint32_t>(lo >> 32), static_cast<uint32_t>(hi), static_cast<uint32_t>(hi >> 32)};
+  }
+  if constexpr (sizeof(T) == 2) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[2 * j] = __uint_as_float(w[j] << 16);
-        v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(w[j]);
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(w[j] << 16);
+      v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < kVec<T>; ++j) v[j] = i + j < end ? muon::Elem<T>::load(row + i + j) : -INFINITY;
+    for (int j = 0; j < 4; ++j) v[j] = __uint_as_float(w[j]);
   }
 }
 
@@ -316,15 +326,20 @@ __device__ __forceinline__ VerifyEnd find_end(const VerifyArgs& a, int b, int le
   return end;
 }
 
-__device__ __forceinline__ double block_sum(double v) {
-  __shared__ double lds[kWaves];
-  v = wave_sum(v);
+// The sums of both over a workgroup, in every thread.
+__device__ __forceinline__ double2 block_sums(double x, double y) {
+  __shared__ double2 lds[kWaves];
+  x = wave_sum(x);
+  y = wave_sum(y);
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = make_double2(x, y);
   __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = 0.0;
-  for (int w = 0; w < kWaves; ++w) v += lds[w];
-  return v;
+  x = y = 0.0;
+  for (int w = 0; w < kWaves; ++w) {
+    x += lds[w].x;
+    y += lds[w].y;
+  }
+  __syncthreads();  // (the next sums)
+  return make_double2(x, y);
 }
 
 // The token `next` (-1: none) at the end of a sequence, and what lies behind it;
@@ -400,59 +415,45 @@ __device__ __forceinline__ void pieces(const T* row, int i, int end, float (&v)[
 // without the drafted token, or max(p - q, 0).
 enum Form { P, LESS, REST };
 
-// Scores lo + (h kThreads + thread) kN .. of a slice, both halves h asked for at once.
-template <typename T>
-__device__ __forceinline__ void both_halves(const T* row, int lo, int hi, float (&v)[2][kN]) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int i = lo + (h * kThreads + static_cast<int>(threadIdx.x)) * kN;
-    if (i < hi) pieces(row, i, hi, v[h]);
-  }
-}
-__device__ __forceinline__ bool in_half(int lo, int hi, int h) { return lo + (h * kThreads + static_cast<int>(threadIdx.x)) * kN < hi; }
-
-// Sums of a slice of the row that is drawn from, in every thread: of exp(x)
-// around its maximum, and of exp of the draft's scores, or, without those, of
-// exp(x) without the drafted token.
+// Sums over scores [lo, hi) of the row that is drawn from, in every thread: of
+// exp(x) around its maximum, and of exp of the draft's scores, or, without those,
+// of exp(x) without the drafted token.
 template <typename TX, typename TD>
 __device__ __forceinline__ double2 slice_sums(const VerifyArgs& a, int b, const VerifyEnd& e, bool rest, int lo, int hi, const double* table) {
-  float x[2][kN], d[2][kN];
-  both_halves(row_of<TX>(a.x, b, e.r), lo, hi, x);
-  if (rest) both_halves(row_of<TD>(a.d, b, e.r), lo, hi, d);
   const Exp p(table, a.kd, e.mp), q(table, a.kd, e.mq);
   double sp = 0.0, sq = 0.0;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (!in_half(lo, hi, h)) continue;
-    const int i = lo + (h * kThreads + static_cast<int>(threadIdx.x)) * kN;
+#pragma unroll 1
+  for (int i = lo + static_cast<int>(threadIdx.x) * kN; i < hi; i += kThreads * kN) {
+    float x[kN], d[kN];
+    pieces(row_of<TX>(a.x, b, e.r), i, hi, x);
+    if (rest) pieces(row_of<TD>(a.d, b, e.r), i, hi, d);
 #pragma unroll
     for (int c = 0; c < kN; ++c) {
-      const double w = p(x[h][c]);
+      const double w = p(x[c]);
       sp += w;
       if (!rest && i + c != e.y) sq += w;
     }
     if (rest) {
 #pragma unroll
-      for (int c = 0; c < kN; ++c) sq += q(d[h][c]);
+      for (int c = 0; c < kN; ++c) sq += q(d[c]);
     }
   }
-  return make_double2(block_sum(sp), block_sum(sq));
+  return block_sums(sp, sq);
 }
 
-// Sum of max(p - q, 0) over a slice, in every thread.
+// Sum of max(p - q, 0) over scores [lo, hi), in every thread.
 template <typename TX, typename TD>
 __device__ __forceinline__ double slice_rest(const VerifyArgs& a, int b, const VerifyEnd& e, const Rest& w, int lo, int hi) {
-  float x[2][kN], d[2][kN];
-  both_halves(row_of<TX>(a.x, b, e.r), lo, hi, x);
-  both_halves(row_of<TD>(a.d, b, e.r), lo, hi, d);
   double s = 0.0;
+#pragma unroll 1
+  for (int i = lo + static_cast<int>(threadIdx.x) * kN; i < hi; i += kThreads * kN) {
+    float x[kN], d[kN];
+    pieces(row_of<TX>(a.x, b, e.r), i, hi, x);
+    pieces(row_of<TD>(a.d, b, e.r), i, hi, d);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (!in_half(lo, hi, h)) continue;
-#pragma unroll
-    for (int c = 0; c < kN; ++c) s += w(x[h][c], d[h][c]);
+    for (int c = 0; c < kN; ++c) s += w(x[c], d[c]);
   }
-  return block_sum(s);
+  return block_sums(s, 0.0).x;
 }
 
 // The lowest token of slice [lo, hi) up to which the weights, on top of `run`,
@@ -740,7 +741,7 @@ hipError_t go(hipStream_t s, VerifyArgs a, int b0, int n) {
   const unsigned nb = static_cast<unsigned>(n);
   // One workgroup for a sequence, against three launches over slices: measured
   // where the rows hold up to kSmall scores in all.
-  if (a.vocab <= kMostCut && a.rows <= kSmallRows && a.rows * a.vocab <= kSmall) {
+  if (a.vocab <= kMostSmall && a.rows <= kSmallRows && a.rows * a.vocab <= kSmall) {
     verify_small_kernel<TX, TD><<<nb, kThreads, 0, s>>>(a);
     return hipGetLastError();
   }
@@ -768,9 +769,9 @@ VerifyPlan verify_plan(int64_t batch, int64_t draft, int64_t vocab, int bytes) {
   p.groups = 2 + (p.rows * p.slices - 1) / kTogether;
   const int64_t most_batch = kExchangeWords / kCounterStride / p.groups;
   p.launch = static_cast<int>(batch < most_batch ? batch : most_batch);
-  // the second reading: slices of 2048 scores, of 4096 where there are many
-  static_assert(MUON_MAX_VOCAB / 2048 <= kMostCuts, "a wave holds a row's sums");
-  const int64_t fine = (vocab + 2047) / 2048, cuts = fine * p.launch > 2048 ? (vocab + kMostCut - 1) / kMostCut : fine;
+  // the second reading
+  static_assert(MUON_MAX_VOCAB / kMostCut <= kMostCuts, "a wave holds a row's sums");
+  const int64_t cuts = (vocab + kMostCut - 1) / kMostCut;
   p.cut = static_cast<int>(((vocab + cuts - 1) / cuts + 7) / 8 * 8);
   p.cuts = static_cast<int>((vocab + p.cut - 1) / p.cut);
   size_t at = 0;
