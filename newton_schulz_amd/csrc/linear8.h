@@ -58,13 +58,13 @@ struct VerifyEnd {  // of a sequence
   int r, y, mode;
   float mp, mq;
   int best;
-  double sp;
+  double sp, sq;  // sums of the first reading
 };
 // Slices of a row in the first reading and in the second, and where in the
 // workspace things lie; `bytes`: of the wider of the scores' types.
 struct VerifyPlan {
   int slices, slice, cuts, cut, rows, groups, launch;
-  size_t parts, ends, sums, weights, total;
+  size_t parts, ends, sums, total;
 };
 VerifyPlan verify_plan(int64_t batch, int64_t draft, int64_t vocab, int bytes);
 
@@ -88,8 +88,7 @@ struct VerifyArgs {
   uint64_t* counters;  // zero between launches
   uint64_t* parts;     // [batch][rows][slices][2]: maximum and its index, sum
   VerifyEnd* ends;
-  uint64_t* sums;      // [batch][cuts][2]
-  uint64_t* weights;   // [batch][cuts]
+  uint64_t* sums;      // [batch][cuts][4]
 };
 hipError_t launch_verify(hipStream_t s, VerifyArgs a, int64_t batch, const VerifyPlan& p, char* ws,
                          Exchange& x);

@@ -17,9 +17,7 @@
 // sequence to finish goes on with what needs all of them.
 //   verify_pairs_kernel: maximum and sum of every row that may be needed (the
 //     bound: HBM and the exponentials); last: which place ends the sequence;
-//   verify_sums_kernel: that row's sums; last, where there are no draft scores:
-//     the token;
-//   verify_weights_kernel: the sums of max(p - q, 0); last: the token.
+//   verify_sums_kernel: that row's sums; last: the token.
 #include <cfloat>
 #include <type_traits>
 
@@ -123,14 +121,17 @@ struct Exp {
   __device__ __forceinline__ Exp(const double* t, double kd, float top) : table(t), k(32.0 * kd), m(static_cast<double>(top)) {}
   __device__ __forceinline__ double operator()(float x) const {
     // (the difference first: scores of any size, the type's lowest too, keep it exact)
-    const double t = fmax((static_cast<double>(x) - m) * k, -34000.0);  // (2^-1062)
-    const double n = rint(t), f = t - n;
-    const int i = static_cast<int>(n);
+    const double t = (static_cast<double>(x) - m) * k;
+    const double big = t + 0x1.8p52, f = t - (big - 0x1.8p52);  // n stands in the sum's last bits
+    const int n = static_cast<int>(__double_as_longlong(big));
     double p = __builtin_fma(f, 0x1.3b2ab6fba4e77p-27, 0x1.c6b08d704a0c0p-20);  // (log 2 / 32)^j / j!
     p = __builtin_fma(f, p, 0x1.ebfbdff82c58fp-13);
     p = __builtin_fma(f, p, 0x1.62e42fefa39efp-6);
     p = __builtin_fma(f, p, 1.0);
-    return ldexp(p * table[i & 31], i >> 5);
+    // 2^(n / 32): the exponent's bits begin 20 bits into the upper word
+    const int64_t root = __double_as_longlong(table[n & 31]);
+    const double w = __longlong_as_double(root + (static_cast<int64_t>((n & ~31) << 15) << 32));
+    return t > -32000.0 ? p * w : 0.0;  // (2^-1000)
   }
 };
 __device__ __forceinline__ void fill_table(double* table) {
@@ -290,12 +291,13 @@ __device__ __forceinline__ VerifyEnd find_end(const VerifyArgs& a, int b, int le
     }
     __syncthreads();
     bool keep = false;
-    VerifyEnd e = {i, -1, 0, 0.0f, 0.0f, 0, 0.0};
+    VerifyEnd e = {i, -1, 0, 0.0f, 0.0f, 0, 0.0, 0.0};
     double lp = 0.0;
     if (mine) {
       const Part P = rows[threadIdx.x];
       const bool ok = has_distribution(P);
       float mq = 0.0f;
+      double sq = 0.0;
       bool near = true;
       if (ok && named) lp = (static_cast<double>(xy) - static_cast<double>(P.m)) * (greedy ? 1.0 : a.inv_t) - log(P.s);
       if (greedy) {
@@ -306,11 +308,12 @@ __device__ __forceinline__ VerifyEnd find_end(const VerifyArgs& a, int b, int le
           const Part Q = rows[n + threadIdx.x];
           near = has_distribution(Q);
           mq = Q.m;
+          sq = Q.s;
           if (near && named) qx = exp((static_cast<double>(dy) - static_cast<double>(Q.m)) * a.inv_t) / Q.s;
         }
         keep = named && near && static_cast<double>(u) * qx < exp(lp);
       }
-      e = {i, named ? static_cast<int>(y) : y >= 0 ? -2 : -1, !ok ? 0 : (y >= 0 && near && !greedy ? 2 : 1), P.m, mq, P.best, P.s};
+      e = {i, named ? static_cast<int>(y) : y >= 0 ? -2 : -1, !ok ? 0 : (y >= 0 && near && !greedy ? 2 : 1), P.m, mq, P.best, P.s, sq};
     }
     // the first place that is not kept (all of them lie in the first wave)
     const uint64_t ends = __ballot(mine && !keep);
@@ -326,20 +329,22 @@ __device__ __forceinline__ VerifyEnd find_end(const VerifyArgs& a, int b, int le
   return end;
 }
 
-// The sums of both over a workgroup, in every thread.
-__device__ __forceinline__ double2 block_sums(double x, double y) {
-  __shared__ double2 lds[kWaves];
-  x = wave_sum(x);
-  y = wave_sum(y);
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = make_double2(x, y);
-  __syncthreads();
-  x = y = 0.0;
-  for (int w = 0; w < kWaves; ++w) {
-    x += lds[w].x;
-    y += lds[w].y;
+// The sums of N values over a workgroup, in every thread.
+template <int N>
+__device__ __forceinline__ void block_sums(double (&x)[N]) {
+  __shared__ double lds[kWaves][N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = wave_sum(x[i]);
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) lds[threadIdx.x >> 6][i] = x[i];
   }
-  __syncthreads();  // (the next sums)
-  return make_double2(x, y);
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = 0.0;
+    for (int w = 0; w < kWaves; ++w) x[i] += lds[w][i];
+  }
 }
 
 // The token `next` (-1: none) at the end of a sequence, and what lies behind it;
@@ -415,45 +420,53 @@ __device__ __forceinline__ void pieces(const T* row, int i, int end, float (&v)[
 // without the drafted token, or max(p - q, 0).
 enum Form { P, LESS, REST };
 
-// Sums over scores [lo, hi) of the row that is drawn from, in every thread: of
-// exp(x) around its maximum, and of exp of the draft's scores, or, without those,
-// of exp(x) without the drafted token.
+// What the second reading sums over a slice of the row that is drawn from: of
+// exp(x) around its maximum, and without draft scores the same without the
+// drafted token; with them of exp of those, and of both over the tokens that
+// have p > q by the first reading's sums.  Those are good to some 2^-27: only
+// a token whose p and q agree as far is taken for one that it is not, and moves
+// the sum of max(p - q, 0) by 2^-27 of what it weighs.
+struct Sums {
+  double p, q, over_p, over_q;
+  __device__ __forceinline__ double left(double ip, double iq) const { return fmax(over_p * ip - over_q * iq, 0.0); }
+};
 template <typename TX, typename TD>
-__device__ __forceinline__ double2 slice_sums(const VerifyArgs& a, int b, const VerifyEnd& e, bool rest, int lo, int hi, const double* table) {
+__device__ __forceinline__ Sums slice_sums(const VerifyArgs& a, int b, const VerifyEnd& e, bool rest, int lo, int hi, const double* table) {
   const Exp p(table, a.kd, e.mp), q(table, a.kd, e.mq);
-  double sp = 0.0, sq = 0.0;
+  const double ratio = rest ? e.sp / e.sq : 0.0;
+  Sums s = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll 1
   for (int i = lo + static_cast<int>(threadIdx.x) * kN; i < hi; i += kThreads * kN) {
     float x[kN], d[kN];
     pieces(row_of<TX>(a.x, b, e.r), i, hi, x);
-    if (rest) pieces(row_of<TD>(a.d, b, e.r), i, hi, d);
-#pragma unroll
-    for (int c = 0; c < kN; ++c) {
-      const double w = p(x[c]);
-      sp += w;
-      if (!rest && i + c != e.y) sq += w;
-    }
     if (rest) {
+      pieces(row_of<TD>(a.d, b, e.r), i, hi, d);
 #pragma unroll
-      for (int c = 0; c < kN; ++c) sq += q(d[c]);
+      for (int c = 0; c < kN; ++c) {
+        const double wp = p(x[c]), wq = q(d[c]);
+        const bool over = wp > wq * ratio;
+        s.p += wp;
+        s.q += wq;
+        s.over_p += over ? wp : 0.0;
+        s.over_q += over ? wq : 0.0;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kN; ++c) {
+        const double w = p(x[c]);
+        s.p += w;
+        if (i + c != e.y) s.q += w;
+      }
     }
   }
-  return block_sums(sp, sq);
-}
-
-// Sum of max(p - q, 0) over scores [lo, hi), in every thread.
-template <typename TX, typename TD>
-__device__ __forceinline__ double slice_rest(const VerifyArgs& a, int b, const VerifyEnd& e, const Rest& w, int lo, int hi) {
-  double s = 0.0;
-#pragma unroll 1
-  for (int i = lo + static_cast<int>(threadIdx.x) * kN; i < hi; i += kThreads * kN) {
-    float x[kN], d[kN];
-    pieces(row_of<TX>(a.x, b, e.r), i, hi, x);
-    pieces(row_of<TD>(a.d, b, e.r), i, hi, d);
-#pragma unroll
-    for (int c = 0; c < kN; ++c) s += w(x[c], d[c]);
+  if (!rest) {
+    double x[2] = {s.p, s.q};
+    block_sums(x);
+    return {x[0], x[1], 0.0, 0.0};
   }
-  return block_sums(s, 0.0).x;
+  double x[4] = {s.p, s.q, s.over_p, s.over_q};
+  block_sums(x);
+  return {x[0], x[1], x[2], x[3]};
 }
 
 // The lowest token of slice [lo, hi) up to which the weights, on top of `run`,
@@ -532,34 +545,39 @@ __device__ __forceinline__ void take_token(const VerifyArgs& a, int b, const Ver
   });
 }
 
-// The token that u picks, by a whole workgroup, once a sequence's sums (and,
-// with draft scores, its weights) are there.
+// The token that u picks, by a whole workgroup, once a sequence's sums are there.
 template <typename TX, typename TD>
 __device__ __forceinline__ void pick_slice(const VerifyArgs& a, int b, const VerifyEnd& e, const double* table) {
   const int lane = threadIdx.x & 63;
   Form form = e.mode == 1 ? P : a.d.base ? REST : LESS;
   const float u = a.uniforms[static_cast<int64_t>(b) * (a.draft + 1) + a.draft];
-  // a lane holds kRun slices' weights
-  double of_p[kRun], of_q[kRun], held[kRun], upto, sum_p = 0.0, sum_q = 0.0;
+  // a lane holds kRun slices' sums
+  Sums of[kRun];
+  double held[kRun], upto, sum_p = 0.0, sum_q = 0.0;
 #pragma unroll
   for (int i = 0; i < kRun; ++i) {
     const int j = kRun * lane + i;
-    const int64_t at = static_cast<int64_t>(b) * a.cuts + j;
-    of_p[i] = of_q[i] = held[i] = 0.0;
+    const uint64_t* at = a.sums + (static_cast<int64_t>(b) * a.cuts + j) * 4;
+    of[i] = {0.0, 0.0, 0.0, 0.0};
     if (j < a.cuts) {
-      of_p[i] = published_double(a.sums + 2 * at);
-      of_q[i] = published_double(a.sums + 2 * at + 1);
-      if (form == REST) held[i] = published_double(a.weights + at);
+      of[i].p = published_double(at);
+      of[i].q = published_double(at + 1);
+      if (form == REST) {
+        of[i].over_p = published_double(at + 2);
+        of[i].over_q = published_double(at + 3);
+      }
     }
   }
 #pragma unroll
   for (int i = 0; i < kRun; ++i) {
-    sum_p += of_p[i];
-    sum_q += of_q[i];
-    if (form != REST) held[i] = form == LESS ? of_q[i] : of_p[i];
+    sum_p += of[i].p;
+    sum_q += of[i].q;
   }
   sum_p = wave_sum(sum_p);
   sum_q = wave_sum(sum_q);
+  const Rest w = {{table, a.kd, e.mp}, {table, a.kd, e.mq}, 1.0 / sum_p, 1.0 / sum_q};
+#pragma unroll
+  for (int i = 0; i < kRun; ++i) held[i] = form == REST ? of[i].left(w.ip, w.iq) : form == LESS ? of[i].q : of[i].p;
   double total = 0.0, own = 0.0;
 #pragma unroll 1
   for (int tries = 0; tries < 2; ++tries) {
@@ -575,7 +593,7 @@ __device__ __forceinline__ void pick_slice(const VerifyArgs& a, int b, const Ver
     if (total > 0.0) break;
     form = P;  // nothing is left over
 #pragma unroll
-    for (int i = 0; i < kRun; ++i) held[i] = of_p[i];
+    for (int i = 0; i < kRun; ++i) held[i] = of[i].p;
   }
   const double want = static_cast<double>(u) * total;
   // the first slice whose running sum exceeds it, else the last with weight
@@ -593,7 +611,6 @@ __device__ __forceinline__ void pick_slice(const VerifyArgs& a, int b, const Ver
   }
   at = __shfl(at, src);
   run = __shfl(run, src);
-  const Rest w = {{table, a.kd, e.mp}, {table, a.kd, e.mq}, 1.0 / sum_p, 1.0 / sum_q};
   const int lo = at * a.cut;
   take_token<TX, TD>(a, b, e, form, w, sum_p, lo, min(lo + a.cut, a.vocab), run, want);
 }
@@ -608,34 +625,16 @@ __global__ __launch_bounds__(kThreads) void verify_sums_kernel(VerifyArgs a) {
   if (e.mode == 0) return;
   const bool rest = e.mode == 2 && a.d.base;
   const int lo = j * a.cut;
-  const double2 s = slice_sums<TX, TD>(a, b, e, rest, lo, min(lo + a.cut, a.vocab), table);
+  const Sums s = slice_sums<TX, TD>(a, b, e, rest, lo, min(lo + a.cut, a.vocab), table);
   if (threadIdx.x == 0) {
-    uint64_t* at = a.sums + (static_cast<int64_t>(b) * a.cuts + j) * 2;
-    publish_double(at, s.x);
-    publish_double(at + 1, s.y);
+    uint64_t* at = a.sums + (static_cast<int64_t>(b) * a.cuts + j) * 4;
+    publish_double(at, s.p);
+    publish_double(at + 1, s.q);
+    if (rest) {
+      publish_double(at + 2, s.over_p);
+      publish_double(at + 3, s.over_q);
+    }
   }
-  if (rest) return;
-  if (last_of_sequence(a, b, j, a.cuts)) pick_slice<TX, TD>(a, b, e, table);
-}
-
-template <typename TX, typename TD>
-__global__ __launch_bounds__(kThreads) void verify_weights_kernel(VerifyArgs a) {
-  __shared__ double table[32];
-  const int b = blockIdx.y, j = blockIdx.x;
-  const VerifyEnd e = a.ends[b];
-  double2 t = make_double2(0.0, 0.0);
-  for (int i = threadIdx.x & 63; i < a.cuts; i += 64) {
-    const double* at = reinterpret_cast<const double*>(a.sums) + (static_cast<int64_t>(b) * a.cuts + i) * 2;
-    t.x += at[0];
-    t.y += at[1];
-  }
-  fill_table(table);
-  __syncthreads();
-  if (e.mode != 2) return;
-  const Rest w = {{table, a.kd, e.mp}, {table, a.kd, e.mq}, 1.0 / wave_sum(t.x), 1.0 / wave_sum(t.y)};
-  const int lo = j * a.cut;
-  const double s = slice_rest<TX, TD>(a, b, e, w, lo, min(lo + a.cut, a.vocab));
-  if (threadIdx.x == 0) publish_double(a.weights + static_cast<int64_t>(b) * a.cuts + j, s);
   if (last_of_sequence(a, b, j, a.cuts)) pick_slice<TX, TD>(a, b, e, table);
 }
 
@@ -721,11 +720,11 @@ __global__ __launch_bounds__(kThreads) void verify_small_kernel(VerifyArgs a) {
   }
   const float u = a.uniforms[static_cast<int64_t>(b) * (a.draft + 1) + a.draft];
   Form form = e.mode == 1 ? P : a.d.base ? REST : LESS;
-  const double2 s = slice_sums<TX, TD>(a, b, e, form == REST, 0, a.vocab, table);
-  const Rest w = {{table, a.kd, e.mp}, {table, a.kd, e.mq}, 1.0 / s.x, 1.0 / s.y};
-  double total = form == REST ? slice_rest<TX, TD>(a, b, e, w, 0, a.vocab) : form == LESS ? s.y : s.x;
-  if (!(total > 0.0)) form = P, total = s.x;
-  take_token<TX, TD>(a, b, e, form, w, s.x, 0, a.vocab, 0.0, static_cast<double>(u) * total);
+  const Sums s = slice_sums<TX, TD>(a, b, e, form == REST, 0, a.vocab, table);
+  const Rest w = {{table, a.kd, e.mp}, {table, a.kd, e.mq}, 1.0 / s.p, 1.0 / s.q};
+  double total = form == REST ? s.left(w.ip, w.iq) : form == LESS ? s.q : s.p;
+  if (!(total > 0.0)) form = P, total = s.p;
+  take_token<TX, TD>(a, b, e, form, w, s.p, 0, a.vocab, 0.0, static_cast<double>(u) * total);
 }
 
 template <typename TX, typename TD>
@@ -751,7 +750,6 @@ hipError_t go(hipStream_t s, VerifyArgs a, int b0, int n) {
   } else {
     verify_pairs_kernel<TX, TD, false><<<grid, kThreads, 0, s>>>(a);
     verify_sums_kernel<TX, TD><<<cuts, kThreads, 0, s>>>(a);
-    if (a.d.base) verify_weights_kernel<TX, TD><<<cuts, kThreads, 0, s>>>(a);
   }
   return hipGetLastError();
 }
@@ -782,8 +780,7 @@ VerifyPlan verify_plan(int64_t batch, int64_t draft, int64_t vocab, int bytes) {
   };
   p.parts = take(2 * sizeof(uint64_t) * static_cast<size_t>(p.launch) * static_cast<size_t>(p.rows) * static_cast<size_t>(p.slices));
   p.ends = take(sizeof(VerifyEnd) * static_cast<size_t>(p.launch));
-  p.sums = take(2 * sizeof(uint64_t) * static_cast<size_t>(p.launch) * static_cast<size_t>(p.cuts));
-  p.weights = take(sizeof(uint64_t) * static_cast<size_t>(p.launch) * static_cast<size_t>(p.cuts));
+  p.sums = take(4 * sizeof(uint64_t) * static_cast<size_t>(p.launch) * static_cast<size_t>(p.cuts));
   p.total = at;
   return p;
 }
@@ -803,7 +800,6 @@ hipError_t launch_verify(hipStream_t s, VerifyArgs a, int64_t batch, const Verif
   a.parts = reinterpret_cast<uint64_t*>(ws + p.parts);
   a.ends = reinterpret_cast<VerifyEnd*>(ws + p.ends);
   a.sums = reinterpret_cast<uint64_t*>(ws + p.sums);
-  a.weights = reinterpret_cast<uint64_t*>(ws + p.weights);
   for (int64_t b0 = 0; b0 < batch; b0 += p.launch) {
     const int n = static_cast<int>(batch - b0 < p.launch ? batch - b0 : p.launch), b = static_cast<int>(b0);
     hipError_t e;

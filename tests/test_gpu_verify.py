@@ -136,6 +136,22 @@ def test_masked_scores(ctx):
     check(ctx, x, y, d, u, 0.0)
 
 
+@pytest.mark.parametrize("vocab", [300, 3001, 40000])
+def test_the_lowest_number_passes_over_masked_tokens(ctx, vocab):
+    """u = 0 takes the first token with any probability, u = 1 the last."""
+    x, y, d, u = make(6, 1, vocab, F32, 8)
+    x[..., :9] = x[..., -5:] = -float("inf")
+    d[:, :, 20:30] = -float("inf")
+    x[1, :, 12] = -2000.0  # as good as masked, in 64 bits too
+    u[:, 0] = 1.0
+    u[::2, 1], u[1::2, 1] = 0.0, 1.0
+    for scores in (d, None):
+        for end in (0.0, 1.0):
+            u[:, 1] = end
+            tokens = check(ctx, x, y, scores, u, 1.0)[0]
+            assert ((tokens < 0) | (tokens >= 9) & (tokens < vocab - 5)).all()
+
+
 @pytest.mark.parametrize("t", [1.0, 0.0])
 @pytest.mark.parametrize("vocab", [40, 3001, 40000])
 def test_rows_without_a_distribution(ctx, vocab, t):
