@@ -31,9 +31,10 @@ _DT = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
 
 
 def _dtype(t: torch.Tensor) -> int:
-    if t.dtype not in _DT:
+    dt = _DT.get(t.dtype)
+    if dt is None:
         raise TypeError(f"unsupported dtype {t.dtype}; libmuon takes float32 or bfloat16")
-    return _DT[t.dtype]
+    return dt
 
 
 def _stream(device: torch.device, stream) -> int:
@@ -215,18 +216,21 @@ def verify_workspace_bytes(batch: int, draft: int, vocab: int) -> int:
 def _rows(t: torch.Tensor, name: str, device: torch.device) -> Rows:
     """Values as [rows, cols], or [..., cols] whose leading dimensions are rows
     at one stride; the columns contiguous."""
-    if not t.is_cuda or t.device != device:
+    if t.device != device:
         raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dim() < 2:
-        raise ValueError(f"{name} must be [rows, cols]")
-    if t.dim() > 2:
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2:
+        if len(shape) < 2:
+            raise ValueError(f"{name} must be [rows, cols]")
         try:
-            t = t.flatten(0, -2) if t.numel() == 0 else t.view(-1, t.shape[-1])
+            t = t.flatten(0, -2) if t.numel() == 0 else t.view(-1, shape[-1])
         except RuntimeError:
             raise ValueError(f"the rows of {name} lie at no one stride") from None
-    if t.shape[1] > 1 and t.stride(1) != 1:
+        shape, stride = t.shape, t.stride()
+    rows, cols = shape
+    if stride[1] != 1 and cols > 1:
         raise ValueError(f"the columns of {name} must be contiguous")
-    return Rows(t.data_ptr(), _dtype(t), t.shape[0], t.shape[1], t.stride(0))
+    return Rows(t.data_ptr(), _dtype(t), rows, cols, stride[0])
 
 
 class Rows8:
@@ -246,9 +250,8 @@ class Rows8:
             raise TypeError("scale must be float32")
         if scale.shape != q.shape[:1]:
             raise ValueError("scale must hold one number per row")
-        self.q, self.scale = q, scale
+        self.q, self.scale, self.device = q, scale, q.device
         self.struct = _lib.Rows8(q.data_ptr(), scale.data_ptr(), q.shape[0], q.shape[1], q.stride(0))
-        self.ref = ctypes.byref(self.struct)
 
     @property
     def shape(self):
@@ -500,29 +503,31 @@ class Context:
         q = torch.empty(rows, (cols + 15) // 16 * 16, dtype=torch.int8, device=self.device)
         return Rows8(q[:, :cols], torch.empty(rows, dtype=torch.float32, device=self.device))
 
+    # (where a pointer is asked for ctypes takes the struct itself, 0.5 us a call
+    # faster than its byref)
     def _rows8(self, x: Rows8, name: str):
-        if x.q.device != self.device:
+        if x.device != self.device:
             raise ValueError(f"{name} must be on {self.device}")
-        return x.ref
+        return x.struct
 
     def quantize_rows(self, x: torch.Tensor, x8: Rows8, stream=None):
         """The rows of x (bf16 or float32, any row stride) in 8 bits with a scale
         each: the largest magnitude becomes 127."""
         r = _rows(x, "x", self.device)
-        self._raise(self.lib.muon_quantize_rows(self.handle, _stream(self.device, stream), ctypes.byref(r),
+        self._raise(self.lib.muon_quantize_rows(self.handle, _stream(self.device, stream), r,
                                                 self._rows8(x8, "x8")), "muon_quantize_rows")
 
     def dequantize_rows(self, x8: Rows8, out: torch.Tensor, stream=None):
         """The values that 8-bit rows stand for (bf16 or float32)."""
         r = _rows(out, "out", self.device)
         self._raise(self.lib.muon_dequantize_rows(self.handle, _stream(self.device, stream), self._rows8(x8, "x8"),
-                                                  ctypes.byref(r)), "muon_dequantize_rows")
+                                                  r), "muon_dequantize_rows")
 
     def matmul8(self, a: Rows8, b: Rows8, out: torch.Tensor, stream=None):
         """out = a b^T, summed in integers (bf16 or float32)."""
         r = _rows(out, "out", self.device)
         self._raise(self.lib.muon_matmul8(self.handle, _stream(self.device, stream), self._rows8(a, "a"),
-                                          self._rows8(b, "b"), ctypes.byref(r)), "muon_matmul8")
+                                          self._rows8(b, "b"), r), "muon_matmul8")
 
     def linear8(self, x: torch.Tensor, w: Rows8, out: torch.Tensor, x8: Optional[Rows8] = None, stream=None):
         """out = x w^T in 8 bits: x [tokens, k] is quantised by token, w holds a
@@ -530,23 +535,23 @@ class Context:
         the backward pass (weight_grad8); None: they are not kept.  As every
         call here no autograd function."""
         r, o = _rows(x, "x", self.device), _rows(out, "out", self.device)
-        self._raise(self.lib.muon_linear8(self.handle, _stream(self.device, stream), ctypes.byref(r), self._rows8(w, "w"),
-                                          None if x8 is None else self._rows8(x8, "x8"), ctypes.byref(o)), "muon_linear8")
+        self._raise(self.lib.muon_linear8(self.handle, _stream(self.device, stream), r, self._rows8(w, "w"),
+                                          None if x8 is None else self._rows8(x8, "x8"), o), "muon_linear8")
 
     def input_grad8(self, grad_y: torch.Tensor, w: Rows8, grad_x: torch.Tensor, accumulate: bool = False, stream=None):
         """Gradient of linear8 in x: grad_x (+)= grad_y w.  grad_y: bf16
         [tokens, n]; grad_x: bf16 or float32."""
         y, o = _rows(grad_y, "grad_y", self.device), _rows(grad_x, "grad_x", self.device)
-        self._raise(self.lib.muon_input_grad8(self.handle, _stream(self.device, stream), ctypes.byref(y), self._rows8(w, "w"),
-                                              ctypes.byref(o), 1 if accumulate else 0), "muon_input_grad8")
+        self._raise(self.lib.muon_input_grad8(self.handle, _stream(self.device, stream), y, self._rows8(w, "w"),
+                                              o, 1 if accumulate else 0), "muon_input_grad8")
 
     def weight_grad8(self, grad_y: torch.Tensor, x8: Rows8, grad_w: torch.Tensor, accumulate: bool = False, stream=None):
         """Gradient of linear8 in the weights, out of the kept activations:
         grad_w (+)= grad_y^T x8.  grad_w: bf16 or float32 [n, k], e.g. a view of
         MuonStep.grad."""
         y, o = _rows(grad_y, "grad_y", self.device), _rows(grad_w, "grad_w", self.device)
-        self._raise(self.lib.muon_weight_grad8(self.handle, _stream(self.device, stream), ctypes.byref(y),
-                                               self._rows8(x8, "x8"), ctypes.byref(o), 1 if accumulate else 0),
+        self._raise(self.lib.muon_weight_grad8(self.handle, _stream(self.device, stream), y,
+                                               self._rows8(x8, "x8"), o, 1 if accumulate else 0),
                     "muon_weight_grad8")
 
     # -- verification of drafted tokens -----------------------------------------
@@ -572,9 +577,9 @@ class Context:
         if draft_logits is not None:
             if draft_logits.shape != (*draft, logits.shape[2]):
                 raise ValueError("draft_logits must be [batch, draft, vocab]")
-            d = ctypes.byref(_logits(draft_logits, "draft_logits", dev))
+            d = _logits(draft_logits, "draft_logits", dev)
         st = self.lib.muon_verify_draft(
-            self.handle, _stream(dev, stream), ctypes.byref(x), _tokens(draft_tokens, "draft_tokens", draft, torch.int64, dev), d,
+            self.handle, _stream(dev, stream), x, _tokens(draft_tokens, "draft_tokens", draft, torch.int64, dev), d,
             _tokens(uniforms, "uniforms", places, torch.float32, dev), temperature,
             _tokens(tokens, "tokens", places, torch.int64, dev), _tokens(accepted, "accepted", places[:1], torch.int64, dev),
             _tokens(logps, "logps", places, torch.float32, dev))

@@ -373,15 +373,23 @@ __global__ __launch_bounds__(256) void grad8_join_kernel(Grad8Args a, TileWork w
   const int64_t m = static_cast<int64_t>(unit.ti) * TM + row, n = static_cast<int64_t>(unit.tj) * TN + c;
   if (m >= a.m || n >= a.n) return;
   float4 v = *reinterpret_cast<const float4*>(part);
+#pragma unroll 4
   for (int p = 1; p < work.splits; ++p) {
     const float4 w = *reinterpret_cast<const float4*>(part + static_cast<int64_t>(p) * (TM * TN));
     v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
   }
   O* to = reinterpret_cast<O*>(a.out.p) + m * a.out.ld + n;
-  const float f[4] = {v.x, v.y, v.z, v.w};
+  float f[4] = {v.x, v.y, v.z, v.w};
+  if (a.accumulate) {  // all of them before the first store, which may be to any
+    float was[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) was[q] = n + q < a.n ? muon::Elem<O>::load(to + q) : 0.0f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) f[q] += was[q];
+  }
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    if (n + q < a.n) muon::Elem<O>::store(to + q, a.accumulate ? muon::Elem<O>::load(to + q) + f[q] : f[q]);
+    if (n + q < a.n) muon::Elem<O>::store(to + q, f[q]);
 }
 
 template <typename O, int TM, int TN, int NWN, int PARTS>

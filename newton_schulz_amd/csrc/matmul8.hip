@@ -551,6 +551,7 @@ __global__ __launch_bounds__(256) void matmul8_join_kernel(Matmul8Args a, TileWo
   const int64_t m = static_cast<int64_t>(unit.ti) * T + row, n = static_cast<int64_t>(unit.tj) * T + c;
   if (m >= a.m || n >= a.n) return;
   i32x4_t v = *reinterpret_cast<const i32x4_t*>(part);
+#pragma unroll 4
   for (int p = 1; p < work.splits; ++p) v += *reinterpret_cast<const i32x4_t*>(part + static_cast<int64_t>(p) * (T * T));
   O* to = reinterpret_cast<O*>(a.out.p) + m * a.out.ld + n;
   const float sa = a.a.scale[m];
