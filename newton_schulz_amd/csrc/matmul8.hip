@@ -233,23 +233,25 @@ hipError_t go_staged(hipStream_t s, const Matmul8Args& a) {
   matmul8_stream_kernel<O, FROM, 1, MG, KS, XB><<<static_cast<unsigned>(groups < cap ? groups : cap), 64 * KS, 0, s>>>(a);
   return hipGetLastError();
 }
-constexpr int kStagedSmall = 16 << 10, kStagedMost = 44 << 10, kStagedWide = 124 << 10;
+// 16 KB of rows leave room for eight workgroups of four waves a CU, 44 KB for three.
+// Beyond, every workgroup reads them through L1: sixteen rows of 4096 (64 KB) for
+// 9728, 32000 (13 rows) and 151936 columns 13, 33 and 153 us, staged by
+// workgroups of sixteen waves 15, 38 and 165.
+constexpr int kStagedSmall = 16 << 10, kStagedMost = 44 << 10;
 inline int64_t staged_bytes(const Matmul8Args& a) { return a.m * ((a.k + 63) / 64) * 64; }
 
 template <typename O, typename FROM, int MG>
 hipError_t go_staged(hipStream_t s, const Matmul8Args& a) {
   if (staged_bytes(a) <= kStagedSmall) return go_staged<O, FROM, MG, 4, kStagedSmall>(s, a);
-  if constexpr (std::is_same_v<FROM, Staged>) {
-    if (staged_bytes(a) <= kStagedMost) return go_staged<O, FROM, MG, 4, kStagedMost>(s, a);
-    return go_staged<O, FROM, MG, 16, kStagedWide>(s, a);
-  }
+  if constexpr (std::is_same_v<FROM, Staged>) return go_staged<O, FROM, MG, 4, kStagedMost>(s, a);
   return hipErrorInvalidValue;
 }
 template <typename O, int NB, int MG>
 hipError_t go_stream(hipStream_t s, const Matmul8Args& a) {
   const int64_t groups = (a.n + 16 * NB - 1) / (16 * NB);
   const unsigned grid = static_cast<unsigned>(groups);
-  // four waves a workgroup, sixteen where there are fewer workgroups than CUs
+  // four waves a workgroup, sixteen where there are fewer workgroups than CUs (one
+  // row of 9728 for 2560 columns 8.5 us against 9.5)
   if constexpr (NB == 1) {
     if (groups < a.cus) {
       matmul8_stream_kernel<O, Bytes8, NB, MG, 16, 0><<<grid, 1024, 0, s>>>(a);
@@ -262,8 +264,9 @@ hipError_t go_stream(hipStream_t s, const Matmul8Args& a) {
 template <typename O, int MG>
 hipError_t go_stream(hipStream_t s, const Matmul8Args& a) {
   if constexpr (MG <= 2) {
-    // (staged rows serve a workgroup's columns one after another: not where there are few)
-    if (staged_bytes(a) <= kStagedWide && a.n >= 16 * a.cus) return go_staged<O, Staged, MG>(s, a);
+    // (staged rows serve a workgroup's columns one after another: not where there are
+    // few; sixteen rows of 2560 for 2560 and 3968 columns 5.1 and 5.3 us, staged 5.8 and 6.5)
+    if (staged_bytes(a) <= kStagedMost && a.n >= 16 * a.cus) return go_staged<O, Staged, MG>(s, a);
   }
   return go_stream<O, 1, MG>(s, a);
 }

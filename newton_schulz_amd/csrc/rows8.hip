@@ -134,8 +134,10 @@ void quantize(hipStream_t s, const Values& x, const Bytes& q, int64_t rows, int 
 template <typename T>
 hipError_t quantize(hipStream_t s, const Values& x, const Bytes& q, int64_t rows, int cols) {
   const int pieces = (cols + Piece<T>::N - 1) / Piece<T>::N;
-  // A wave's lanes hold up to 512 pieces; where there are few rows more threads read one sooner.
-  if (pieces <= 64 * kHeld && (rows >= 1024 || pieces <= 64)) quantize<T, 64>(s, x, q, rows, cols);
+  // A row per wave up to five pieces a lane where there are many, else per workgroup:
+  // 8192 x 2560 bf16 16 us against 18, 4096 x 1024 5 against 8; 8192 x 4096 23 against
+  // 21, 1024 x 4096 8 against 5 (there and for few rows a workgroup asks for one sooner).
+  if (pieces <= 64 || (pieces <= 5 * 64 && rows >= 2048)) quantize<T, 64>(s, x, q, rows, cols);
   else if (pieces <= 256 * kHeld) quantize<T, 256>(s, x, q, rows, cols);
   else quantize<T, 1024>(s, x, q, rows, cols);
   return hipGetLastError();

@@ -37,7 +37,6 @@ namespace {
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr int kRun = 4, kMostCuts = 64 * kRun;  // slices of the second reading that a lane holds, and of a row
 constexpr int kN = 8, kMostCut = kThreads * kN;  // scores that a thread takes at a time, and of a slice of the second reading
-constexpr int kMostSmall = 2 * kMostCut;         // of a row that one workgroup takes
 // Counters of a sequence: of 32 workgroups each, then one of those; in lines of their own.
 constexpr int kTogether = 32, kCounterStride = 8;
 constexpr float kLowest = -FLT_MAX;
@@ -638,8 +637,11 @@ __global__ __launch_bounds__(kThreads) void verify_sums_kernel(VerifyArgs a) {
   if (last_of_sequence(a, b, j, a.cuts)) pick_slice<TX, TD>(a, b, e, table);
 }
 
-// Vocabularies of one slice and few rows: all of it in one workgroup a sequence.
-constexpr int kSmallRows = 32, kSmall = 1 << 15;
+// Few rows, three a wave at once, of one slice of the second reading: all of it in
+// one workgroup a sequence.  Against the launches over slices (2 draft + 1 rows):
+// 9 x 1000 scores 12.6 us against 14.2, 11 x 1000 12.5 against 14.3, 64 sequences of
+// 9 x 2048 15.1 against 16.3; 17 x 64 15.0 against 14.7, 5 x 3000 17.5 against 13.9.
+constexpr int kAtOnceRows = 3, kSmallRows = kAtOnceRows * kWaves, kSmall = kMostCut;
 
 template <typename TX, typename TD>
 __global__ __launch_bounds__(kThreads) void verify_small_kernel(VerifyArgs a) {
@@ -650,65 +652,62 @@ __global__ __launch_bounds__(kThreads) void verify_small_kernel(VerifyArgs a) {
   const Scale q(a);
   fill_table(table);
   const int len = drafted_places(a, b);
-  // a wave per row, three rows of a wave at once
-  constexpr int R = 3;
-  for (int i0 = wave; i0 < a.rows; i0 += R * kWaves) {
-    float m[R];
-    double s[R];
-    int best[R];
-    auto place_of = [&](int i) { return i <= a.draft ? i : i - a.draft - 1; };
-    auto needed = [&](int i) { return i < a.rows && (i <= a.draft ? i <= len : place_of(i) < len); };
+  constexpr int R = kAtOnceRows;
+  float m[R];
+  double sum[R];
+  int best[R];
+  auto place_of = [&](int i) { return i <= a.draft ? i : i - a.draft - 1; };
+  auto needed = [&](int i) { return i < a.rows && (i <= a.draft ? i <= len : place_of(i) < len); };
 #pragma unroll
-    for (int r = 0; r < R; ++r) m[r] = kLowest, s[r] = 0.0, best[r] = INT32_MAX;
+  for (int r = 0; r < R; ++r) m[r] = kLowest, sum[r] = 0.0, best[r] = INT32_MAX;
 #pragma unroll 1
-    for (int v0 = lane * kN; v0 - lane * kN < a.vocab; v0 += 128 * kN) {
-      float v[R][2 * kN];
+  for (int v0 = lane * kN; v0 - lane * kN < a.vocab; v0 += 128 * kN) {
+    float v[R][2 * kN];
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const int i = i0 + r * kWaves;
-        if (!needed(i)) continue;
+    for (int r = 0; r < R; ++r) {
+      const int i = wave + r * kWaves;
+      if (!needed(i)) continue;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float half[kN];
-          if (i <= a.draft) pieces(row_of<TX>(a.x, b, i), v0 + h * 64 * kN, a.vocab, half);
-          else pieces(row_of<TD>(a.d, b, place_of(i)), v0 + h * 64 * kN, a.vocab, half);
+      for (int h = 0; h < 2; ++h) {
+        float half[kN];
+        if (i <= a.draft) pieces(row_of<TX>(a.x, b, i), v0 + h * 64 * kN, a.vocab, half);
+        else pieces(row_of<TD>(a.d, b, place_of(i)), v0 + h * 64 * kN, a.vocab, half);
 #pragma unroll
-          for (int c = 0; c < kN; ++c) v[r][h * kN + c] = half[c];
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < R; ++r) {
-        if (!needed(i0 + r * kWaves)) continue;
-        float top = m[r];
-#pragma unroll
-        for (int c = 0; c < 2 * kN; ++c) top = fmaxf(top, v[r][c]);
-        top = wave_max(top);
-        if (top > m[r]) {
-          s[r] *= q.exp(m[r] - top);
-          m[r] = top;
-          best[r] = INT32_MAX;
-        }
-        float e[2 * kN];
-#pragma unroll
-        for (int c = 2 * kN - 1; c >= 0; --c) {
-          e[c] = __builtin_amdgcn_exp2f((v[r][c] - top) * q.each[c % 8]);
-          if (v[r][c] == top) best[r] = min(best[r], v0 + (c / kN) * 64 * kN + c % kN);
-        }
-#pragma unroll
-        for (int h = kN; h > 0; h /= 2)
-#pragma unroll
-          for (int c = 0; c < h; ++c) e[c] += e[c + h];
-        s[r] += static_cast<double>(e[0]);
+        for (int c = 0; c < kN; ++c) v[r][h * kN + c] = half[c];
       }
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const int i = i0 + r * kWaves;
-      if (!needed(i)) continue;
-      const double sum = wave_sum(s[r]);
-      const int at = wave_min(best[r]);
-      if (lane == 0) parts[i] = {m[r], at, m[r] == INFINITY ? static_cast<double>(NAN) : sum};
+      if (!needed(wave + r * kWaves)) continue;
+      float top = m[r];
+#pragma unroll
+      for (int c = 0; c < 2 * kN; ++c) top = fmaxf(top, v[r][c]);
+      top = wave_max(top);
+      if (top > m[r]) {
+        sum[r] *= q.exp(m[r] - top);
+        m[r] = top;
+        best[r] = INT32_MAX;
+      }
+      float e[2 * kN];
+#pragma unroll
+      for (int c = 2 * kN - 1; c >= 0; --c) {
+        e[c] = __builtin_amdgcn_exp2f((v[r][c] - top) * q.each[c % 8]);
+        if (v[r][c] == top) best[r] = min(best[r], v0 + (c / kN) * 64 * kN + c % kN);
+      }
+#pragma unroll
+      for (int h = kN; h > 0; h /= 2)
+#pragma unroll
+        for (int c = 0; c < h; ++c) e[c] += e[c + h];
+      sum[r] += static_cast<double>(e[0]);
     }
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int i = wave + r * kWaves;
+    if (!needed(i)) continue;
+    const double all = wave_sum(sum[r]);
+    const int at = wave_min(best[r]);
+    if (lane == 0) parts[i] = {m[r], at, m[r] == INFINITY ? static_cast<double>(NAN) : all};
   }
   __syncthreads();
   const VerifyEnd e = find_end<TX, TD>(a, b, len, 1, [&](int row, int) { return parts[row]; });
@@ -738,9 +737,7 @@ hipError_t go(hipStream_t s, VerifyArgs a, int b0, int n) {
   a.accepted += b0;
   if (a.logps) a.logps += places;
   const unsigned nb = static_cast<unsigned>(n);
-  // One workgroup for a sequence, against three launches over slices: measured
-  // where the rows hold up to kSmall scores in all.
-  if (a.vocab <= kMostSmall && a.rows <= kSmallRows && a.rows * a.vocab <= kSmall) {
+  if (a.vocab <= kSmall && a.rows <= kSmallRows) {
     verify_small_kernel<TX, TD><<<nb, kThreads, 0, s>>>(a);
     return hipGetLastError();
   }
