@@ -678,7 +678,7 @@ muon_status_t muon_linear8(muon_ctx_t* ctx, void* stream, const muon_rows_t* x,
  * grad_y: tokens x n, BF16.  bf16 matrix products accumulated in fp32.  For a
  * BF16 output the values of w (x) are rounded to bf16 (2^-8, what activations
  * kept in bf16 would have); for an F32 output they enter as the fp32 values
-  * scale * q (as three bf16 parts).  accumulate != 0: the sum is added to what
+ * scale * q (as three bf16 parts).  accumulate != 0: the sum is added to what
  * the output holds (in fp32, one rounding), else it replaces it. */
 muon_status_t muon_input_grad8(muon_ctx_t* ctx, void* stream, const muon_rows_t* grad_y,
                                const muon_rows8_t* w, const muon_rows_t* grad_x,
@@ -713,8 +713,10 @@ size_t muon_verify_workspace_bytes(int64_t batch, int64_t draft, int64_t vocab);
  * token v that is drawn by u = uniforms[draft] from the weights
  *     w_v = max(p_r(v) - q_r(v), 0)     (no drafted token, or all of them 0: p_r(v)):
  * the lowest v with w_v > 0 and sum_{j <= v} w_j > u sum_j w_j (if none: the
- * last with w_v > 0).  Probabilities are compared, and the weights formed and
- * added, in binary64.  temperature 0: a drafted token is kept while it is the
+ * last with w_v > 0).  The comparison's probabilities divide by sums of fp32
+ * exponentials, added in binary64 (good to 2^-22); the weights are formed and
+ * added in binary64, exponentials below 2^-1000 of a row's largest are 0.
+ * temperature 0: a drafted token is kept while it is the
  * row's largest score (ties: the lowest index), and that is the token taken
  * at place r; uniforms and draft_logits are not read.
  * A row with NaN or +infinity among its scores, or nothing but -infinity, has
