@@ -44,9 +44,11 @@ __device__ __forceinline__ i32x4_t row_tail(const int8_t* row, int k, int end) {
   return i32x4_t{static_cast<int>(lo), static_cast<int>(lo >> 32), static_cast<int>(hi), static_cast<int>(hi >> 32)};
 }
 
-// Bound: HBM, the bytes of b.  One row of 2560 for 9728 columns 8.4 us with its call
-// (rounded in the same launch), for 151936 columns 80 (4.9 TB/s), sixteen 87.
-// Asking for the next columns' bytes before the sums are joined made 92 us 97.
+// Bound: HBM, the bytes of b.  One row of 2560 for 9728 columns 7.6 us with its call
+// (rounded in the same launch), for 151936 columns 69 (5.6 TB/s), six 79, sixteen
+// 87 (4.6 TB/s).  Asking for each next batch before the one in front is used, over
+// the columns' ends, made 92 us 97, batches of ten instead of eight 86 to 92 (and of
+// twelve, sixteen, or of all alike, no better).
 //
 // Up to 16 MG rows of a by 16 NB columns (rows of b) at a time; a workgroup's KS
 // waves share the contraction.  b's 16 rows by 64 bytes are one matrix-core
@@ -72,6 +74,19 @@ __global__ __launch_bounds__(64 * KS) void matmul8_stream_kernel(Matmul8Args a) 
   const int steps = (a.k + 63) / 64, per = (steps + KS - 1) / KS, s0 = min(wave * per, steps), s1 = min(s0 + per, steps), full = min(s1, a.k / 64);
   const int8_t* pa[MG];
   const char* xa[MG];
+  // the first steps' bytes of b are on their way while the rows are rounded (one row
+  // for 9728 columns 8.3 us against 9.1)
+  constexpr bool AHEAD = LDS && !std::is_same_v<FROM, Staged>;
+  const bool ahead = AHEAD && s0 + U <= full;
+  i32x4_t first[AHEAD ? U : 1];
+  if constexpr (AHEAD) {
+    static_assert(NB == 1, "one operand of b a step");
+    if (ahead) {
+      const int8_t* at = a.b.p + min(static_cast<int64_t>(blockIdx.x) * 16 + r, a.n - 1) * a.b.ld;
+#pragma unroll
+      for (int u = 0; u < U; ++u) first[u] = *reinterpret_cast<const i32x4_t*>(at + 64 * (s0 + u) + 16 * h);
+    }
+  }
   if constexpr (LDS) {
     // 16-byte chunk c of row i at (c m + i) 16: a step's operand lies together;
     // zeros behind k, so that whatever b's rows hold there meets nothing
@@ -181,6 +196,15 @@ __global__ __launch_bounds__(64 * KS) void matmul8_stream_kernel(Matmul8Args a) 
           for (int j = 0; j < MG; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vb[u][i], va[u][j], acc[i][j], 0, 0, 0);
     };
     int s = s0;
+    if constexpr (AHEAD) {
+      if (ahead && g == blockIdx.x) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int j = 0; j < MG; ++j) acc[0][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(first[u], of_a(s + u, j), acc[0][j], 0, 0, 0);
+        s += U;
+      }
+    }
     for (; s + U <= full; s += U) some(s, ic<U>{});
     if constexpr (U > 2)
       for (; s + 2 <= full; s += 2) some(s, ic<2>{});
@@ -229,15 +253,17 @@ __global__ __launch_bounds__(64 * KS) void matmul8_stream_kernel(Matmul8Args a) 
   }
 }
 
-// a in LDS: as many workgroups as find room on the CUs.
+// a in LDS: as many workgroups as find room on the CUs, by LDS and by registers (some
+// 110 a lane: four waves a SIMD).  With eight asked for where four fit, the columns
+// of those that wait come last: one row for 151936 columns 74 us against 69.
 template <typename O, typename FROM, int MG, int KS, int XB>
 hipError_t go_staged(hipStream_t s, const Matmul8Args& a) {
-  constexpr int bytes = XB + KS * MG * 1024 + 64 * MG, room = 160 * 1024 / bytes, waves = 32 / KS;
+  constexpr int bytes = XB + KS * MG * 1024 + 64 * MG, room = 160 * 1024 / bytes, waves = 16 / KS;
   const int64_t groups = (a.n + 15) / 16, cap = static_cast<int64_t>(a.cus) * (room < waves ? room : waves);
   matmul8_stream_kernel<O, FROM, 1, MG, KS, XB><<<static_cast<unsigned>(groups < cap ? groups : cap), 64 * KS, 0, s>>>(a);
   return hipGetLastError();
 }
-// 16 KB of rows leave room for eight workgroups of four waves a CU, 44 KB for three.
+// 16 KB of rows leave room for eight workgroups a CU, 44 KB for three.
 // Beyond, every workgroup reads them through L1: sixteen rows of 4096 (64 KB) for
 // 9728, 32000 (13 rows) and 151936 columns 13, 33 and 153 us, staged by
 // workgroups of sixteen waves 15, 38 and 165.
