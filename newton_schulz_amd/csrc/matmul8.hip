@@ -401,8 +401,14 @@ __global__ __launch_bounds__(T == 256 ? 512 : 256, 1) void matmul8_tile_kernel(M
 
   const int G = static_cast<int>(gridDim.x), hw = static_cast<int>(blockIdx.x);
   const int first = G % 8 == 0 ? (hw % 8) * (G / 8) + hw / 8 : hw;
-  for (int l = first; l < work.units; l += G) {
-    const TileUnit unit = tile_unit(work, l);
+  // The XCDs begin at four places of their tiles: those cut into parts then end the
+  // others' out of step, and not all stores come at once.  8192 x 9728 x 2560 243 us
+  // with its rounding in step, 239 with every other XCD's in reverse, 235 so.
+  const int count = (work.units - first + G - 1) / G;
+  const int shift = (hw & 3) * count >> 2;
+  for (int i = 0; i < count; ++i) {
+    const int nth = i + shift;
+    const TileUnit unit = tile_unit(work, first + (nth < count ? nth : nth - count) * G);
     const int64_t m0 = static_cast<int64_t>(unit.ti) * T, n0 = static_cast<int64_t>(unit.tj) * T;
 
     i32x16_t acc[FM][FN];
