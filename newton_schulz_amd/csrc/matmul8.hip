@@ -317,9 +317,9 @@ hipError_t go_stream(hipStream_t s, const Matmul8Args& a) {
 // so that the waves' reads meet no conflict.  256 x 256: eight waves of 128 x 64,
 // eight products of 32 x 32 x 32 for six reads, 128 KB of LDS, one workgroup a CU;
 // 128 x 128: four waves of 64 x 64, two a CU, where the plan finds those sooner.
-// 8192 x 9728 x 2560 with bf16 outputs: 230 to 242 us, 1.69 to 1.77 POP/s (a
-// library's product that leaves 32-bit integers 212); matrix cores busy 0.45 of
-// the cycles, a stage 1.9 us, start and end of a tile 9.  Tiles of 256 x 128 by four
+// 8192 x 9728 x 2560 with bf16 outputs: 222 to 227 us, 1.8 POP/s (a library's
+// product that leaves 32-bit integers 212); matrix cores busy 0.48 of the
+// cycles, a stage 1.9 us, start and end of a tile 9.  Tiles of 256 x 128 by four
 // waves, two workgroups a CU, whose ends would overlap: 254 us.
 // ---------------------------------------------------------------------------
 constexpr int kBytes = 128;  // of k in a stage
