@@ -5,7 +5,7 @@
 // whole rounds would keep few of them busy, so each of those tiles is cut along
 // the contraction into `splits` parts, whose sums go to the workspace and are
 // joined, in order, by a launch more.  8192 x 2560 out of 9728 (gradient of the
-// inputs, 320 tiles of 256 x 256 on 256 CUs): 645 us in two rounds, 457 with
+// inputs, 320 tiles of 256 x 256 on 256 CUs): 645 us in two rounds, 430 with
 // the last 64 tiles in four parts each.
 #pragma once
 

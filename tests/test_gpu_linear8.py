@@ -524,3 +524,36 @@ def test_workspace_is_what_a_call_needs():
     c.weight_grad8(gy, eight(c, t, k, 3), torch.empty(n, k, device=DEV))
     torch.cuda.synchronize()
     c.close()
+
+
+@pytest.mark.parametrize("rows,cols", [(2047, 2560), (2048, 2560), (2049, 2561), (2048, 2568), (1030, 1281), (3, 512), (3, 513)])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_rows_of_a_wave_and_of_a_workgroup(ctx, dtype, rows, cols):
+    """Either side of the sizes at which a row goes to a wave or to a workgroup."""
+    x, out = values(rows, cols, dtype, cols), ctx.rows8(rows, cols)
+    ctx.quantize_rows(x, out)
+    q, s = lo.quantize_ref(x.float().cpu().numpy())
+    assert np.array_equal(out.scale.cpu().numpy(), s) and np.array_equal(out.q.cpu().numpy(), q)
+
+
+@pytest.mark.parametrize("m,n,k", [
+    (13, 17003, 2560), (16, 4096, 2816), (16, 4096, 2817), (16, 4095, 2816), (32, 4100, 1408), (5, 20005, 3000),
+    (17, 30001, 100), (16, 4099, 1024), (16, 4099, 1025), (64, 8192, 130), (64, 8193, 130),
+])
+def test_few_rows_by_many_columns(ctx, m, n, k):
+    """Rows held by workgroups that walk the columns, up to what one holds, and beyond."""
+    check_product(ctx, eight(ctx, m, k, m + k, least=-128), eight(ctx, n, k, n, least=-128), BF)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("m,n,k", [(1, 40003, 2560), (6, 17000, 2560), (1, 20000, 2047), (3, 30005, 200), (16, 20001, 1024), (20, 9000, 777),
+                                   (4, 40, 4096), (4, 17001, 4097)])
+def test_rounding_on_the_way_to_many_columns(ctx, dtype, m, n, k):
+    """linear8 in one launch, several columns' groups a workgroup; and just beyond its room."""
+    x, w, x8 = values(m, k, dtype, m + n), eight(ctx, n, k, 9), ctx.rows8(m, k)
+    out = torch.empty(m, n, dtype=BF, device=DEV)
+    ctx.linear8(x, w, out, x8=x8)
+    q, s = lo.quantize_ref(x.float().cpu().numpy())
+    want = torch.from_numpy(lo.matmul8_ref(q, s, w.q.cpu().numpy(), w.scale.cpu().numpy())).to(BF)
+    assert torch.equal(bits(out), bits(want))
+    assert np.array_equal(x8.q.cpu().numpy(), q) and np.array_equal(x8.scale.cpu().numpy(), s)

@@ -261,3 +261,15 @@ def test_empty_batch_and_exact_workspace(ctx):
     x, y, d, u = make(5, 4, 151936, BF, 12)
     check(c, x, y, d, u, 1.0)
     c.close()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("shape", [(2, 5, 2047, 1), (2, 5, 2048, 0), (2, 5, 2049, 0), (3, 6, 40, 0), (3, 6, 2048, 3), (4, 11, 500, 0),
+                                   (4, 12, 500, 0), (2, 1, 8192, 0), (2, 1, 16385, 0)])
+@pytest.mark.parametrize("t", [0.9, 0.0])
+def test_either_side_of_one_workgroup(ctx, dtype, shape, t):
+    """Rows and vocabularies up to what one workgroup takes, and just beyond, with
+    a draft model and without."""
+    b, k, v, pad = shape
+    check(ctx, *make(b, k, v, dtype, b + k + v + 1, t=t, pad=pad), t)
+    check(ctx, *make(b, k, v, dtype, b + k + v + 2, t=t, pad=pad, with_draft=False, ragged=True), t)
